@@ -144,6 +144,74 @@ int moe_route_slots(const int32_t* topk_ids, const float* topk_w, int32_t T, int
                     float* slot_weight, int32_t* token_slot, int32_t* tile_table,
                     void* ws, size_t ws_bytes, void* stream);
 
+/* -------------------------------------------------------------------- gate
+ * The routing gate in front of moe_route_slots: expert ids and weights from
+ * router logits [T, E] (row-major, BF16 or float; each finite, or -inf for an
+ * expert the token must not use). E <= 1024, 1 <= k <= min(E, 64), T*k < 2^30.
+ *
+ *   score  MOE_SCORE_SOFTMAX        s = softmax over the row
+ *          MOE_SCORE_SIGMOID        s = 1 / (1 + e^-x)
+ *          MOE_SCORE_SQRT_SOFTPLUS  s = sqrt(log(1 + e^x))
+ *   key    s + bias[e] (float [E] or NULL), compared as float64 numbers; with
+ *          neither bias nor groups the logit itself (the same order)
+ *   groups the experts form n_group runs of E / n_group (n_group <= 64). A
+ *          group's value is the sum of its two highest keys (one key where it
+ *          has one); the topk_group highest groups stay (ties: lower group).
+ *          k <= topk_group * E / n_group.
+ *   choice the k highest keys of the row, highest first, ties to the lower id:
+ *            topk_ids int32 [T, k],
+ *            topk_w   float [T, k] = scale * s, or with renormalize = 1
+ *                     scale * s / (sum of the k scores), 0 if that sum is 0.
+ * Where fewer than k experts can be chosen the rest is id -1, weight 0 (and
+ * dropped by moe_route_slots). token_mask (uint8 [T] or NULL): tokens with
+ * mask 0 get ids -1 and weights 0, and their logits are not used (any bits).
+ * One launch.
+ */
+enum { NVFP4_DT_BF16 = 0, NVFP4_DT_F32 = 1 };
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRT_SOFTPLUS = 2 };
+int moe_gate_topk(const void* logits, int32_t logits_dtype, const float* bias, const uint8_t* token_mask,
+                  int32_t T, int32_t E, int32_t k, int32_t score, int32_t n_group, int32_t topk_group,
+                  int32_t renormalize, float scale, int32_t* topk_ids, float* topk_w, void* stream);
+
+/* Balance loss of the choices, and how often each expert was chosen.
+ * cu_seqlens int32 [B + 1] (device, nondecreasing, within [0, T]): sequence b
+ * is tokens [cu[b], cu[b+1]); tokens in no sequence do not count. NULL with
+ * B = 1: all T tokens. B <= 65535. A token is live when its mask is not 0 and
+ * one of its logits is above -inf; N_b = live tokens of sequence b.
+ *   counts int32 [B, E]   pairs (t, j) of live tokens with topk_ids[t, j] = e
+ *                         (ids outside [0, E) are skipped)
+ *   tokens int32 [B + 2]  N_0 .. N_{B-1}, their sum N, and the number B' of
+ *                         sequences with N_b > 0
+ *   loss   float [2]      [0] mean over those sequences of
+ *                             E * sum_e (counts_be / (N_b k)) * (sum_t q_te / N_b),
+ *                             q = s / (row sum of s)
+ *                         [1] mean over the N live tokens of logsumexp(x_t)^2
+ *                         (0 where there is nothing to average)
+ * ws: at least moe_balance_loss_ws_bytes(T, E, B) bytes (0 for sizes that are
+ * refused). Two launches; the result does not depend on their timing.
+ */
+size_t moe_balance_loss_ws_bytes(int32_t T, int32_t E, int32_t B);
+int moe_balance_loss(const void* logits, int32_t logits_dtype, const int32_t* topk_ids, const uint8_t* token_mask,
+                     const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t E, int32_t k, int32_t score,
+                     float* loss, int32_t* counts, int32_t* tokens, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the logits, d_logits [T, E] (the logits' type, every element
+ * written), as the sum of
+ *   - the gradient through the weights, when d_topk_w (float [T, k]) is given:
+ *     topk_ids, score, renormalize and scale as in moe_gate_topk; the choice
+ *     itself is constant. Ids outside [0, E) take no part; an expert listed
+ *     twice gets both gradients;
+ *   - the gradient of the losses, when d_loss (float [2], device) is given:
+ *     d_loss[i] times that of loss[i], with counts, tokens, cu_seqlens and B
+ *     from moe_balance_loss of the same logits, ids and mask (the counts are
+ *     constant; topk_ids may be NULL when d_topk_w is).
+ * At least one of the two is needed. Rows of masked tokens are 0. One launch.
+ */
+int moe_gate_backward(const void* logits, int32_t logits_dtype, const int32_t* topk_ids, const uint8_t* token_mask,
+                      int32_t T, int32_t E, int32_t k, int32_t score, int32_t renormalize, float scale,
+                      const float* d_topk_w, const float* d_loss, const int32_t* counts, const int32_t* tokens,
+                      const int32_t* cu_seqlens, int32_t B, void* d_logits, void* stream);
+
 /* ---------------------------------------------------------- weight packing
  * Offline weight preparation, step three (after quantize and fold): the
  * grouped GEMM reads weights in a packed order that matches its MFMA operand

@@ -21,7 +21,8 @@ __all__ = [
     "nvfp4_pack_weights", "nvfp4_moe_forward", "nvfp4_quantize_static", "nvfp4_grouped_gemm_silu_nvfp4",
     "nvfp4_moe_forward_static", "calibrate_static_gs", "nvfp4_moe_forward_stage_events", "STAGES",
     "nvfp4_moe_ws_bytes", "nvfp4_moe_ws_layout", "nvfp4_moe_tile_m", "MoEWeights", "prepare_weights",
-    "ws_view",
+    "ws_view", "SCORE_SOFTMAX", "SCORE_SIGMOID", "SCORE_SQRT_SOFTPLUS", "moe_gate_topk", "moe_balance_loss",
+    "moe_balance_loss_ws_bytes", "moe_gate_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
@@ -30,10 +31,12 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 EPI_BF16, EPI_SILU_MUL, EPI_SILU_MUL_DUAL = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRT_SOFTPLUS = 0, 1, 2
 WS_REGIONS = ["x_q", "x_sf", "scalars", "counts", "offsets", "slot_token", "slot_expert", "slot_weight",
               "token_slot", "tiles", "route_scratch", "h", "h_q", "h_sf", "y", "quant_scratch", "end"]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 class _Weights(ctypes.Structure):
@@ -76,6 +79,13 @@ _forward_stages = _sig("nvfp4_moe_forward_stage_events", ctypes.c_int, ctypes.PO
                        _vp, _i32, _i32, _vp, _vp, _sz, ctypes.POINTER(_vp), _vp)
 _forward_static = _sig("nvfp4_moe_forward_static", ctypes.c_int, ctypes.POINTER(_Weights), _vp, _i32, _vp, _vp,
                        _i32, _i32, _vp, _vp, _vp, _sz, _vp)
+_gate_topk = _sig("moe_gate_topk", ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+                  _vp, _vp, _vp)
+_balance_ws = _sig("moe_balance_loss_ws_bytes", _sz, _i32, _i32, _i32)
+_balance = _sig("moe_balance_loss", ctypes.c_int, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                _vp, _vp, _vp, _vp, _sz, _vp)
+_gate_backward = _sig("moe_gate_backward", ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
+                      _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp)
 
 
 class NVFP4Error(RuntimeError):
@@ -224,6 +234,116 @@ def moe_route_slots(topk_ids, topk_w, expert_start, num_local, tile_m):
                   _ptr(out["slot_weight"]), _ptr(out["token_slot"]), _ptr(out["tile_table"]),
                   _ptr(ws), ws.numel(), _stream()), "moe_route_slots")
     return out
+
+
+# -------------------------------------------------------------------------- gate
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _float_dev(t, name):
+    """t as _dev, BF16 or float32; returns its NVFP4_DT_* code."""
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name}: expected BF16 or float32, got {t.dtype}")
+    _dev(t, t.dtype, name)
+    return _DTYPES[t.dtype]
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _opt(t, dtype, shape, name):
+    """An optional input tensor of exactly this shape."""
+    if t is None:
+        return None
+    _dev(t, dtype, name)
+    return _shape(t, shape, name)
+
+
+def moe_gate_topk(logits, k, score=SCORE_SOFTMAX, bias=None, token_mask=None, n_group=1, topk_group=1,
+                  renormalize=True, scale=1.0, topk_ids=None, topk_w=None):
+    """Router logits BF16 or float32 [T, E] -> (topk_ids int32 [T, k], topk_w float32 [T, k]), as moe_route_slots
+    and nvfp4_moe_forward take them. bias: float32 [E], added to the scores for the choice alone; token_mask: uint8
+    [T], 0 for padding (ids -1, weights 0); n_group / topk_group: choose within the best groups of experts."""
+    dt = _float_dev(logits, "logits")
+    T, E = _matrix(logits, "logits")
+    dev = logits.device
+    _opt(bias, torch.float32, (E,), "bias")
+    _opt(token_mask, torch.uint8, (T,), "token_mask")
+    topk_ids = (torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None
+                else _buf(topk_ids, torch.int32, T * k, "topk_ids"))
+    topk_w = (torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None
+              else _buf(topk_w, torch.float32, T * k, "topk_w"))
+    _check(_gate_topk(_ptr(logits), dt, _ptr(bias), _ptr(token_mask), T, E, k, score, n_group, topk_group,
+                      int(renormalize), scale, _ptr(topk_ids), _ptr(topk_w), _stream()), "moe_gate_topk")
+    return topk_ids, topk_w
+
+
+def moe_balance_loss_ws_bytes(T, E, B) -> int:
+    return int(_balance_ws(T, E, B))
+
+
+def _num_seqs(cu_seqlens):
+    if cu_seqlens is None:
+        return 1
+    _dev(cu_seqlens, torch.int32, "cu_seqlens")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError(f"cu_seqlens: expected [B + 1] with B >= 1, got shape {tuple(cu_seqlens.shape)}")
+    return cu_seqlens.numel() - 1
+
+
+def moe_balance_loss(logits, topk_ids, score=SCORE_SOFTMAX, token_mask=None, cu_seqlens=None, loss=None, counts=None,
+                     tokens=None, ws=None):
+    """Balance loss and mean squared log-sum of the logits over the gate's choices -> (loss float32 [2], counts
+    int32 [B, E], tokens int32 [B + 2]); counts and tokens are what moe_gate_backward takes. cu_seqlens: int32
+    [B + 1] sequence bounds (None: all tokens are one sequence)."""
+    dt = _float_dev(logits, "logits")
+    T, E = _matrix(logits, "logits")
+    _dev(topk_ids, torch.int32, "topk_ids")
+    _shape(topk_ids, (T, _matrix(topk_ids, "topk_ids")[1]), "topk_ids")
+    k = topk_ids.shape[1]
+    B = _num_seqs(cu_seqlens)
+    dev = logits.device
+    _opt(token_mask, torch.uint8, (T,), "token_mask")
+    loss = torch.empty(2, dtype=torch.float32, device=dev) if loss is None else _buf(loss, torch.float32, 2, "loss")
+    counts = (torch.empty((B, E), dtype=torch.int32, device=dev) if counts is None
+              else _buf(counts, torch.int32, B * E, "counts"))
+    tokens = (torch.empty(B + 2, dtype=torch.int32, device=dev) if tokens is None
+              else _buf(tokens, torch.int32, B + 2, "tokens"))
+    ws = _alloc_ws(moe_balance_loss_ws_bytes(T, E, B), dev) if ws is None else _buf(ws, torch.uint8, 0, "ws")
+    _check(_balance(_ptr(logits), dt, _ptr(topk_ids), _ptr(token_mask), _ptr(cu_seqlens), B, T, E, k, score,
+                    _ptr(loss), _ptr(counts), _ptr(tokens), _ptr(ws), ws.numel(), _stream()), "moe_balance_loss")
+    return loss, counts, tokens
+
+
+def moe_gate_backward(logits, topk_ids, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, token_mask=None,
+                      d_topk_w=None, d_loss=None, counts=None, tokens=None, cu_seqlens=None, d_logits=None):
+    """Gradient of the logits (their type and shape): through the weights when d_topk_w (float32 [T, k]) is given
+    (score, renormalize and scale as in moe_gate_topk), of the losses when d_loss (float32 [2]) is given (counts
+    and tokens from moe_balance_loss, the same cu_seqlens), or the sum of both."""
+    dt = _float_dev(logits, "logits")
+    T, E = _matrix(logits, "logits")
+    _dev(topk_ids, torch.int32, "topk_ids")
+    k = _matrix(topk_ids, "topk_ids")[1]
+    _shape(topk_ids, (T, k), "topk_ids")
+    _opt(token_mask, torch.uint8, (T,), "token_mask")
+    _opt(d_topk_w, torch.float32, (T, k), "d_topk_w")
+    B = 1
+    if d_loss is not None:
+        B = _num_seqs(cu_seqlens)
+        _opt(d_loss, torch.float32, (2,), "d_loss")
+        if counts is None or tokens is None:
+            raise ValueError("d_loss needs counts and tokens of moe_balance_loss")
+        _buf(counts, torch.int32, B * E, "counts")
+        _buf(tokens, torch.int32, B + 2, "tokens")
+    d_logits = torch.empty_like(logits) if d_logits is None else _buf(d_logits, logits.dtype, T * E, "d_logits")
+    _check(_gate_backward(_ptr(logits), dt, _ptr(topk_ids), _ptr(token_mask), T, E, k, score, int(renormalize), scale,
+                          _ptr(d_topk_w), _ptr(d_loss), _ptr(counts), _ptr(tokens), _ptr(cu_seqlens), B,
+                          _ptr(d_logits), _stream()), "moe_gate_backward")
+    return d_logits
 
 
 # ------------------------------------------------------------------ grouped GEMM

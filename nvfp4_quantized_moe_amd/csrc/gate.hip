@@ -1,0 +1,879 @@
+// The routing gate in front of the layer: scores of a token's logits, the k
+// highest, their weights; the balance loss over these choices with per-expert
+// counts; and the gradient of both with respect to the logits.
+//
+// Score of a logit x: softmax over the row, 1 / (1 + e^-x), or
+// sqrt(log(1 + e^x)). The choice goes by key = score + bias (float64 order,
+// see gate_topk_kernel), the weight by the score alone.
+//
+// One wave owns one token in every kernel here: lane l holds logits l,
+// l + 64, ... (any E and any row alignment give coalesced loads), row
+// reductions are register-only (wave.h), and a workgroup needs no barrier.
+#include <type_traits>
+
+#include "common.h"
+#include "internal.h"
+#include "wave.h"
+
+namespace nvfp4 {
+
+constexpr int kGateWaves = 4;      // tokens per workgroup
+constexpr int kGateMaxExperts = 1024;
+constexpr int kGateMaxK = 64;      // lane j holds choice j
+constexpr float kInf = __builtin_inff();
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p, size_t i);
+template <>
+__device__ __forceinline__ float load_logit<float>(const float* p, size_t i) {
+  return p[i];
+}
+template <>
+__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p, size_t i) {
+  return bf16_to_f32(p[i]);
+}
+__device__ __forceinline__ void store_logit(float* p, size_t i, float v) { p[i] = v; }
+__device__ __forceinline__ void store_logit(uint16_t* p, size_t i, float v) { p[i] = (uint16_t)f32_to_bf16(v); }
+
+// Scores that depend on one logit alone (x = -inf gives 0).
+__device__ __forceinline__ float sigmoid_score(float x) { return 1.0f / (1.0f + expf(-x)); }
+__device__ __forceinline__ double sigmoid_score(double x) { return 1.0 / (1.0 + exp(-x)); }
+// sqrt(log(1 + e^x)) with the large term outside the logarithm. Far below 0
+// it equals e^(x/2) to the last bit, and e^x itself would underflow first.
+__device__ __forceinline__ float sqrt_softplus(float x) {
+  return x < -20.0f ? expf(0.5f * x) : sqrtf(fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))));
+}
+__device__ __forceinline__ double sqrt_softplus(double x) {
+  return x < -40.0 ? exp(0.5 * x) : sqrt(fmax(x, 0.0) + log1p(exp(-fabs(x))));
+}
+template <typename F>
+__device__ __forceinline__ F pointwise_score(F x, int score) {
+  return score == MOE_SCORE_SIGMOID ? sigmoid_score(x) : sqrt_softplus(x);
+}
+// derivative of a pointwise score s = score(x); the sigmoid's from e^-|x|,
+// since 1 - s has lost its digits where s is near 1
+__device__ __forceinline__ float score_slope(float x, float s, int score) {
+  if (score == MOE_SCORE_SIGMOID) {
+    const float e = expf(-fabsf(x));
+    return e / ((1.0f + e) * (1.0f + e));
+  }
+  return x < -20.0f ? 0.5f * s : 0.5f * sigmoid_score(x) / s;
+}
+
+struct GateShape {
+  int T, E, k, score;
+  int n_group, topk_group, group_size;
+  int renormalize;
+  float scale;
+};
+
+// Key of every logit of the lane, in F (float or double): the logits
+// themselves when the order of scores is theirs (no bias, one group).
+template <typename F, int VPT>
+__device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bias, const GateShape& g, F (&key)[VPT]) {
+  const int lane = threadIdx.x & 63;
+  const F inf = (F)kInf;
+  if (!bias && g.n_group == 1) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) key[v] = (F)x[v];
+    return;
+  }
+  if (g.score == MOE_SCORE_SOFTMAX) {
+    F top = -inf, sum = 0;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) top = (F)x[v] > top ? (F)x[v] : top;
+    top = wave_all_max(top);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      key[v] = x[v] > -kInf ? exp((F)x[v] - top) : (F)0;
+      sum += key[v];
+    }
+    sum = wave_all_sum(sum);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) key[v] = key[v] / sum;
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) key[v] = pointwise_score((F)x[v], g.score);
+  }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = v * 64 + lane;
+    if (bias && e < g.E) key[v] += (F)bias[e];
+    if (!(x[v] > -kInf)) key[v] = -inf;
+  }
+}
+
+// Drops the experts of the groups that are not kept: a group's value is the
+// sum of its two highest keys; the topk_group highest values stay, ties to the
+// lower group. Returns how far apart the last kept and the first dropped value
+// are, relative to their size (float keys: whether float64 could decide
+// otherwise), in *gap and *size. keys: LDS, E of them, this wave's own.
+template <typename F, int VPT>
+__device__ __forceinline__ void keep_groups(F (&key)[VPT], const GateShape& g, F* keys, F* gap, F* size) {
+  const int lane = threadIdx.x & 63;
+  const F inf = (F)kInf;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    if (v * 64 + lane < g.E) keys[v * 64 + lane] = key[v];
+  wave_lds_fence();
+  int per = 64;  // lanes per group: a power of two, per * n_group <= 64
+  while (per * g.n_group > 64) per >>= 1;
+  const int mine = lane / per, sub = lane % per;
+  F a = -inf, b = -inf;  // the two highest of this lane's share, a >= b
+  if (mine < g.n_group)
+    for (int i = sub; i < g.group_size; i += per) {
+      const F v = keys[mine * g.group_size + i];
+      b = fmax(b, fmin(a, v));
+      a = fmax(a, v);
+    }
+  for (int o = 1; o < per; o <<= 1) {
+    const F a2 = __shfl_xor(a, o, 64), b2 = __shfl_xor(b, o, 64);
+    b = fmax(fmax(b, b2), fmin(a, a2));
+    a = fmax(a, a2);
+  }
+  const F value = a + (b > -inf ? b : (F)0);  // -inf when nothing in the group can be chosen
+  int rank = 0;
+  for (int j = 0; j < g.n_group; ++j) {
+    const F o = lane_value(value, j * per);
+    rank += (o > value || (o == value && j < mine)) ? 1 : 0;
+  }
+  const bool kept = mine < g.n_group && rank < g.topk_group;
+  const F lowest = -wave_all_max(kept ? -value : -inf);
+  const F highest = wave_all_max(mine < g.n_group && !kept ? value : -inf);
+  *gap = lowest - highest;
+  *size = fmax(fabs(lowest), fabs(highest));
+  const uint64_t stays = __ballot(kept);
+  const uint32_t magic = ((1u << 20) + (uint32_t)g.group_size - 1u) / (uint32_t)g.group_size;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    // e / group_size: exact for e, group_size <= 1024
+    const uint32_t grp = ((uint32_t)(v * 64 + lane) * magic) >> 20;
+    if (!((stays >> ((grp * (uint32_t)per) & 63u)) & 1u)) key[v] = -inf;
+  }
+  wave_lds_fence();
+}
+
+// The `want` highest keys, one wave maximum at a time, ties to the lowest
+// expert: lane j < want gets the j-th (id -1 when none is left).
+template <typename F, int VPT>
+__device__ __forceinline__ void pick_by_rounds(F (&key)[VPT], int want, int* id, F* at) {
+  const int lane = threadIdx.x & 63;
+  const F inf = (F)kInf;
+  *id = -1;
+  *at = -inf;
+  for (int r = 0; r < want; ++r) {
+    F top = -inf;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) top = fmax(top, key[v]);
+    top = wave_all_max(top);
+    if (!(top > -inf)) break;
+    int e = 0x7FFFFFFF;
+#pragma unroll
+    for (int v = VPT - 1; v >= 0; --v)
+      if (key[v] == top) e = v * 64 + lane;
+    e = wave_all_min_i32(e);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      if (v * 64 + lane == e) key[v] = -inf;
+    if (lane == r) {
+      *id = e;
+      *at = top;
+    }
+  }
+}
+
+// The weights of the choices (lane j < k: expert id) and the stores.
+template <typename L, int VPT>
+__device__ __forceinline__ void write_choices(const L* logits, size_t row, const float (&x)[VPT], const GateShape& g,
+                                              int id, size_t t, int32_t* ids, float* w) {
+  const int lane = threadIdx.x & 63;
+  const bool on = lane < g.k && id >= 0;
+  const float xl = on ? load_logit(logits, row + (on ? id : 0)) : -kInf;
+  float s;
+  if (g.score == MOE_SCORE_SOFTMAX) {
+    if (g.renormalize) {  // the softmax over the choices alone: nothing of the row's sum is left in it
+      const float top = wave_all_max(xl);
+      s = on ? expf(xl - top) : 0.0f;
+    } else {
+      float top = -kInf, sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) top = fmaxf(top, x[v]);
+      top = wave_all_max(top);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) sum += x[v] > -kInf ? expf(x[v] - top) : 0.0f;
+      sum = wave_all_sum(sum);
+      s = on ? expf(xl - top) / sum : 0.0f;
+    }
+  } else {
+    s = on ? pointwise_score(xl, g.score) : 0.0f;
+  }
+  if (g.renormalize) {
+    const float sum = wave_all_sum(s);
+    s = sum > 0.0f ? s / sum : 0.0f;
+  }
+  if (lane < g.k) {
+    ids[t * g.k + lane] = on ? id : -1;
+    w[t * g.k + lane] = s * g.scale;
+  }
+}
+
+// One wave per token. The order of the choices is that of the keys in
+// float64; float32 keys decide it wherever two neighbours are further apart
+// than their rounding (2^-20 of the scores; 2^-17 for softmax, whose argument
+// x - max is rounded first) or are the same sum of the same numbers, and the
+// row is done again in float64 where they are not.
+template <typename L, int VPT>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __restrict__ logits,
+                                                                    const float* __restrict__ bias,
+                                                                    const uint8_t* __restrict__ mask, GateShape g,
+                                                                    int32_t* __restrict__ ids, float* __restrict__ w) {
+  extern __shared__ double lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
+  if (t >= g.T) return;
+  if (mask && mask[t] == 0) {
+    if (lane < g.k) {
+      ids[t * g.k + lane] = -1;
+      w[t * g.k + lane] = 0.0f;
+    }
+    return;
+  }
+  const size_t row = (size_t)t * g.E;
+  float x[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) x[v] = v * 64 + lane < g.E ? load_logit(logits, row + v * 64 + lane) : -kInf;
+
+  const bool by_logit = !bias && g.n_group == 1;
+  float key[VPT];
+  int id;
+  float at;
+  gate_keys(x, bias, g, key);
+  bool doubt = false;
+  const float tol = g.score == MOE_SCORE_SOFTMAX ? 0x1p-17f : 0x1p-20f;
+  if (g.n_group > 1) {
+    float gap, size;
+    keep_groups(key, g, reinterpret_cast<float*>(lds + (size_t)wave * g.E), &gap, &size);
+    // a value is a sum of two keys, each score + bias, |bias| <= bmax
+    float bmax = 0.0f;
+    if (bias)
+      for (int e = lane; e < g.E; e += 64) bmax = fmaxf(bmax, fabsf(bias[e]));
+    bmax = wave_all_max(bmax);
+    doubt = !(gap > 4.0f * tol * (size + 2.0f * bmax));
+    if (g.topk_group == g.n_group) doubt = false;
+  }
+  const int want = by_logit ? g.k : min(g.k + 1, 64);
+  pick_by_rounds(key, want, &id, &at);
+  if (!by_logit) {
+    const float xl = id >= 0 ? load_logit(logits, row + id) : -kInf;
+    const float bl = id >= 0 && bias ? bias[id] : 0.0f;
+    const float next = __shfl_down(at, 1, 64), xn = __shfl_down(xl, 1, 64), bn = __shfl_down(bl, 1, 64);
+    const int idn = __shfl_down(id, 1, 64);
+    const bool same = xl == xn && bl == bn;
+    const float size = fabsf(at) + fabsf(next) + fabsf(bl) + fabsf(bn);
+    const bool close = lane + 1 < want && idn >= 0 && !same && !(at - next > 2.0f * tol * size);
+    doubt = doubt || __ballot(close) != 0 || want == g.k;
+  }
+  if (doubt) {
+    double key64[VPT], gap, size, at64;
+    gate_keys(x, bias, g, key64);
+    if (g.n_group > 1) keep_groups(key64, g, lds + (size_t)wave * g.E, &gap, &size);
+    pick_by_rounds(key64, g.k, &id, &at64);
+  }
+  if (lane >= g.k) id = -1;
+  write_choices(logits, row, x, g, id, (size_t)t, ids, w);
+}
+
+// ---------------------------------------------------------------- balance loss
+//
+// Per sequence b with N_b live tokens (mask nonzero, some logit above -inf):
+//   share P_be = (1/N_b) sum_t q_te,   f_be = counts_be / (N_b k),
+//   L = mean over the sequences with N_b > 0 of E sum_e f_be P_be,
+//   z = mean over all live tokens of logsumexp(x_t)^2,
+// with q the score divided by its row sum. Two launches: workgroups own runs
+// of at most `chunk` tokens of one sequence and leave partial sums (slots, no
+// float atomics: the result does not depend on the order they finish in); the
+// second joins them per sequence and column block, and its last workgroup to
+// finish adds the terms.
+
+struct BalanceShape {
+  int T, E, k, B, score;
+  int chunk, max_chunks, col_blocks;
+};
+struct BalanceWs {
+  float* q;          // [max_chunks][E] sums of q
+  int32_t* counts;   // [max_chunks][E]
+  double* z;         // [max_chunks] sums of logsumexp^2
+  int32_t* live;     // [max_chunks]
+  double* term;      // [B][col_blocks] this sequence's share of L before the mean
+  double* z_seq;     // [B]
+  uint32_t* done;    // workgroups of the second launch that have finished
+};
+
+struct Span {
+  int seq, begin, end;  // tokens [begin, end) of sequence seq; empty when there is no such chunk
+};
+__device__ __forceinline__ int2 seq_bounds(const int32_t* cu, int s, int T) {
+  if (!cu) return make_int2(0, T);
+  const int b = min(max(cu[s], 0), T);
+  return make_int2(b, max(b, min(cu[s + 1], T)));
+}
+// Chunk number i over all sequences in order (wave-uniform).
+__device__ Span find_chunk(const int32_t* cu, const BalanceShape& g, int i) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int base = 0; base < g.B; base += 64) {
+    const int s = base + lane;
+    const int2 r = s < g.B ? seq_bounds(cu, s, g.T) : make_int2(0, 0);
+    const int n = (r.y - r.x + g.chunk - 1) / g.chunk;
+    int incl = n;
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    const uint64_t past = __ballot(before + incl > i);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int first = before + __shfl(incl - n, l, 64);
+      const int begin = __shfl(r.x, l, 64) + (i - first) * g.chunk;
+      return {base + l, begin, min(begin + g.chunk, __shfl(r.y, l, 64))};
+    }
+    before += __shfl(incl, 63, 64);
+  }
+  return {0, 0, 0};
+}
+
+// Normalized scores of a row (lane l: experts l, l + 64, ...). Returns false
+// for a row without a logit above -inf. sum: of the scores, lse: log of the
+// sum of e^x; e[v] = e^(x - lse).
+struct RowSums {
+  float sum, lse;
+};
+template <int VPT>
+__device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, float (&q)[VPT], float (&p)[VPT],
+                                           RowSums* r) {
+  float top = -kInf;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) top = fmaxf(top, x[v]);
+  top = wave_all_max(top);
+  if (!(top > -kInf)) return false;
+  float es = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    p[v] = x[v] > -kInf ? expf(x[v] - top) : 0.0f;
+    es += p[v];
+  }
+  es = wave_all_sum(es);
+  r->lse = top + logf(es);
+  const float inv = 1.0f / es;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) p[v] *= inv;
+  if (score == MOE_SCORE_SOFTMAX) {
+    r->sum = 1.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) q[v] = p[v];
+    return true;
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    q[v] = x[v] > -kInf ? pointwise_score(x[v], score) : 0.0f;
+    sum += q[v];
+  }
+  sum = wave_all_sum(sum);
+  r->sum = sum;
+  const float is = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) q[v] *= is;
+  return true;
+}
+
+template <typename L, int VPT>
+__global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const L* __restrict__ logits,
+                                                                          const int32_t* __restrict__ ids,
+                                                                          const uint8_t* __restrict__ mask,
+                                                                          const int32_t* __restrict__ cu,
+                                                                          BalanceShape g, BalanceWs ws) {
+  extern __shared__ double lds[];
+  float* q_sh = reinterpret_cast<float*>(lds);                    // [kGateWaves][E]
+  int32_t* hist = reinterpret_cast<int32_t*>(q_sh + kGateWaves * g.E);  // [E]
+  __shared__ double z_sh[kGateWaves];
+  __shared__ int n_sh[kGateWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.done = 0u;
+  for (int e = threadIdx.x; e < g.E; e += blockDim.x) hist[e] = 0;
+  const Span span = find_chunk(cu, g, (int)blockIdx.x);
+  if (span.begin >= span.end) return;  // whole workgroup
+  __syncthreads();
+  float acc[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) acc[v] = 0.0f;
+  double z = 0.0;
+  int n = 0;
+  for (int t = span.begin + wave; t < span.end; t += kGateWaves) {
+    if (mask && mask[t] == 0) continue;
+    float x[VPT], q[VPT], p[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      x[v] = v * 64 + lane < g.E ? load_logit(logits, (size_t)t * g.E + v * 64 + lane) : -kInf;
+    RowSums r;
+    if (!row_scores(x, g.score, q, p, &r)) continue;
+    const int id = lane < g.k ? ids[(size_t)t * g.k + lane] : -1;
+    if (id >= 0 && id < g.E) atomicAdd(&hist[id], 1);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) acc[v] += q[v];
+    z += (double)r.lse * (double)r.lse;
+    ++n;
+  }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    if (v * 64 + lane < g.E) q_sh[wave * g.E + v * 64 + lane] = acc[v];
+  if (lane == 0) {
+    z_sh[wave] = z;
+    n_sh[wave] = n;
+  }
+  __syncthreads();
+  const size_t at = (size_t)blockIdx.x * g.E;
+  for (int e = threadIdx.x; e < g.E; e += blockDim.x) {
+    float s = q_sh[e];
+    for (int w = 1; w < kGateWaves; ++w) s += q_sh[w * g.E + e];
+    ws.q[at + e] = s;
+    ws.counts[at + e] = hist[e];
+  }
+  if (threadIdx.x == 0) {
+    double zs = 0.0;
+    int ns = 0;
+    for (int w = 0; w < kGateWaves; ++w) {
+      zs += z_sh[w];
+      ns += n_sh[w];
+    }
+    ws.z[blockIdx.x] = zs;
+    ws.live[blockIdx.x] = ns;
+  }
+}
+
+// Workgroup (c, b): experts [64c, 64c + 64) of sequence b.
+constexpr int kJoinWaves = 4;
+__global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(const int32_t* __restrict__ cu, BalanceShape g,
+                                                                       BalanceWs ws, int32_t* __restrict__ counts,
+                                                                       int32_t* __restrict__ tokens,
+                                                                       float* __restrict__ loss) {
+  __shared__ double q_sh[kJoinWaves][64], red_d[2][kJoinWaves];
+  __shared__ int c_sh[kJoinWaves][64], red_i[2][kJoinWaves], s_last;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int b = blockIdx.y, e = blockIdx.x * 64 + lane;
+  // this sequence's chunks: [first, first + n)
+  int first = 0;
+  if (cu) {
+    for (int base = 0; base < b; base += 64) {
+      const int s = base + lane;
+      int v = 0;
+      if (s < b) {
+        const int2 r = seq_bounds(cu, s, g.T);
+        v = (r.y - r.x + g.chunk - 1) / g.chunk;
+      }
+      for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+      first += v;
+    }
+  }
+  const int2 range = seq_bounds(cu, b, g.T);
+  const int end = min(first + (range.y - range.x + g.chunk - 1) / g.chunk, g.max_chunks);
+  double q = 0.0;
+  int cnt = 0;
+  if (e < g.E)
+    for (int c = first + wave; c < end; c += kJoinWaves) {
+      q += (double)ws.q[(size_t)c * g.E + e];
+      cnt += ws.counts[(size_t)c * g.E + e];
+    }
+  q_sh[wave][lane] = q;
+  c_sh[wave][lane] = cnt;
+  int n = 0;
+  double z = 0.0;
+  for (int c = first + (int)threadIdx.x; c < end; c += blockDim.x) {
+    n += ws.live[c];
+    z += ws.z[c];
+  }
+  for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
+  z = wave_all_sum(z);
+  if (lane == 0) {
+    red_i[0][wave] = n;
+    red_d[0][wave] = z;
+  }
+  __syncthreads();
+  n = 0;
+  z = 0.0;
+  for (int w = 0; w < kJoinWaves; ++w) {
+    n += red_i[0][w];
+    z += red_d[0][w];
+  }
+  if (wave == 0) {
+    q = 0.0;
+    cnt = 0;
+    for (int w = 0; w < kJoinWaves; ++w) {
+      q += q_sh[w][lane];
+      cnt += c_sh[w][lane];
+    }
+    if (e < g.E) counts[(size_t)b * g.E + e] = cnt;
+    const double sum = wave_all_sum(e < g.E ? (double)cnt * q : 0.0);
+    if (lane == 0) {
+      ws.term[(size_t)b * g.col_blocks + blockIdx.x] = n > 0 ? sum * g.E / ((double)n * n * g.k) : 0.0;
+      if (blockIdx.x == 0) {
+        tokens[b] = n;
+        ws.z_seq[b] = z;
+      }
+      __threadfence();
+      s_last = atomicAdd(ws.done, 1u) == gridDim.x * gridDim.y - 1u;
+      __threadfence();
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  // the last workgroup: agent-scope loads, since the terms come from other XCDs
+  double term = 0.0, zs = 0.0;
+  int total = 0, seqs = 0;
+  for (int s = threadIdx.x; s < g.B; s += blockDim.x) {
+    const int m = __hip_atomic_load(&tokens[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    total += m;
+    seqs += m > 0;
+    zs += __hip_atomic_load(&ws.z_seq[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int c = 0; c < g.col_blocks; ++c)
+      term += __hip_atomic_load(&ws.term[(size_t)s * g.col_blocks + c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  for (int o = 1; o < 64; o <<= 1) {
+    total += __shfl_xor(total, o, 64);
+    seqs += __shfl_xor(seqs, o, 64);
+  }
+  term = wave_all_sum(term);
+  zs = wave_all_sum(zs);
+  __syncthreads();
+  if (lane == 0) {
+    red_d[0][wave] = term;
+    red_d[1][wave] = zs;
+    red_i[0][wave] = total;
+    red_i[1][wave] = seqs;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    term = zs = 0.0;
+    total = seqs = 0;
+    for (int w = 0; w < kJoinWaves; ++w) {
+      term += red_d[0][w];
+      zs += red_d[1][w];
+      total += red_i[0][w];
+      seqs += red_i[1][w];
+    }
+    tokens[g.B] = total;
+    tokens[g.B + 1] = seqs;
+    loss[0] = seqs > 0 ? (float)(term / seqs) : 0.0f;
+    loss[1] = total > 0 ? (float)(zs / total) : 0.0f;
+  }
+}
+
+// -------------------------------------------------------------------- gradient
+//
+// dL/dx of one token, from the gradient of its weights and (or) of the two
+// losses:
+//   weights  w_j = c s_j / S:  ds_j = (c dw_j - sum_m c dw_m s_m / S) / S, or c dw_j
+//            without renormalization; softmax weights renormalized are the
+//            softmax over the choices, dx_j = w_j (c dw_j - sum_m c dw_m w_m)
+//   balance  dq_e = g0 E counts_be / (B' N_b^2 k), then ds_e = (dq_e - sum dq q) / sum s
+//   z        2 g1 lse p_e / N
+// and dx_e = s'(x_e) ds_e, or p_e (ds_e - sum ds p) for softmax.
+struct GateGradArgs {
+  const int32_t* ids;
+  const float* d_w;      // NULL: no gradient through the weights
+  const float* d_loss;   // NULL: none through the losses
+  const int32_t* counts;
+  const int32_t* tokens;
+  const int32_t* cu;
+  const uint8_t* mask;
+  int T, E, k, B, score, renormalize;
+  float scale;
+};
+
+template <typename L, int VPT>
+__global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L* __restrict__ logits, GateGradArgs a,
+                                                                        L* __restrict__ d_logits) {
+  extern __shared__ double lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
+  if (t >= a.T) return;
+  float* direct = reinterpret_cast<float*>(lds) + (size_t)wave * a.E;
+  const size_t row = (size_t)t * a.E;
+  float x[VPT], dx[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) dx[v] = 0.0f;
+  bool live = !(a.mask && a.mask[t] == 0);
+  if (live) {
+    float top = -kInf;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      x[v] = v * 64 + lane < a.E ? load_logit(logits, row + v * 64 + lane) : -kInf;
+      top = fmaxf(top, x[v]);
+    }
+    live = wave_all_max(top) > -kInf;
+  }
+  if (live) {
+    // sequence of the token; -1: it lies in none and the losses do not see it
+    int seq = 0;
+    if (a.d_loss && a.cu) {
+      int lo = 0, hi = a.B + 1;  // cu entries <= t
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu[mid] <= (int)t) lo = mid + 1;
+        else hi = mid;
+      }
+      seq = lo - 1 < a.B ? lo - 1 : -1;
+    }
+    const bool in_loss = a.d_loss && seq >= 0;
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    const bool row_softmax = a.d_w && softmax && !a.renormalize;
+    float q[VPT], p[VPT];
+    RowSums r = {1.0f, 0.0f};
+    if (in_loss || row_softmax) row_scores(x, a.score, q, p, &r);
+    float inner = 0.0f;  // softmax: sum over the row of (gradient of p) p
+    if (a.d_w) {
+      const int id = lane < a.k ? a.ids[(size_t)t * a.k + lane] : -1;
+      const bool on = id >= 0 && id < a.E;
+      const float xl = on ? load_logit(logits, row + id) : -kInf;
+      const bool some = on && xl > -kInf;
+      const float c = some ? a.scale * a.d_w[(size_t)t * a.k + lane] : 0.0f;
+      float d;  // dx of this choice, apart from the softmax row term
+      if (softmax && a.renormalize) {
+        const float m = wave_all_max(some ? xl : -kInf);
+        float e = some ? expf(xl - m) : 0.0f;
+        e = e / fmaxf(wave_all_sum(e), 1.0f);  // the largest is e^0; 1 also where nothing is chosen
+        d = e * (c - wave_all_sum(c * e));
+      } else {
+        const float s = !some ? 0.0f : softmax ? expf(xl - r.lse) : pointwise_score(xl, a.score);
+        float ds = c;
+        if (a.renormalize) {
+          const float sum = wave_all_sum(s);
+          const float is = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const float dot = wave_all_sum(c * s) * is;
+          ds = some ? (c - dot) * is : 0.0f;
+        }
+        if (softmax) {
+          d = s * ds;
+          inner = wave_all_sum(d);
+        } else {
+          d = some ? ds * score_slope(xl, s, a.score) : 0.0f;
+        }
+      }
+      // an expert listed twice gets both gradients: every lane of it holds the sum
+      float all = 0.0f;
+      for (int j = 0; j < a.k; ++j) {
+        const int other = __builtin_amdgcn_readlane(id, j);
+        const float dj = lane_value(d, j);
+        all += other == id ? dj : 0.0f;
+      }
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        if (v * 64 + lane < a.E) direct[v * 64 + lane] = 0.0f;
+      wave_lds_fence();
+      if (on) direct[id] = all;
+      wave_lds_fence();
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        if (v * 64 + lane < a.E) dx[v] = direct[v * 64 + lane];
+    }
+    float dq[VPT];
+    float zc = 0.0f;
+    if (in_loss) {
+      const float n = (float)a.tokens[seq];
+      const float f0 = a.d_loss[0] * (float)a.E / ((float)a.tokens[a.B + 1] * n * n * (float)a.k);
+      float dot = 0.0f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int e = v * 64 + lane;
+        dq[v] = e < a.E ? f0 * (float)a.counts[(size_t)seq * a.E + e] : 0.0f;
+        dot += dq[v] * q[v];
+      }
+      dot = wave_all_sum(dot);
+      zc = 2.0f * a.d_loss[1] * r.lse / (float)a.tokens[a.B];
+      if (softmax) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) dx[v] += p[v] * (dq[v] - dot - inner + zc);
+      } else {
+        const float is = r.sum > 0.0f ? 1.0f / r.sum : 0.0f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const float slope = x[v] > -kInf ? score_slope(x[v], q[v] * r.sum, a.score) : 0.0f;
+          dx[v] += (dq[v] - dot) * is * slope + zc * p[v];
+        }
+      }
+    } else if (row_softmax) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) dx[v] -= p[v] * inner;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    if (v * 64 + lane < a.E) store_logit(d_logits, row + v * 64 + lane, dx[v]);
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+static int gate_check(const void* logits, int32_t dtype, int32_t T, int32_t E, int32_t k, int32_t score) {
+  if (T < 0 || E < 1 || E > kGateMaxExperts || k < 1 || k > kGateMaxK || k > E) return NVFP4_ERR_SHAPE;
+  if ((int64_t)T * k >= (1ll << 30)) return NVFP4_ERR_SHAPE;
+  if (dtype != NVFP4_DT_BF16 && dtype != NVFP4_DT_F32) return NVFP4_ERR_ARG;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SQRT_SOFTPLUS)
+    return NVFP4_ERR_ARG;
+  if (T > 0 && !logits) return NVFP4_ERR_NULL;
+  if (T > 0 && !nvfp4_aligned16(logits)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
+// Values per lane for E experts: the kernels are built for these.
+template <typename Fn>
+static int gate_by_width(int32_t E, Fn fn) {
+  const int need = (E + 63) / 64;
+  if (need <= 1) return fn(std::integral_constant<int, 1>());
+  if (need <= 2) return fn(std::integral_constant<int, 2>());
+  if (need <= 4) return fn(std::integral_constant<int, 4>());
+  if (need <= 6) return fn(std::integral_constant<int, 6>());
+  if (need <= 8) return fn(std::integral_constant<int, 8>());
+  return fn(std::integral_constant<int, 16>());
+}
+
+extern "C" int moe_gate_topk(const void* logits, int32_t logits_dtype, const float* bias, const uint8_t* token_mask,
+                             int32_t T, int32_t E, int32_t k, int32_t score, int32_t n_group, int32_t topk_group,
+                             int32_t renormalize, float scale, int32_t* topk_ids, float* topk_w, void* stream) {
+  const int st = gate_check(logits, logits_dtype, T, E, k, score);
+  if (st) return st;
+  if (n_group < 1 || n_group > 64 || E % n_group != 0 || topk_group < 1 || topk_group > n_group)
+    return NVFP4_ERR_SHAPE;
+  if (k > topk_group * (E / n_group)) return NVFP4_ERR_SHAPE;
+  if (renormalize != 0 && renormalize != 1) return NVFP4_ERR_ARG;
+  if (T == 0) return NVFP4_OK;
+  if (!topk_ids || !topk_w) return NVFP4_ERR_NULL;
+  if (!nvfp4_aligned16(topk_ids) || !nvfp4_aligned16(topk_w) || !nvfp4_aligned16(bias) ||
+      !nvfp4_aligned16(token_mask))
+    return NVFP4_ERR_ALIGN;
+  const GateShape g = {T, E, k, score, n_group, topk_group, E / n_group, renormalize, scale};
+  const unsigned grid = (unsigned)((T + kGateWaves - 1) / kGateWaves);
+  const size_t lds = n_group > 1 ? (size_t)kGateWaves * E * sizeof(double) : 0;
+  return gate_by_width(E, [&](auto vpt) -> int {
+    constexpr int VPT = decltype(vpt)::value;
+    if (logits_dtype == NVFP4_DT_F32)
+      hipLaunchKernelGGL((gate_topk_kernel<float, VPT>), dim3(grid), dim3(64 * kGateWaves), lds, (hipStream_t)stream,
+                         reinterpret_cast<const float*>(logits), bias, token_mask, g, topk_ids, topk_w);
+    else
+      hipLaunchKernelGGL((gate_topk_kernel<uint16_t, VPT>), dim3(grid), dim3(64 * kGateWaves), lds,
+                         (hipStream_t)stream, reinterpret_cast<const uint16_t*>(logits), bias, token_mask, g,
+                         topk_ids, topk_w);
+    NVFP4_CHECK_LAUNCH();
+    return NVFP4_OK;
+  });
+}
+
+// Tokens of one partial sum: about two workgroups per CU for large batches
+// (512 chunks), at least 16 so that a chunk amortizes its E-wide partial row.
+static int balance_chunk(int32_t T) {
+  const int per = ((T + 511) / 512 + kGateWaves - 1) / kGateWaves * kGateWaves;
+  return per < 16 ? 16 : per;
+}
+static size_t balance_layout(int32_t T, int32_t E, int32_t B, BalanceShape* g, char* base, BalanceWs* ws) {
+  const int chunk = balance_chunk(T);
+  const int max_chunks = (T + chunk - 1) / chunk + B;  // every sequence may end inside a chunk
+  const int cols = (E + 63) / 64;
+  size_t p = 0;
+  auto put = [&](size_t bytes) {
+    char* at = base + p;
+    p += nvfp4_align256(bytes);
+    return at;
+  };
+  BalanceWs w;
+  w.q = reinterpret_cast<float*>(put((size_t)max_chunks * E * 4));
+  w.counts = reinterpret_cast<int32_t*>(put((size_t)max_chunks * E * 4));
+  w.z = reinterpret_cast<double*>(put((size_t)max_chunks * 8));
+  w.live = reinterpret_cast<int32_t*>(put((size_t)max_chunks * 4));
+  w.term = reinterpret_cast<double*>(put((size_t)B * cols * 8));
+  w.z_seq = reinterpret_cast<double*>(put((size_t)B * 8));
+  w.done = reinterpret_cast<uint32_t*>(put(4));
+  if (g) {
+    g->chunk = chunk;
+    g->max_chunks = max_chunks;
+    g->col_blocks = cols;
+  }
+  if (ws) *ws = w;
+  return p;
+}
+
+static bool balance_sizes_ok(int32_t T, int32_t E, int32_t B) {
+  return T >= 0 && T < (1 << 30) && E >= 1 && E <= kGateMaxExperts && B >= 1 && B <= 65535;
+}
+
+extern "C" size_t moe_balance_loss_ws_bytes(int32_t T, int32_t E, int32_t B) {
+  return balance_sizes_ok(T, E, B) ? balance_layout(T, E, B, nullptr, nullptr, nullptr) : 0;
+}
+
+extern "C" int moe_balance_loss(const void* logits, int32_t logits_dtype, const int32_t* topk_ids,
+                                const uint8_t* token_mask, const int32_t* cu_seqlens, int32_t B, int32_t T, int32_t E,
+                                int32_t k, int32_t score, float* loss, int32_t* counts, int32_t* tokens, void* ws,
+                                size_t ws_bytes, void* stream) {
+  const int st = gate_check(logits, logits_dtype, T, E, k, score);
+  if (st) return st;
+  if (!balance_sizes_ok(T, E, B) || (!cu_seqlens && B != 1)) return NVFP4_ERR_SHAPE;
+  if ((T > 0 && !topk_ids) || !loss || !counts || !tokens || !ws) return NVFP4_ERR_NULL;
+  if (!nvfp4_aligned16(topk_ids) || !nvfp4_aligned16(token_mask) || !nvfp4_aligned16(cu_seqlens) ||
+      !nvfp4_aligned16(loss) || !nvfp4_aligned16(counts) || !nvfp4_aligned16(tokens) || !nvfp4_aligned16(ws))
+    return NVFP4_ERR_ALIGN;
+  BalanceShape g = {T, E, k, B, score, 0, 0, 0};
+  BalanceWs w;
+  if (ws_bytes < balance_layout(T, E, B, &g, reinterpret_cast<char*>(ws), &w)) return NVFP4_ERR_WORKSPACE;
+  const size_t lds = (size_t)(kGateWaves + 1) * E * 4;
+  return gate_by_width(E, [&](auto vpt) -> int {
+    constexpr int VPT = decltype(vpt)::value;
+    if (logits_dtype == NVFP4_DT_F32)
+      hipLaunchKernelGGL((balance_partial_kernel<float, VPT>), dim3(g.max_chunks), dim3(64 * kGateWaves), lds,
+                         (hipStream_t)stream, reinterpret_cast<const float*>(logits), topk_ids, token_mask,
+                         cu_seqlens, g, w);
+    else
+      hipLaunchKernelGGL((balance_partial_kernel<uint16_t, VPT>), dim3(g.max_chunks), dim3(64 * kGateWaves), lds,
+                         (hipStream_t)stream, reinterpret_cast<const uint16_t*>(logits), topk_ids, token_mask,
+                         cu_seqlens, g, w);
+    NVFP4_CHECK_LAUNCH();
+    hipLaunchKernelGGL(balance_join_kernel, dim3(g.col_blocks, B), dim3(64 * kJoinWaves), 0, (hipStream_t)stream,
+                       cu_seqlens, g, w, counts, tokens, loss);
+    NVFP4_CHECK_LAUNCH();
+    return NVFP4_OK;
+  });
+}
+
+extern "C" int moe_gate_backward(const void* logits, int32_t logits_dtype, const int32_t* topk_ids,
+                                 const uint8_t* token_mask, int32_t T, int32_t E, int32_t k, int32_t score,
+                                 int32_t renormalize, float scale, const float* d_topk_w, const float* d_loss,
+                                 const int32_t* counts, const int32_t* tokens, const int32_t* cu_seqlens, int32_t B,
+                                 void* d_logits, void* stream) {
+  const int st = gate_check(logits, logits_dtype, T, E, k, score);
+  if (st) return st;
+  if (renormalize != 0 && renormalize != 1) return NVFP4_ERR_ARG;
+  if (T > 0 && !d_topk_w && !d_loss) return NVFP4_ERR_NULL;
+  if (d_loss && (!balance_sizes_ok(T, E, B) || (!cu_seqlens && B != 1))) return NVFP4_ERR_SHAPE;
+  if (T == 0) return NVFP4_OK;
+  if (!d_logits || (d_topk_w && !topk_ids) || (d_loss && (!counts || !tokens))) return NVFP4_ERR_NULL;
+  if (!nvfp4_aligned16(topk_ids) || !nvfp4_aligned16(token_mask) || !nvfp4_aligned16(d_topk_w) ||
+      !nvfp4_aligned16(d_loss) || !nvfp4_aligned16(counts) || !nvfp4_aligned16(tokens) ||
+      !nvfp4_aligned16(cu_seqlens) || !nvfp4_aligned16(d_logits))
+    return NVFP4_ERR_ALIGN;
+  const GateGradArgs a = {topk_ids, d_topk_w, d_loss, counts, tokens, cu_seqlens, token_mask,
+                          T, E, k, B, score, renormalize, scale};
+  const unsigned grid = (unsigned)((T + kGateWaves - 1) / kGateWaves);
+  const size_t lds = d_topk_w ? (size_t)kGateWaves * E * 4 : 0;
+  return gate_by_width(E, [&](auto vpt) -> int {
+    constexpr int VPT = decltype(vpt)::value;
+    if (logits_dtype == NVFP4_DT_F32)
+      hipLaunchKernelGGL((gate_backward_kernel<float, VPT>), dim3(grid), dim3(64 * kGateWaves), lds,
+                         (hipStream_t)stream, reinterpret_cast<const float*>(logits), a,
+                         reinterpret_cast<float*>(d_logits));
+    else
+      hipLaunchKernelGGL((gate_backward_kernel<uint16_t, VPT>), dim3(grid), dim3(64 * kGateWaves), lds,
+                         (hipStream_t)stream, reinterpret_cast<const uint16_t*>(logits), a,
+                         reinterpret_cast<uint16_t*>(d_logits));
+    NVFP4_CHECK_LAUNCH();
+    return NVFP4_OK;
+  });
+}

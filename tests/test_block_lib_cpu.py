@@ -1,0 +1,80 @@
+"""The operators around the expert FFN refuse what they cannot compute, on the host, before any launch (CPU: the
+pointers are fake and must never reach a kernel)."""
+import ctypes
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "nvfp4_quantized_moe_amd", "libnvfp4moe.so")
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="library not built (run build())")
+
+NULL, SHAPE, ALIGN, WORKSPACE, ARG = 1, 2, 3, 4, 6
+P, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(4100)
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import nvfp4_quantized_moe_amd as nv
+    return nv
+
+
+def test_gate_topk(nv):
+    def call(logits=P, dtype=1, bias=None, mask=None, T=4, E=64, k=8, score=0, groups=1, top=1, renorm=1, ids=P, w=P):
+        return nv._gate_topk(logits, dtype, bias, mask, T, E, k, score, groups, top, renorm, 1.0, ids, w, None)
+    for bad in (dict(T=-1), dict(E=0), dict(E=1025), dict(k=0), dict(k=65, E=128), dict(k=9, E=8), dict(T=1 << 28),
+                dict(groups=0), dict(groups=3), dict(groups=128, E=128), dict(groups=8, top=9), dict(groups=8, top=0),
+                dict(groups=16, top=1, k=5)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(dtype=2), dict(score=3), dict(score=-1), dict(renorm=2)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(logits=None), dict(ids=None), dict(w=None)):
+        assert call(**bad) == NULL, bad
+    for bad in (dict(logits=ODD), dict(ids=ODD), dict(w=ODD), dict(bias=ODD), dict(mask=ODD)):
+        assert call(**bad) == ALIGN, bad
+    assert call(T=0, logits=None, ids=None, w=None) == 0
+
+
+def test_balance_loss(nv):
+    need = nv.moe_balance_loss_ws_bytes(4, 64, 2)
+    assert need > 0 and nv.moe_balance_loss_ws_bytes(4, 64, 0) == 0 and nv.moe_balance_loss_ws_bytes(4, 2000, 1) == 0
+
+    def call(logits=P, dtype=1, ids=P, mask=None, cu=P, B=2, T=4, E=64, k=8, score=0, loss=P, counts=P, tokens=P, ws=P,
+             n=need):
+        return nv._balance(logits, dtype, ids, mask, cu, B, T, E, k, score, loss, counts, tokens, ws, n, None)
+    for bad in (dict(T=-1), dict(E=1025), dict(k=65), dict(B=0), dict(B=65536), dict(cu=None)):
+        assert call(**bad) == SHAPE, bad
+    assert call(dtype=9) == ARG and call(score=4) == ARG
+    for bad in ("logits", "ids", "loss", "counts", "tokens", "ws"):
+        assert call(**{bad: None}) == NULL, bad
+    for bad in ("logits", "ids", "mask", "cu", "loss", "counts", "tokens", "ws"):
+        assert call(**{bad: ODD}) == ALIGN, bad
+    assert call(n=need - 1) == WORKSPACE
+
+
+def test_gate_backward(nv):
+    def call(logits=P, dtype=1, ids=P, mask=None, T=4, E=64, k=8, score=0, renorm=1, d_w=P, d_loss=P, counts=P, tokens=P,
+             cu=P, B=2, out=P):
+        return nv._gate_backward(logits, dtype, ids, mask, T, E, k, score, renorm, 1.0, d_w, d_loss, counts, tokens, cu,
+                                 B, out, None)
+    for bad in (dict(T=-1), dict(E=0), dict(k=65), dict(B=0), dict(cu=None)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(dtype=5), dict(score=7), dict(renorm=3)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(logits=None), dict(ids=None), dict(d_w=None, d_loss=None), dict(counts=None), dict(tokens=None),
+                dict(out=None)):
+        assert call(**bad) == NULL, bad
+    for bad in ("logits", "ids", "mask", "d_w", "d_loss", "counts", "tokens", "cu", "out"):
+        assert call(**{bad: ODD}) == ALIGN, bad
+    assert call(T=0) == 0
+
+
+def test_binding_refuses_tensors_on_the_host(nv):
+    import torch
+    x = torch.zeros(4, 16)
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: nv.moe_gate_topk(x, 2), lambda: nv.moe_balance_loss(x, ids),
+                 lambda: nv.moe_gate_backward(x, ids, d_topk_w=torch.zeros(4, 2)),
+                 lambda: nv.moe_gate_topk(x.double(), 2)):
+        with pytest.raises(ValueError):
+            call()
