@@ -212,6 +212,44 @@ int moe_gate_backward(const void* logits, int32_t logits_dtype, const int32_t* t
                       const float* d_topk_w, const float* d_loss, const int32_t* counts, const int32_t* tokens,
                       const int32_t* cu_seqlens, int32_t B, void* d_logits, void* stream);
 
+/* ------------------------------------------------------- norms of the block
+ * The residual update behind one block and the norm in front of the next, in
+ * one pass (around this layer: x its output, y its next input):
+ *   n  = x * rsqrt(mean(x^2) + eps) * w_post     (w_post NULL: n = x)
+ *   r' = residual + scale * gate * n             -> residual_out, rounded once
+ *   y  = r' * rsqrt(mean(r'^2) + eps) * w_pre    -> y, from r' as stored
+ * x, y [T, H] of x_dtype; residual (NULL: zeros), residual_out [T, H] of
+ * res_dtype (NVFP4_DT_*, any combination); w_pre, w_post float [H]; gate float
+ * [H] (MOE_GATE_CHANNEL), [T] (MOE_GATE_TOKEN) or unused (MOE_GATE_NONE, 1).
+ * w_pre NULL: no y. residual_out may be residual, y may be x. Sums in float32.
+ * gs_in (float [1], device) writes y as NVFP4 too: y_q uint8 [T, H/2], y_sf
+ * uint8 [T, H/16], exactly what nvfp4_quantize_static makes of the BF16 y; it
+ * needs w_pre, x_dtype BF16 and H % 32 == 0, and y may then be NULL.
+ * Requires T >= 0, 0 < H <= 16384, H % 8 == 0. One launch.
+ */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+int moe_block_norm(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype, int32_t T, int32_t H,
+                   const float* w_pre, const float* w_post, const float* gate, int32_t gate_mode, float scale,
+                   float eps, void* residual_out, void* y, const float* gs_in, uint8_t* y_q, uint8_t* y_sf,
+                   void* stream);
+
+/* Its gradients. d_y [T, H] of x_dtype (needed with w_pre), d_residual_out
+ * [T, H] of res_dtype (the gradient of r' from elsewhere; NULL: zeros; needed
+ * without w_pre); x and residual_out as moe_block_norm read and left them (the
+ * rounding of r' counts as the identity).
+ *   d_x [T, H] of x_dtype, d_residual [T, H] of res_dtype (may be d_y and
+ *   d_residual_out where the types agree); float d_w_pre [H] (with w_pre),
+ *   d_w_post [H] (with w_post), d_gate [H] or [T] (by gate_mode).
+ * ws: at least moe_block_norm_backward_ws_bytes(T, H) bytes. Sums over tokens
+ * have a fixed order. Two launches.
+ */
+size_t moe_block_norm_backward_ws_bytes(int32_t T, int32_t H);
+int moe_block_norm_backward(const void* d_y, const void* d_residual_out, const void* x, int32_t x_dtype,
+                            const void* residual_out, int32_t res_dtype, int32_t T, int32_t H, const float* w_pre,
+                            const float* w_post, const float* gate, int32_t gate_mode, float scale, float eps,
+                            void* d_x, void* d_residual, float* d_w_pre, float* d_w_post, float* d_gate, void* ws,
+                            size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------- weight packing
  * Offline weight preparation, step three (after quantize and fold): the
  * grouped GEMM reads weights in a packed order that matches its MFMA operand

@@ -22,7 +22,8 @@ __all__ = [
     "nvfp4_moe_forward_static", "calibrate_static_gs", "nvfp4_moe_forward_stage_events", "STAGES",
     "nvfp4_moe_ws_bytes", "nvfp4_moe_ws_layout", "nvfp4_moe_tile_m", "MoEWeights", "prepare_weights",
     "ws_view", "SCORE_SOFTMAX", "SCORE_SIGMOID", "SCORE_SQRT_SOFTPLUS", "moe_gate_topk", "moe_balance_loss",
-    "moe_balance_loss_ws_bytes", "moe_gate_backward",
+    "moe_balance_loss_ws_bytes", "moe_gate_backward", "moe_block_norm", "moe_block_norm_backward",
+    "moe_block_norm_backward_ws_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
@@ -86,6 +87,11 @@ _balance = _sig("moe_balance_loss", ctypes.c_int, _vp, _i32, _vp, _vp, _vp, _i32
                 _vp, _vp, _vp, _vp, _sz, _vp)
 _gate_backward = _sig("moe_gate_backward", ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
                       _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp)
+_block_norm = _sig("moe_block_norm", ctypes.c_int, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _f32, _f32,
+                   _vp, _vp, _vp, _vp, _vp, _vp)
+_block_norm_ws = _sig("moe_block_norm_backward_ws_bytes", _sz, _i32, _i32)
+_block_norm_backward = _sig("moe_block_norm_backward", ctypes.c_int, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                            _vp, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
 
 
 class NVFP4Error(RuntimeError):
@@ -344,6 +350,94 @@ def moe_gate_backward(logits, topk_ids, score=SCORE_SOFTMAX, renormalize=True, s
                           _ptr(d_topk_w), _ptr(d_loss), _ptr(counts), _ptr(tokens), _ptr(cu_seqlens), B,
                           _ptr(d_logits), _stream()), "moe_gate_backward")
     return d_logits
+
+
+# ------------------------------------------------------------ norms of the block
+
+def _gate_mode(gate, T, H):
+    """MOE_GATE_* of a gate float32 [H] (channels) or [T, 1] (tokens)."""
+    if gate is None:
+        return 0
+    _dev(gate, torch.float32, "gate")
+    if tuple(gate.shape) == (H,):
+        return 1
+    if tuple(gate.shape) == (T, 1):
+        return 2
+    raise ValueError(f"gate: expected shape ({H},) or ({T}, 1), got {tuple(gate.shape)}")
+
+
+def moe_block_norm(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0, eps=1e-6, gs=None, residual_out=None,
+                   y=None, y_q=None, y_sf=None):
+    """The residual update behind a block and the norm in front of the next: n = rms_norm(x) * w_post (or x),
+    residual_out = residual + scale * gate * n, y = rms_norm(residual_out) * w_pre -> (residual_out, y), y None
+    without w_pre. x, residual: BF16 or float32 [T, H] (residual None: zeros, of x's type); w_pre, w_post: float32
+    [H]; gate: float32 [H] or [T, 1]. With gs (float32 [1], device) also y as NVFP4 with that fixed global scale:
+    (residual_out, y, y_q, y_sf)."""
+    dt = _float_dev(x, "x")
+    T, H = _matrix(x, "x")
+    dev = x.device
+    rdt = dt
+    rtype = x.dtype
+    if residual is not None:
+        rdt = _float_dev(residual, "residual")
+        rtype = residual.dtype
+        _shape(residual, (T, H), "residual")
+    elif residual_out is not None:
+        rdt = _float_dev(residual_out, "residual_out")
+        rtype = residual_out.dtype
+    _opt(w_pre, torch.float32, (H,), "w_pre")
+    _opt(w_post, torch.float32, (H,), "w_post")
+    mode = _gate_mode(gate, T, H)
+    residual_out = (torch.empty((T, H), dtype=rtype, device=dev) if residual_out is None
+                    else _buf(residual_out, rtype, T * H, "residual_out"))
+    if w_pre is not None:
+        y = torch.empty((T, H), dtype=x.dtype, device=dev) if y is None else _buf(y, x.dtype, T * H, "y")
+    if gs is not None:
+        _opt(gs, torch.float32, (1,), "gs")
+        y_q = (torch.empty((T, H // 2), dtype=torch.uint8, device=dev) if y_q is None
+               else _buf(y_q, torch.uint8, T * H // 2, "y_q"))
+        y_sf = (torch.empty((T, H // 16), dtype=torch.uint8, device=dev) if y_sf is None
+                else _buf(y_sf, torch.uint8, T * H // 16, "y_sf"))
+    _check(_block_norm(_ptr(x), dt, _ptr(residual), rdt, T, H, _ptr(w_pre), _ptr(w_post), _ptr(gate), mode, scale, eps,
+                       _ptr(residual_out), _ptr(y), _ptr(gs), _ptr(y_q), _ptr(y_sf), _stream()), "moe_block_norm")
+    return (residual_out, y) if gs is None else (residual_out, y, y_q, y_sf)
+
+
+def moe_block_norm_backward_ws_bytes(T, H) -> int:
+    return int(_block_norm_ws(T, H))
+
+
+def moe_block_norm_backward(d_y, d_residual_out, x, residual_out, w_pre=None, w_post=None, gate=None, scale=1.0,
+                            eps=1e-6, d_x=None, d_residual=None, d_w_pre=None, d_w_post=None, d_gate=None, ws=None):
+    """Gradients of moe_block_norm from d_y (None without w_pre) and d_residual_out (None: zeros), with the x and the
+    residual_out of the forward call -> dict of d_x, d_residual, d_w_pre, d_w_post, d_gate (None where there is no
+    such input)."""
+    dt = _float_dev(x, "x")
+    T, H = _matrix(x, "x")
+    rdt = _float_dev(residual_out, "residual_out")
+    _shape(residual_out, (T, H), "residual_out")
+    _opt(d_y, x.dtype, (T, H), "d_y")
+    _opt(d_residual_out, residual_out.dtype, (T, H), "d_residual_out")
+    _opt(w_pre, torch.float32, (H,), "w_pre")
+    _opt(w_post, torch.float32, (H,), "w_post")
+    mode = _gate_mode(gate, T, H)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    d_x = torch.empty_like(x) if d_x is None else _buf(d_x, x.dtype, T * H, "d_x")
+    d_residual = (torch.empty_like(residual_out) if d_residual is None
+                  else _buf(d_residual, residual_out.dtype, T * H, "d_residual"))
+
+    def grad(buf, of, name):
+        if of is None:
+            return None
+        return torch.empty(of.shape, **f32) if buf is None else _buf(buf, torch.float32, of.numel(), name)
+    d_w_pre, d_w_post = grad(d_w_pre, w_pre, "d_w_pre"), grad(d_w_post, w_post, "d_w_post")
+    d_gate = grad(d_gate, gate, "d_gate")
+    ws = _alloc_ws(moe_block_norm_backward_ws_bytes(T, H), x.device) if ws is None else _buf(ws, torch.uint8, 0, "ws")
+    _check(_block_norm_backward(_ptr(d_y), _ptr(d_residual_out), _ptr(x), dt, _ptr(residual_out), rdt, T, H,
+                                _ptr(w_pre), _ptr(w_post), _ptr(gate), mode, scale, eps, _ptr(d_x), _ptr(d_residual),
+                                _ptr(d_w_pre), _ptr(d_w_post), _ptr(d_gate), _ptr(ws), ws.numel(), _stream()),
+           "moe_block_norm_backward")
+    return dict(d_x=d_x, d_residual=d_residual, d_w_pre=d_w_pre, d_w_post=d_w_post, d_gate=d_gate)
 
 
 # ------------------------------------------------------------------ grouped GEMM

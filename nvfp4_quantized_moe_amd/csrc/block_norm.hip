@@ -1,0 +1,438 @@
+// The norms around the expert FFN, fused with its gate and residual scale,
+// and their gradients:
+//   n  = x * rsqrt(mean x^2 + eps) * w_post        (or n = x)
+//   r' = residual + scale * gate * n               stored in the residual's type
+//   y  = r' * rsqrt(mean r'^2 + eps) * w_pre       from r' as stored; also as NVFP4
+// One pass: a row's elements stay in registers between the two reductions.
+//
+// A workgroup owns whole rows; thread i holds the row's 8-element chunks i,
+// i + blockDim.x, ... (16-byte loads). Sums are float32: the lanes of a wave
+// by DPP, then the waves through LDS in wave order, so results repeat bit for
+// bit.
+#include <type_traits>
+
+#include "common.h"
+#include "internal.h"
+#include "quant_block.h"
+#include "wave.h"
+
+namespace nvfp4 {
+
+constexpr int kNormMaxH = 16384;
+constexpr int kNormMaxWaves = 16;
+
+template <typename T>
+struct Vec8;  // eight elements as loaded
+template <>
+struct Vec8<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = (&v.x)[i >> 1];
+    return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ float get(int i) const { return i < 4 ? (&a.x)[i] : (&b.x)[i - 4]; }
+};
+// Stores f[0..8) rounded to the type and leaves the stored values in f.
+__device__ __forceinline__ uint4 store8(uint16_t* p, float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = f32x2_to_bf16x2(f[2 * i], f[2 * i + 1]);
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+  if (p) *reinterpret_cast<uint4*>(p) = v;
+  return v;
+}
+__device__ __forceinline__ uint4 store8(float* p, float (&f)[8]) {
+  if (p) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  return make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void load_weights8(const float* p, int at, float absent, float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = absent;
+  if (p) {
+    Vec8<float> v;
+    v.load(p + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = v.get(i);
+  }
+}
+
+// Sums of N values per thread over the workgroup, in every thread. `scratch`
+// must not be the one of the previous call (a wave may still be reading that).
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*scratch)[N]) {
+  const int waves = (int)blockDim.x >> 6;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_all_sum(v[i]);
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) scratch[threadIdx.x >> 6][i] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  for (int w = 0; w < waves; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += scratch[w][i];
+}
+
+struct NormArgs {
+  int T, H;
+  const float* w_pre;    // NULL: no y
+  const float* w_post;   // NULL: no norm of x
+  const float* gate;     // [H], [T] or NULL
+  int gate_tokens;       // gate is [T]
+  float scale, eps;
+};
+
+template <typename X, typename R, int CH, bool QUANT>
+__global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_kernel(const X* x, const R* residual, NormArgs a,
+                                                                          R* residual_out, X* y, const float* gs_in,
+                                                                          uint8_t* y_q, uint8_t* y_sf) {
+  __shared__ float scratch[2][kNormMaxWaves][1];
+  __shared__ uint4 lut[QUANT ? kLutWords / 4 : 1];
+  const int nchunk = a.H / 8;
+  float gs = 0.0f;
+  if constexpr (QUANT) {
+    gs = gs_in[0];
+    build_threshold_lut(gs, reinterpret_cast<uint32_t*>(lut), threadIdx.x, blockDim.x);
+    __syncthreads();
+  }
+  const float inv_h = 1.0f / (float)a.H;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t row = (size_t)t * a.H;
+    float f[CH][8], s[1] = {0.0f};
+    Vec8<R> rv[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      if (ch < nchunk) {
+        Vec8<X> xv;
+        xv.load(x + row + ch * 8);
+        if (residual) rv[c].load(residual + row + ch * 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[c][i] = xv.get(i);
+          s[0] += f[c][i] * f[c][i];
+        }
+      }
+    }
+    float sig = a.scale * ((a.gate && a.gate_tokens) ? a.gate[t] : 1.0f);
+    if (a.w_post) {
+      block_sums(s, scratch[0]);
+      sig *= rsqrtf(s[0] * inv_h + a.eps);
+    }
+    s[0] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      if (ch < nchunk) {
+        float w[8], g[8];
+        load_weights8(a.w_post, ch * 8, 1.0f, w);
+        load_weights8(a.gate_tokens ? nullptr : a.gate, ch * 8, 1.0f, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[c][i] = f[c][i] * sig * (w[i] * g[i]);
+          if (residual) f[c][i] += rv[c].get(i);
+        }
+        store8(residual_out + row + ch * 8, f[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] += f[c][i] * f[c][i];
+      }
+    }
+    if (!a.w_pre) continue;
+    block_sums(s, scratch[1]);
+    const float rho = rsqrtf(s[0] * inv_h + a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      uint4 bits = make_uint4(0, 0, 0, 0);
+      if (ch < nchunk) {
+        float w[8];
+        load_weights8(a.w_pre, ch * 8, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[c][i] = f[c][i] * rho * w[i];
+        bits = store8(y ? y + row + ch * 8 : nullptr, f[c]);
+      }
+      if constexpr (QUANT) {
+        // a 16-element block is the chunks of two neighbouring lanes (an even
+        // number of chunks in a row): the even lane takes the odd one's words
+        const uint4 next = make_uint4((uint32_t)dpp_i32<kDppXor1>((int)bits.x), (uint32_t)dpp_i32<kDppXor1>((int)bits.y),
+                                      (uint32_t)dpp_i32<kDppXor1>((int)bits.z), (uint32_t)dpp_i32<kDppXor1>((int)bits.w));
+        if (ch < nchunk && (threadIdx.x & 1) == 0) {
+          const uint32_t w[8] = {bits.x, bits.y, bits.z, bits.w, next.x, next.y, next.z, next.w};
+          uint2 packed;
+          const uint32_t code = quantize_block16(w, quant_scale(gs), lut, &packed);
+          const size_t blk = (row >> 4) + (ch >> 1);
+          *reinterpret_cast<uint2*>(y_q + blk * 8) = packed;
+          y_sf[blk] = (uint8_t)code;
+        }
+      }
+    }
+  }
+}
+
+// Backward of one row, with rn = r' rho, dn = d_y w_pre, xn = x sig:
+//   d_r = d_r' + rho (dn - rn mean(dn rn)),  d_w_pre += d_y rn
+//   db  = scale d_r,  d_gate = db n (summed over the row or the batch)
+//   db' = db gate,    d_w_post += db' xn
+//   d_x = sig (db' w_post - xn mean(db' w_post xn)),  or db' without w_post
+// Two reductions per row (the second needs the first's result). The column
+// sums d_w_pre, d_w_post, d_gate stay in registers over all rows of the
+// workgroup and leave it once, as a row of partial sums that
+// norm_columns_kernel adds in workgroup order.
+constexpr int kNormGrid = 256;  // workgroups of the backward pass: one per CU
+template <typename X, typename R, int CH>
+__global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_backward_kernel(
+    const X* d_y, const R* d_res_out, const X* x, const R* res_out,
+    NormArgs a, X* d_x, R* d_res, float* d_gate_tokens, float* partial) {
+  __shared__ float scratch_a[kNormMaxWaves][3];
+  __shared__ float scratch_b[kNormMaxWaves][2];
+  const int nchunk = a.H / 8;
+  const float inv_h = 1.0f / (float)a.H;
+  float c_pre[CH][8], c_post[CH][8], c_gate[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c_pre[c][i] = c_post[c][i] = c_gate[c][i] = 0.0f;
+  const float* gate_cols = a.gate_tokens ? nullptr : a.gate;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t row = (size_t)t * a.H;
+    Vec8<X> xv[CH], yv[CH];
+    Vec8<R> rv[CH], dv[CH];
+    float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      if (ch < nchunk) {
+        xv[c].load(x + row + ch * 8);
+        if (d_res_out) dv[c].load(d_res_out + row + ch * 8);
+        if (a.w_pre) {
+          float w[8];
+          yv[c].load(d_y + row + ch * 8);
+          rv[c].load(res_out + row + ch * 8);
+          load_weights8(a.w_pre, ch * 8, 1.0f, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            s[0] += rv[c].get(i) * rv[c].get(i);
+            s[1] += yv[c].get(i) * w[i] * rv[c].get(i);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[2] += xv[c].get(i) * xv[c].get(i);
+      }
+    }
+    block_sums(s, scratch_a);
+    const float rho = rsqrtf(s[0] * inv_h + a.eps);
+    const float mean = s[1] * rho * inv_h;  // of dn rn
+    const float sig = a.w_post ? rsqrtf(s[2] * inv_h + a.eps) : 1.0f;
+    const float g_row = (a.gate && a.gate_tokens) ? a.gate[t] : 1.0f;
+    float u[2] = {0.0f, 0.0f};
+    float dxn[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      if (ch < nchunk) {
+        float dr[8], w_pre[8], w_post[8], gate[8];
+        load_weights8(a.w_pre, ch * 8, 0.0f, w_pre);
+        load_weights8(a.w_post, ch * 8, 1.0f, w_post);
+        load_weights8(gate_cols, ch * 8, g_row, gate);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dr[i] = d_res_out ? dv[c].get(i) : 0.0f;
+          if (a.w_pre) {
+            const float rn = rv[c].get(i) * rho;
+            dr[i] += rho * (yv[c].get(i) * w_pre[i] - rn * mean);
+            c_pre[c][i] += yv[c].get(i) * rn;
+          }
+          const float xn = xv[c].get(i) * sig;
+          const float db = a.scale * dr[i];
+          const float dg = db * xn * w_post[i];
+          c_gate[c][i] += dg;
+          u[1] += dg;
+          const float dbg = db * gate[i];
+          c_post[c][i] += dbg * xn;
+          dxn[c][i] = dbg * w_post[i];
+          u[0] += dxn[c][i] * xn;
+        }
+        store8(d_res + row + ch * 8, dr);
+      }
+    }
+    if (a.w_post || d_gate_tokens) block_sums(u, scratch_b);
+    else __syncthreads();  // scratch_a is written again in the next row
+    if (d_gate_tokens && threadIdx.x == 0) d_gate_tokens[t] = u[1];
+    const float mx = a.w_post ? u[0] * inv_h : 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      if (ch < nchunk) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          o[i] = a.w_post ? sig * (dxn[c][i] - xv[c].get(i) * sig * mx) : dxn[c][i];
+        store8(d_x + row + ch * 8, o);
+      }
+    }
+  }
+  // partial sums of this workgroup: [workgroup][3][H]
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int ch = threadIdx.x + c * blockDim.x;
+    if (ch < nchunk) {
+      float* p = partial + (size_t)blockIdx.x * 3 * a.H + ch * 8;
+      store8(p, c_pre[c]);
+      store8(p + a.H, c_post[c]);
+      store8(p + 2 * a.H, c_gate[c]);
+    }
+  }
+}
+
+// Column sums over the workgroups' partial rows: workgroup (b, s) adds 64
+// columns of sum s; its waves take every fourth row, and are added in order.
+__global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restrict__ partial, int rows, int H,
+                                                           float* d_pre, float* d_post, float* d_gate) {
+  __shared__ float sh[4][64];
+  float* out = blockIdx.y == 0 ? d_pre : blockIdx.y == 1 ? d_post : d_gate;
+  if (!out) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (col < H) {
+    const float* p = partial + (size_t)blockIdx.y * H + col;
+    for (int r = wave; r < rows; r += 4) s += p[(size_t)r * 3 * H];
+  }
+  sh[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && col < H) out[col] = (sh[0][lane] + sh[1][lane]) + (sh[2][lane] + sh[3][lane]);
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+static int norm_check(int32_t T, int32_t H, int32_t x_dtype, int32_t res_dtype, const float* gate, int32_t gate_mode) {
+  if (T < 0 || H <= 0 || H % 8 != 0 || H > kNormMaxH) return NVFP4_ERR_SHAPE;
+  if ((x_dtype != NVFP4_DT_BF16 && x_dtype != NVFP4_DT_F32) ||
+      (res_dtype != NVFP4_DT_BF16 && res_dtype != NVFP4_DT_F32))
+    return NVFP4_ERR_ARG;
+  if (gate_mode != MOE_GATE_NONE && gate_mode != MOE_GATE_CHANNEL && gate_mode != MOE_GATE_TOKEN)
+    return NVFP4_ERR_ARG;
+  if (gate_mode != MOE_GATE_NONE && !gate && T > 0) return NVFP4_ERR_NULL;
+  return NVFP4_OK;
+}
+
+// Threads for rows of H elements at CH chunks of 8 per thread.
+static unsigned norm_threads(int32_t H, int ch) { return (unsigned)(((H / 8 + ch - 1) / ch + 63) / 64 * 64); }
+
+template <typename Fn>
+static int norm_by_types(int32_t x_dtype, int32_t res_dtype, Fn fn) {
+  if (x_dtype == NVFP4_DT_BF16)
+    return res_dtype == NVFP4_DT_BF16 ? fn(uint16_t(), uint16_t()) : fn(uint16_t(), float());
+  return res_dtype == NVFP4_DT_BF16 ? fn(float(), uint16_t()) : fn(float(), float());
+}
+
+extern "C" int moe_block_norm(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype, int32_t T,
+                              int32_t H, const float* w_pre, const float* w_post, const float* gate,
+                              int32_t gate_mode, float scale, float eps, void* residual_out, void* y,
+                              const float* gs_in, uint8_t* y_q, uint8_t* y_sf, void* stream) {
+  const int st = norm_check(T, H, x_dtype, res_dtype, gate, gate_mode);
+  if (st) return st;
+  if (gs_in && H % 32 != 0) return NVFP4_ERR_SHAPE;
+  if (gs_in && x_dtype != NVFP4_DT_BF16) return NVFP4_ERR_ARG;
+  if (T == 0) return NVFP4_OK;
+  if (!x || !residual_out || (w_pre && !y && !gs_in) || (gs_in && (!w_pre || !y_q || !y_sf))) return NVFP4_ERR_NULL;
+  if (!nvfp4_aligned16(x) || !nvfp4_aligned16(residual) || !nvfp4_aligned16(residual_out) || !nvfp4_aligned16(y) ||
+      !nvfp4_aligned16(w_pre) || !nvfp4_aligned16(w_post) || !nvfp4_aligned16(gate) || !nvfp4_aligned16(gs_in) ||
+      !nvfp4_aligned16(y_q) || !nvfp4_aligned16(y_sf))
+    return NVFP4_ERR_ALIGN;
+  const NormArgs a = {T, H, w_pre, w_post, gate_mode == MOE_GATE_NONE ? nullptr : gate, gate_mode == MOE_GATE_TOKEN,
+                      scale, eps};
+  return norm_by_types(x_dtype, res_dtype, [&](auto xt, auto rt) -> int {
+    using X = decltype(xt);
+    using R = decltype(rt);
+    auto go = [&](auto ch, auto quant) -> int {
+      constexpr int CH = decltype(ch)::value;
+      const unsigned threads = norm_threads(H, CH);
+      hipLaunchKernelGGL((block_norm_kernel<X, R, CH, decltype(quant)::value>), dim3((unsigned)T), dim3(threads), 0,
+                         (hipStream_t)stream, reinterpret_cast<const X*>(x), reinterpret_cast<const R*>(residual), a,
+                         reinterpret_cast<R*>(residual_out), reinterpret_cast<X*>(y), gs_in, y_q, y_sf);
+      NVFP4_CHECK_LAUNCH();
+      return NVFP4_OK;
+    };
+    auto by_width = [&](auto quant) -> int {
+      return H <= 8192 ? go(std::integral_constant<int, 1>(), quant) : go(std::integral_constant<int, 4>(), quant);
+    };
+    if constexpr (std::is_same<X, uint16_t>::value)
+      if (gs_in) return by_width(std::true_type());
+    return by_width(std::false_type());
+  });
+}
+
+extern "C" size_t moe_block_norm_backward_ws_bytes(int32_t T, int32_t H) {
+  if (T < 0 || H <= 0 || H % 8 != 0 || H > kNormMaxH) return 0;
+  return (size_t)kNormGrid * 3 * H * sizeof(float);
+}
+
+extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_out, const void* x, int32_t x_dtype,
+                                       const void* residual_out, int32_t res_dtype, int32_t T, int32_t H,
+                                       const float* w_pre, const float* w_post, const float* gate, int32_t gate_mode,
+                                       float scale, float eps, void* d_x, void* d_residual, float* d_w_pre,
+                                       float* d_w_post, float* d_gate, void* ws, size_t ws_bytes, void* stream) {
+  const int st = norm_check(T, H, x_dtype, res_dtype, gate, gate_mode);
+  if (st) return st;
+  if (T > 0 && (!x || !d_x || !d_residual || (w_pre && (!d_y || !residual_out)) || (!w_pre && !d_residual_out)))
+    return NVFP4_ERR_NULL;
+  if ((w_pre && !d_w_pre) || (w_post && !d_w_post) || (gate_mode == MOE_GATE_CHANNEL && !d_gate) ||
+      (gate_mode == MOE_GATE_TOKEN && T > 0 && !d_gate) || !ws)
+    return NVFP4_ERR_NULL;
+  if (!nvfp4_aligned16(d_y) || !nvfp4_aligned16(d_residual_out) || !nvfp4_aligned16(x) ||
+      !nvfp4_aligned16(residual_out) || !nvfp4_aligned16(w_pre) || !nvfp4_aligned16(w_post) ||
+      !nvfp4_aligned16(gate) || !nvfp4_aligned16(d_x) || !nvfp4_aligned16(d_residual) || !nvfp4_aligned16(d_w_pre) ||
+      !nvfp4_aligned16(d_w_post) || !nvfp4_aligned16(d_gate) || !nvfp4_aligned16(ws))
+    return NVFP4_ERR_ALIGN;
+  if (ws_bytes < moe_block_norm_backward_ws_bytes(T, H)) return NVFP4_ERR_WORKSPACE;
+  const bool per_token = gate_mode == MOE_GATE_TOKEN;
+  const NormArgs a = {T, H, w_pre, w_post, gate_mode == MOE_GATE_NONE ? nullptr : gate, per_token, scale, eps};
+  const unsigned grid = (unsigned)(T < kNormGrid ? T : kNormGrid);
+  if (T > 0) {
+    const int r = norm_by_types(x_dtype, res_dtype, [&](auto xt, auto rt) -> int {
+      using X = decltype(xt);
+      using R = decltype(rt);
+      auto go = [&](auto ch) -> int {
+        constexpr int CH = decltype(ch)::value;
+        hipLaunchKernelGGL((block_norm_backward_kernel<X, R, CH>), dim3(grid), dim3(norm_threads(H, CH)), 0,
+                           (hipStream_t)stream, reinterpret_cast<const X*>(d_y),
+                           reinterpret_cast<const R*>(d_residual_out), reinterpret_cast<const X*>(x),
+                           reinterpret_cast<const R*>(residual_out), a, reinterpret_cast<X*>(d_x),
+                           reinterpret_cast<R*>(d_residual), per_token ? d_gate : nullptr,
+                           reinterpret_cast<float*>(ws));
+        NVFP4_CHECK_LAUNCH();
+        return NVFP4_OK;
+      };
+      return H <= 8192 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 4>());
+    });
+    if (r) return r;
+  }
+  // T = 0: the sums over no rows, zeros
+  float* gate_cols = gate_mode == MOE_GATE_CHANNEL ? d_gate : nullptr;
+  hipLaunchKernelGGL(norm_columns_kernel, dim3((H + 63) / 64, 3), dim3(256), 0, (hipStream_t)stream,
+                     reinterpret_cast<const float*>(ws), (int)grid, H, w_pre ? d_w_pre : nullptr,
+                     w_post ? d_w_post : nullptr, gate_cols);
+  NVFP4_CHECK_LAUNCH();
+  return NVFP4_OK;
+}

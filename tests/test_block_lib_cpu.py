@@ -78,3 +78,39 @@ def test_binding_refuses_tensors_on_the_host(nv):
                  lambda: nv.moe_gate_topk(x.double(), 2)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_block_norm(nv):
+    def call(x=P, xt=0, r=P, rt=0, T=4, H=64, w_pre=P, w_post=P, gate=P, mode=1, out=P, y=P, gs=None, q=None, sf=None):
+        return nv._block_norm(x, xt, r, rt, T, H, w_pre, w_post, gate, mode, 1.0, 1e-6, out, y, gs, q, sf, None)
+    for bad in (dict(T=-1), dict(H=0), dict(H=60), dict(H=16392), dict(H=40, gs=P, q=P, sf=P)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(xt=2), dict(rt=-1), dict(mode=3), dict(xt=1, gs=P, q=P, sf=P)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(x=None), dict(out=None), dict(y=None), dict(gate=None), dict(gs=P), dict(gs=P, q=P),
+                dict(gs=P, q=P, sf=P, w_pre=None)):
+        assert call(**bad) == NULL, bad
+    for bad in ("x", "r", "w_pre", "w_post", "gate", "out", "y"):
+        assert call(**{bad: ODD}) == ALIGN, bad
+    assert call(gs=ODD, q=P, sf=P) == ALIGN and call(gs=P, q=ODD, sf=P) == ALIGN and call(gs=P, q=P, sf=ODD) == ALIGN
+    assert call(T=0, x=None, r=None, out=None, y=None) == 0
+
+
+def test_block_norm_backward(nv):
+    need = nv.moe_block_norm_backward_ws_bytes(4, 64)
+    assert need > 0 and nv.moe_block_norm_backward_ws_bytes(4, 60) == 0
+
+    def call(d_y=P, d_r=P, x=P, xt=0, r=P, rt=0, T=4, H=64, w_pre=P, w_post=P, gate=P, mode=1, dx=P, dr=P, a=P, b=P, c=P,
+             ws=P, n=need):
+        return nv._block_norm_backward(d_y, d_r, x, xt, r, rt, T, H, w_pre, w_post, gate, mode, 1.0, 1e-6, dx, dr, a, b,
+                                       c, ws, n, None)
+    for bad in (dict(T=-1), dict(H=4), dict(H=16392)):
+        assert call(**bad) == SHAPE, bad
+    for bad in (dict(xt=3), dict(rt=3), dict(mode=5)):
+        assert call(**bad) == ARG, bad
+    for bad in (dict(d_y=None), dict(x=None), dict(r=None), dict(dx=None), dict(dr=None), dict(a=None), dict(b=None),
+                dict(c=None), dict(gate=None), dict(ws=None), dict(w_pre=None, d_r=None)):
+        assert call(**bad) == NULL, bad
+    for bad in ("d_y", "d_r", "x", "r", "w_pre", "w_post", "gate", "dx", "dr", "a", "b", "c", "ws"):
+        assert call(**{bad: ODD}) == ALIGN, bad
+    assert call(n=need - 1) == WORKSPACE
