@@ -327,6 +327,41 @@ int nvfp4_grouped_gemm_silu_nvfp4(const uint8_t* a_q, const uint8_t* a_sf, const
                                   int32_t rows_cap, int32_t N, int32_t K, int32_t tile_m, const float* out_gs,
                                   uint8_t* d_q, uint8_t* d_sf, void* stream);
 
+/* ------------------------------------------------- 8-bit integer products
+ * Row quantizer: for each row m of x [M, K] (BF16 or float, row-major)
+ *   scale[m] = RN_f32(max_k |x[m, k]| / 127)
+ *   q[m, k]  = the integer nearest to x[m, k] / scale[m], ties to even (as on
+ *              the real quotient), at most 127 in size; 0 where scale is 0.
+ * q int8 [M, K]; scale float [M]. For activations a row is a token, for
+ * weights [N, K] an output channel. K % 16 == 0, 0 < K <= 65536. One launch.
+ */
+int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int32_t K, int8_t* q, float* scale, void* stream);
+
+/* G[m, n] = a_scale[m] * b_scale[n] * sum_k a_q[m, k] * b_q[n, k], the sum
+ * exact, the rest in float32. a_q int8 [M, K] with a_scale float [M], b_q int8
+ * [N, K] with b_scale float [N], all row-major.
+ * epilogue NVFP4_EPI_BF16:     d BF16 [M, N], d = RN_bf16(G [+ add]); N % 8 == 0
+ * epilogue NVFP4_EPI_SILU_MUL: gate rows [0, I), up rows [I, 2I) of b_q, N = 2I:
+ *   d BF16 [M, I], d = RN_bf16(silu(G[m, n]) * G[m, I + n] [+ add]); I % 8 == 0
+ * add: BF16 of d's shape, or NULL; may be d itself. K % 16 == 0, K <= 65536,
+ * M <= 64 * 65535. One launch.
+ */
+int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int32_t M, int32_t N,
+              int32_t K, int32_t epilogue, const void* add_bf16, void* d_bf16, void* stream);
+
+/* Dense (shared) expert FFN in 8-bit integers: quantize x, the gate+up product
+ * with the SiLU epilogue into BF16 h, quantize h, the down product, and add:
+ *   out[t] = RN_bf16(w2 (silu(w1_gate x[t]) * (w1_up x[t])) + add[t])
+ * w1_q int8 [2I, H] (gate rows, then up rows) with w1_scale [2I]; w2_q int8
+ * [H, I] with w2_scale [H]; x, out BF16 [T, H]; add BF16 [T, H] (such as the
+ * output of nvfp4_moe_forward; may be out) or NULL. H % 16 == 0, I % 16 == 0,
+ * both <= 65536, T <= 64 * 65535. ws: at least int8_ffn_ws_bytes(T, H, I).
+ */
+size_t int8_ffn_ws_bytes(int32_t T, int32_t hidden, int32_t inter);
+int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const int8_t* w2_q, const float* w2_scale,
+                     const void* x_bf16, int32_t T, int32_t hidden, int32_t inter, const void* add_bf16,
+                     void* out_bf16, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------- weighted scatter
  * out[t, :] = RN_bf16( sum over j = 0..k-1 with token_slot[t*k+j] >= 0 of
  *                      topk_w[t, j] * y[token_slot[t*k+j], :] ), float32, increasing j;

@@ -23,7 +23,8 @@ __all__ = [
     "nvfp4_moe_ws_bytes", "nvfp4_moe_ws_layout", "nvfp4_moe_tile_m", "MoEWeights", "prepare_weights",
     "ws_view", "SCORE_SOFTMAX", "SCORE_SIGMOID", "SCORE_SQRT_SOFTPLUS", "moe_gate_topk", "moe_balance_loss",
     "moe_balance_loss_ws_bytes", "moe_gate_backward", "moe_block_norm", "moe_block_norm_backward",
-    "moe_block_norm_backward_ws_bytes",
+    "moe_block_norm_backward_ws_bytes", "int8_quantize_rows", "int8_gemm", "int8_ffn_forward", "int8_ffn_ws_bytes",
+    "Int8FFNWeights", "prepare_int8_weights",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
@@ -92,6 +93,10 @@ _block_norm = _sig("moe_block_norm", ctypes.c_int, _vp, _i32, _vp, _i32, _i32, _
 _block_norm_ws = _sig("moe_block_norm_backward_ws_bytes", _sz, _i32, _i32)
 _block_norm_backward = _sig("moe_block_norm_backward", ctypes.c_int, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
                             _vp, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
+_int8_rows = _sig("int8_quantize_rows", ctypes.c_int, _vp, _i32, _i32, _i32, _vp, _vp, _vp)
+_int8_gemm = _sig("int8_gemm", ctypes.c_int, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp)
+_int8_ffn_ws = _sig("int8_ffn_ws_bytes", _sz, _i32, _i32, _i32)
+_int8_ffn = _sig("int8_ffn_forward", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp)
 
 
 class NVFP4Error(RuntimeError):
@@ -554,6 +559,84 @@ def nvfp4_fold_scales(w1_sf, gs_gate, gs_up, gs1=None):
     _check(_fold(_ptr(w1_sf), _ptr(gs_gate), _ptr(gs_up), _ptr(gs1), L, two_i // 2, k16 * 16, _stream()),
            "nvfp4_fold_scales")
     return gs1
+
+
+# -------------------------------------------------------- 8-bit integer products
+
+def int8_quantize_rows(x, q=None, scale=None):
+    """x BF16 or float32 [M, K] -> (q int8 [M, K], scale float32 [M] = row amax / 127)."""
+    dt = _float_dev(x, "x")
+    M, K = _matrix(x, "x")
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device) if q is None else _buf(q, torch.int8, M * K, "q")
+    scale = (torch.empty(M, dtype=torch.float32, device=x.device) if scale is None
+             else _buf(scale, torch.float32, M, "scale"))
+    _check(_int8_rows(_ptr(x), dt, M, K, _ptr(q), _ptr(scale), _stream()), "int8_quantize_rows")
+    return q, scale
+
+
+def int8_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, d=None):
+    """a_q int8 [M, K], a_scale float32 [M], b_q int8 [N, K], b_scale float32 [N] -> BF16 [M, N] (EPI_BF16), or
+    [M, N / 2] of silu(gate) * up with the gate rows of b_q first (EPI_SILU_MUL); add: BF16 of that shape."""
+    _dev(a_q, torch.int8, "a_q")
+    _dev(b_q, torch.int8, "b_q")
+    M, K = _matrix(a_q, "a_q")
+    N = _matrix(b_q, "b_q")[0]
+    _shape(b_q, (N, K), "b_q")
+    _opt(a_scale, torch.float32, (M,), "a_scale")
+    _opt(b_scale, torch.float32, (N,), "b_scale")
+    n_out = N // 2 if epilogue == EPI_SILU_MUL else N
+    _opt(add, torch.bfloat16, (M, n_out), "add")
+    d = (torch.empty((M, n_out), dtype=torch.bfloat16, device=a_q.device) if d is None
+         else _buf(d, torch.bfloat16, M * n_out, "d"))
+    _check(_int8_gemm(_ptr(a_q), _ptr(a_scale), _ptr(b_q), _ptr(b_scale), M, N, K, epilogue, _ptr(add), _ptr(d),
+                      _stream()), "int8_gemm")
+    return d
+
+
+class Int8FFNWeights:
+    """Device weights of a dense expert: w1_q int8 [2I, H] (gate rows, then up rows) with w1_scale float32 [2I], and
+    w2_q int8 [H, I] with w2_scale float32 [H]."""
+
+    def __init__(self, w1_q, w1_scale, w2_q, w2_scale):
+        _dev(w1_q, torch.int8, "w1_q")
+        _dev(w2_q, torch.int8, "w2_q")
+        two_i, self.hidden = _matrix(w1_q, "w1_q")
+        self.inter = two_i // 2
+        _shape(w2_q, (self.hidden, self.inter), "w2_q")
+        if two_i % 2:
+            raise ValueError(f"w1_q: an even number of rows (gate and up), got {two_i}")
+        _opt(w1_scale, torch.float32, (two_i,), "w1_scale")
+        _opt(w2_scale, torch.float32, (self.hidden,), "w2_scale")
+        self.w1_q, self.w1_scale, self.w2_q, self.w2_scale = w1_q, w1_scale, w2_q, w2_scale
+
+
+def prepare_int8_weights(w_gate, w_up, w_down) -> Int8FFNWeights:
+    """Offline: BF16 or float32 w_gate, w_up [I, H] and w_down [H, I], quantized per output channel."""
+    w1_q, w1_scale = int8_quantize_rows(torch.cat([w_gate, w_up], dim=0).contiguous())
+    w2_q, w2_scale = int8_quantize_rows(w_down.contiguous())
+    return Int8FFNWeights(w1_q, w1_scale, w2_q, w2_scale)
+
+
+def int8_ffn_ws_bytes(T, hidden, inter) -> int:
+    return int(_int8_ffn_ws(T, hidden, inter))
+
+
+def int8_ffn_forward(weights: Int8FFNWeights, x, add=None, out=None, ws=None):
+    """Dense expert FFN of x BF16 [T, H] in 8-bit integers -> BF16 [T, H], plus add (BF16 [T, H], such as the routed
+    experts' output; may be out) when given."""
+    w = weights
+    _dev(x, torch.bfloat16, "x")
+    T = _matrix(x, "x")[0]
+    _shape(x, (T, w.hidden), "x")
+    _dev(w.w1_q, torch.int8, "weights.w1_q")
+    _opt(add, torch.bfloat16, (T, w.hidden), "add")
+    out = (torch.empty((T, w.hidden), dtype=torch.bfloat16, device=x.device) if out is None
+           else _buf(out, torch.bfloat16, T * w.hidden, "out"))
+    ws = (_alloc_ws(int8_ffn_ws_bytes(T, w.hidden, w.inter), x.device) if ws is None
+          else _buf(ws, torch.uint8, 0, "ws"))
+    _check(_int8_ffn(_ptr(w.w1_q), _ptr(w.w1_scale), _ptr(w.w2_q), _ptr(w.w2_scale), _ptr(x), T, w.hidden, w.inter,
+                     _ptr(add), _ptr(out), _ptr(ws), ws.numel(), _stream()), "int8_ffn_forward")
+    return out
 
 
 # --------------------------------------------------------------------- the layer

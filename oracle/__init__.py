@@ -28,7 +28,7 @@ from .formats import (E2M1_MAGNITUDES, E4M3_MAX_CODE, bf16_to_f32, bf16_to_f64, 
 from .quantize import quantize, quantize_batched, dequantize, global_scale
 from .route import route, tile_schedule
 from .fold import fold_gate_up, prepare_weights
-from . import gate, norm
+from . import gate, int8, norm
 from .layer import (grouped_gemm, silu_mul, scatter, moe_forward, bf16_reference_layer,
                     cosine, OracleTrace)
 
@@ -37,5 +37,5 @@ __all__ = [
     "e4m3_decode", "e4m3_encode", "e2m1_decode", "pack_nibbles", "unpack_nibbles",
     "quantize", "quantize_batched", "dequantize", "global_scale", "route", "tile_schedule",
     "fold_gate_up", "prepare_weights", "grouped_gemm", "silu_mul", "scatter", "moe_forward",
-    "bf16_reference_layer", "cosine", "OracleTrace", "gate", "norm",
+    "bf16_reference_layer", "cosine", "OracleTrace", "gate", "int8", "norm",
 ]

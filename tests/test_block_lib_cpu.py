@@ -114,3 +114,35 @@ def test_block_norm_backward(nv):
     for bad in ("d_y", "d_r", "x", "r", "w_pre", "w_post", "gate", "dx", "dr", "a", "b", "c", "ws"):
         assert call(**{bad: ODD}) == ALIGN, bad
     assert call(n=need - 1) == WORKSPACE
+
+
+def test_int8(nv):
+    def rows(x=P, xt=0, M=4, K=64, q=P, s=P):
+        return nv._int8_rows(x, xt, M, K, q, s, None)
+    for bad in (dict(M=-1), dict(K=0), dict(K=24), dict(K=65552)):
+        assert rows(**bad) == SHAPE, bad
+    assert rows(xt=2) == ARG
+    for bad in ("x", "q", "s"):
+        assert rows(**{bad: None}) == NULL and rows(**{bad: ODD}) == ALIGN, bad
+    assert rows(M=0, x=None) == 0
+
+    def gemm(a=P, a_s=P, b=P, b_s=P, M=4, N=64, K=64, epi=0, add=None, d=P):
+        return nv._int8_gemm(a, a_s, b, b_s, M, N, K, epi, add, d, None)
+    for bad in (dict(M=-1), dict(N=0), dict(N=12), dict(N=24, epi=1), dict(K=8), dict(K=40), dict(K=65552),
+                dict(M=64 * 65535 + 1)):
+        assert gemm(**bad) == SHAPE, bad
+    assert gemm(epi=2) == ARG and gemm(epi=-1) == ARG
+    for bad in ("a", "a_s", "b", "b_s", "d"):
+        assert gemm(**{bad: None}) == NULL and gemm(**{bad: ODD}) == ALIGN, bad
+    assert gemm(add=ODD) == ALIGN and gemm(M=0, a=None) == 0
+
+    need = nv.int8_ffn_ws_bytes(4, 64, 32)
+    assert need > 0 and nv.int8_ffn_ws_bytes(4, 64, 24) == 0
+
+    def ffn(w1=P, s1=P, w2=P, s2=P, x=P, T=4, H=64, I=32, add=None, out=P, ws=P, n=need):
+        return nv._int8_ffn(w1, s1, w2, s2, x, T, H, I, add, out, ws, n, None)
+    for bad in (dict(T=-1), dict(H=40), dict(I=24), dict(H=0), dict(I=65552), dict(T=64 * 65535 + 1)):
+        assert ffn(**bad) == SHAPE, bad
+    for bad in ("w1", "s1", "w2", "s2", "x", "out", "ws"):
+        assert ffn(**{bad: None}) == NULL and ffn(**{bad: ODD}) == ALIGN, bad
+    assert ffn(add=ODD) == ALIGN and ffn(n=need - 1) == WORKSPACE and ffn(T=0, x=None, out=None) == 0
