@@ -329,7 +329,7 @@ int nvfp4_grouped_gemm_silu_nvfp4(const uint8_t* a_q, const uint8_t* a_sf, const
 
 /* ------------------------------------------------- 8-bit integer products
  * Row quantizer: for each row m of x [M, K] (BF16 or float, row-major)
- *   scale[m] = RN_f32(max_k |x[m, k]| / 127)
+ *   scale[m] = RN_f32(max_k |x[m, k]| * RN_f32(1 / 127))
  *   q[m, k]  = the integer nearest to x[m, k] / scale[m], ties to even (as on
  *              the real quotient), at most 127 in size; 0 where scale is 0.
  * q int8 [M, K]; scale float [M]. For activations a row is a token, for

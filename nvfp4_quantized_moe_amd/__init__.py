@@ -564,7 +564,7 @@ def nvfp4_fold_scales(w1_sf, gs_gate, gs_up, gs1=None):
 # -------------------------------------------------------- 8-bit integer products
 
 def int8_quantize_rows(x, q=None, scale=None):
-    """x BF16 or float32 [M, K] -> (q int8 [M, K], scale float32 [M] = row amax / 127)."""
+    """x BF16 or float32 [M, K] -> (q int8 [M, K], scale float32 [M] = row amax * (1 / 127))."""
     dt = _float_dev(x, "x")
     M, K = _matrix(x, "x")
     q = torch.empty((M, K), dtype=torch.int8, device=x.device) if q is None else _buf(q, torch.int8, M * K, "q")

@@ -1,6 +1,6 @@
 // Products of 8-bit integers with a scale per token and per output channel,
 // for the dense expert that runs beside the routed ones:
-//   q[m, k] = rne(x[m, k] / s_m), s_m = amax_k |x[m, k]| / 127
+//   q[m, k] = rne(x[m, k] / s_m), s_m = amax_k |x[m, k]| * (1 / 127)
 //   C[m, n] = a_s[m] * b_s[n] * sum_k a_q[m, k] b_q[n, k]
 // The sum is exact in int32 (K <= 65536: |sum| <= 2^30), so neither the order
 // of K nor its split can change a result; the scales are applied to it in
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(const T* __restrict__ x,
   __syncthreads();
   m = red[0];
   for (int w = 1; w < (int)blockDim.x / 64; ++w) m = fmaxf(m, red[w]);
-  float s = m / 127.0f;
+  float s = m * (1.0f / 127.0f);
   if (threadIdx.x == 0) scale[blockIdx.x] = s;
   // rows of the smallest numbers are lifted by 2^100 (exactly, like their
   // scale), so that neither 1 / s nor the residual leaves the float32 range

@@ -5,9 +5,9 @@ import numpy as np
 
 
 def quantize_rows(x):
-    """x float64 [M, K] -> (q int8, scale float32): scale = RN_f32(amax / 127), q = rne(x / scale)."""
+    """x float64 [M, K] -> (q int8, scale float32): scale = RN_f32(amax * RN_f32(1 / 127)), q = rne(x / scale)."""
     x = np.asarray(x, np.float64)
-    s = (np.abs(x).max(1).astype(np.float32) / np.float32(127)).astype(np.float32)
+    s = (np.abs(x).max(1).astype(np.float32) * (np.float32(1) / np.float32(127))).astype(np.float32)
     d = np.where(s > 0, s, 1).astype(np.float64)[:, None]
     q = np.rint(x / d)
     # x / d in float64 may land on a half that the real quotient only comes close to: as a fraction it is exact
