@@ -101,8 +101,6 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(const T* __restrict__ x,
 
 // ------------------------------------------------------------------- product
 
-constexpr int kInt8BK = 128;  // K bytes per stage: one 128-byte line per row
-
 struct Int8Args {
   const int8_t* a;
   const float* a_s;
@@ -120,66 +118,112 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return (g < 0.0f ? g * e : g) / (1.0f + e) * u;
 }
 
-// Weight row of row i of a column tile starting at output column n0. SILU:
-// the rows alternate in runs of 32 between gate (row n) and up (row I + n), so
-// that a wave holds both halves of an output in the same lane.
-template <bool SILU>
-__device__ __forceinline__ int tile_weight_row(int i, int n0, int half) {
-  if (!SILU) return n0 + i;
-  const int n = n0 + (i >> 6) * 32 + (i & 31);
-  return (i & 32) ? half + n : n;
+// Tiles in runs of kTileGroup row tiles by all column tiles, so that the
+// workgroups that run at one time share both operands' tiles; consecutive
+// tiles go to one XCD (own L2). Returns (row tile, column tile).
+constexpr int kTileGroup = 8;
+__device__ __forceinline__ int2 tile_of_block(int bid, int mt, int nt) {
+  const int total = mt * nt, whole = total / kXcds * kXcds;
+  const int t = bid < whole ? (bid % kXcds) * (whole / kXcds) + bid / kXcds : bid;
+  const int per = kTileGroup * nt, grp = t / per, rem = t - grp * per;
+  const int rows = min(kTileGroup, mt - grp * kTileGroup);
+  return make_int2(grp * kTileGroup + rem % rows, rem / rows);
 }
 
-// Workgroup tile BM x BN of 2 x 2 waves. MFMA 32x32x32 with the weights as
-// its first operand, so a lane holds four neighbouring output columns of one
-// token. K stages of 128 bytes pass through registers into LDS (two buffers);
-// a row's eight 16-byte chunks are stored at chunk ^ (row & 7), which spreads
-// the 32 rows that a fragment read touches over all banks.
-template <int BM, int BN, bool SILU>
-__global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args g) {
-  constexpr int SM = BM / 64, SN = BN / 64;  // 32-wide subtiles per wave and side
-  static_assert(!SILU || SN % 2 == 0, "gate and up halves in one wave");
-  constexpr int PA = BM * 8 / 256, PB = BN * 8 / 256;  // 16-byte chunks per thread and stage
-  __shared__ uint4 lds[2][(BM + BN) * 8];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave & 1, wn = wave >> 1;
-  const int m0 = blockIdx.y * BM, n0 = blockIdx.x * (SILU ? BN / 2 : BN);
-  const int half = g.N / 2;
-  // rows past the end repeat the last one: their results are not stored
-  const int8_t* pa[PA];
-  const int8_t* pb[PB];
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t int8_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+constexpr int kInt8Out = (int)0x80000000u;  // a buffer offset past every range: such loads give zeros
+
+// 16 bytes per lane from memory to LDS, the lanes' side by side from `to` (the
+// same for the whole wave) on.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, int4v* to, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, voff, soff, 0, 0);
+}
+
+// Eight outputs of one row from their integer sums.
+__device__ __forceinline__ void store_out8(const Int8Args& g, int m, int n, const float (&o)[8], int width) {
+  float f[8];
+  const size_t at = (size_t)m * g.n_out + n;
 #pragma unroll
-  for (int i = 0; i < PA; ++i) {
-    const int row = (threadIdx.x + i * 256) >> 3;
-    pa[i] = g.a + (size_t)min(m0 + row, g.M - 1) * g.K;
+  for (int e = 0; e < 8; ++e) f[e] = o[e];
+  if (width == 8) {
+    if (g.add) {
+      const uint4 v = *reinterpret_cast<const uint4*>(g.add + at);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[2 * e] += __uint_as_float(w[e] << 16);
+        f[2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    }
+    *reinterpret_cast<uint4*>(g.d + at) = make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]),
+                                                     f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7]));
+  } else {
+    if (g.add) {
+      const uint2 v = *reinterpret_cast<const uint2*>(g.add + at);
+      f[0] += __uint_as_float(v.x << 16);
+      f[1] += __uint_as_float(v.x & 0xFFFF0000u);
+      f[2] += __uint_as_float(v.y << 16);
+      f[3] += __uint_as_float(v.y & 0xFFFF0000u);
+    }
+    *reinterpret_cast<uint2*>(g.d + at) = make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
   }
+}
+
+// Workgroup tile BM x BN of WM x WN waves; MFMA 32x32x32 with the weights as
+// its first operand, so a lane holds runs of four output columns of one token.
+//
+// K passes in stages of 64 bytes through four LDS buffers, filled straight
+// from memory (buffer loads to LDS: no registers, and the row step is a scalar
+// offset) three stages ahead; the wait before a stage leaves the two younger
+// stages in flight. A row's four 16-byte chunks are stored at chunk ^
+// ((row / 2) & 3), which spreads the rows that eight lanes of a fragment read
+// touch over all banks; the loads apply it to the address they read. Inside a
+// stage the next fragments are read between the MFMAs of the current ones.
+//
+// SILU: the tile's weight rows alternate in runs of 32 between gate (row n)
+// and up (row I + n), so that a wave holds both halves of an output.
+constexpr int kBK = 64;
+template <int BM, int BN, int WM, int WN, bool SILU>
+__global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, int mt, int nt) {
+  constexpr int TH = 64 * WM * WN;
+  constexpr int SM = BM / WM / 32, SN = BN / WN / 32;  // 32 x 32 subtiles of a wave
+  static_assert(!SILU || SN % 2 == 0, "gate and up halves in one wave");
+  constexpr int RPI = TH / 4;                          // rows of one load instruction of the workgroup
+  constexpr int PA = BM / RPI, PB = BN / RPI, PL = PA + PB;
+  constexpr int BUF = (BM + BN) * 4;                   // 16-byte chunks of a buffer: A rows, then B rows
+  __shared__ int4v l0[BUF], l1[BUF], l2[BUF], l3[BUF];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int2 tile = tile_of_block(blockIdx.x, mt, nt);
+  const int m0 = tile.x * BM, n0 = tile.y * (SILU ? BN / 2 : BN), half = g.N / 2;
+  // This thread's chunk of every load: row trow + RPI i of the tile (the last
+  // row of the matrix again where there is none: its results are not stored),
+  // K bytes tk of a stage. SILU: the 16 rows of a wave lie in one half.
+  const int trow = threadIdx.x >> 2, tk = ((threadIdx.x & 3) ^ ((trow >> 1) & 3)) * 16;
+  const int a_rows = min(BM, g.M - m0), b_rows = min(SILU ? BN / 2 : BN, (SILU ? half : g.N) - n0);
+  const int b0 = SILU && ((wave >> 1) & 1) ? half + n0 : n0;
+  const __amdgpu_buffer_rsrc_t ra = int8_rsrc(g.a + (size_t)m0 * g.K, (uint32_t)(a_rows * g.K));
+  const __amdgpu_buffer_rsrc_t rb = int8_rsrc(g.b + (size_t)b0 * g.K, (uint32_t)(b_rows * g.K));
+  int va[PA], vb[PB];
+#pragma unroll
+  for (int i = 0; i < PA; ++i) va[i] = min(trow + i * RPI, a_rows - 1) * g.K + tk;
 #pragma unroll
   for (int i = 0; i < PB; ++i) {
-    const int row = (threadIdx.x + i * 256) >> 3;
-    pb[i] = g.b + (size_t)min(tile_weight_row<SILU>(row, n0, half), g.N - 1) * g.K;
+    const int row = SILU ? (trow >> 6) * 32 + (trow & 31) + i * (RPI / 2) : trow + i * RPI;
+    vb[i] = min(row, b_rows - 1) * g.K + tk;
   }
-  const int kc = (threadIdx.x & 7) * 16;
-  uint4 ra[PA], rb[PB];
-  auto fetch = [&](int k0) {
-    const bool in = k0 + kc < g.K;
+  static_assert(!SILU || RPI % 64 == 0, "a wave's rows of every load lie in one half");
+  auto fetch = [&](int k0, int4v* to) {
+    const bool in = k0 + tk < g.K;            // zeros past the end of a row
+    const int ks = k0 < g.K ? k0 : 0;         // the scalar offset stays inside the range
 #pragma unroll
     for (int i = 0; i < PA; ++i)
-      ra[i] = in ? *reinterpret_cast<const uint4*>(pa[i] + k0 + kc) : make_uint4(0, 0, 0, 0);
+      load_lds16(ra, to + wave * 64 + i * TH, in ? va[i] : kInt8Out, ks);
 #pragma unroll
     for (int i = 0; i < PB; ++i)
-      rb[i] = in ? *reinterpret_cast<const uint4*>(pb[i] + k0 + kc) : make_uint4(0, 0, 0, 0);
-  };
-  auto place = [&](uint4* to) {
-#pragma unroll
-    for (int i = 0; i < PA; ++i) {
-      const int row = (threadIdx.x + i * 256) >> 3;
-      to[row * 8 + ((threadIdx.x & 7) ^ (row & 7))] = ra[i];
-    }
-#pragma unroll
-    for (int i = 0; i < PB; ++i) {
-      const int row = (threadIdx.x + i * 256) >> 3;
-      to[(BM + row) * 8 + ((threadIdx.x & 7) ^ (row & 7))] = rb[i];
-    }
+      load_lds16(rb, to + BM * 4 + wave * 64 + i * TH, in ? vb[i] : kInt8Out, ks);
   };
   int16v acc[SN][SM];
 #pragma unroll
@@ -188,68 +232,138 @@ __global__ __launch_bounds__(256) void int8_tile_kernel(Int8Args g) {
     for (int j = 0; j < SM; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  const int stages = (g.K + kInt8BK - 1) / kInt8BK;
-  fetch(0);
-  place(lds[0]);
-  __syncthreads();
   const int r = lane & 31, hi = lane >> 5;
-  for (int s = 0; s < stages; ++s) {
-    if (s + 1 < stages) fetch((s + 1) * kInt8BK);
-    const uint4* at = lds[s & 1];
+  int fa_at[2], fb_at[2];
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      int4v fa[SM], fb[SN];
-      const int c = ks * 2 + hi;
-#pragma unroll
-      for (int j = 0; j < SM; ++j)
-        fa[j] = __builtin_bit_cast(int4v, at[(wm * 32 * SM + j * 32 + r) * 8 + (c ^ (r & 7))]);
-#pragma unroll
-      for (int i = 0; i < SN; ++i)
-        fb[i] = __builtin_bit_cast(int4v, at[(BM + wn * 32 * SN + i * 32 + r) * 8 + (c ^ (r & 7))]);
-#pragma unroll
-      for (int i = 0; i < SN; ++i)
-#pragma unroll
-        for (int j = 0; j < SM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[i], fa[j], acc[i][j], 0, 0, 0);
-    }
-    if (s + 1 < stages) place(lds[(s + 1) & 1]);
-    __syncthreads();
+  for (int ks = 0; ks < 2; ++ks) {
+    const int c = (ks * 2 + hi) ^ ((r >> 1) & 3);
+    fa_at[ks] = (wm * 32 * SM + r) * 4 + c;
+    fb_at[ks] = (BM + wn * 32 * SN + r) * 4 + c;
   }
-  // lane: token column r of a subtile, weight rows 8 q + 4 hi + 0..3 for q = 0..3
+  auto compute = [&](const int4v* at) {
+    int4v fa[2][SM], fb[2][SN];
+    auto read = [&](int ks) {
 #pragma unroll
-  for (int j = 0; j < SM; ++j) {
-    const int m = m0 + wm * 32 * SM + j * 32 + r;
-    if (m >= g.M) continue;
-    const float as = g.a_s[m];
+      for (int j = 0; j < SM; ++j) fa[ks][j] = at[fa_at[ks] + j * 128];
 #pragma unroll
-    for (int i = 0; i < SN; i += SILU ? 2 : 1) {
-      const int col0 = SILU ? n0 + (wn * SN + i) / 2 * 32 : n0 + (wn * SN + i) * 32;
+      for (int i = 0; i < SN; ++i) fb[ks][i] = at[fb_at[ks] + i * 128];
+    };
+    read(0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = col0 + 8 * q + 4 * hi;
-        if (n >= g.n_out) continue;
-        const float4 bs = *reinterpret_cast<const float4*>(g.b_s + n);
-        float o[4];
-        if constexpr (SILU) {
-          const float4 us = *reinterpret_cast<const float4*>(g.b_s + half + n);
+    for (int ks = 0; ks < 2; ++ks) {
+      if (ks == 0) read(1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = silu_mul((float)acc[i][j][4 * q + e] * (as * (&bs.x)[e]),
-                            (float)acc[i + 1][j][4 * q + e] * (as * (&us.x)[e]));
-        } else {
+      for (int i = 0; i < SN; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = (float)acc[i][j][4 * q + e] * (as * (&bs.x)[e]);
+        for (int j = 0; j < SM; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][i], fa[ks][j], acc[i][j], 0, 0, 0);
+      if constexpr (SM * SN >= SM + SN) {
+        if (ks == 0) {  // one fragment read after each MFMA
+#pragma unroll
+          for (int u = 0; u < SM + SN; ++u) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
+          __builtin_amdgcn_sched_group_barrier(0x8, SM * SN - SM - SN, 0);
         }
-        const size_t at = (size_t)m * g.n_out + n;
-        if (g.add) {
-          const uint2 v = *reinterpret_cast<const uint2*>(g.add + at);
-          o[0] += __uint_as_float(v.x << 16);
-          o[1] += __uint_as_float(v.x & 0xFFFF0000u);
-          o[2] += __uint_as_float(v.y << 16);
-          o[3] += __uint_as_float(v.y & 0xFFFF0000u);
-        }
-        *reinterpret_cast<uint2*>(g.d + at) = make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
       }
     }
+  };
+  // Waits until at most `left` of this wave's loads are in flight, then for
+  // all waves. The loads of a wave complete in order.
+  auto wait = [](auto left) {
+    constexpr int n = decltype(left)::value;
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 7 << 4);  // vmcnt(n), lgkmcnt(0), no export count
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0> none;
+  constexpr std::integral_constant<int, 2 * PL> two_stages;
+  const int stages = (g.K + kBK - 1) / kBK;
+  fetch(0, l0);
+  fetch(kBK, l1);
+  fetch(2 * kBK, l2);
+  // stage s: its own loads have arrived; every wave is past stage s - 1, whose
+  // buffer takes the loads of stage s + 3 (zeros where there is none, so that
+  // the count of younger loads is always the same)
+  auto stage = [&](int s, const int4v* cur, int4v* next) {
+    wait(two_stages);
+    fetch((s + 3) * kBK, next);
+    compute(cur);
+  };
+  for (int s = 0; s < stages; s += 4) {
+    stage(s, l0, l3);
+    if (s + 1 < stages) stage(s + 1, l1, l0);
+    if (s + 2 < stages) stage(s + 2, l2, l1);
+    if (s + 3 < stages) stage(s + 3, l3, l2);
+  }
+  wait(none);
+
+  // Epilogue, each wave by itself: 32 tokens x 32 SN columns of sums through
+  // LDS, so that a lane takes eight neighbouring columns of a token (four for
+  // SILU) and its neighbours the rest of whole 64-byte lines. Stored
+  // straight from the MFMA layout (8 bytes here and there in 32 rows), the
+  // down product of 8192 tokens ran 30 us longer.
+  constexpr int COLS = 32 * SN, PITCH = COLS + 4;
+  constexpr int WPB = BUF * 16 / (32 * PITCH * 4);  // waves whose block fits one buffer
+  static_assert(WPB * 4 >= WM * WN, "the LDS buffers hold every wave's block");
+  int4v* const buf = wave / WPB == 0 ? l0 : wave / WPB == 1 ? l1 : wave / WPB == 2 ? l2 : l3;
+  int* const sums = reinterpret_cast<int*>(buf) + (wave % WPB) * 32 * PITCH;
+  constexpr int LPR = COLS / 8, RPS = 64 / LPR;  // lanes of a row, rows of a step
+  const int col = lane % LPR;
+  // output column and scales of this lane, the same for all its rows
+  const int oc = SILU ? (col / 8) * 32 + (col % 8) * 4 : col * 8;  // within the wave's outputs
+  const int n = n0 + wn * (SILU ? COLS / 2 : COLS) + oc;
+  const bool n_ok = n < g.n_out;
+  float bs[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bs[e] = 0.0f;
+  if (n_ok) {
+    const float4 s0 = *reinterpret_cast<const float4*>(g.b_s + n);
+    const float4 s1 = *reinterpret_cast<const float4*>(g.b_s + (SILU ? half + n : n + 4));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bs[e] = (&s0.x)[e];
+      bs[4 + e] = (&s1.x)[e];
+    }
+  }
+  // where the lane's sums lie in a row: eight in a run, or four gate and the
+  // four up sums 32 columns on
+  const int c0 = SILU ? (col / 8) * 64 + (col % 8) * 4 : col * 8, c1 = SILU ? c0 + 32 : c0 + 4;
+#pragma unroll
+  for (int j = 0; j < SM; ++j) {
+#pragma unroll
+    for (int i = 0; i < SN; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<int4v*>(sums + r * PITCH + i * 32 + 8 * q + 4 * hi) =
+            int4v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    wave_lds_fence();
+#pragma unroll
+    for (int st = 0; st < 32 / RPS; ++st) {
+      const int row = st * RPS + lane / LPR;
+      const int m = m0 + wm * 32 * SM + j * 32 + row;
+      if (m < g.M && n_ok) {
+        const int4v v0 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c0);
+        const int4v v1 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c1);
+        const float as = g.a_s[m];
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[e] = (float)v0[e] * (as * bs[e]);
+          o[4 + e] = (float)v1[e] * (as * bs[4 + e]);
+        }
+        if constexpr (SILU) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = silu_mul(o[e], o[4 + e]);
+        }
+        store_out8(g, m, n, o, SILU ? 4 : 8);
+      }
+    }
+    wave_lds_fence();
   }
 }
 
@@ -284,21 +398,23 @@ static int int8_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue) {
   return NVFP4_OK;
 }
 
-template <bool SILU>
-static int launch_int8(const Int8Args& g, hipStream_t stream) {
-  // 128 x 128 tiles where they fill the 256 CUs, else 64 x 64 (64 x 128 for
-  // SILU, whose waves need a gate and an up subtile)
-  const int64_t big = (int64_t)((g.M + 127) / 128) * ((g.N + 127) / 128);
-  if (big >= 256) {
-    hipLaunchKernelGGL((int8_tile_kernel<128, 128, SILU>), dim3((g.N + 127) / 128, (g.M + 127) / 128), dim3(256), 0,
-                       stream, g);
-  } else {
-    constexpr int BN = SILU ? 128 : 64;
-    hipLaunchKernelGGL((int8_tile_kernel<64, BN, SILU>), dim3((g.N + BN - 1) / BN, (g.M + 63) / 64), dim3(256), 0,
-                       stream, g);
-  }
+template <int BM, int BN, int WM, int WN, bool SILU>
+static int launch_int8_tile(const Int8Args& g, hipStream_t stream) {
+  const int mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN;
+  if ((int64_t)mt * nt >= (1ll << 31)) return NVFP4_ERR_SHAPE;
+  hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, SILU>), dim3((unsigned)mt * nt), dim3(64 * WM * WN), 0, stream,
+                     g, mt, nt);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
+}
+
+template <bool SILU>
+static int launch_int8(const Int8Args& g, hipStream_t stream) {
+  // the largest tile that still gives most of the 256 CUs one
+  const auto tiles = [&](int bm, int bn) { return (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
+  if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, SILU>(g, stream);
+  if (tiles(128, 128) >= 192) return launch_int8_tile<128, 128, 2, 2, SILU>(g, stream);
+  return launch_int8_tile<64, SILU ? 128 : 64, 2, 2, SILU>(g, stream);
 }
 
 extern "C" int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int32_t M,
