@@ -141,46 +141,36 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, int4v* to, 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, voff, soff, 0, 0);
 }
 
-// Eight outputs of one row from their integer sums.
-__device__ __forceinline__ void store_out8(const Int8Args& g, int m, int n, const float (&o)[8], int width) {
-  float f[8];
-  const size_t at = (size_t)m * g.n_out + n;
+// W = 8 or 4 outputs of one row, with the BF16 values to be added.
+template <int W>
+struct OutVec;
+template <>
+struct OutVec<8> {
+  typedef uint32_t type __attribute__((ext_vector_type(4)));
+};
+template <>
+struct OutVec<4> {
+  typedef uint32_t type __attribute__((ext_vector_type(2)));
+};
+template <int W>
+__device__ __forceinline__ typename OutVec<W>::type add_and_round(const float (&o)[8], typename OutVec<W>::type add) {
+  typename OutVec<W>::type r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = o[e];
-  if (width == 8) {
-    if (g.add) {
-      const uint4 v = *reinterpret_cast<const uint4*>(g.add + at);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[2 * e] += __uint_as_float(w[e] << 16);
-        f[2 * e + 1] += __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-    }
-    *reinterpret_cast<uint4*>(g.d + at) = make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]),
-                                                     f32x2_to_bf16x2(f[4], f[5]), f32x2_to_bf16x2(f[6], f[7]));
-  } else {
-    if (g.add) {
-      const uint2 v = *reinterpret_cast<const uint2*>(g.add + at);
-      f[0] += __uint_as_float(v.x << 16);
-      f[1] += __uint_as_float(v.x & 0xFFFF0000u);
-      f[2] += __uint_as_float(v.y << 16);
-      f[3] += __uint_as_float(v.y & 0xFFFF0000u);
-    }
-    *reinterpret_cast<uint2*>(g.d + at) = make_uint2(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]));
-  }
+  for (int e = 0; e < W / 2; ++e)
+    r[e] = f32x2_to_bf16x2(o[2 * e] + __uint_as_float(add[e] << 16),
+                           o[2 * e + 1] + __uint_as_float(add[e] & 0xFFFF0000u));
+  return r;
 }
 
 // Workgroup tile BM x BN of WM x WN waves; MFMA 32x32x32 with the weights as
 // its first operand, so a lane holds runs of four output columns of one token.
 //
 // K passes in stages of 64 bytes through four LDS buffers, filled straight
-// from memory (buffer loads to LDS: no registers, and the row step is a scalar
-// offset) three stages ahead; the wait before a stage leaves the two younger
+// from memory (buffer loads to LDS pass no register) three stages ahead; the wait before a stage leaves the two younger
 // stages in flight. A row's four 16-byte chunks are stored at chunk ^
 // ((row / 2) & 3), which spreads the rows that eight lanes of a fragment read
 // touch over all banks; the loads apply it to the address they read. Inside a
-// stage the next fragments are read between the MFMAs of the current ones.
+// stage the second half's fragments are read under the first half's MFMAs.
 //
 // SILU: the tile's weight rows alternate in runs of 32 between gate (row n)
 // and up (row I + n), so that a wave holds both halves of an output.
@@ -257,16 +247,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
 #pragma unroll
         for (int j = 0; j < SM; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][i], fa[ks][j], acc[i][j], 0, 0, 0);
-      if constexpr (SM * SN >= SM + SN) {
-        if (ks == 0) {  // one fragment read after each MFMA
-#pragma unroll
-          for (int u = 0; u < SM + SN; ++u) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-          }
-          __builtin_amdgcn_sched_group_barrier(0x8, SM * SN - SM - SN, 0);
-        }
-      }
     }
   };
   // Waits until at most `left` of this wave's loads are in flight, then for
@@ -333,6 +313,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   // where the lane's sums lie in a row: eight in a run, or four gate and the
   // four up sums 32 columns on
   const int c0 = SILU ? (col / 8) * 64 + (col % 8) * 4 : col * 8, c1 = SILU ? c0 + 32 : c0 + 4;
+  // the rows' scales and the values to add are loaded one subtile ahead
+  constexpr int STEPS = 32 / RPS, W = SILU ? 4 : 8;
+  typedef typename OutVec<W>::type vec_t;
+  float as[2][STEPS];
+  vec_t add[2][STEPS];
+  auto row_of = [&](int j, int st) { return m0 + wm * 32 * SM + j * 32 + st * RPS + lane / LPR; };
+  auto load_rows = [&](int j) {
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+      const int m = row_of(j, st);
+      const bool ok = m < g.M && n_ok;
+      as[j & 1][st] = ok ? g.a_s[m] : 0.0f;
+      add[j & 1][st] = vec_t(0u);
+      if (g.add && ok) add[j & 1][st] = *reinterpret_cast<const vec_t*>(g.add + (size_t)m * g.n_out + n);
+    }
+  };
+  load_rows(0);
 #pragma unroll
   for (int j = 0; j < SM; ++j) {
 #pragma unroll
@@ -342,28 +339,104 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
         *reinterpret_cast<int4v*>(sums + r * PITCH + i * 32 + 8 * q + 4 * hi) =
             int4v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     wave_lds_fence();
+    if (j + 1 < SM) load_rows(j + 1);
 #pragma unroll
-    for (int st = 0; st < 32 / RPS; ++st) {
-      const int row = st * RPS + lane / LPR;
-      const int m = m0 + wm * 32 * SM + j * 32 + row;
-      if (m < g.M && n_ok) {
-        const int4v v0 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c0);
-        const int4v v1 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c1);
-        const float as = g.a_s[m];
-        float o[8];
+    for (int st = 0; st < STEPS; ++st) {
+      const int row = st * RPS + lane / LPR, m = row_of(j, st);
+      const int4v v0 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c0);
+      const int4v v1 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c1);
+      float o[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[e] = (float)v0[e] * (as * bs[e]);
-          o[4 + e] = (float)v1[e] * (as * bs[4 + e]);
-        }
-        if constexpr (SILU) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = silu_mul(o[e], o[4 + e]);
-        }
-        store_out8(g, m, n, o, SILU ? 4 : 8);
+      for (int e = 0; e < 4; ++e) {
+        o[e] = (float)v0[e] * (as[j & 1][st] * bs[e]);
+        o[4 + e] = (float)v1[e] * (as[j & 1][st] * bs[4 + e]);
       }
+      if constexpr (SILU) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = silu_mul(o[e], o[4 + e]);
+      }
+      if (m < g.M && n_ok)
+        *reinterpret_cast<vec_t*>(g.d + (size_t)m * g.n_out + n) = add_and_round<W>(o, add[j & 1][st]);
     }
     wave_lds_fence();
+  }
+}
+
+// Few tokens (up to 16 MT per workgroup): the weights' bytes count, and every
+// wave of the chip has to read some. A workgroup takes 16 weight rows (SILU: 8
+// gate and their 8 up rows) and its eight waves split K; nothing is staged, a
+// wave streams both operands' MFMA 16x16x64 fragments from memory (64
+// contiguous bytes of each of 16 rows per load) with the next group in
+// flight, and the eight partial sums, exact integers, meet in LDS.
+constexpr int kSkinnyWaves = 8;
+template <int MT, bool SILU>
+__global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8Args g) {
+  constexpr int U = MT == 4 ? 2 : 4;  // 64-byte steps of a group
+  __shared__ int sums[kSkinnyWaves][MT][16][17];  // [wave][subtile][token][weight row], padded against conflicts
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = lane & 15, kq = (lane >> 4) * 16;
+  const int m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * (SILU ? 8 : 16), half = g.N / 2;
+  const int row = SILU ? (i < 8 ? n0 + i : half + n0 + i - 8) : min(n0 + i, g.N - 1);
+  const int steps = (g.K + 63) / 64;
+  const int per = ((steps + kSkinnyWaves - 1) / kSkinnyWaves + 1) & ~1;  // whole 128-byte lines per wave
+  const int s0 = wave * per, s1 = min(s0 + per, steps);
+  const int8_t* pb = g.b + (size_t)row * g.K + kq;
+  const int8_t* pa[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) pa[j] = g.a + (size_t)min(m0 + 16 * j + i, g.M - 1) * g.K + kq;
+  int4v acc[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) acc[j] = int4v{0, 0, 0, 0};
+  int4v fa[2][U][MT], fb[2][U];
+  auto load = [&](int s, int4v (&a)[U][MT], int4v (&b)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (s + u) * 64;
+      const bool in = s + u < s1 && k + kq < g.K;  // else zeros: past this wave's share or the row
+      b[u] = int4v{0, 0, 0, 0};
+      if (in) b[u] = *reinterpret_cast<const int4v*>(pb + k);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        a[u][j] = int4v{0, 0, 0, 0};
+        if (in) a[u][j] = *reinterpret_cast<const int4v*>(pa[j] + k);
+      }
+    }
+  };
+  auto multiply = [&](const int4v (&a)[U][MT], const int4v (&b)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[u], a[u][j], acc[j], 0, 0, 0);
+  };
+  load(s0, fa[0], fb[0]);
+  for (int s = s0; s < s1; s += 2 * U) {
+    load(s + U, fa[1], fb[1]);
+    multiply(fa[0], fb[0]);
+    load(s + 2 * U, fa[0], fb[0]);
+    multiply(fa[1], fb[1]);
+  }
+  // lane: token i of a subtile, weight rows 4 (lane / 16) + 0..3
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sums[wave][j][i][4 * (lane >> 4) + v] = acc[j][v];
+  __syncthreads();
+  constexpr int COLS = SILU ? 8 : 16;
+  for (int at = threadIdx.x; at < MT * 16 * COLS; at += 64 * kSkinnyWaves) {
+    const int c = at % COLS, tok = at / COLS, m = m0 + tok, n = n0 + c;
+    if (m >= g.M || n >= g.n_out) continue;
+    int s = 0, u = 0;
+#pragma unroll
+    for (int w = 0; w < kSkinnyWaves; ++w) {
+      s += sums[w][tok >> 4][tok & 15][c];
+      if (SILU) u += sums[w][tok >> 4][tok & 15][c + 8];
+    }
+    const float as = g.a_s[m];
+    float o = (float)s * (as * g.b_s[n]);
+    if (SILU) o = silu_mul(o, (float)u * (as * g.b_s[half + n]));
+    const size_t d = (size_t)m * g.n_out + n;
+    if (g.add) o += bf16_to_f32(g.add[d]);
+    g.d[d] = (uint16_t)f32_to_bf16(o);
   }
 }
 
@@ -408,8 +481,23 @@ static int launch_int8_tile(const Int8Args& g, hipStream_t stream) {
   return NVFP4_OK;
 }
 
+template <int MT, bool SILU>
+static int launch_int8_skinny(const Int8Args& g, hipStream_t stream) {
+  const int cols = SILU ? 8 : 16;
+  hipLaunchKernelGGL((int8_skinny_kernel<MT, SILU>), dim3((g.n_out + cols - 1) / cols, (g.M + 16 * MT - 1) / (16 * MT)),
+                     dim3(64 * kSkinnyWaves), 0, stream, g);
+  NVFP4_CHECK_LAUNCH();
+  return NVFP4_OK;
+}
+
+constexpr int kSkinnyM = 64;
 template <bool SILU>
 static int launch_int8(const Int8Args& g, hipStream_t stream) {
+  if (g.M <= kSkinnyM) {
+    if (g.M <= 16) return launch_int8_skinny<1, SILU>(g, stream);
+    if (g.M <= 32) return launch_int8_skinny<2, SILU>(g, stream);
+    return launch_int8_skinny<4, SILU>(g, stream);
+  }
   // the largest tile that still gives most of the 256 CUs one
   const auto tiles = [&](int bm, int bn) { return (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
   if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, SILU>(g, stream);
