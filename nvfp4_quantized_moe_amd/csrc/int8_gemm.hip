@@ -266,9 +266,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   fetch(0, l0);
   fetch(kBK, l1);
   fetch(2 * kBK, l2);
-  // stage s: its own loads have arrived; every wave is past stage s - 1, whose
-  // buffer takes the loads of stage s + 3 (zeros where there is none, so that
-  // the count of younger loads is always the same)
+  // Stage s: its own loads have arrived; every wave is past stage s - 1, whose
+  // buffer takes the loads of stage s + 3. Up to three stages past the end of K
+  // load and add zeros: with a branch around them the compiler no longer knows
+  // which buffer a load fills, and waits for all of them before it reads any.
   auto stage = [&](int s, const int4v* cur, int4v* next) {
     wait(two_stages);
     fetch((s + 3) * kBK, next);
@@ -276,9 +277,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   };
   for (int s = 0; s < stages; s += 4) {
     stage(s, l0, l3);
-    if (s + 1 < stages) stage(s + 1, l1, l0);
-    if (s + 2 < stages) stage(s + 2, l2, l1);
-    if (s + 3 < stages) stage(s + 3, l3, l2);
+    stage(s + 1, l1, l0);
+    stage(s + 2, l2, l1);
+    stage(s + 3, l3, l2);
   }
   wait(none);
 
@@ -321,12 +322,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   auto row_of = [&](int j, int st) { return m0 + wm * 32 * SM + j * 32 + st * RPS + lane / LPR; };
   auto load_rows = [&](int j) {
 #pragma unroll
-    for (int st = 0; st < STEPS; ++st) {
-      const int m = row_of(j, st);
-      const bool ok = m < g.M && n_ok;
-      as[j & 1][st] = ok ? g.a_s[m] : 0.0f;
-      add[j & 1][st] = vec_t(0u);
-      if (g.add && ok) add[j & 1][st] = *reinterpret_cast<const vec_t*>(g.add + (size_t)m * g.n_out + n);
+    for (int st = 0; st < STEPS; ++st) as[j & 1][st] = g.a_s[min(row_of(j, st), g.M - 1)];
+    if (g.add) {
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st)
+        add[j & 1][st] = *reinterpret_cast<const vec_t*>(g.add + (size_t)min(row_of(j, st), g.M - 1) * g.n_out +
+                                                         (n_ok ? n : 0));
+    } else {
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) add[j & 1][st] = vec_t(0u);
     }
   };
   load_rows(0);
