@@ -344,10 +344,14 @@ int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int32_t K, int
  * epilogue NVFP4_EPI_SILU_MUL: gate rows [0, I), up rows [I, 2I) of b_q, N = 2I:
  *   d BF16 [M, I], d = RN_bf16(silu(G[m, n]) * G[m, I + n] [+ add]); I % 8 == 0
  * add: BF16 of d's shape, or NULL; may be d itself. K % 16 == 0, K <= 65536,
- * M <= 64 * 65535. One launch.
+ * M <= 64 * 65535. ws: at least int8_gemm_ws_bytes(M, N, K) bytes (the sums of
+ * the parts of K where few tokens split it; 0 otherwise, then ws may be NULL).
+ * One launch, or two with parts.
  */
+size_t int8_gemm_ws_bytes(int32_t M, int32_t N, int32_t K);
 int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int32_t M, int32_t N,
-              int32_t K, int32_t epilogue, const void* add_bf16, void* d_bf16, void* stream);
+              int32_t K, int32_t epilogue, const void* add_bf16, void* d_bf16, void* ws, size_t ws_bytes,
+              void* stream);
 
 /* Dense (shared) expert FFN in 8-bit integers: quantize x, the gate+up product
  * with the SiLU epilogue into BF16 h, quantize h, the down product, and add:

@@ -23,7 +23,7 @@ __all__ = [
     "nvfp4_moe_ws_bytes", "nvfp4_moe_ws_layout", "nvfp4_moe_tile_m", "MoEWeights", "prepare_weights",
     "ws_view", "SCORE_SOFTMAX", "SCORE_SIGMOID", "SCORE_SQRT_SOFTPLUS", "moe_gate_topk", "moe_balance_loss",
     "moe_balance_loss_ws_bytes", "moe_gate_backward", "moe_block_norm", "moe_block_norm_backward",
-    "moe_block_norm_backward_ws_bytes", "int8_quantize_rows", "int8_gemm", "int8_ffn_forward", "int8_ffn_ws_bytes",
+    "moe_block_norm_backward_ws_bytes", "int8_quantize_rows", "int8_gemm", "int8_gemm_ws_bytes", "int8_ffn_forward", "int8_ffn_ws_bytes",
     "Int8FFNWeights", "prepare_int8_weights",
 ]
 
@@ -94,7 +94,8 @@ _block_norm_ws = _sig("moe_block_norm_backward_ws_bytes", _sz, _i32, _i32)
 _block_norm_backward = _sig("moe_block_norm_backward", ctypes.c_int, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
                             _vp, _vp, _vp, _i32, _f32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
 _int8_rows = _sig("int8_quantize_rows", ctypes.c_int, _vp, _i32, _i32, _i32, _vp, _vp, _vp)
-_int8_gemm = _sig("int8_gemm", ctypes.c_int, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp)
+_int8_gemm_ws = _sig("int8_gemm_ws_bytes", _sz, _i32, _i32, _i32)
+_int8_gemm = _sig("int8_gemm", ctypes.c_int, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp)
 _int8_ffn_ws = _sig("int8_ffn_ws_bytes", _sz, _i32, _i32, _i32)
 _int8_ffn = _sig("int8_ffn_forward", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp)
 
@@ -574,7 +575,11 @@ def int8_quantize_rows(x, q=None, scale=None):
     return q, scale
 
 
-def int8_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, d=None):
+def int8_gemm_ws_bytes(M, N, K) -> int:
+    return int(_int8_gemm_ws(M, N, K))
+
+
+def int8_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, d=None, ws=None):
     """a_q int8 [M, K], a_scale float32 [M], b_q int8 [N, K], b_scale float32 [N] -> BF16 [M, N] (EPI_BF16), or
     [M, N / 2] of silu(gate) * up with the gate rows of b_q first (EPI_SILU_MUL); add: BF16 of that shape."""
     _dev(a_q, torch.int8, "a_q")
@@ -588,8 +593,9 @@ def int8_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, d=None):
     _opt(add, torch.bfloat16, (M, n_out), "add")
     d = (torch.empty((M, n_out), dtype=torch.bfloat16, device=a_q.device) if d is None
          else _buf(d, torch.bfloat16, M * n_out, "d"))
+    ws = _alloc_ws(int8_gemm_ws_bytes(M, N, K), a_q.device) if ws is None else _buf(ws, torch.uint8, 0, "ws")
     _check(_int8_gemm(_ptr(a_q), _ptr(a_scale), _ptr(b_q), _ptr(b_scale), M, N, K, epilogue, _ptr(add), _ptr(d),
-                      _stream()), "int8_gemm")
+                      _ptr(ws), ws.numel(), _stream()), "int8_gemm")
     return d
 
 

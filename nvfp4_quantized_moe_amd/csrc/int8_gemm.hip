@@ -59,6 +59,34 @@ __device__ __forceinline__ void load16<float>(const float* p, float (&f)[16]) {
   }
 }
 
+// Scale of a row from each thread's largest magnitude. Rows of the smallest
+// numbers are lifted by 2^100 (exactly, like their scale), so that neither
+// 1 / s nor the residual above leaves the float32 range.
+struct RowScale {
+  float stored, s, inv, lift;
+};
+__device__ __forceinline__ RowScale row_scale(float m, float* red) {
+  m = wave_all_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = red[0];
+  for (int w = 1; w < (int)blockDim.x / 64; ++w) m = fmaxf(m, red[w]);
+  RowScale r;
+  r.stored = m * (1.0f / 127.0f);
+  r.lift = r.stored < 0x1p-100f ? 0x1p100f : 1.0f;
+  r.s = r.stored * r.lift;
+  r.inv = r.s > 0.0f ? 1.0f / r.s : 0.0f;
+  return r;
+}
+// Codes of four values, the first in the low byte (zeros in a row of zeros).
+__device__ __forceinline__ uint32_t quantize4(const float* f, const RowScale& r) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w |= (uint32_t)((r.s > 0.0f ? quantize_int8(f[i] * r.lift, r.s, r.inv) : 0) & 0xFF) << (8 * i);
+  return w;
+}
+
 // One workgroup per row; thread i takes the 16-element chunks i, i + blockDim.x, ...
 // The second pass over a row reads it from the cache.
 template <typename T>
@@ -73,29 +101,12 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(const T* __restrict__ x,
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
   }
-  m = wave_all_max(m);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = red[0];
-  for (int w = 1; w < (int)blockDim.x / 64; ++w) m = fmaxf(m, red[w]);
-  float s = m * (1.0f / 127.0f);
-  if (threadIdx.x == 0) scale[blockIdx.x] = s;
-  // rows of the smallest numbers are lifted by 2^100 (exactly, like their
-  // scale), so that neither 1 / s nor the residual leaves the float32 range
-  const float lift = s < 0x1p-100f ? 0x1p100f : 1.0f;
-  s *= lift;
-  const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+  const RowScale rs = row_scale(m, red);
+  if (threadIdx.x == 0) scale[blockIdx.x] = rs.stored;
   for (int c = threadIdx.x; c < n; c += blockDim.x) {
     load16(x + row + c * 16, f);
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[j] |= (uint32_t)((s > 0.0f ? quantize_int8(f[4 * j + i] * lift, s, inv) : 0) & 0xFF) << (8 * i);
-    }
-    *reinterpret_cast<uint4*>(q + row + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(q + row + c * 16) =
+        make_uint4(quantize4(f, rs), quantize4(f + 4, rs), quantize4(f + 8, rs), quantize4(f + 12, rs));
   }
 }
 
@@ -109,7 +120,10 @@ struct Int8Args {
   const uint16_t* add;  // BF16 [M, n_out] or NULL
   uint16_t* d;          // BF16 [M, n_out]
   int M, N, K, n_out;
+  int splits, k_split;  // K in `splits` parts of k_split bytes (a multiple of a stage)
+  int32_t* part;        // their sums, int32 [splits][M][N], when splits > 1
 };
+enum { kInt8Bf16, kInt8Silu, kInt8Part };  // what a tile writes
 
 // silu(g) u = g u / (1 + e^-g), by e^-|g|: e^-g itself would leave the range
 // of float32 below g = -88 and take the result with it
@@ -175,8 +189,9 @@ __device__ __forceinline__ typename OutVec<W>::type add_and_round(const float (&
 // SILU: the tile's weight rows alternate in runs of 32 between gate (row n)
 // and up (row I + n), so that a wave holds both halves of an output.
 constexpr int kBK = 64;
-template <int BM, int BN, int WM, int WN, bool SILU>
+template <int BM, int BN, int WM, int WN, int OUT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, int mt, int nt) {
+  constexpr bool SILU = OUT == kInt8Silu;
   constexpr int TH = 64 * WM * WN;
   constexpr int SM = BM / WM / 32, SN = BN / WN / 32;  // 32 x 32 subtiles of a wave
   static_assert(!SILU || SN % 2 == 0, "gate and up halves in one wave");
@@ -205,9 +220,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
     vb[i] = min(row, b_rows - 1) * g.K + tk;
   }
   static_assert(!SILU || RPI % 64 == 0, "a wave's rows of every load lie in one half");
+  const int k_begin = (int)blockIdx.y * g.k_split, k_end = min(g.K, k_begin + g.k_split);
   auto fetch = [&](int k0, int4v* to) {
-    const bool in = k0 + tk < g.K;            // zeros past the end of a row
-    const int ks = k0 < g.K ? k0 : 0;         // the scalar offset stays inside the range
+    const bool in = k0 + tk < k_end;     // zeros past the end of a row (or of this part of K)
+    const int ks = k0 < k_end ? k0 : 0;  // the scalar offset stays inside the range
 #pragma unroll
     for (int i = 0; i < PA; ++i)
       load_lds16(ra, to + wave * 64 + i * TH, in ? va[i] : kInt8Out, ks);
@@ -262,17 +278,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   };
   constexpr std::integral_constant<int, 0> none;
   constexpr std::integral_constant<int, 2 * PL> two_stages;
-  const int stages = (g.K + kBK - 1) / kBK;
-  fetch(0, l0);
-  fetch(kBK, l1);
-  fetch(2 * kBK, l2);
+  const int stages = (k_end - k_begin + kBK - 1) / kBK;
+  fetch(k_begin, l0);
+  fetch(k_begin + kBK, l1);
+  fetch(k_begin + 2 * kBK, l2);
   // Stage s: its own loads have arrived; every wave is past stage s - 1, whose
   // buffer takes the loads of stage s + 3. Up to three stages past the end of K
   // load and add zeros: with a branch around them the compiler no longer knows
   // which buffer a load fills, and waits for all of them before it reads any.
   auto stage = [&](int s, const int4v* cur, int4v* next) {
     wait(two_stages);
-    fetch((s + 3) * kBK, next);
+    fetch(k_begin + (s + 3) * kBK, next);
     compute(cur);
   };
   for (int s = 0; s < stages; s += 4) {
@@ -298,11 +314,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   // output column and scales of this lane, the same for all its rows
   const int oc = SILU ? (col / 8) * 32 + (col % 8) * 4 : col * 8;  // within the wave's outputs
   const int n = n0 + wn * (SILU ? COLS / 2 : COLS) + oc;
-  const bool n_ok = n < g.n_out;
+  const bool n_ok = n < (OUT == kInt8Part ? g.N : g.n_out);
   float bs[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) bs[e] = 0.0f;
-  if (n_ok) {
+  if (n_ok && OUT != kInt8Part) {
     const float4 s0 = *reinterpret_cast<const float4*>(g.b_s + n);
     const float4 s1 = *reinterpret_cast<const float4*>(g.b_s + (SILU ? half + n : n + 4));
 #pragma unroll
@@ -321,6 +337,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   vec_t add[2][STEPS];
   auto row_of = [&](int j, int st) { return m0 + wm * 32 * SM + j * 32 + st * RPS + lane / LPR; };
   auto load_rows = [&](int j) {
+    if constexpr (OUT == kInt8Part) return;
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) as[j & 1][st] = g.a_s[min(row_of(j, st), g.M - 1)];
     if (g.add) {
@@ -349,6 +366,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
       const int row = st * RPS + lane / LPR, m = row_of(j, st);
       const int4v v0 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c0);
       const int4v v1 = *reinterpret_cast<const int4v*>(sums + row * PITCH + c1);
+      if constexpr (OUT == kInt8Part) {
+        if (m < g.M && n_ok) {
+          int32_t* to = g.part + ((size_t)blockIdx.y * g.M + m) * g.N + n;
+          *reinterpret_cast<int4v*>(to) = v0;
+          *reinterpret_cast<int4v*>(to + 4) = v1;
+        }
+        continue;
+      }
       float o[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -363,6 +388,72 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
         *reinterpret_cast<vec_t*>(g.d + (size_t)m * g.n_out + n) = add_and_round<W>(o, add[j & 1][st]);
     }
     wave_lds_fence();
+  }
+}
+
+// Joins the parts of K: eight outputs (and their sums' columns) of row m from n on.
+template <bool SILU>
+__device__ __forceinline__ void join8(const Int8Args& g, int m, int n, float (&o)[8]) {
+  const int half = g.N / 2;
+  int4v s[2] = {int4v{0, 0, 0, 0}, int4v{0, 0, 0, 0}}, u[2] = {int4v{0, 0, 0, 0}, int4v{0, 0, 0, 0}};
+  const int32_t* p = g.part + (size_t)m * g.N + n;
+  for (int i = 0; i < g.splits; ++i, p += (size_t)g.M * g.N) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s[h] += *reinterpret_cast<const int4v*>(p + 4 * h);
+      if (SILU) u[h] += *reinterpret_cast<const int4v*>(p + half + 4 * h);
+    }
+  }
+  const float as = g.a_s[m];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    o[e] = (float)s[e >> 2][e & 3] * (as * g.b_s[n + e]);
+    if (SILU) o[e] = silu_mul(o[e], (float)u[e >> 2][e & 3] * (as * g.b_s[half + n + e]));
+  }
+}
+
+template <bool SILU>
+__global__ __launch_bounds__(256) void int8_join_kernel(Int8Args g) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= (int64_t)g.M * g.n_out) return;
+  const int m = (int)(at / g.n_out), n = (int)(at - (int64_t)m * g.n_out);
+  float o[8];
+  join8<SILU>(g, m, n, o);
+  typename OutVec<8>::type add = OutVec<8>::type(0u);
+  if (g.add) add = *reinterpret_cast<const OutVec<8>::type*>(g.add + at);
+  *reinterpret_cast<OutVec<8>::type*>(g.d + at) = add_and_round<8>(o, add);
+}
+
+// The same for the dense expert's h, quantized in the same pass: workgroup m
+// joins row m, writes it as BF16 to d, and its codes and scale as
+// int8_rows_kernel would from there.
+__global__ __launch_bounds__(256) void int8_join_rows_kernel(Int8Args g, int8_t* __restrict__ q,
+                                                             float* __restrict__ scale) {
+  __shared__ float red[4];
+  const int m = blockIdx.x;
+  uint16_t* h = g.d + (size_t)m * g.n_out;
+  float top = 0.0f;
+  for (int n = threadIdx.x * 8; n < g.n_out; n += 2048) {
+    float o[8];
+    join8<true>(g, m, n, o);
+    const OutVec<8>::type v = add_and_round<8>(o, OutVec<8>::type(0u));
+    *reinterpret_cast<OutVec<8>::type*>(h + n) = v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
+  }
+  const RowScale rs = row_scale(top, red);
+  if (threadIdx.x == 0) scale[m] = rs.stored;
+  for (int n = threadIdx.x * 8; n < g.n_out; n += 2048) {  // each thread its own values again
+    const OutVec<8>::type v = *reinterpret_cast<const OutVec<8>::type*>(h + n);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(v[e] << 16);
+      f[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
+    }
+    *reinterpret_cast<uint2*>(q + (size_t)m * g.n_out + n) =
+        make_uint2(quantize4(f, rs), quantize4(f + 4, rs));
   }
 }
 
@@ -475,12 +566,12 @@ static int int8_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue) {
   return NVFP4_OK;
 }
 
-template <int BM, int BN, int WM, int WN, bool SILU>
+template <int BM, int BN, int WM, int WN, int OUT>
 static int launch_int8_tile(const Int8Args& g, hipStream_t stream) {
   const int mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN;
   if ((int64_t)mt * nt >= (1ll << 31)) return NVFP4_ERR_SHAPE;
-  hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, SILU>), dim3((unsigned)mt * nt), dim3(64 * WM * WN), 0, stream,
-                     g, mt, nt);
+  hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, OUT>), dim3((unsigned)mt * nt, g.splits),
+                     dim3(64 * WM * WN), 0, stream, g, mt, nt);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
 }
@@ -494,40 +585,73 @@ static int launch_int8_skinny(const Int8Args& g, hipStream_t stream) {
   return NVFP4_OK;
 }
 
-constexpr int kSkinnyM = 64;
+// Parts of K for a product: 1, or as many as bring 64 x 128 tiles to about one
+// per CU, each of at least kMinSplit bytes.
+constexpr int kSkinnyM = 16, kMinSplit = 512;
+static int int8_splits(int64_t M, int64_t N, int64_t K) {
+  if (M <= kSkinnyM) return 1;
+  const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
+  int64_t s = 256 / tiles;
+  if (s > K / kMinSplit) s = K / kMinSplit;
+  return s < 2 || K < 4096 ? 1 : (int)s;
+}
+static Int8Args int8_args(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s, int M, int N, int K,
+                          bool silu, const void* add, void* d, void* ws) {
+  const int want = int8_splits(M, N, K);
+  const int per = ((K + want - 1) / want + kBK - 1) / kBK * kBK;
+  return {a_q, a_s, b_q, b_s, reinterpret_cast<const uint16_t*>(add), reinterpret_cast<uint16_t*>(d), M, N, K,
+          silu ? N / 2 : N, (K + per - 1) / per, per, reinterpret_cast<int32_t*>(ws)};
+}
+static size_t int8_part_bytes(int64_t M, int64_t N, int64_t K) {
+  const int s = int8_splits(M, N, K);
+  return s > 1 ? (size_t)s * M * N * 4 : 0;
+}
+
 template <bool SILU>
 static int launch_int8(const Int8Args& g, hipStream_t stream) {
-  if (g.M <= kSkinnyM) {
-    if (g.M <= 16) return launch_int8_skinny<1, SILU>(g, stream);
-    if (g.M <= 32) return launch_int8_skinny<2, SILU>(g, stream);
-    return launch_int8_skinny<4, SILU>(g, stream);
+  constexpr int OUT = SILU ? kInt8Silu : kInt8Bf16;
+  if (g.splits > 1) {
+    const int st = launch_int8_tile<64, 128, 2, 2, kInt8Part>(g, stream);
+    if (st) return st;
+    hipLaunchKernelGGL(int8_join_kernel<SILU>, dim3((unsigned)(((int64_t)g.M * g.n_out / 8 + 255) / 256)), dim3(256), 0,
+                       stream, g);
+    NVFP4_CHECK_LAUNCH();
+    return NVFP4_OK;
   }
+  if (g.M <= kSkinnyM) return launch_int8_skinny<1, SILU>(g, stream);
   // the largest tile that still gives most of the 256 CUs one
   const auto tiles = [&](int bm, int bn) { return (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, SILU>(g, stream);
-  if (tiles(128, 128) >= 192) return launch_int8_tile<128, 128, 2, 2, SILU>(g, stream);
-  return launch_int8_tile<64, SILU ? 128 : 64, 2, 2, SILU>(g, stream);
+  if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, OUT>(g, stream);
+  if (tiles(128, 128) >= 192) return launch_int8_tile<128, 128, 2, 2, OUT>(g, stream);
+  return launch_int8_tile<64, SILU ? 128 : 64, 2, 2, OUT>(g, stream);
+}
+
+extern "C" size_t int8_gemm_ws_bytes(int32_t M, int32_t N, int32_t K) {
+  if (int8_gemm_check(M, N, K, NVFP4_EPI_BF16)) return 0;
+  return int8_part_bytes(M, N, K);
 }
 
 extern "C" int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int32_t M,
-                         int32_t N, int32_t K, int32_t epilogue, const void* add_bf16, void* d_bf16, void* stream) {
+                         int32_t N, int32_t K, int32_t epilogue, const void* add_bf16, void* d_bf16, void* ws,
+                         size_t ws_bytes, void* stream) {
   const int st = int8_gemm_check(M, N, K, epilogue);
   if (st) return st;
   if (M == 0) return NVFP4_OK;
-  if (!a_q || !a_scale || !b_q || !b_scale || !d_bf16) return NVFP4_ERR_NULL;
+  const size_t need = int8_part_bytes(M, N, K);
+  if (!a_q || !a_scale || !b_q || !b_scale || !d_bf16 || (need && !ws)) return NVFP4_ERR_NULL;
   if (!nvfp4_aligned16(a_q) || !nvfp4_aligned16(a_scale) || !nvfp4_aligned16(b_q) || !nvfp4_aligned16(b_scale) ||
-      !nvfp4_aligned16(add_bf16) || !nvfp4_aligned16(d_bf16))
+      !nvfp4_aligned16(add_bf16) || !nvfp4_aligned16(d_bf16) || !nvfp4_aligned16(ws))
     return NVFP4_ERR_ALIGN;
+  if (ws_bytes < need) return NVFP4_ERR_WORKSPACE;
   const bool silu = epilogue == NVFP4_EPI_SILU_MUL;
-  const Int8Args g = {a_q, a_scale, b_q, b_scale, reinterpret_cast<const uint16_t*>(add_bf16),
-                      reinterpret_cast<uint16_t*>(d_bf16), M, N, K, silu ? N / 2 : N};
+  const Int8Args g = int8_args(a_q, a_scale, b_q, b_scale, M, N, K, silu, add_bf16, d_bf16, ws);
   return silu ? launch_int8<true>(g, (hipStream_t)stream) : launch_int8<false>(g, (hipStream_t)stream);
 }
 
 // ------------------------------------------------------------- dense expert
 
 struct Int8FfnWs {
-  size_t x_q, x_s, h, h_q, h_s, end;
+  size_t x_q, x_s, h, h_q, h_s, part, end;
 };
 static Int8FfnWs int8_ffn_layout(int64_t T, int64_t hidden, int64_t inter) {
   Int8FfnWs w;
@@ -542,6 +666,8 @@ static Int8FfnWs int8_ffn_layout(int64_t T, int64_t hidden, int64_t inter) {
   w.h = put((size_t)T * inter * 2);
   w.h_q = put((size_t)T * inter);
   w.h_s = put((size_t)T * 4);
+  const size_t p1 = int8_part_bytes(T, 2 * inter, hidden), p2 = int8_part_bytes(T, hidden, inter);
+  w.part = put(p1 > p2 ? p1 : p2);
   w.end = p;
   return w;
 }
@@ -575,9 +701,18 @@ extern "C" int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const
   float* h_s = reinterpret_cast<float*>(base + l.h_s);
   st = int8_quantize_rows(x_bf16, NVFP4_DT_BF16, T, hidden, x_q, x_s, stream);
   if (st) return st;
-  st = int8_gemm(x_q, x_s, w1_q, w1_scale, T, 2 * inter, hidden, NVFP4_EPI_SILU_MUL, nullptr, base + l.h, stream);
-  if (st) return st;
-  st = int8_quantize_rows(base + l.h, NVFP4_DT_BF16, T, inter, h_q, h_s, stream);
-  if (st) return st;
-  return int8_gemm(h_q, h_s, w2_q, w2_scale, T, hidden, inter, NVFP4_EPI_BF16, add_bf16, out_bf16, stream);
+  const Int8Args up = int8_args(x_q, x_s, w1_q, w1_scale, T, 2 * inter, hidden, true, nullptr, base + l.h, base + l.part);
+  if (up.splits > 1) {  // the join quantizes h as well
+    st = launch_int8_tile<64, 128, 2, 2, kInt8Part>(up, (hipStream_t)stream);
+    if (st) return st;
+    hipLaunchKernelGGL(int8_join_rows_kernel, dim3(T), dim3(256), 0, (hipStream_t)stream, up, h_q, h_s);
+    NVFP4_CHECK_LAUNCH();
+  } else {
+    st = launch_int8<true>(up, (hipStream_t)stream);
+    if (st) return st;
+    st = int8_quantize_rows(base + l.h, NVFP4_DT_BF16, T, inter, h_q, h_s, stream);
+    if (st) return st;
+  }
+  return launch_int8<false>(int8_args(h_q, h_s, w2_q, w2_scale, T, hidden, inter, false, add_bf16, out_bf16,
+                                      base + l.part), (hipStream_t)stream);
 }

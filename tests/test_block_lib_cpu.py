@@ -126,8 +126,8 @@ def test_int8(nv):
         assert rows(**{bad: None}) == NULL and rows(**{bad: ODD}) == ALIGN, bad
     assert rows(M=0, x=None) == 0
 
-    def gemm(a=P, a_s=P, b=P, b_s=P, M=4, N=64, K=64, epi=0, add=None, d=P):
-        return nv._int8_gemm(a, a_s, b, b_s, M, N, K, epi, add, d, None)
+    def gemm(a=P, a_s=P, b=P, b_s=P, M=4, N=64, K=64, epi=0, add=None, d=P, ws=None, n=0):
+        return nv._int8_gemm(a, a_s, b, b_s, M, N, K, epi, add, d, ws, n, None)
     for bad in (dict(M=-1), dict(N=0), dict(N=12), dict(N=24, epi=1), dict(K=8), dict(K=40), dict(K=65552),
                 dict(M=64 * 65535 + 1)):
         assert gemm(**bad) == SHAPE, bad
@@ -135,6 +135,10 @@ def test_int8(nv):
     for bad in ("a", "a_s", "b", "b_s", "d"):
         assert gemm(**{bad: None}) == NULL and gemm(**{bad: ODD}) == ALIGN, bad
     assert gemm(add=ODD) == ALIGN and gemm(M=0, a=None) == 0
+    parts = nv.int8_gemm_ws_bytes(64, 512, 8192)
+    assert parts > 0 and nv.int8_gemm_ws_bytes(8192, 4096, 8192) == 0 and nv.int8_gemm_ws_bytes(64, 12, 8192) == 0
+    assert gemm(M=64, N=512, K=8192) == NULL and gemm(M=64, N=512, K=8192, ws=ODD, n=parts) == ALIGN
+    assert gemm(M=64, N=512, K=8192, ws=P, n=parts - 1) == WORKSPACE
 
     need = nv.int8_ffn_ws_bytes(4, 64, 32)
     assert need > 0 and nv.int8_ffn_ws_bytes(4, 64, 24) == 0

@@ -48,7 +48,7 @@ def test_rows(nv, M, K, kind, dtype):
 
 
 SHAPES = [(1, 8, 16), (1, 7168, 2048), (2, 16, 32), (5, 1000, 1040), (16, 4096, 7168), (17, 264, 7168), (33, 40, 144),
-          (64, 4096, 7168), (63, 7168, 2048), (65, 128, 128), (128, 256, 65536), (333, 1000, 1040), (500, 520, 272),
+          (64, 4096, 7168), (63, 7168, 2048), (33, 72, 4112), (100, 1096, 7168), (65, 128, 128), (128, 256, 65536), (333, 1000, 1040), (500, 520, 272),
           (1030, 2056, 1168), (2048, 2048, 256), (2049, 4104, 400), (4100, 1536, 128)]
 
 
@@ -100,7 +100,7 @@ def test_product_silu(nv, M, N, K, with_add):
     assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) / np.maximum(tol, 1e-30)))
 
 
-@pytest.mark.parametrize("T,H,I", [(1, 7168, 2048), (3, 64, 16), (64, 1040, 528), (200, 512, 256), (1100, 1024, 512)])
+@pytest.mark.parametrize("T,H,I", [(1, 7168, 2048), (3, 64, 16), (40, 4112, 2064), (70, 5120, 80), (64, 1040, 528), (200, 512, 256), (1100, 1024, 512)])
 def test_dense_expert_is_its_steps(nv, T, H, I):
     """The forward equals its public steps bit for bit (each checked above), on a dirty workspace."""
     g = torch.Generator(device=DEV).manual_seed(T)
