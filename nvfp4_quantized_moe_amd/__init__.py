@@ -112,11 +112,17 @@ def _check(status: int, call: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream and device as plain integers: the objects of torch.cuda
+# take longer to make (3 us a stream) than the smallest kernels here to run.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return _raw_stream(_current_device())
 
 
 def _dev(t, dtype, name):
@@ -124,8 +130,8 @@ def _dev(t, dtype, name):
     device whose current stream the call is issued on)."""
     if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor, got {t.dtype} on {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_current_device()}")
     return t
 
 
@@ -593,9 +599,10 @@ def int8_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, d=None, w
     _opt(add, torch.bfloat16, (M, n_out), "add")
     d = (torch.empty((M, n_out), dtype=torch.bfloat16, device=a_q.device) if d is None
          else _buf(d, torch.bfloat16, M * n_out, "d"))
-    ws = _alloc_ws(int8_gemm_ws_bytes(M, N, K), a_q.device) if ws is None else _buf(ws, torch.uint8, 0, "ws")
+    need = _int8_gemm_ws(M, N, K) if ws is None else 0
+    ws = (_alloc_ws(need, a_q.device) if need else None) if ws is None else _buf(ws, torch.uint8, 0, "ws")
     _check(_int8_gemm(_ptr(a_q), _ptr(a_scale), _ptr(b_q), _ptr(b_scale), M, N, K, epilogue, _ptr(add), _ptr(d),
-                      _ptr(ws), ws.numel(), _stream()), "int8_gemm")
+                      _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "int8_gemm")
     return d
 
 
