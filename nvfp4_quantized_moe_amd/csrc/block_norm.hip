@@ -6,9 +6,11 @@
 // One pass: a row's elements stay in registers between the two reductions.
 //
 // A workgroup owns whole rows; thread i holds the row's 8-element chunks i,
-// i + blockDim.x, ... (16-byte loads). Sums are float32: the lanes of a wave
-// by DPP, then the waves through LDS in wave order, so results repeat bit for
-// bit.
+// i + blockDim.x, ... (16-byte loads). It walks the rows of its share with the
+// next row's loads in flight and its columns' weights in registers: read
+// again for every row, the three float32 vectors would be as many bytes from
+// L2 as the row is from memory. Sums are float32: the lanes of a wave by DPP,
+// then the waves through LDS in wave order, so results repeat bit for bit.
 #include <type_traits>
 
 #include "common.h"
@@ -72,8 +74,9 @@ __device__ __forceinline__ void load_weights8(const float* p, int at, float abse
   }
 }
 
-// Sums of N values per thread over the workgroup, in every thread. `scratch`
-// must not be the one of the previous call (a wave may still be reading that).
+// Sums of N values per thread over the workgroup, in every thread. A scratch
+// array may be used again two calls later (in between, every wave has passed
+// another call's barrier).
 template <int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float (*scratch)[N]) {
   const int waves = (int)blockDim.x >> 6;
@@ -100,11 +103,57 @@ struct NormArgs {
   float scale, eps;
 };
 
+// Column weights of a thread's chunks: in registers for all rows, or (KEEP
+// false, rows too wide for that) loaded at each use.
+template <int CH, bool KEEP>
+struct Columns {
+  float w[KEEP ? CH : 1][8];
+  const float* p;
+  float absent;
+  __device__ __forceinline__ void init(const float* from, float if_absent, int nchunk) {
+    p = from;
+    absent = if_absent;
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int ch = threadIdx.x + c * blockDim.x;
+        load_weights8(ch < nchunk ? p : nullptr, ch * 8, absent, w[c]);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int c, float (&o)[8]) const {
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = w[c][i];
+    } else {
+      load_weights8(p, (int)(threadIdx.x + c * blockDim.x) * 8, absent, o);
+    }
+  }
+};
+
+template <typename X, typename R, int CH>
+struct NormRow {  // a row's inputs as loaded
+  Vec8<X> x[CH];
+  Vec8<R> r[CH];
+  __device__ __forceinline__ void load(const X* px, const R* pr, size_t row, int nchunk) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      if (ch < nchunk) {
+        x[c].load(px + row + ch * 8);
+        if (pr) r[c].load(pr + row + ch * 8);
+      }
+    }
+  }
+};
+
+constexpr int kNormCus = 256;
+
 template <typename X, typename R, int CH, bool QUANT>
-__global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_kernel(const X* x, const R* residual, NormArgs a,
-                                                                          R* residual_out, X* y, const float* gs_in,
-                                                                          uint8_t* y_q, uint8_t* y_sf) {
-  __shared__ float scratch[2][kNormMaxWaves][1];
+__global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* residual, NormArgs a, R* residual_out,
+                                                         X* y, const float* gs_in, uint8_t* y_q, uint8_t* y_sf) {
+  constexpr bool KEEP = CH <= 2;
+  __shared__ float scratch[4][kNormMaxWaves][1];
   __shared__ uint4 lut[QUANT ? kLutWords / 4 : 1];
   const int nchunk = a.H / 8;
   float gs = 0.0f;
@@ -113,28 +162,33 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_kernel(const 
     build_threshold_lut(gs, reinterpret_cast<uint32_t*>(lut), threadIdx.x, blockDim.x);
     __syncthreads();
   }
+  Columns<CH, KEEP> w_pre, w_post, gate;
+  w_pre.init(a.w_pre, 1.0f, nchunk);
+  w_post.init(a.w_post, 1.0f, nchunk);
+  gate.init(a.gate_tokens ? nullptr : a.gate, 1.0f, nchunk);
   const float inv_h = 1.0f / (float)a.H;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  NormRow<X, R, CH> in;
+  in.load(x, residual, (size_t)blockIdx.x * a.H, nchunk);
+  int parity = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
     const size_t row = (size_t)t * a.H;
+    const NormRow<X, R, CH> now = in;
+    if (t + gridDim.x < a.T) in.load(x, residual, row + (size_t)gridDim.x * a.H, nchunk);
     float f[CH][8], s[1] = {0.0f};
-    Vec8<R> rv[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int ch = threadIdx.x + c * blockDim.x;
       if (ch < nchunk) {
-        Vec8<X> xv;
-        xv.load(x + row + ch * 8);
-        if (residual) rv[c].load(residual + row + ch * 8);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          f[c][i] = xv.get(i);
+          f[c][i] = now.x[c].get(i);
           s[0] += f[c][i] * f[c][i];
         }
       }
     }
     float sig = a.scale * ((a.gate && a.gate_tokens) ? a.gate[t] : 1.0f);
     if (a.w_post) {
-      block_sums(s, scratch[0]);
+      block_sums(s, scratch[parity]);
       sig *= rsqrtf(s[0] * inv_h + a.eps);
     }
     s[0] = 0.0f;
@@ -143,12 +197,12 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_kernel(const 
       const int ch = threadIdx.x + c * blockDim.x;
       if (ch < nchunk) {
         float w[8], g[8];
-        load_weights8(a.w_post, ch * 8, 1.0f, w);
-        load_weights8(a.gate_tokens ? nullptr : a.gate, ch * 8, 1.0f, g);
+        w_post.get(c, w);
+        gate.get(c, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           f[c][i] = f[c][i] * sig * (w[i] * g[i]);
-          if (residual) f[c][i] += rv[c].get(i);
+          if (residual) f[c][i] += now.r[c].get(i);
         }
         store8(residual_out + row + ch * 8, f[c]);
 #pragma unroll
@@ -156,7 +210,7 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_kernel(const 
       }
     }
     if (!a.w_pre) continue;
-    block_sums(s, scratch[1]);
+    block_sums(s, scratch[parity + 1]);
     const float rho = rsqrtf(s[0] * inv_h + a.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -164,7 +218,7 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_kernel(const 
       uint4 bits = make_uint4(0, 0, 0, 0);
       if (ch < nchunk) {
         float w[8];
-        load_weights8(a.w_pre, ch * 8, 1.0f, w);
+        w_pre.get(c, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[c][i] = f[c][i] * rho * w[i];
         bits = store8(y ? y + row + ch * 8 : nullptr, f[c]);
@@ -196,13 +250,31 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_kernel(const 
 // sums d_w_pre, d_w_post, d_gate stay in registers over all rows of the
 // workgroup and leave it once, as a row of partial sums that
 // norm_columns_kernel adds in workgroup order.
-constexpr int kNormGrid = 256;  // workgroups of the backward pass: one per CU
 template <typename X, typename R, int CH>
-__global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_backward_kernel(
-    const X* d_y, const R* d_res_out, const X* x, const R* res_out,
-    NormArgs a, X* d_x, R* d_res, float* d_gate_tokens, float* partial) {
-  __shared__ float scratch_a[kNormMaxWaves][3];
-  __shared__ float scratch_b[kNormMaxWaves][2];
+struct NormGradRow {
+  Vec8<X> x[CH], y[CH];
+  Vec8<R> r[CH], d[CH];
+  __device__ __forceinline__ void load(const X* px, const X* py, const R* pr, const R* pd, size_t row, int nchunk) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int ch = threadIdx.x + c * blockDim.x;
+      if (ch < nchunk) {
+        x[c].load(px + row + ch * 8);
+        if (py) y[c].load(py + row + ch * 8);
+        if (py) r[c].load(pr + row + ch * 8);
+        if (pd) d[c].load(pd + row + ch * 8);
+      }
+    }
+  }
+};
+
+template <typename X, typename R, int CH>
+__global__ __launch_bounds__(512) void block_norm_backward_kernel(const X* d_y, const R* d_res_out, const X* x,
+                                                                  const R* res_out, NormArgs a, X* d_x, R* d_res,
+                                                                  float* d_gate_tokens, float* partial) {
+  constexpr bool KEEP = CH <= 2;
+  __shared__ float scratch_a[2][kNormMaxWaves][3];
+  __shared__ float scratch_b[2][kNormMaxWaves][2];
   const int nchunk = a.H / 8;
   const float inv_h = 1.0f / (float)a.H;
   float c_pre[CH][8], c_post[CH][8], c_gate[CH][8];
@@ -210,34 +282,37 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_backward_kern
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) c_pre[c][i] = c_post[c][i] = c_gate[c][i] = 0.0f;
-  const float* gate_cols = a.gate_tokens ? nullptr : a.gate;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  Columns<CH, KEEP> k_pre, k_post, k_gate;
+  k_pre.init(a.w_pre, 0.0f, nchunk);
+  k_post.init(a.w_post, 1.0f, nchunk);
+  k_gate.init(a.gate_tokens ? nullptr : a.gate, 1.0f, nchunk);
+  const X* py = a.w_pre ? d_y : nullptr;
+  NormGradRow<X, R, CH> in;
+  in.load(x, py, res_out, d_res_out, (size_t)blockIdx.x * a.H, nchunk);
+  int parity = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
     const size_t row = (size_t)t * a.H;
-    Vec8<X> xv[CH], yv[CH];
-    Vec8<R> rv[CH], dv[CH];
+    const NormGradRow<X, R, CH> now = in;
+    if (KEEP && t + gridDim.x < a.T) in.load(x, py, res_out, d_res_out, row + (size_t)gridDim.x * a.H, nchunk);
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int ch = threadIdx.x + c * blockDim.x;
       if (ch < nchunk) {
-        xv[c].load(x + row + ch * 8);
-        if (d_res_out) dv[c].load(d_res_out + row + ch * 8);
         if (a.w_pre) {
           float w[8];
-          yv[c].load(d_y + row + ch * 8);
-          rv[c].load(res_out + row + ch * 8);
-          load_weights8(a.w_pre, ch * 8, 1.0f, w);
+          k_pre.get(c, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            s[0] += rv[c].get(i) * rv[c].get(i);
-            s[1] += yv[c].get(i) * w[i] * rv[c].get(i);
+            s[0] += now.r[c].get(i) * now.r[c].get(i);
+            s[1] += now.y[c].get(i) * w[i] * now.r[c].get(i);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[2] += xv[c].get(i) * xv[c].get(i);
+        for (int i = 0; i < 8; ++i) s[2] += now.x[c].get(i) * now.x[c].get(i);
       }
     }
-    block_sums(s, scratch_a);
+    block_sums(s, scratch_a[parity]);
     const float rho = rsqrtf(s[0] * inv_h + a.eps);
     const float mean = s[1] * rho * inv_h;  // of dn rn
     const float sig = a.w_post ? rsqrtf(s[2] * inv_h + a.eps) : 1.0f;
@@ -249,23 +324,23 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_backward_kern
       const int ch = threadIdx.x + c * blockDim.x;
       if (ch < nchunk) {
         float dr[8], w_pre[8], w_post[8], gate[8];
-        load_weights8(a.w_pre, ch * 8, 0.0f, w_pre);
-        load_weights8(a.w_post, ch * 8, 1.0f, w_post);
-        load_weights8(gate_cols, ch * 8, g_row, gate);
+        k_pre.get(c, w_pre);
+        k_post.get(c, w_post);
+        k_gate.get(c, gate);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          dr[i] = d_res_out ? dv[c].get(i) : 0.0f;
+          dr[i] = d_res_out ? now.d[c].get(i) : 0.0f;
           if (a.w_pre) {
-            const float rn = rv[c].get(i) * rho;
-            dr[i] += rho * (yv[c].get(i) * w_pre[i] - rn * mean);
-            c_pre[c][i] += yv[c].get(i) * rn;
+            const float rn = now.r[c].get(i) * rho;
+            dr[i] += rho * (now.y[c].get(i) * w_pre[i] - rn * mean);
+            c_pre[c][i] += now.y[c].get(i) * rn;
           }
-          const float xn = xv[c].get(i) * sig;
+          const float xn = now.x[c].get(i) * sig;
           const float db = a.scale * dr[i];
           const float dg = db * xn * w_post[i];
           c_gate[c][i] += dg;
           u[1] += dg;
-          const float dbg = db * gate[i];
+          const float dbg = db * (gate[i] * g_row);
           c_post[c][i] += dbg * xn;
           dxn[c][i] = dbg * w_post[i];
           u[0] += dxn[c][i] * xn;
@@ -273,8 +348,7 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_backward_kern
         store8(d_res + row + ch * 8, dr);
       }
     }
-    if (a.w_post || d_gate_tokens) block_sums(u, scratch_b);
-    else __syncthreads();  // scratch_a is written again in the next row
+    if (a.w_post || d_gate_tokens) block_sums(u, scratch_b[parity]);
     if (d_gate_tokens && threadIdx.x == 0) d_gate_tokens[t] = u[1];
     const float mx = a.w_post ? u[0] * inv_h : 0.0f;
 #pragma unroll
@@ -284,10 +358,11 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_backward_kern
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          o[i] = a.w_post ? sig * (dxn[c][i] - xv[c].get(i) * sig * mx) : dxn[c][i];
+          o[i] = a.w_post ? sig * (dxn[c][i] - now.x[c].get(i) * sig * mx) : dxn[c][i];
         store8(d_x + row + ch * 8, o);
       }
     }
+    if (!KEEP && t + gridDim.x < a.T) in.load(x, py, res_out, d_res_out, row + (size_t)gridDim.x * a.H, nchunk);
   }
   // partial sums of this workgroup: [workgroup][3][H]
 #pragma unroll
@@ -303,10 +378,14 @@ __global__ __launch_bounds__(CH == 1 ? 1024 : 512) void block_norm_backward_kern
 }
 
 // Column sums over the workgroups' partial rows: workgroup (b, s) adds 64
-// columns of sum s; its waves take every fourth row, and are added in order.
-__global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restrict__ partial, int rows, int H,
-                                                           float* d_pre, float* d_post, float* d_gate) {
-  __shared__ float sh[4][64];
+// columns of sum s. Its 16 waves take every 16th row, eight loads in flight,
+// and are added in wave order (with 4 waves and one load in flight this took
+// 20 us for 256 rows of 3 x 7168, now 6).
+constexpr int kColumnWaves = 16;
+__global__ __launch_bounds__(64 * kColumnWaves) void norm_columns_kernel(const float* __restrict__ partial, int rows,
+                                                                         int H, float* d_pre, float* d_post,
+                                                                         float* d_gate) {
+  __shared__ float sh[kColumnWaves][64];
   float* out = blockIdx.y == 0 ? d_pre : blockIdx.y == 1 ? d_post : d_gate;
   if (!out) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -314,11 +393,24 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restri
   float s = 0.0f;
   if (col < H) {
     const float* p = partial + (size_t)blockIdx.y * H + col;
-    for (int r = wave; r < rows; r += 4) s += p[(size_t)r * 3 * H];
+    for (int r = wave; r < rows; r += 8 * kColumnWaves) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int ru = r + u * kColumnWaves;
+        v[u] = ru < rows ? p[(size_t)ru * 3 * H] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
   }
   sh[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < H) out[col] = (sh[0][lane] + sh[1][lane]) + (sh[2][lane] + sh[3][lane]);
+  if (wave == 0 && col < H) {
+    s = 0.0f;
+    for (int w = 0; w < kColumnWaves; ++w) s += sh[w][lane];
+    out[col] = s;
+  }
 }
 
 }  // namespace nvfp4
@@ -336,8 +428,20 @@ static int norm_check(int32_t T, int32_t H, int32_t x_dtype, int32_t res_dtype, 
   return NVFP4_OK;
 }
 
-// Threads for rows of H elements at CH chunks of 8 per thread.
+// Threads for rows of H elements at CH chunks of 8 per thread: at most 512.
 static unsigned norm_threads(int32_t H, int ch) { return (unsigned)(((H / 8 + ch - 1) / ch + 63) / 64 * 64); }
+// Workgroups that walk T rows: as many per CU as give it about `waves` waves.
+static unsigned norm_grid(int32_t T, unsigned threads, int waves) {
+  int per_cu = waves / (int)(threads / 64);
+  if (per_cu < 1) per_cu = 1;
+  return (unsigned)(T < kNormCus * per_cu ? T : kNormCus * per_cu);
+}
+template <typename Fn>
+static int norm_by_width(int32_t H, Fn fn) {
+  if (H <= 4096) return fn(std::integral_constant<int, 1>());
+  if (H <= 8192) return fn(std::integral_constant<int, 2>());
+  return fn(std::integral_constant<int, 4>());
+}
 
 template <typename Fn>
 static int norm_by_types(int32_t x_dtype, int32_t res_dtype, Fn fn) {
@@ -368,14 +472,14 @@ extern "C" int moe_block_norm(const void* x, int32_t x_dtype, const void* residu
     auto go = [&](auto ch, auto quant) -> int {
       constexpr int CH = decltype(ch)::value;
       const unsigned threads = norm_threads(H, CH);
-      hipLaunchKernelGGL((block_norm_kernel<X, R, CH, decltype(quant)::value>), dim3((unsigned)T), dim3(threads), 0,
-                         (hipStream_t)stream, reinterpret_cast<const X*>(x), reinterpret_cast<const R*>(residual), a,
+      hipLaunchKernelGGL((block_norm_kernel<X, R, CH, decltype(quant)::value>), dim3(norm_grid(T, threads, 28)),
+                         dim3(threads), 0, (hipStream_t)stream, reinterpret_cast<const X*>(x), reinterpret_cast<const R*>(residual), a,
                          reinterpret_cast<R*>(residual_out), reinterpret_cast<X*>(y), gs_in, y_q, y_sf);
       NVFP4_CHECK_LAUNCH();
       return NVFP4_OK;
     };
     auto by_width = [&](auto quant) -> int {
-      return H <= 8192 ? go(std::integral_constant<int, 1>(), quant) : go(std::integral_constant<int, 4>(), quant);
+      return norm_by_width(H, [&](auto ch) { return go(ch, quant); });
     };
     if constexpr (std::is_same<X, uint16_t>::value)
       if (gs_in) return by_width(std::true_type());
@@ -383,9 +487,14 @@ extern "C" int moe_block_norm(const void* x, int32_t x_dtype, const void* residu
   });
 }
 
+static unsigned norm_backward_grid(int32_t T, int32_t H) {
+  const int ch = H <= 4096 ? 1 : H <= 8192 ? 2 : 4;
+  return norm_grid(T < 1 ? 1 : T, norm_threads(H, ch), 12);
+}
+
 extern "C" size_t moe_block_norm_backward_ws_bytes(int32_t T, int32_t H) {
   if (T < 0 || H <= 0 || H % 8 != 0 || H > kNormMaxH) return 0;
-  return (size_t)kNormGrid * 3 * H * sizeof(float);
+  return (size_t)norm_backward_grid(T, H) * 3 * H * sizeof(float);
 }
 
 extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_out, const void* x, int32_t x_dtype,
@@ -408,7 +517,7 @@ extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_o
   if (ws_bytes < moe_block_norm_backward_ws_bytes(T, H)) return NVFP4_ERR_WORKSPACE;
   const bool per_token = gate_mode == MOE_GATE_TOKEN;
   const NormArgs a = {T, H, w_pre, w_post, gate_mode == MOE_GATE_NONE ? nullptr : gate, per_token, scale, eps};
-  const unsigned grid = (unsigned)(T < kNormGrid ? T : kNormGrid);
+  const unsigned grid = norm_backward_grid(T, H);
   if (T > 0) {
     const int r = norm_by_types(x_dtype, res_dtype, [&](auto xt, auto rt) -> int {
       using X = decltype(xt);
@@ -424,14 +533,14 @@ extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_o
         NVFP4_CHECK_LAUNCH();
         return NVFP4_OK;
       };
-      return H <= 8192 ? go(std::integral_constant<int, 1>()) : go(std::integral_constant<int, 4>());
+      return norm_by_width(H, go);
     });
     if (r) return r;
   }
   // T = 0: the sums over no rows, zeros
   float* gate_cols = gate_mode == MOE_GATE_CHANNEL ? d_gate : nullptr;
-  hipLaunchKernelGGL(norm_columns_kernel, dim3((H + 63) / 64, 3), dim3(256), 0, (hipStream_t)stream,
-                     reinterpret_cast<const float*>(ws), (int)grid, H, w_pre ? d_w_pre : nullptr,
+  hipLaunchKernelGGL(norm_columns_kernel, dim3((H + 63) / 64, 3), dim3(64 * kColumnWaves), 0, (hipStream_t)stream,
+                     reinterpret_cast<const float*>(ws), T > 0 ? (int)grid : 0, H, w_pre ? d_w_pre : nullptr,
                      w_post ? d_w_post : nullptr, gate_cols);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
