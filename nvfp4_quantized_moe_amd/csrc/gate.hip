@@ -60,6 +60,37 @@ __device__ __forceinline__ float score_slope(float x, float s, int score) {
   return x < -20.0f ? 0.5f * s : 0.5f * sigmoid_score(x) / s;
 }
 
+// The same scores where they are summed or multiplied into a gradient rather
+// than compared: hardware exponential, logarithm and reciprocal, each within
+// one or two float32 steps, e^x through 2^(x log2 e) with |x| half steps more.
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ float fast_log1p(float t) {  // t >= 0
+  // below 2^-6 the series (next term t^4 / 5 < 2^-26): 1 + t has rounded t away
+  return t < 0x1p-6f ? t * (1.0f - t * (0.5f - t * (1.0f / 3.0f - t * 0.25f)))
+                     : __builtin_amdgcn_logf(1.0f + t) * kLn2;
+}
+// score and slope of a logit above -inf
+template <bool SLOPE>
+__device__ __forceinline__ float fast_score(float x, int score, float* slope) {
+  const float e = fast_exp(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
+  const float sig = x < 0.0f ? e * r : r;
+  if (score == MOE_SCORE_SIGMOID) {
+    if (SLOPE) *slope = e * r * r;
+    return sig;
+  }
+  const bool low = x < -20.0f;
+  const float s = low ? fast_exp(0.5f * x) : __builtin_amdgcn_sqrtf(fmaxf(x, 0.0f) + fast_log1p(e));
+  if (SLOPE) *slope = low ? 0.5f * s : 0.5f * sig * __builtin_amdgcn_rcpf(s);
+  return s;
+}
+
+// Score for a key: float keys may be two steps off (see gate_topk_kernel).
+__device__ __forceinline__ float key_score(float x, int score) {
+  return score == MOE_SCORE_SIGMOID ? __builtin_amdgcn_rcpf(1.0f + expf(-x)) : sqrt_softplus(x);
+}
+__device__ __forceinline__ double key_score(double x, int score) { return pointwise_score(x, score); }
+
 struct GateShape {
   int T, E, k, score;
   int n_group, topk_group, group_size;
@@ -93,7 +124,7 @@ __device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bi
     for (int v = 0; v < VPT; ++v) key[v] = key[v] / sum;
   } else {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) key[v] = pointwise_score((F)x[v], g.score);
+    for (int v = 0; v < VPT; ++v) key[v] = key_score((F)x[v], g.score);
   }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -182,6 +213,68 @@ __device__ __forceinline__ void pick_by_rounds(F (&key)[VPT], int want, int* id,
   }
 }
 
+// The `want` highest float keys, want <= 16, without a chain of wave maxima.
+// The wave's lanes fall into `groups` >= k runs; the lowest of the runs' maxima
+// is at most the groups-th highest key, so the keys from it on (about 17 of
+// 384 for 8 runs) hold the k highest. They are compacted in expert order, one
+// per lane, and each counts those before it. Returns false, having done
+// nothing, when more than 64 remain (many equal keys); *all tells whether the
+// want-th is among them.
+constexpr int kFastK = 16;
+template <int VPT>
+__device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, int want, uint2* lds, int* id, float* at,
+                                              bool* all) {
+  const int lane = threadIdx.x & 63;
+  float m = key[0];
+#pragma unroll
+  for (int v = 1; v < VPT; ++v) m = fmaxf(m, key[v]);
+  const auto up = [](float a, float b) { return fmaxf(a, b); };
+  const auto down = [](float a, float b) { return fminf(a, b); };
+  // steps 1, 2, 4, 8, 16, 32 of the reduction: maxima inside a run, then minima over the runs
+  const auto step = [&](bool inside, float other) { return inside ? up(m, other) : down(m, other); };
+  m = step(true, dpp_f32<kDppXor1>(m));
+  m = step(true, dpp_f32<kDppXor2>(m));
+  m = step(k <= 8, dpp_f32<kDppHalfMirror>(m));
+  m = step(k <= 4, dpp_f32<kDppMirror>(m));
+  u32x2_t r = rows16(__float_as_uint(m));
+  m = k <= 2 ? up(__uint_as_float(r[0]), __uint_as_float(r[1])) : down(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = rows32(__float_as_uint(m));
+  m = k <= 1 ? up(__uint_as_float(r[0]), __uint_as_float(r[1])) : down(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  uint64_t mine[VPT];
+  int n = 0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    mine[v] = __ballot(key[v] >= m && key[v] > -kInf);
+    n += __popcll(mine[v]);
+  }
+  if (n > 64) return false;
+  int before = 0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if ((mine[v] >> lane) & 1u)
+      lds[before + __popcll(mine[v] & ((1ull << lane) - 1ull))] = make_uint2(__float_as_uint(key[v]), v * 64 + lane);
+    before += __popcll(mine[v]);
+  }
+  wave_lds_fence();
+  const uint2 c = lds[lane];  // past n: left over, never counted
+  const float kv = __uint_as_float(c.x);
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const float kj = lane_value(kv, j);
+    rank += (kj > kv || (kj == kv && j < lane)) ? 1 : 0;
+  }
+  wave_lds_fence();
+  if (lane < n && rank < want) lds[rank] = c;
+  wave_lds_fence();
+  const int have = min(n, want);
+  const uint2 got = lds[lane];
+  *id = lane < have ? (int)got.y : -1;
+  *at = lane < have ? __uint_as_float(got.x) : -kInf;
+  *all = n >= want;
+  wave_lds_fence();
+  return true;
+}
+
 // The weights of the choices (lane j < k: expert id) and the stores.
 template <typename L, int VPT>
 __device__ __forceinline__ void write_choices(const L* logits, size_t row, const float (&x)[VPT], const GateShape& g,
@@ -228,6 +321,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
                                                                     const uint8_t* __restrict__ mask, GateShape g,
                                                                     int32_t* __restrict__ ids, float* __restrict__ w) {
   extern __shared__ double lds[];
+  __shared__ uint2 picked[kGateWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
   if (t >= g.T) return;
@@ -262,7 +356,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
     if (g.topk_group == g.n_group) doubt = false;
   }
   const int want = by_logit ? g.k : min(g.k + 1, 64);
-  pick_by_rounds(key, want, &id, &at);
+  bool all = true;
+  if (g.k > kFastK || !pick_by_count(key, g.k, want, picked[wave], &id, &at, &all)) pick_by_rounds(key, want, &id, &at);
   if (!by_logit) {
     const float xl = id >= 0 ? load_logit(logits, row + id) : -kInf;
     const float bl = id >= 0 && bias ? bias[id] : 0.0f;
@@ -271,7 +366,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
     const bool same = xl == xn && bl == bn;
     const float size = fabsf(at) + fabsf(next) + fabsf(bl) + fabsf(bn);
     const bool close = lane + 1 < want && idn >= 0 && !same && !(at - next > 2.0f * tol * size);
-    doubt = doubt || __ballot(close) != 0 || want == g.k;
+    doubt = doubt || __ballot(close) != 0 || want == g.k || !all;  // !all: the first key left out is unknown
   }
   if (doubt) {
     double key64[VPT], gap, size, at64;
@@ -345,12 +440,13 @@ __device__ Span find_chunk(const int32_t* cu, const BalanceShape& g, int i) {
 // Normalized scores of a row (lane l: experts l, l + 64, ...). Returns false
 // for a row without a logit above -inf. sum: of the scores, lse: log of the
 // sum of e^x; e[v] = e^(x - lse).
+// slope[v]: of the pointwise scores, with SLOPE.
 struct RowSums {
-  float sum, lse;
+  float sum, inv, lse;  // inv = 1 / sum, 0 for 0
 };
-template <int VPT>
+template <bool SLOPE, int VPT>
 __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, float (&q)[VPT], float (&p)[VPT],
-                                           RowSums* r) {
+                                           float (&slope)[VPT], RowSums* r) {
   float top = -kInf;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) top = fmaxf(top, x[v]);
@@ -359,16 +455,16 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
   float es = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    p[v] = x[v] > -kInf ? expf(x[v] - top) : 0.0f;
+    p[v] = fast_exp(x[v] - top);  // 0 at -inf
     es += p[v];
   }
   es = wave_all_sum(es);
-  r->lse = top + logf(es);
-  const float inv = 1.0f / es;
+  r->lse = top + __builtin_amdgcn_logf(es) * kLn2;
+  const float inv = __builtin_amdgcn_rcpf(es);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) p[v] *= inv;
   if (score == MOE_SCORE_SOFTMAX) {
-    r->sum = 1.0f;
+    r->sum = r->inv = 1.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) q[v] = p[v];
     return true;
@@ -376,14 +472,15 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
   float sum = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    q[v] = x[v] > -kInf ? pointwise_score(x[v], score) : 0.0f;
+    q[v] = fast_score<SLOPE>(x[v], score, &slope[v]);
+    if (!(x[v] > -kInf)) q[v] = slope[v] = 0.0f;
     sum += q[v];
   }
   sum = wave_all_sum(sum);
   r->sum = sum;
-  const float is = sum > 0.0f ? 1.0f / sum : 0.0f;
+  r->inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) q[v] *= is;
+  for (int v = 0; v < VPT; ++v) q[v] *= r->inv;
   return true;
 }
 
@@ -411,13 +508,13 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
   int n = 0;
   for (int t = span.begin + wave; t < span.end; t += kGateWaves) {
     if (mask && mask[t] == 0) continue;
-    float x[VPT], q[VPT], p[VPT];
+    float x[VPT], q[VPT], p[VPT], unused[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
       x[v] = v * 64 + lane < g.E ? load_logit(logits, (size_t)t * g.E + v * 64 + lane) : -kInf;
-    RowSums r;
-    if (!row_scores(x, g.score, q, p, &r)) continue;
     const int id = lane < g.k ? ids[(size_t)t * g.k + lane] : -1;
+    RowSums r;
+    if (!row_scores<false>(x, g.score, q, p, unused, &r)) continue;
     if (id >= 0 && id < g.E) atomicAdd(&hist[id], 1);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) acc[v] += q[v];
@@ -627,9 +724,9 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
     const bool in_loss = a.d_loss && seq >= 0;
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
     const bool row_softmax = a.d_w && softmax && !a.renormalize;
-    float q[VPT], p[VPT];
-    RowSums r = {1.0f, 0.0f};
-    if (in_loss || row_softmax) row_scores(x, a.score, q, p, &r);
+    float q[VPT], p[VPT], slope[VPT];
+    RowSums r = {1.0f, 1.0f, 0.0f};
+    if (in_loss || row_softmax) row_scores<true>(x, a.score, q, p, slope, &r);
     float inner = 0.0f;  // softmax: sum over the row of (gradient of p) p
     if (a.d_w) {
       const int id = lane < a.k ? a.ids[(size_t)t * a.k + lane] : -1;
@@ -694,12 +791,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
 #pragma unroll
         for (int v = 0; v < VPT; ++v) dx[v] += p[v] * (dq[v] - dot - inner + zc);
       } else {
-        const float is = r.sum > 0.0f ? 1.0f / r.sum : 0.0f;
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          const float slope = x[v] > -kInf ? score_slope(x[v], q[v] * r.sum, a.score) : 0.0f;
-          dx[v] += (dq[v] - dot) * is * slope + zc * p[v];
-        }
+        for (int v = 0; v < VPT; ++v) dx[v] += (dq[v] - dot) * r.inv * slope[v] + zc * p[v];
       }
     } else if (row_softmax) {
 #pragma unroll
