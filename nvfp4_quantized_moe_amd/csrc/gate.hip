@@ -35,6 +35,19 @@ __device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p, size_t 
 __device__ __forceinline__ void store_logit(float* p, size_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, size_t i, float v) { p[i] = (uint16_t)f32_to_bf16(v); }
 
+// The lane's logits of row `row`; -inf past E. The index is clamped rather than
+// the load masked: fewer instructions, and all loads leave together.
+template <typename L, int VPT>
+__device__ __forceinline__ void load_row(const L* logits, size_t row, int E, float (&x)[VPT]) {
+  const int lane = threadIdx.x & 63;
+  const L* p = logits + row;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) x[v] = load_logit(p, (uint32_t)min(v * 64 + lane, E - 1));
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    if (v * 64 + lane >= E) x[v] = -kInf;
+}
+
 // Scores that depend on one logit alone (x = -inf gives 0).
 __device__ __forceinline__ float sigmoid_score(float x) { return 1.0f / (1.0f + expf(-x)); }
 __device__ __forceinline__ double sigmoid_score(double x) { return 1.0 / (1.0 + exp(-x)); }
@@ -334,8 +347,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
   }
   const size_t row = (size_t)t * g.E;
   float x[VPT];
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) x[v] = v * 64 + lane < g.E ? load_logit(logits, row + v * 64 + lane) : -kInf;
+  load_row(logits, row, g.E, x);
 
   const bool by_logit = !bias && g.n_group == 1;
   float key[VPT];
@@ -384,24 +396,22 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
 //   share P_be = (1/N_b) sum_t q_te,   f_be = counts_be / (N_b k),
 //   L = mean over the sequences with N_b > 0 of E sum_e f_be P_be,
 //   z = mean over all live tokens of logsumexp(x_t)^2,
-// with q the score divided by its row sum. Two launches: workgroups own runs
+// with q the score divided by its row sum. Three launches: workgroups own runs
 // of at most `chunk` tokens of one sequence and leave partial sums (slots, no
 // float atomics: the result does not depend on the order they finish in); the
-// second joins them per sequence and column block, and its last workgroup to
-// finish adds the terms.
+// second joins them per sequence and column block; the third adds the terms.
 
 struct BalanceShape {
   int T, E, k, B, score;
-  int chunk, max_chunks, col_blocks;
+  int chunk, max_chunks;
 };
 struct BalanceWs {
   float* q;          // [max_chunks][E] sums of q
   int32_t* counts;   // [max_chunks][E]
   double* z;         // [max_chunks] sums of logsumexp^2
   int32_t* live;     // [max_chunks]
-  double* term;      // [B][col_blocks] this sequence's share of L before the mean
+  double* term;      // [B][column blocks] this sequence's share of L before the mean
   double* z_seq;     // [B]
-  uint32_t* done;    // workgroups of the second launch that have finished
 };
 
 struct Span {
@@ -496,7 +506,6 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
   __shared__ double z_sh[kGateWaves];
   __shared__ int n_sh[kGateWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.done = 0u;
   for (int e = threadIdx.x; e < g.E; e += blockDim.x) hist[e] = 0;
   const Span span = find_chunk(cu, g, (int)blockIdx.x);
   if (span.begin >= span.end) return;  // whole workgroup
@@ -509,9 +518,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
   for (int t = span.begin + wave; t < span.end; t += kGateWaves) {
     if (mask && mask[t] == 0) continue;
     float x[VPT], q[VPT], p[VPT], unused[VPT];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-      x[v] = v * 64 + lane < g.E ? load_logit(logits, (size_t)t * g.E + v * 64 + lane) : -kInf;
+    load_row(logits, (size_t)t * g.E, g.E, x);
     const int id = lane < g.k ? ids[(size_t)t * g.k + lane] : -1;
     RowSums r;
     if (!row_scores<false>(x, g.score, q, p, unused, &r)) continue;
@@ -548,17 +555,18 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
   }
 }
 
-// Workgroup (c, b): experts [64c, 64c + 64) of sequence b.
-constexpr int kJoinWaves = 4;
-__global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(const int32_t* __restrict__ cu, BalanceShape g,
-                                                                       BalanceWs ws, int32_t* __restrict__ counts,
-                                                                       int32_t* __restrict__ tokens,
-                                                                       float* __restrict__ loss) {
-  __shared__ double q_sh[kJoinWaves][64], red_d[2][kJoinWaves];
-  __shared__ int c_sh[kJoinWaves][64], red_i[2][kJoinWaves], s_last;
+// Workgroup (c, b): experts [COLS c, COLS (c + 1)) of sequence b. A wave takes
+// 64 / COLS chunks at a time, eight steps in flight.
+template <int COLS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void balance_join_kernel(const int32_t* __restrict__ cu, BalanceShape g,
+                                                                  BalanceWs ws, int32_t* __restrict__ counts,
+                                                                  int32_t* __restrict__ tokens) {
+  __shared__ double q_sh[WAVES][COLS], z_sh[WAVES];
+  __shared__ int c_sh[WAVES][COLS], n_sh[WAVES];
+  constexpr int SUB = 64 / COLS, STEP = WAVES * SUB;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int b = blockIdx.y, e = blockIdx.x * 64 + lane;
-  // this sequence's chunks: [first, first + n)
+  const int b = blockIdx.y, e = blockIdx.x * COLS + lane % COLS;
+  // this sequence's chunks: [first, end)
   int first = 0;
   if (cu) {
     for (int base = 0; base < b; base += 64) {
@@ -576,13 +584,26 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(const int
   const int end = min(first + (range.y - range.x + g.chunk - 1) / g.chunk, g.max_chunks);
   double q = 0.0;
   int cnt = 0;
-  if (e < g.E)
-    for (int c = first + wave; c < end; c += kJoinWaves) {
-      q += (double)ws.q[(size_t)c * g.E + e];
-      cnt += ws.counts[(size_t)c * g.E + e];
+  for (int c0 = first + wave * SUB + lane / COLS; c0 < end; c0 += 8 * STEP) {
+    float v[8];
+    int n[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t at = (size_t)min(c0 + u * STEP, end - 1) * g.E + min(e, g.E - 1);
+      v[u] = ws.q[at];
+      n[u] = ws.counts[at];
     }
-  q_sh[wave][lane] = q;
-  c_sh[wave][lane] = cnt;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const bool in = c0 + u * STEP < end;
+      q += in ? (double)v[u] : 0.0;
+      cnt += in ? n[u] : 0;
+    }
+  }
+  for (int o = COLS; o < 64; o <<= 1) {
+    q += __shfl_xor(q, o, 64);
+    cnt += __shfl_xor(cnt, o, 64);
+  }
   int n = 0;
   double z = 0.0;
   for (int c = first + (int)threadIdx.x; c < end; c += blockDim.x) {
@@ -591,78 +612,82 @@ __global__ __launch_bounds__(64 * kJoinWaves) void balance_join_kernel(const int
   }
   for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
   z = wave_all_sum(z);
+  if (lane < COLS) {
+    q_sh[wave][lane] = q;
+    c_sh[wave][lane] = cnt;
+  }
   if (lane == 0) {
-    red_i[0][wave] = n;
-    red_d[0][wave] = z;
+    n_sh[wave] = n;
+    z_sh[wave] = z;
   }
   __syncthreads();
+  if (wave != 0) return;
   n = 0;
-  z = 0.0;
-  for (int w = 0; w < kJoinWaves; ++w) {
-    n += red_i[0][w];
-    z += red_d[0][w];
+  z = q = 0.0;
+  cnt = 0;
+  for (int w = 0; w < WAVES; ++w) {
+    n += n_sh[w];
+    z += z_sh[w];
+    q += q_sh[w][lane % COLS];
+    cnt += c_sh[w][lane % COLS];
   }
-  if (wave == 0) {
-    q = 0.0;
-    cnt = 0;
-    for (int w = 0; w < kJoinWaves; ++w) {
-      q += q_sh[w][lane];
-      cnt += c_sh[w][lane];
-    }
-    if (e < g.E) counts[(size_t)b * g.E + e] = cnt;
-    const double sum = wave_all_sum(e < g.E ? (double)cnt * q : 0.0);
-    if (lane == 0) {
-      ws.term[(size_t)b * g.col_blocks + blockIdx.x] = n > 0 ? sum * g.E / ((double)n * n * g.k) : 0.0;
-      if (blockIdx.x == 0) {
-        tokens[b] = n;
-        ws.z_seq[b] = z;
-      }
-      __threadfence();
-      s_last = atomicAdd(ws.done, 1u) == gridDim.x * gridDim.y - 1u;
-      __threadfence();
+  const bool mine = lane < COLS && e < g.E;
+  if (mine) counts[(size_t)b * g.E + e] = cnt;
+  const double sum = wave_all_sum(mine ? (double)cnt * q : 0.0);
+  if (lane == 0) {
+    ws.term[(size_t)b * gridDim.x + blockIdx.x] = n > 0 ? sum * g.E / ((double)n * n * g.k) : 0.0;
+    if (blockIdx.x == 0) {
+      tokens[b] = n;
+      ws.z_seq[b] = z;
     }
   }
-  __syncthreads();
-  if (!s_last) return;
-  // the last workgroup: agent-scope loads, since the terms come from other XCDs
-  double term = 0.0, zs = 0.0;
+}
+
+// The two losses from the sequences' terms, one workgroup. (In the join
+// itself, by the workgroup that finishes last, it took longer: the release
+// that this needs writes back each L2.)
+constexpr int kLossWaves = 4;
+__global__ __launch_bounds__(64 * kLossWaves) void balance_loss_kernel(BalanceShape g, BalanceWs ws, int cols,
+                                                                       int32_t* __restrict__ tokens,
+                                                                       float* __restrict__ loss) {
+  __shared__ double d_sh[2][kLossWaves];
+  __shared__ int n_sh[2][kLossWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double term = 0.0, z = 0.0;
   int total = 0, seqs = 0;
+  for (int64_t i = threadIdx.x; i < (int64_t)g.B * cols; i += blockDim.x) term += ws.term[i];
   for (int s = threadIdx.x; s < g.B; s += blockDim.x) {
-    const int m = __hip_atomic_load(&tokens[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int m = tokens[s];
     total += m;
     seqs += m > 0;
-    zs += __hip_atomic_load(&ws.z_seq[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int c = 0; c < g.col_blocks; ++c)
-      term += __hip_atomic_load(&ws.term[(size_t)s * g.col_blocks + c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    z += ws.z_seq[s];
   }
   for (int o = 1; o < 64; o <<= 1) {
     total += __shfl_xor(total, o, 64);
     seqs += __shfl_xor(seqs, o, 64);
   }
   term = wave_all_sum(term);
-  zs = wave_all_sum(zs);
-  __syncthreads();
+  z = wave_all_sum(z);
   if (lane == 0) {
-    red_d[0][wave] = term;
-    red_d[1][wave] = zs;
-    red_i[0][wave] = total;
-    red_i[1][wave] = seqs;
+    d_sh[0][wave] = term;
+    d_sh[1][wave] = z;
+    n_sh[0][wave] = total;
+    n_sh[1][wave] = seqs;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    term = zs = 0.0;
-    total = seqs = 0;
-    for (int w = 0; w < kJoinWaves; ++w) {
-      term += red_d[0][w];
-      zs += red_d[1][w];
-      total += red_i[0][w];
-      seqs += red_i[1][w];
-    }
-    tokens[g.B] = total;
-    tokens[g.B + 1] = seqs;
-    loss[0] = seqs > 0 ? (float)(term / seqs) : 0.0f;
-    loss[1] = total > 0 ? (float)(zs / total) : 0.0f;
+  if (threadIdx.x != 0) return;
+  term = z = 0.0;
+  total = seqs = 0;
+  for (int w = 0; w < kLossWaves; ++w) {
+    term += d_sh[0][w];
+    z += d_sh[1][w];
+    total += n_sh[0][w];
+    seqs += n_sh[1][w];
   }
+  tokens[g.B] = total;
+  tokens[g.B + 1] = seqs;
+  loss[0] = seqs > 0 ? (float)(term / seqs) : 0.0f;
+  loss[1] = total > 0 ? (float)(z / total) : 0.0f;
 }
 
 // -------------------------------------------------------------------- gradient
@@ -699,19 +724,9 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
   float x[VPT], dx[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) dx[v] = 0.0f;
-  bool live = !(a.mask && a.mask[t] == 0);
-  if (live) {
-    float top = -kInf;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      x[v] = v * 64 + lane < a.E ? load_logit(logits, row + v * 64 + lane) : -kInf;
-      top = fmaxf(top, x[v]);
-    }
-    live = wave_all_max(top) > -kInf;
-  }
-  if (live) {
+  if (!(a.mask && a.mask[t] == 0)) {
     // sequence of the token; -1: it lies in none and the losses do not see it
-    int seq = 0;
+    int seq = a.d_loss ? 0 : -1;
     if (a.d_loss && a.cu) {
       int lo = 0, hi = a.B + 1;  // cu entries <= t
       while (lo < hi) {
@@ -721,12 +736,14 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
       }
       seq = lo - 1 < a.B ? lo - 1 : -1;
     }
-    const bool in_loss = a.d_loss && seq >= 0;
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-    const bool row_softmax = a.d_w && softmax && !a.renormalize;
+    bool in_loss = seq >= 0, row_softmax = a.d_w && softmax && !a.renormalize;
     float q[VPT], p[VPT], slope[VPT];
     RowSums r = {1.0f, 1.0f, 0.0f};
-    if (in_loss || row_softmax) row_scores<true>(x, a.score, q, p, slope, &r);
+    if (in_loss || row_softmax) {  // else only the chosen logits matter
+      load_row(logits, row, a.E, x);
+      if (!row_scores<true>(x, a.score, q, p, slope, &r)) in_loss = row_softmax = false;  // not one choice either
+    }
     float inner = 0.0f;  // softmax: sum over the row of (gradient of p) p
     if (a.d_w) {
       const int id = lane < a.k ? a.ids[(size_t)t * a.k + lane] : -1;
@@ -862,16 +879,17 @@ extern "C" int moe_gate_topk(const void* logits, int32_t logits_dtype, const flo
   });
 }
 
-// Tokens of one partial sum: about two workgroups per CU for large batches
-// (512 chunks), at least 16 so that a chunk amortizes its E-wide partial row.
+// Tokens of one partial sum: 16, and more for batches of over 16384 tokens, so
+// that the partial rows (8 E bytes each) stay a small part of the logits'
+// bytes. (32 tokens at 16384, half as many waves: 16.6 instead of 10 us.)
 static int balance_chunk(int32_t T) {
-  const int per = ((T + 511) / 512 + kGateWaves - 1) / kGateWaves * kGateWaves;
+  const int per = ((T + 1023) / 1024 + kGateWaves - 1) / kGateWaves * kGateWaves;
   return per < 16 ? 16 : per;
 }
 static size_t balance_layout(int32_t T, int32_t E, int32_t B, BalanceShape* g, char* base, BalanceWs* ws) {
   const int chunk = balance_chunk(T);
   const int max_chunks = (T + chunk - 1) / chunk + B;  // every sequence may end inside a chunk
-  const int cols = (E + 63) / 64;
+  const int cols = (E + 15) / 16;  // column blocks, at most
   size_t p = 0;
   auto put = [&](size_t bytes) {
     char* at = base + p;
@@ -885,11 +903,9 @@ static size_t balance_layout(int32_t T, int32_t E, int32_t B, BalanceShape* g, c
   w.live = reinterpret_cast<int32_t*>(put((size_t)max_chunks * 4));
   w.term = reinterpret_cast<double*>(put((size_t)B * cols * 8));
   w.z_seq = reinterpret_cast<double*>(put((size_t)B * 8));
-  w.done = reinterpret_cast<uint32_t*>(put(4));
   if (g) {
     g->chunk = chunk;
     g->max_chunks = max_chunks;
-    g->col_blocks = cols;
   }
   if (ws) *ws = w;
   return p;
@@ -914,7 +930,7 @@ extern "C" int moe_balance_loss(const void* logits, int32_t logits_dtype, const 
   if (!nvfp4_aligned16(topk_ids) || !nvfp4_aligned16(token_mask) || !nvfp4_aligned16(cu_seqlens) ||
       !nvfp4_aligned16(loss) || !nvfp4_aligned16(counts) || !nvfp4_aligned16(tokens) || !nvfp4_aligned16(ws))
     return NVFP4_ERR_ALIGN;
-  BalanceShape g = {T, E, k, B, score, 0, 0, 0};
+  BalanceShape g = {T, E, k, B, score, 0, 0};
   BalanceWs w;
   if (ws_bytes < balance_layout(T, E, B, &g, reinterpret_cast<char*>(ws), &w)) return NVFP4_ERR_WORKSPACE;
   const size_t lds = (size_t)(kGateWaves + 1) * E * 4;
@@ -929,8 +945,18 @@ extern "C" int moe_balance_loss(const void* logits, int32_t logits_dtype, const 
                          (hipStream_t)stream, reinterpret_cast<const uint16_t*>(logits), topk_ids, token_mask,
                          cu_seqlens, g, w);
     NVFP4_CHECK_LAUNCH();
-    hipLaunchKernelGGL(balance_join_kernel, dim3(g.col_blocks, B), dim3(64 * kJoinWaves), 0, (hipStream_t)stream,
-                       cu_seqlens, g, w, counts, tokens, loss);
+    // long sequences: more workgroups and waves over the same chunks
+    const bool tall = T / B >= 64 * g.chunk;
+    const int cols = tall ? (E + 15) / 16 : (E + 63) / 64;
+    if (tall)
+      hipLaunchKernelGGL((balance_join_kernel<16, 16>), dim3(cols, B), dim3(1024), 0, (hipStream_t)stream, cu_seqlens,
+                         g, w, counts, tokens);
+    else
+      hipLaunchKernelGGL((balance_join_kernel<64, 4>), dim3(cols, B), dim3(256), 0, (hipStream_t)stream, cu_seqlens, g,
+                         w, counts, tokens);
+    NVFP4_CHECK_LAUNCH();
+    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(64 * kLossWaves), 0, (hipStream_t)stream, g, w, cols, tokens,
+                       loss);
     NVFP4_CHECK_LAUNCH();
     return NVFP4_OK;
   });
