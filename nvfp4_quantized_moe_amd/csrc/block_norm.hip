@@ -396,12 +396,10 @@ __global__ __launch_bounds__(64 * kColumnWaves) void norm_columns_kernel(const f
     for (int r = wave; r < rows; r += 8 * kColumnWaves) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int ru = r + u * kColumnWaves;
-        v[u] = ru < rows ? p[(size_t)ru * 3 * H] : 0.0f;
-      }
+      for (int u = 0; u < 8; ++u)
+        v[u] = p[(size_t)min(r + u * kColumnWaves, rows - 1) * 3 * H];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) s += v[u];
+      for (int u = 0; u < 8; ++u) s += r + u * kColumnWaves < rows ? v[u] : 0.0f;
     }
   }
   sh[wave][lane] = s;
