@@ -34,23 +34,18 @@ __device__ __forceinline__ int quantize_int8(float x, float s, float inv) {
   return x < 0.0f ? -n : n;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&f)[16]);
-template <>
-__device__ __forceinline__ void load16<uint16_t>(const uint16_t* p, float (&f)[16]) {
-  const uint4* v = reinterpret_cast<const uint4*>(p);
-  const uint4 a = v[0], b = v[1];
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     f[2 * i] = __uint_as_float(w[i] << 16);
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float (&f)[16]) {
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const float4 v = reinterpret_cast<const float4*>(p)[i];
     f[4 * i] = v.x;
     f[4 * i + 1] = v.y;
@@ -112,30 +107,31 @@ __device__ __forceinline__ void quantize_codes(const float* f, const RowScale& r
   }
 }
 
-// One workgroup per row; thread i holds the row's 16-element chunks i, i +
-// blockDim.x, ... between the maximum and the rounding (read a second time
-// from the cache, 8192 x 7168 took 46 us instead of 36).
+// One workgroup per row; thread i holds the row's 8-element chunks i, i +
+// blockDim.x, ... between the maximum and the rounding. (8192 x 7168: with 16
+// elements per thread, whose two loads each touch every line of 2 KB, 45 us;
+// with the row read a second time from the cache 46 us.)
 template <typename T, int CH>
 __global__ __launch_bounds__(1024) void int8_rows_kernel(const T* __restrict__ x, int K, int8_t* __restrict__ q,
                                                          float* __restrict__ scale) {
   __shared__ float red[16];
   const size_t row = (size_t)blockIdx.x * K;
-  const int n = K / 16;
-  float m = 0.0f, f[CH][16];
+  const int n = K / 8;
+  float m = 0.0f, f[CH][8];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) load16(x + row + min((int)(threadIdx.x + c * blockDim.x), n - 1) * 16, f[c]);
+  for (int c = 0; c < CH; ++c) load8(x + row + min((int)(threadIdx.x + c * blockDim.x), n - 1) * 8, f[c]);
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[c][i]));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[c][i]));
   const RowScale rs = row_scale(m, red);
   if (threadIdx.x == 0) scale[blockIdx.x] = rs.stored;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int ch = threadIdx.x + c * blockDim.x;
-    uint32_t w[4];
-    quantize_codes<16>(f[c], rs, w);
-    if (ch < n) *reinterpret_cast<uint4*>(q + row + ch * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    uint32_t w[2];
+    quantize_codes<8>(f[c], rs, w);
+    if (ch < n) *reinterpret_cast<uint2*>(q + row + ch * 8) = make_uint2(w[0], w[1]);
   }
 }
 
@@ -426,12 +422,26 @@ __device__ __forceinline__ void join8(const Int8Args& g, int m, int n, float (&o
   const int half = g.N / 2;
   int4v s[2] = {int4v{0, 0, 0, 0}, int4v{0, 0, 0, 0}}, u[2] = {int4v{0, 0, 0, 0}, int4v{0, 0, 0, 0}};
   const int32_t* p = g.part + (size_t)m * g.N + n;
-  for (int i = 0; i < g.splits; ++i, p += (size_t)g.M * g.N) {
+  const size_t step = (size_t)g.M * g.N;
+  for (int i = 0; i < g.splits; i += 4) {  // four parts in flight
+    int4v vs[4][2], vu[4][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s[h] += *reinterpret_cast<const int4v*>(p + 4 * h);
-      if (SILU) u[h] += *reinterpret_cast<const int4v*>(p + half + 4 * h);
-    }
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int32_t* at = p + (size_t)min(i + j, g.splits - 1) * step + 4 * h;
+        vs[j][h] = *reinterpret_cast<const int4v*>(at);
+        if (SILU) vu[j][h] = *reinterpret_cast<const int4v*>(at + half);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < g.splits) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s[h] += vs[j][h];
+          if (SILU) u[h] += vu[j][h];
+        }
+      }
   }
   const float as = g.a_s[m];
 #pragma unroll
@@ -578,16 +588,16 @@ extern "C" int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int
   const auto go = [&](auto xt, auto ch) -> int {
     using T = decltype(xt);
     constexpr int CH = decltype(ch)::value;
-    const int threads = ((K / 16 + CH - 1) / CH + 63) / 64 * 64;
+    const int threads = ((K / 8 + CH - 1) / CH + 63) / 64 * 64;
     hipLaunchKernelGGL((int8_rows_kernel<T, CH>), dim3(M), dim3(threads), 0, (hipStream_t)stream,
                        reinterpret_cast<const T*>(x), K, q, scale);
     NVFP4_CHECK_LAUNCH();
     return NVFP4_OK;
   };
-  constexpr std::integral_constant<int, 1> one;
-  constexpr std::integral_constant<int, 4> four;  // rows past 1024 chunks
-  if (x_dtype == NVFP4_DT_BF16) return K <= 16384 ? go(uint16_t(), one) : go(uint16_t(), four);
-  return K <= 16384 ? go(float(), one) : go(float(), four);
+  constexpr std::integral_constant<int, 2> two;
+  constexpr std::integral_constant<int, 8> eight;  // rows past 2048 chunks
+  if (x_dtype == NVFP4_DT_BF16) return K <= 16384 ? go(uint16_t(), two) : go(uint16_t(), eight);
+  return K <= 16384 ? go(float(), two) : go(float(), eight);
 }
 
 static int int8_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue) {
