@@ -188,7 +188,7 @@ int moe_gate_topk(const void* logits, int32_t logits_dtype, const float* bias, c
  *                         [1] mean over the N live tokens of logsumexp(x_t)^2
  *                         (0 where there is nothing to average)
  * ws: at least moe_balance_loss_ws_bytes(T, E, B) bytes (0 for sizes that are
- * refused). Three launches; the result does not depend on their timing.
+ * refused). Two or three launches; the result does not depend on their timing.
  */
 size_t moe_balance_loss_ws_bytes(int32_t T, int32_t E, int32_t B);
 int moe_balance_loss(const void* logits, int32_t logits_dtype, const int32_t* topk_ids, const uint8_t* token_mask,

@@ -147,7 +147,7 @@ def _buf(t, dtype, numel, name):
 
 
 def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 

@@ -113,9 +113,12 @@ struct GateShape {
 
 // Key of every logit of the lane, in F (float or double): the logits
 // themselves when the order of scores is theirs (no bias, one group).
+// *bmax: the lane's largest |bias|.
 template <typename F, int VPT>
-__device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bias, const GateShape& g, F (&key)[VPT]) {
+__device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bias, const GateShape& g, F (&key)[VPT],
+                                          float* bmax) {
   const int lane = threadIdx.x & 63;
+  *bmax = 0.0f;
   const F inf = (F)kInf;
   if (!bias && g.n_group == 1) {
 #pragma unroll
@@ -141,8 +144,11 @@ __device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bi
   }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    const int e = v * 64 + lane;
-    if (bias && e < g.E) key[v] += (F)bias[e];
+    if (bias) {
+      const float b = bias[min(v * 64 + lane, g.E - 1)];
+      *bmax = fmaxf(*bmax, fabsf(b));
+      key[v] += (F)b;
+    }
     if (!(x[v] > -kInf)) key[v] = -inf;
   }
 }
@@ -270,11 +276,15 @@ __device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, in
   }
   wave_lds_fence();
   const uint2 c = lds[lane];  // past n: left over, never counted
-  const float kv = __uint_as_float(c.x);
+  // higher key first, then the lower place: one comparison of the key's bits
+  // (in an order of integers) above the place
+  const uint32_t bits = c.x == 0x80000000u ? 0u : c.x;  // -0 equals 0
+  const uint32_t order = bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
+  const uint64_t mine64 = ((uint64_t)order << 32) | (uint32_t)(63 - lane);
   int rank = 0;
   for (int j = 0; j < n; ++j) {
-    const float kj = lane_value(kv, j);
-    rank += (kj > kv || (kj == kv && j < lane)) ? 1 : 0;
+    const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)order, j) << 32) | (uint32_t)(63 - j);
+    rank += other > mine64 ? 1 : 0;
   }
   wave_lds_fence();
   if (lane < n && rank < want) lds[rank] = c;
@@ -353,16 +363,14 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
   float key[VPT];
   int id;
   float at;
-  gate_keys(x, bias, g, key);
+  float bmax;
+  gate_keys(x, bias, g, key, &bmax);
   bool doubt = false;
   const float tol = g.score == MOE_SCORE_SOFTMAX ? 0x1p-17f : 0x1p-20f;
   if (g.n_group > 1) {
     float gap, size;
     keep_groups(key, g, reinterpret_cast<float*>(lds + (size_t)wave * g.E), &gap, &size);
     // a value is a sum of two keys, each score + bias, |bias| <= bmax
-    float bmax = 0.0f;
-    if (bias)
-      for (int e = lane; e < g.E; e += 64) bmax = fmaxf(bmax, fabsf(bias[e]));
     bmax = wave_all_max(bmax);
     doubt = !(gap > 4.0f * tol * (size + 2.0f * bmax));
     if (g.topk_group == g.n_group) doubt = false;
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
   }
   if (doubt) {
     double key64[VPT], gap, size, at64;
-    gate_keys(x, bias, g, key64);
+    gate_keys(x, bias, g, key64, &bmax);
     if (g.n_group > 1) keep_groups(key64, g, lds + (size_t)wave * g.E, &gap, &size);
     pick_by_rounds(key64, g.k, &id, &at64);
   }
@@ -399,7 +407,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
 // with q the score divided by its row sum. Three launches: workgroups own runs
 // of at most `chunk` tokens of one sequence and leave partial sums (slots, no
 // float atomics: the result does not depend on the order they finish in); the
-// second joins them per sequence and column block; the third adds the terms.
+// second joins them per sequence and column block; the third adds the terms
+// (a single workgroup of the second does it itself).
 
 struct BalanceShape {
   int T, E, k, B, score;
@@ -560,7 +569,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
 template <int COLS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void balance_join_kernel(const int32_t* __restrict__ cu, BalanceShape g,
                                                                   BalanceWs ws, int32_t* __restrict__ counts,
-                                                                  int32_t* __restrict__ tokens) {
+                                                                  int32_t* __restrict__ tokens,
+                                                                  float* __restrict__ loss) {
   __shared__ double q_sh[WAVES][COLS], z_sh[WAVES];
   __shared__ int c_sh[WAVES][COLS], n_sh[WAVES];
   constexpr int SUB = 64 / COLS, STEP = WAVES * SUB;
@@ -639,6 +649,12 @@ __global__ __launch_bounds__(64 * WAVES) void balance_join_kernel(const int32_t*
     if (blockIdx.x == 0) {
       tokens[b] = n;
       ws.z_seq[b] = z;
+    }
+    if (gridDim.x * gridDim.y == 1) {  // nothing else to add up
+      tokens[1] = n;
+      tokens[2] = n > 0;
+      loss[0] = n > 0 ? (float)(sum * g.E / ((double)n * n * g.k)) : 0.0f;
+      loss[1] = n > 0 ? (float)(z / n) : 0.0f;
     }
   }
 }
@@ -950,11 +966,12 @@ extern "C" int moe_balance_loss(const void* logits, int32_t logits_dtype, const 
     const int cols = tall ? (E + 15) / 16 : (E + 63) / 64;
     if (tall)
       hipLaunchKernelGGL((balance_join_kernel<16, 16>), dim3(cols, B), dim3(1024), 0, (hipStream_t)stream, cu_seqlens,
-                         g, w, counts, tokens);
+                         g, w, counts, tokens, loss);
     else
       hipLaunchKernelGGL((balance_join_kernel<64, 4>), dim3(cols, B), dim3(256), 0, (hipStream_t)stream, cu_seqlens, g,
-                         w, counts, tokens);
+                         w, counts, tokens, loss);
     NVFP4_CHECK_LAUNCH();
+    if (cols * B == 1) return NVFP4_OK;
     hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(64 * kLossWaves), 0, (hipStream_t)stream, g, w, cols, tokens,
                        loss);
     NVFP4_CHECK_LAUNCH();
