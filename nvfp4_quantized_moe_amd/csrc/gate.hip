@@ -98,11 +98,29 @@ __device__ __forceinline__ float fast_score(float x, int score, float* slope) {
   return s;
 }
 
-// Score for a key: float keys may be two steps off (see gate_topk_kernel).
+// e^x within two float32 steps: the hardware's 2^t at t = x log2 e, corrected
+// by what the product's rounding (and that of log2 e) left out. Past +-88,
+// the edge of float32, e^x stays what it is there.
+__device__ __forceinline__ float near_exp(float x) {
+  x = fminf(fmaxf(x, -88.0f), 88.0f);
+  const float t = x * kLog2e;
+  const float rest = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, kLog2e, -t));  // log2 e - kLog2e
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e * kLn2, rest, e);
+}
+// Score for a key (see gate_topk_kernel for what float keys may be off by).
 __device__ __forceinline__ float key_score(float x, int score) {
-  return score == MOE_SCORE_SIGMOID ? __builtin_amdgcn_rcpf(1.0f + expf(-x)) : sqrt_softplus(x);
+  return score == MOE_SCORE_SIGMOID ? __builtin_amdgcn_rcpf(1.0f + near_exp(-x)) : fast_score<false>(x, score, nullptr);
 }
 __device__ __forceinline__ double key_score(double x, int score) { return pointwise_score(x, score); }
+__device__ __forceinline__ float key_exp(float x) { return near_exp(x); }
+__device__ __forceinline__ double key_exp(double x) { return exp(x); }
+
+// Bits of a key in the order of unsigned integers (-0 as 0).
+__device__ __forceinline__ uint32_t order_bits(float key) {
+  const uint32_t bits = __float_as_uint(key + 0.0f);
+  return bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
+}
 
 struct GateShape {
   int T, E, k, score;
@@ -132,12 +150,12 @@ __device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bi
     top = wave_all_max(top);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      key[v] = x[v] > -kInf ? exp((F)x[v] - top) : (F)0;
+      key[v] = x[v] > -kInf ? key_exp((F)x[v] - top) : (F)0;
       sum += key[v];
     }
-    sum = wave_all_sum(sum);
+    sum = (F)1 / wave_all_sum(sum);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) key[v] = key[v] / sum;
+    for (int v = 0; v < VPT; ++v) key[v] *= sum;
   } else {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) key[v] = key_score((F)x[v], g.score);
@@ -183,9 +201,18 @@ __device__ __forceinline__ void keep_groups(F (&key)[VPT], const GateShape& g, F
   }
   const F value = a + (b > -inf ? b : (F)0);  // -inf when nothing in the group can be chosen
   int rank = 0;
-  for (int j = 0; j < g.n_group; ++j) {
-    const F o = lane_value(value, j * per);
-    rank += (o > value || (o == value && j < mine)) ? 1 : 0;
+  if constexpr (sizeof(F) == 4) {  // one comparison: the value's bits above the group
+    const uint32_t order = order_bits(value);
+    const uint64_t mine64 = ((uint64_t)order << 32) | (uint32_t)(63 - mine);
+    for (int j = 0; j < g.n_group; ++j) {
+      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)order, j * per);
+      rank += (((uint64_t)o << 32) | (uint32_t)(63 - j)) > mine64 ? 1 : 0;
+    }
+  } else {
+    for (int j = 0; j < g.n_group; ++j) {
+      const F o = lane_value(value, j * per);
+      rank += (o > value || (o == value && j < mine)) ? 1 : 0;
+    }
   }
   const bool kept = mine < g.n_group && rank < g.topk_group;
   const F lowest = -wave_all_max(kept ? -value : -inf);
@@ -278,8 +305,7 @@ __device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, in
   const uint2 c = lds[lane];  // past n: left over, never counted
   // higher key first, then the lower place: one comparison of the key's bits
   // (in an order of integers) above the place
-  const uint32_t bits = c.x == 0x80000000u ? 0u : c.x;  // -0 equals 0
-  const uint32_t order = bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
+  const uint32_t order = order_bits(__uint_as_float(c.x));
   const uint64_t mine64 = ((uint64_t)order << 32) | (uint32_t)(63 - lane);
   int rank = 0;
   for (int j = 0; j < n; ++j) {
@@ -309,14 +335,14 @@ __device__ __forceinline__ void write_choices(const L* logits, size_t row, const
   if (g.score == MOE_SCORE_SOFTMAX) {
     if (g.renormalize) {  // the softmax over the choices alone: nothing of the row's sum is left in it
       const float top = wave_all_max(xl);
-      s = on ? expf(xl - top) : 0.0f;
+      s = on ? near_exp(xl - top) : 0.0f;
     } else {
       float top = -kInf, sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) top = fmaxf(top, x[v]);
       top = wave_all_max(top);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) sum += x[v] > -kInf ? expf(x[v] - top) : 0.0f;
+      for (int v = 0; v < VPT; ++v) sum += x[v] > -kInf ? near_exp(x[v] - top) : 0.0f;
       sum = wave_all_sum(sum);
       s = on ? expf(xl - top) / sum : 0.0f;
     }
@@ -325,7 +351,7 @@ __device__ __forceinline__ void write_choices(const L* logits, size_t row, const
   }
   if (g.renormalize) {
     const float sum = wave_all_sum(s);
-    s = sum > 0.0f ? s / sum : 0.0f;
+    s = sum > 0x1p-100f ? s * __builtin_amdgcn_rcpf(sum) : sum > 0.0f ? s / sum : 0.0f;
   }
   if (lane < g.k) {
     ids[t * g.k + lane] = on ? id : -1;
@@ -335,9 +361,11 @@ __device__ __forceinline__ void write_choices(const L* logits, size_t row, const
 
 // One wave per token. The order of the choices is that of the keys in
 // float64; float32 keys decide it wherever two neighbours are further apart
-// than their rounding (2^-20 of the scores; 2^-17 for softmax, whose argument
-// x - max is rounded first) or are the same sum of the same numbers, and the
-// row is done again in float64 where they are not.
+// than their rounding (2^-20 of the scores for the sigmoid; 2^-17 for softmax,
+// whose argument x - max is rounded first, and for sqrt-softplus, from the
+// hardware's logarithm) or are the same sum of the same numbers, and the row
+// is done again in float64 where they are not (0.4 % of the rows at 16384 x 256
+// with a bias and groups).
 template <typename L, int VPT>
 __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __restrict__ logits,
                                                                     const float* __restrict__ bias,
@@ -366,7 +394,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
   float bmax;
   gate_keys(x, bias, g, key, &bmax);
   bool doubt = false;
-  const float tol = g.score == MOE_SCORE_SOFTMAX ? 0x1p-17f : 0x1p-20f;
+  const float tol = g.score == MOE_SCORE_SIGMOID ? 0x1p-20f : 0x1p-17f;
   if (g.n_group > 1) {
     float gap, size;
     keep_groups(key, g, reinterpret_cast<float*>(lds + (size_t)wave * g.E), &gap, &size);
