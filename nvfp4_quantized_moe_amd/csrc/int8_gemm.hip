@@ -204,25 +204,27 @@ __device__ __forceinline__ typename OutVec<W>::type add_and_round(const float (&
 // Workgroup tile BM x BN of WM x WN waves; MFMA 32x32x32 with the weights as
 // its first operand, so a lane holds runs of four output columns of one token.
 //
-// K passes in stages of 64 bytes through four LDS buffers, filled straight
-// from memory (buffer loads to LDS pass no register) three stages ahead; the wait before a stage leaves the two younger
-// stages in flight. A row's four 16-byte chunks are stored at chunk ^
-// ((row / 2) & 3), which spreads the rows that eight lanes of a fragment read
-// touch over all banks; the loads apply it to the address they read. Inside a
-// stage the second half's fragments are read under the first half's MFMAs.
+// K passes in stages of BK bytes through four LDS buffers, filled straight from
+// memory (buffer loads to LDS pass no register) three stages ahead; the wait
+// before a stage leaves the two younger stages in flight. Stages of 64 bytes
+// where the tile fills the LDS; of 128 in the small tiles of few tokens, whose
+// time is the number of stages (512 x 4096 x 7168: 39 -> 28 us). A row's
+// 16-byte chunks are permuted by its number, which spreads the rows that
+// eight lanes of a fragment read touch over all banks; the loads apply it to
+// the address they read.
 //
 // SILU: the tile's weight rows alternate in runs of 32 between gate (row n)
 // and up (row I + n), so that a wave holds both halves of an output.
-constexpr int kBK = 64;
-template <int BM, int BN, int WM, int WN, int OUT>
-__global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, int mt, int nt) {
+template <int BM, int BN, int WM, int WN, int BK, int OUT>
+__global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(Int8Args g, int mt, int nt) {
   constexpr bool SILU = OUT == kInt8Silu;
   constexpr int TH = 64 * WM * WN;
   constexpr int SM = BM / WM / 32, SN = BN / WN / 32;  // 32 x 32 subtiles of a wave
   static_assert(!SILU || SN % 2 == 0, "gate and up halves in one wave");
-  constexpr int RPI = TH / 4;                          // rows of one load instruction of the workgroup
+  constexpr int CPR = BK / 16, KS = BK / 32;           // chunks of a row and MFMA steps of a stage
+  constexpr int RPI = TH / CPR;                        // rows of one load instruction of the workgroup
   constexpr int PA = BM / RPI, PB = BN / RPI, PL = PA + PB;
-  constexpr int BUF = (BM + BN) * 4;                   // 16-byte chunks of a buffer: A rows, then B rows
+  constexpr int BUF = (BM + BN) * CPR;                 // 16-byte chunks of a buffer: A rows, then B rows
   __shared__ int4v l0[BUF], l1[BUF], l2[BUF], l3[BUF];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
@@ -230,21 +232,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   const int m0 = tile.x * BM, n0 = tile.y * (SILU ? BN / 2 : BN), half = g.N / 2;
   // This thread's chunk of every load: row trow + RPI i of the tile (the last
   // row of the matrix again where there is none: its results are not stored),
-  // K bytes tk of a stage. SILU: the 16 rows of a wave lie in one half.
-  const int trow = threadIdx.x >> 2, tk = ((threadIdx.x & 3) ^ ((trow >> 1) & 3)) * 16;
+  // K bytes tk of a stage. SILU: the rows of one load of a wave lie in one half,
+  // by the wave (RPI a multiple of 64) or by the load (RPI 32).
+  const auto swizzle = [](int row, int chunk) { return CPR == 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3); };
+  const int trow = threadIdx.x / CPR, tk = swizzle(trow, threadIdx.x % CPR) * 16;
+  static_assert(!SILU || RPI == 32 || RPI % 64 == 0, "the rows of a load of a wave lie in one half");
   const int a_rows = min(BM, g.M - m0), b_rows = min(SILU ? BN / 2 : BN, (SILU ? half : g.N) - n0);
-  const int b0 = SILU && ((wave >> 1) & 1) ? half + n0 : n0;
+  const bool up_wave = SILU && RPI != 32 && (wave * (64 / CPR) / 32) % 2 == 1;
   const __amdgpu_buffer_rsrc_t ra = int8_rsrc(g.a + (size_t)m0 * g.K, (uint32_t)(a_rows * g.K));
-  const __amdgpu_buffer_rsrc_t rb = int8_rsrc(g.b + (size_t)b0 * g.K, (uint32_t)(b_rows * g.K));
+  const __amdgpu_buffer_rsrc_t rb = int8_rsrc(g.b + (size_t)(n0 + (up_wave ? half : 0)) * g.K, (uint32_t)(b_rows * g.K));
+  const __amdgpu_buffer_rsrc_t ru = int8_rsrc(g.b + (size_t)(n0 + half) * g.K, (uint32_t)(b_rows * g.K));
   int va[PA], vb[PB];
 #pragma unroll
   for (int i = 0; i < PA; ++i) va[i] = min(trow + i * RPI, a_rows - 1) * g.K + tk;
 #pragma unroll
   for (int i = 0; i < PB; ++i) {
-    const int row = SILU ? (trow >> 6) * 32 + (trow & 31) + i * (RPI / 2) : trow + i * RPI;
+    const int at = trow + i * RPI;  // in the tile
+    const int row = SILU ? (at >> 6) * 32 + (at & 31) : at;
     vb[i] = min(row, b_rows - 1) * g.K + tk;
   }
-  static_assert(!SILU || RPI % 64 == 0, "a wave's rows of every load lie in one half");
   const int k_begin = (int)blockIdx.y * g.k_split, k_end = min(g.K, k_begin + g.k_split);
   auto fetch = [&](int k0, int4v* to) {
     const bool in = k0 + tk < k_end;     // zeros past the end of a row (or of this part of K)
@@ -254,7 +260,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
       load_lds16(ra, to + wave * 64 + i * TH, in ? va[i] : kInt8Out, ks);
 #pragma unroll
     for (int i = 0; i < PB; ++i)
-      load_lds16(rb, to + BM * 4 + wave * 64 + i * TH, in ? vb[i] : kInt8Out, ks);
+      load_lds16(SILU && RPI == 32 && i % 2 == 1 ? ru : rb, to + BM * CPR + wave * 64 + i * TH,
+                 in ? vb[i] : kInt8Out, ks);
   };
   int16v acc[SN][SM];
 #pragma unroll
@@ -264,30 +271,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
   const int r = lane & 31, hi = lane >> 5;
-  int fa_at[2], fb_at[2];
+  int fa_at[KS], fb_at[KS];
 #pragma unroll
-  for (int ks = 0; ks < 2; ++ks) {
-    const int c = (ks * 2 + hi) ^ ((r >> 1) & 3);
-    fa_at[ks] = (wm * 32 * SM + r) * 4 + c;
-    fb_at[ks] = (BM + wn * 32 * SN + r) * 4 + c;
+  for (int ks = 0; ks < KS; ++ks) {
+    const int c = swizzle(r, ks * 2 + hi);
+    fa_at[ks] = (wm * 32 * SM + r) * CPR + c;
+    fb_at[ks] = (BM + wn * 32 * SN + r) * CPR + c;
   }
   auto compute = [&](const int4v* at) {
     int4v fa[2][SM], fb[2][SN];
     auto read = [&](int ks) {
 #pragma unroll
-      for (int j = 0; j < SM; ++j) fa[ks][j] = at[fa_at[ks] + j * 128];
+      for (int j = 0; j < SM; ++j) fa[ks & 1][j] = at[fa_at[ks] + j * 32 * CPR];
 #pragma unroll
-      for (int i = 0; i < SN; ++i) fb[ks][i] = at[fb_at[ks] + i * 128];
+      for (int i = 0; i < SN; ++i) fb[ks & 1][i] = at[fb_at[ks] + i * 32 * CPR];
     };
     read(0);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if (ks == 0) read(1);
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks + 1 < KS) read(ks + 1);
 #pragma unroll
       for (int i = 0; i < SN; ++i)
 #pragma unroll
         for (int j = 0; j < SM; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks][i], fa[ks][j], acc[i][j], 0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks & 1][i], fa[ks & 1][j], acc[i][j], 0, 0, 0);
     }
   };
   // Waits until at most `left` of this wave's loads are in flight, then for
@@ -303,24 +310,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void int8_tile_kernel(Int8Args g, 
   };
   constexpr std::integral_constant<int, 0> none;
   constexpr std::integral_constant<int, 2 * PL> two_stages;
-  const int stages = (k_end - k_begin + kBK - 1) / kBK;
+  const int stages = (k_end - k_begin + BK - 1) / BK;
   fetch(k_begin, l0);
-  fetch(k_begin + kBK, l1);
-  fetch(k_begin + 2 * kBK, l2);
+  fetch(k_begin + BK, l1);
+  fetch(k_begin + 2 * BK, l2);
   // Stage s: its own loads have arrived; every wave is past stage s - 1, whose
-  // buffer takes the loads of stage s + 3. Up to three stages past the end of K
-  // load and add zeros: with a branch around them the compiler no longer knows
-  // which buffer a load fills, and waits for all of them before it reads any.
+  // buffer takes the loads of stage s + 3 (zeros past the end of K). No branch
+  // inside the loop: around the stages it leaves the compiler unsure which
+  // buffer a load fills, and it waits for all of them before it reads any.
   auto stage = [&](int s, const int4v* cur, int4v* next) {
     wait(two_stages);
-    fetch(k_begin + (s + 3) * kBK, next);
+    fetch(k_begin + (s + 3) * BK, next);
     compute(cur);
   };
-  for (int s = 0; s < stages; s += 4) {
+  int s = 0;
+  for (; s + 4 <= stages; s += 4) {
     stage(s, l0, l3);
     stage(s + 1, l1, l0);
     stage(s + 2, l2, l1);
     stage(s + 3, l3, l2);
+  }
+  if (s < stages) {
+    stage(s, l0, l3);
+    if (s + 1 < stages) {
+      stage(s + 1, l1, l0);
+      if (s + 2 < stages) stage(s + 2, l2, l1);
+    }
   }
   wait(none);
 
@@ -608,11 +623,11 @@ static int int8_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue) {
   return NVFP4_OK;
 }
 
-template <int BM, int BN, int WM, int WN, int OUT>
+template <int BM, int BN, int WM, int WN, int BK, int OUT>
 static int launch_int8_tile(const Int8Args& g, hipStream_t stream) {
   const int mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN;
   if ((int64_t)mt * nt >= (1ll << 31)) return NVFP4_ERR_SHAPE;
-  hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, OUT>), dim3((unsigned)mt * nt, g.splits),
+  hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, BK, OUT>), dim3((unsigned)mt * nt, g.splits),
                      dim3(64 * WM * WN), 0, stream, g, mt, nt);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
@@ -640,7 +655,7 @@ static int int8_splits(int64_t M, int64_t N, int64_t K) {
 static Int8Args int8_args(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s, int M, int N, int K,
                           bool silu, const void* add, void* d, void* ws) {
   const int want = int8_splits(M, N, K);
-  const int per = ((K + want - 1) / want + kBK - 1) / kBK * kBK;
+  const int per = ((K + want - 1) / want + 127) / 128 * 128;
   return {a_q, a_s, b_q, b_s, reinterpret_cast<const uint16_t*>(add), reinterpret_cast<uint16_t*>(d), M, N, K,
           silu ? N / 2 : N, (K + per - 1) / per, per, reinterpret_cast<int32_t*>(ws)};
 }
@@ -653,7 +668,7 @@ template <bool SILU>
 static int launch_int8(const Int8Args& g, hipStream_t stream) {
   constexpr int OUT = SILU ? kInt8Silu : kInt8Bf16;
   if (g.splits > 1) {
-    const int st = launch_int8_tile<64, 128, 2, 2, kInt8Part>(g, stream);
+    const int st = launch_int8_tile<64, 128, 2, 2, 128, kInt8Part>(g, stream);
     if (st) return st;
     hipLaunchKernelGGL(int8_join_kernel<SILU>, dim3((unsigned)(((int64_t)g.M * g.n_out / 8 + 255) / 256)), dim3(256), 0,
                        stream, g);
@@ -663,9 +678,9 @@ static int launch_int8(const Int8Args& g, hipStream_t stream) {
   if (g.M <= kSkinnyM) return launch_int8_skinny<1, SILU>(g, stream);
   // the largest tile that still gives most of the 256 CUs one
   const auto tiles = [&](int bm, int bn) { return (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, OUT>(g, stream);
-  if (tiles(128, 128) >= 192) return launch_int8_tile<128, 128, 2, 2, OUT>(g, stream);
-  return launch_int8_tile<64, SILU ? 128 : 64, 2, 2, OUT>(g, stream);
+  if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, 64, OUT>(g, stream);
+  if (tiles(128, 128) >= 192) return launch_int8_tile<128, 128, 2, 2, 64, OUT>(g, stream);
+  return launch_int8_tile<64, SILU ? 128 : 64, 2, 2, 128, OUT>(g, stream);
 }
 
 extern "C" size_t int8_gemm_ws_bytes(int32_t M, int32_t N, int32_t K) {
@@ -745,7 +760,7 @@ extern "C" int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const
   if (st) return st;
   const Int8Args up = int8_args(x_q, x_s, w1_q, w1_scale, T, 2 * inter, hidden, true, nullptr, base + l.h, base + l.part);
   if (up.splits > 1) {  // the join quantizes h as well
-    st = launch_int8_tile<64, 128, 2, 2, kInt8Part>(up, (hipStream_t)stream);
+    st = launch_int8_tile<64, 128, 2, 2, 128, kInt8Part>(up, (hipStream_t)stream);
     if (st) return st;
     hipLaunchKernelGGL(int8_join_rows_kernel, dim3(T), dim3(256), 0, (hipStream_t)stream, up, h_q, h_s);
     NVFP4_CHECK_LAUNCH();
