@@ -74,12 +74,23 @@ __device__ __forceinline__ void load_weights8(const float* p, int at, float abse
   }
 }
 
-// Sums of N values per thread over the workgroup, in every thread. A scratch
+// A thread's place: `group` of the workgroup's row groups (whole waves), each
+// with a row of its own, and `tid` of the `threads` of its group.
+struct Place {
+  int group, tid, threads;
+};
+__device__ __forceinline__ Place place_of(int threads) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave / (threads >> 6);
+  return {group, (int)threadIdx.x - group * threads, threads};
+}
+
+// Sums of N values per thread over the row group, in every thread. A scratch
 // array may be used again two calls later (in between, every wave has passed
 // another call's barrier).
 template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float (*scratch)[N]) {
-  const int waves = (int)blockDim.x >> 6;
+__device__ __forceinline__ void group_sums(const Place& at, float (&v)[N], float (*scratch)[N]) {
+  const int waves = at.threads >> 6, first = at.group * waves;
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_all_sum(v[i]);
   if (waves == 1) return;
@@ -89,7 +100,7 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float (*scratch)[N]) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.0f;
-  for (int w = 0; w < waves; ++w)
+  for (int w = first; w < first + waves; ++w)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += scratch[w][i];
 }
@@ -110,23 +121,23 @@ struct Columns {
   float w[KEEP ? CH : 1][8];
   const float* p;
   float absent;
-  __device__ __forceinline__ void init(const float* from, float if_absent, int nchunk) {
+  __device__ __forceinline__ void init(const Place& at, const float* from, float if_absent, int nchunk) {
     p = from;
     absent = if_absent;
     if constexpr (KEEP) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int ch = threadIdx.x + c * blockDim.x;
+        const int ch = at.tid + c * at.threads;
         load_weights8(ch < nchunk ? p : nullptr, ch * 8, absent, w[c]);
       }
     }
   }
-  __device__ __forceinline__ void get(int c, float (&o)[8]) const {
+  __device__ __forceinline__ void get(const Place& at, int c, float (&o)[8]) const {
     if constexpr (KEEP) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[i] = w[c][i];
     } else {
-      load_weights8(p, (int)(threadIdx.x + c * blockDim.x) * 8, absent, o);
+      load_weights8(p, (at.tid + c * at.threads) * 8, absent, o);
     }
   }
 };
@@ -135,10 +146,10 @@ template <typename X, typename R, int CH>
 struct NormRow {  // a row's inputs as loaded
   Vec8<X> x[CH];
   Vec8<R> r[CH];
-  __device__ __forceinline__ void load(const X* px, const R* pr, size_t row, int nchunk) {
+  __device__ __forceinline__ void load(const Place& at, const X* px, const R* pr, size_t row, int nchunk) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
+      const int ch = at.tid + c * at.threads;
       if (ch < nchunk) {
         x[c].load(px + row + ch * 8);
         if (pr) r[c].load(pr + row + ch * 8);
@@ -156,6 +167,7 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
   __shared__ float scratch[4][kNormMaxWaves][1];
   __shared__ uint4 lut[QUANT ? kLutWords / 4 : 1];
   const int nchunk = a.H / 8;
+  const Place at = {0, (int)threadIdx.x, (int)blockDim.x};
   float gs = 0.0f;
   if constexpr (QUANT) {
     gs = gs_in[0];
@@ -163,21 +175,21 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
     __syncthreads();
   }
   Columns<CH, KEEP> w_pre, w_post, gate;
-  w_pre.init(a.w_pre, 1.0f, nchunk);
-  w_post.init(a.w_post, 1.0f, nchunk);
-  gate.init(a.gate_tokens ? nullptr : a.gate, 1.0f, nchunk);
+  w_pre.init(at, a.w_pre, 1.0f, nchunk);
+  w_post.init(at, a.w_post, 1.0f, nchunk);
+  gate.init(at, a.gate_tokens ? nullptr : a.gate, 1.0f, nchunk);
   const float inv_h = 1.0f / (float)a.H;
   NormRow<X, R, CH> in;
-  in.load(x, residual, (size_t)blockIdx.x * a.H, nchunk);
+  in.load(at, x, residual, (size_t)blockIdx.x * a.H, nchunk);
   int parity = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
     const size_t row = (size_t)t * a.H;
     const NormRow<X, R, CH> now = in;
-    if (t + gridDim.x < a.T) in.load(x, residual, row + (size_t)gridDim.x * a.H, nchunk);
+    if (t + gridDim.x < a.T) in.load(at, x, residual, row + (size_t)gridDim.x * a.H, nchunk);
     float f[CH][8], s[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
+      const int ch = at.tid + c * at.threads;
       if (ch < nchunk) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -188,17 +200,17 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
     }
     float sig = a.scale * ((a.gate && a.gate_tokens) ? a.gate[t] : 1.0f);
     if (a.w_post) {
-      block_sums(s, scratch[parity]);
+      group_sums(at, s, scratch[parity]);
       sig *= rsqrtf(s[0] * inv_h + a.eps);
     }
     s[0] = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
+      const int ch = at.tid + c * at.threads;
       if (ch < nchunk) {
         float w[8], g[8];
-        w_post.get(c, w);
-        gate.get(c, g);
+        w_post.get(at, c, w);
+        gate.get(at, c, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           f[c][i] = f[c][i] * sig * (w[i] * g[i]);
@@ -210,15 +222,15 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
       }
     }
     if (!a.w_pre) continue;
-    block_sums(s, scratch[parity + 1]);
+    group_sums(at, s, scratch[parity + 1]);
     const float rho = rsqrtf(s[0] * inv_h + a.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
+      const int ch = at.tid + c * at.threads;
       uint4 bits = make_uint4(0, 0, 0, 0);
       if (ch < nchunk) {
         float w[8];
-        w_pre.get(c, w);
+        w_pre.get(at, c, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[c][i] = f[c][i] * rho * w[i];
         bits = store8(y ? y + row + ch * 8 : nullptr, f[c]);
@@ -248,16 +260,19 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
 //   d_x = sig (db' w_post - xn mean(db' w_post xn)),  or db' without w_post
 // Two reductions per row (the second needs the first's result). The column
 // sums d_w_pre, d_w_post, d_gate stay in registers over all rows of the
-// workgroup and leave it once, as a row of partial sums that
-// norm_columns_kernel adds in workgroup order.
+// thread; the workgroup's row groups add theirs in LDS, one after the other,
+// and it leaves one row of partial sums, which norm_columns_kernel adds in
+// workgroup order. (With a workgroup for each row group, twice the partial
+// rows: 2047 x 2888 took 36 us.)
 template <typename X, typename R, int CH>
 struct NormGradRow {
   Vec8<X> x[CH], y[CH];
   Vec8<R> r[CH], d[CH];
-  __device__ __forceinline__ void load(const X* px, const X* py, const R* pr, const R* pd, size_t row, int nchunk) {
+  __device__ __forceinline__ void load(const Place& at, const X* px, const X* py, const R* pr, const R* pd, size_t row,
+                                       int nchunk) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
+      const int ch = at.tid + c * at.threads;
       if (ch < nchunk) {
         x[c].load(px + row + ch * 8);
         if (py) y[c].load(py + row + ch * 8);
@@ -269,13 +284,17 @@ struct NormGradRow {
 };
 
 template <typename X, typename R, int CH>
-__global__ __launch_bounds__(512) void block_norm_backward_kernel(const X* d_y, const R* d_res_out, const X* x,
-                                                                  const R* res_out, NormArgs a, X* d_x, R* d_res,
-                                                                  float* d_gate_tokens, float* partial) {
+__global__ __launch_bounds__(CH == 1 ? 768 : 512) void block_norm_backward_kernel(const X* d_y, const R* d_res_out, const X* x,
+                                                                  const R* res_out, NormArgs a, int row_threads,
+                                                                  X* d_x, R* d_res, float* d_gate_tokens,
+                                                                  float* partial) {
   constexpr bool KEEP = CH <= 2;
+  extern __shared__ float columns[];  // [3][H], with more than one row group
   __shared__ float scratch_a[2][kNormMaxWaves][3];
   __shared__ float scratch_b[2][kNormMaxWaves][2];
   const int nchunk = a.H / 8;
+  const Place at = place_of(row_threads);
+  const int groups = (int)blockDim.x / row_threads, step = (int)gridDim.x * groups;
   const float inv_h = 1.0f / (float)a.H;
   float c_pre[CH][8], c_post[CH][8], c_gate[CH][8];
 #pragma unroll
@@ -283,25 +302,30 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(const X* d_y, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) c_pre[c][i] = c_post[c][i] = c_gate[c][i] = 0.0f;
   Columns<CH, KEEP> k_pre, k_post, k_gate;
-  k_pre.init(a.w_pre, 0.0f, nchunk);
-  k_post.init(a.w_post, 1.0f, nchunk);
-  k_gate.init(a.gate_tokens ? nullptr : a.gate, 1.0f, nchunk);
+  k_pre.init(at, a.w_pre, 0.0f, nchunk);
+  k_post.init(at, a.w_post, 1.0f, nchunk);
+  k_gate.init(at, a.gate_tokens ? nullptr : a.gate, 1.0f, nchunk);
   const X* py = a.w_pre ? d_y : nullptr;
   NormGradRow<X, R, CH> in;
-  in.load(x, py, res_out, d_res_out, (size_t)blockIdx.x * a.H, nchunk);
+  // all row groups make the same number of turns (they share the barriers); a
+  // group without a row of its own repeats the last one and keeps nothing
+  const int64_t first = (int64_t)blockIdx.x * groups;
+  in.load(at, x, py, res_out, d_res_out, (size_t)min(first + at.group, (int64_t)a.T - 1) * a.H, nchunk);
   int parity = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
+  for (int64_t t0 = first; t0 < a.T; t0 += step, parity ^= 1) {
+    const bool mine = t0 + at.group < a.T;
+    const int64_t t = mine ? t0 + at.group : a.T - 1, next = min(t0 + step + at.group, (int64_t)a.T - 1);
     const size_t row = (size_t)t * a.H;
     const NormGradRow<X, R, CH> now = in;
-    if (KEEP && t + gridDim.x < a.T) in.load(x, py, res_out, d_res_out, row + (size_t)gridDim.x * a.H, nchunk);
+    if (KEEP && t0 + step < a.T) in.load(at, x, py, res_out, d_res_out, (size_t)next * a.H, nchunk);
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
+      const int ch = at.tid + c * at.threads;
       if (ch < nchunk) {
         if (a.w_pre) {
           float w[8];
-          k_pre.get(c, w);
+          k_pre.get(at, c, w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             s[0] += now.r[c].get(i) * now.r[c].get(i);
@@ -312,7 +336,7 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(const X* d_y, 
         for (int i = 0; i < 8; ++i) s[2] += now.x[c].get(i) * now.x[c].get(i);
       }
     }
-    block_sums(s, scratch_a[parity]);
+    group_sums(at, s, scratch_a[parity]);
     const float rho = rsqrtf(s[0] * inv_h + a.eps);
     const float mean = s[1] * rho * inv_h;  // of dn rn
     const float sig = a.w_post ? rsqrtf(s[2] * inv_h + a.eps) : 1.0f;
@@ -321,12 +345,12 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(const X* d_y, 
     float dxn[CH][8];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
-      if (ch < nchunk) {
+      const int ch = at.tid + c * at.threads;
+      if (ch < nchunk && mine) {
         float dr[8], w_pre[8], w_post[8], gate[8];
-        k_pre.get(c, w_pre);
-        k_post.get(c, w_post);
-        k_gate.get(c, gate);
+        k_pre.get(at, c, w_pre);
+        k_post.get(at, c, w_post);
+        k_gate.get(at, c, gate);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           dr[i] = d_res_out ? now.d[c].get(i) : 0.0f;
@@ -348,13 +372,13 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(const X* d_y, 
         store8(d_res + row + ch * 8, dr);
       }
     }
-    if (a.w_post || d_gate_tokens) block_sums(u, scratch_b[parity]);
-    if (d_gate_tokens && threadIdx.x == 0) d_gate_tokens[t] = u[1];
+    if (a.w_post || d_gate_tokens) group_sums(at, u, scratch_b[parity]);
+    if (d_gate_tokens && at.tid == 0 && mine) d_gate_tokens[t] = u[1];
     const float mx = a.w_post ? u[0] * inv_h : 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int ch = threadIdx.x + c * blockDim.x;
-      if (ch < nchunk) {
+      const int ch = at.tid + c * at.threads;
+      if (ch < nchunk && mine) {
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -362,18 +386,33 @@ __global__ __launch_bounds__(512) void block_norm_backward_kernel(const X* d_y, 
         store8(d_x + row + ch * 8, o);
       }
     }
-    if (!KEEP && t + gridDim.x < a.T) in.load(x, py, res_out, d_res_out, row + (size_t)gridDim.x * a.H, nchunk);
+    if (!KEEP && t0 + step < a.T) in.load(at, x, py, res_out, d_res_out, (size_t)next * a.H, nchunk);
   }
-  // partial sums of this workgroup: [workgroup][3][H]
+  for (int g = 0; g < groups; ++g) {
+    const bool last = g + 1 == groups;
+    if (at.group == g) {
+      // the last group writes the workgroup's partial sums: [workgroup][3][H]
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int ch = threadIdx.x + c * blockDim.x;
-    if (ch < nchunk) {
-      float* p = partial + (size_t)blockIdx.x * 3 * a.H + ch * 8;
-      store8(p, c_pre[c]);
-      store8(p + a.H, c_post[c]);
-      store8(p + 2 * a.H, c_gate[c]);
+      for (int c = 0; c < CH; ++c) {
+        const int ch = at.tid + c * at.threads;
+        if (ch < nchunk) {
+          float* out = partial + (size_t)blockIdx.x * 3 * a.H + ch * 8;
+          float(*v[3])[8] = {&c_pre[c], &c_post[c], &c_gate[c]};
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            float* sum = columns + (size_t)i * a.H + ch * 8;
+            if (g > 0) {
+              Vec8<float> was;
+              was.load(sum);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) (*v[i])[e] += was.get(e);
+            }
+            store8(last ? out + (size_t)i * a.H : sum, *v[i]);
+          }
+        }
+      }
     }
+    if (!last) __syncthreads();
   }
 }
 
@@ -485,14 +524,28 @@ extern "C" int moe_block_norm(const void* x, int32_t x_dtype, const void* residu
   });
 }
 
-static unsigned norm_backward_grid(int32_t T, int32_t H) {
+// One workgroup per CU, of as many row groups as give it 12 waves (8 with two
+// chunks per thread, whose registers allow no more), fewer where the rows run
+// out.
+struct NormGradShape {
+  unsigned row_threads, groups, grid;
+};
+static NormGradShape norm_grad_shape(int32_t T, int32_t H) {
   const int ch = H <= 4096 ? 1 : H <= 8192 ? 2 : 4;
-  return norm_grid(T < 1 ? 1 : T, norm_threads(H, ch), 12);
+  NormGradShape s;
+  s.row_threads = norm_threads(H, ch);
+  s.groups = (ch == 1 ? 768 : 512) / s.row_threads;
+  const unsigned rows = T < 1 ? 1 : (unsigned)T, want = (rows + kNormCus - 1) / kNormCus;
+  if (s.groups > want) s.groups = want;
+  if (s.groups < 1) s.groups = 1;
+  const unsigned all = (rows + s.groups - 1) / s.groups;
+  s.grid = all < (unsigned)kNormCus ? all : kNormCus;
+  return s;
 }
 
 extern "C" size_t moe_block_norm_backward_ws_bytes(int32_t T, int32_t H) {
   if (T < 0 || H <= 0 || H % 8 != 0 || H > kNormMaxH) return 0;
-  return (size_t)norm_backward_grid(T, H) * 3 * H * sizeof(float);
+  return (size_t)norm_grad_shape(T, H).grid * 3 * H * sizeof(float);
 }
 
 extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_out, const void* x, int32_t x_dtype,
@@ -515,17 +568,19 @@ extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_o
   if (ws_bytes < moe_block_norm_backward_ws_bytes(T, H)) return NVFP4_ERR_WORKSPACE;
   const bool per_token = gate_mode == MOE_GATE_TOKEN;
   const NormArgs a = {T, H, w_pre, w_post, gate_mode == MOE_GATE_NONE ? nullptr : gate, per_token, scale, eps};
-  const unsigned grid = norm_backward_grid(T, H);
+  const NormGradShape shape = norm_grad_shape(T, H);
   if (T > 0) {
     const int r = norm_by_types(x_dtype, res_dtype, [&](auto xt, auto rt) -> int {
       using X = decltype(xt);
       using R = decltype(rt);
       auto go = [&](auto ch) -> int {
         constexpr int CH = decltype(ch)::value;
-        hipLaunchKernelGGL((block_norm_backward_kernel<X, R, CH>), dim3(grid), dim3(norm_threads(H, CH)), 0,
-                           (hipStream_t)stream, reinterpret_cast<const X*>(d_y),
-                           reinterpret_cast<const R*>(d_residual_out), reinterpret_cast<const X*>(x),
-                           reinterpret_cast<const R*>(residual_out), a, reinterpret_cast<X*>(d_x),
+        const size_t lds = shape.groups > 1 ? (size_t)3 * H * sizeof(float) : 0;
+        hipLaunchKernelGGL((block_norm_backward_kernel<X, R, CH>), dim3(shape.grid),
+                           dim3(shape.row_threads * shape.groups), lds, (hipStream_t)stream,
+                           reinterpret_cast<const X*>(d_y), reinterpret_cast<const R*>(d_residual_out),
+                           reinterpret_cast<const X*>(x), reinterpret_cast<const R*>(residual_out), a,
+                           (int)shape.row_threads, reinterpret_cast<X*>(d_x),
                            reinterpret_cast<R*>(d_residual), per_token ? d_gate : nullptr,
                            reinterpret_cast<float*>(ws));
         NVFP4_CHECK_LAUNCH();
@@ -538,7 +593,7 @@ extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_o
   // T = 0: the sums over no rows, zeros
   float* gate_cols = gate_mode == MOE_GATE_CHANNEL ? d_gate : nullptr;
   hipLaunchKernelGGL(norm_columns_kernel, dim3((H + 63) / 64, 3), dim3(64 * kColumnWaves), 0, (hipStream_t)stream,
-                     reinterpret_cast<const float*>(ws), T > 0 ? (int)grid : 0, H, w_pre ? d_w_pre : nullptr,
+                     reinterpret_cast<const float*>(ws), T > 0 ? (int)shape.grid : 0, H, w_pre ? d_w_pre : nullptr,
                      w_post ? d_w_post : nullptr, gate_cols);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
