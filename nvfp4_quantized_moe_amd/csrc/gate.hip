@@ -43,9 +43,11 @@ __device__ __forceinline__ void load_row(const L* logits, size_t row, int E, flo
   const L* p = logits + row;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) x[v] = load_logit(p, (uint32_t)min(v * 64 + lane, E - 1));
+  if (E < VPT * 64) {
 #pragma unroll
-  for (int v = 0; v < VPT; ++v)
-    if (v * 64 + lane >= E) x[v] = -kInf;
+    for (int v = 0; v < VPT; ++v)
+      if (v * 64 + lane >= E) x[v] = -kInf;
+  }
 }
 
 // Scores that depend on one logit alone (x = -inf gives 0).
@@ -83,18 +85,22 @@ __device__ __forceinline__ float fast_log1p(float t) {  // t >= 0
   return t < 0x1p-6f ? t * (1.0f - t * (0.5f - t * (1.0f / 3.0f - t * 0.25f)))
                      : __builtin_amdgcn_logf(1.0f + t) * kLn2;
 }
-// score and slope of a logit above -inf
+// score and (with SLOPE) slope; both 0 at x = -inf
 template <bool SLOPE>
-__device__ __forceinline__ float fast_score(float x, int score, float* slope) {
+__device__ __forceinline__ float fast_sigmoid(float x, float* slope) {
   const float e = fast_exp(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
-  const float sig = x < 0.0f ? e * r : r;
-  if (score == MOE_SCORE_SIGMOID) {
-    if (SLOPE) *slope = e * r * r;
-    return sig;
-  }
+  if (SLOPE) *slope = e * r * r;
+  return x < 0.0f ? e * r : r;
+}
+template <bool SLOPE>
+__device__ __forceinline__ float fast_sqrt_softplus(float x, float* slope) {
+  const float e = fast_exp(-fabsf(x));
   const bool low = x < -20.0f;
   const float s = low ? fast_exp(0.5f * x) : __builtin_amdgcn_sqrtf(fmaxf(x, 0.0f) + fast_log1p(e));
-  if (SLOPE) *slope = low ? 0.5f * s : 0.5f * sig * __builtin_amdgcn_rcpf(s);
+  if (SLOPE) {
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    *slope = low ? 0.5f * s : 0.5f * (x < 0.0f ? e * r : r) * __builtin_amdgcn_rcpf(s);
+  }
   return s;
 }
 
@@ -110,7 +116,7 @@ __device__ __forceinline__ float near_exp(float x) {
 }
 // Score for a key (see gate_topk_kernel for what float keys may be off by).
 __device__ __forceinline__ float key_score(float x, int score) {
-  return score == MOE_SCORE_SIGMOID ? __builtin_amdgcn_rcpf(1.0f + near_exp(-x)) : fast_score<false>(x, score, nullptr);
+  return score == MOE_SCORE_SIGMOID ? __builtin_amdgcn_rcpf(1.0f + near_exp(-x)) : fast_sqrt_softplus<false>(x, nullptr);
 }
 __device__ __forceinline__ double key_score(double x, int score) { return pointwise_score(x, score); }
 __device__ __forceinline__ float key_exp(float x) { return near_exp(x); }
@@ -157,8 +163,13 @@ __device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bi
 #pragma unroll
     for (int v = 0; v < VPT; ++v) key[v] *= sum;
   } else {
+    if (g.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) key[v] = key_score((F)x[v], g.score);
+      for (int v = 0; v < VPT; ++v) key[v] = key_score((F)x[v], MOE_SCORE_SIGMOID);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) key[v] = key_score((F)x[v], MOE_SCORE_SQRT_SOFTPLUS);
+    }
   }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -517,12 +528,15 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
     return true;
   }
   float sum = 0.0f;
+  if (score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    q[v] = fast_score<SLOPE>(x[v], score, &slope[v]);
-    if (!(x[v] > -kInf)) q[v] = slope[v] = 0.0f;
-    sum += q[v];
+    for (int v = 0; v < VPT; ++v) q[v] = fast_sigmoid<SLOPE>(x[v], &slope[v]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) q[v] = fast_sqrt_softplus<SLOPE>(x[v], &slope[v]);
   }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) sum += q[v];
   sum = wave_all_sum(sum);
   r->sum = sum;
   r->inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;

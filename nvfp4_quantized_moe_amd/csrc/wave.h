@@ -12,14 +12,16 @@ constexpr int kDppXor2 = 0x4E;         // quad_perm [2, 3, 0, 1]
 constexpr int kDppHalfMirror = 0x141;  // joins the quads of 8 lanes, once each quad holds one value
 constexpr int kDppMirror = 0x140;      // joins the halves of 16 lanes, once each half holds one value
 
-template <int CTRL>
-__device__ __forceinline__ float dpp_f32(float v) {
-  const int i = __builtin_bit_cast(int, v);
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
-}
+// (Every lane of these patterns has a source, so the value for lanes without one
+// is never taken; as the constant 0 it lets the compiler fold the move into
+// the operation that uses it.)
 template <int CTRL>
 __device__ __forceinline__ int dpp_i32(int v) {
-  return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __builtin_bit_cast(float, dpp_i32<CTRL>(__builtin_bit_cast(int, v)));
 }
 
 // The two operands of the step across rows of 16 (or halves of 32): the value
