@@ -783,6 +783,10 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
 #pragma unroll
   for (int v = 0; v < VPT; ++v) dx[v] = 0.0f;
   if (!(a.mask && a.mask[t] == 0)) {
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    bool row_softmax = a.d_w && softmax && !a.renormalize;
+    // (the row's loads first: the search below is a chain of its own)
+    if (a.d_loss || row_softmax) load_row(logits, row, a.E, x);  // else only the chosen logits matter
     // sequence of the token; -1: it lies in none and the losses do not see it
     int seq = a.d_loss ? 0 : -1;
     if (a.d_loss && a.cu) {
@@ -794,12 +798,15 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
       }
       seq = lo - 1 < a.B ? lo - 1 : -1;
     }
-    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
-    bool in_loss = seq >= 0, row_softmax = a.d_w && softmax && !a.renormalize;
+    bool in_loss = seq >= 0;
     float q[VPT], p[VPT], slope[VPT];
     RowSums r = {1.0f, 1.0f, 0.0f};
-    if (in_loss || row_softmax) {  // else only the chosen logits matter
-      load_row(logits, row, a.E, x);
+    int32_t chosen[VPT];
+    if (in_loss) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) chosen[v] = a.counts[(size_t)seq * a.E + min(v * 64 + lane, a.E - 1)];
+    }
+    if (in_loss || row_softmax) {
       if (!row_scores<true>(x, a.score, q, p, slope, &r)) in_loss = row_softmax = false;  // not one choice either
     }
     float inner = 0.0f;  // softmax: sum over the row of (gradient of p) p
@@ -856,9 +863,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
       float dot = 0.0f;
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        const int e = v * 64 + lane;
-        dq[v] = e < a.E ? f0 * (float)a.counts[(size_t)seq * a.E + e] : 0.0f;
-        dot += dq[v] * q[v];
+        dq[v] = f0 * (float)chosen[v];
+        dot += dq[v] * q[v];  // q is 0 past E
       }
       dot = wave_all_sum(dot);
       zc = 2.0f * a.d_loss[1] * r.lse / (float)a.tokens[a.B];
