@@ -11,6 +11,11 @@
 #include "internal.h"
 #include "wave.h"
 
+// Every rounding as it is written (the fmas below are explicit): a token's
+// outputs are the same whichever of the kernels computes them, so they do not
+// depend on how many other tokens the call has.
+#pragma clang fp contract(off)
+
 namespace nvfp4 {
 
 typedef int int4v __attribute__((ext_vector_type(4)));
@@ -512,33 +517,29 @@ __global__ __launch_bounds__(256) void int8_join_rows_kernel(Int8Args g, int8_t*
   }
 }
 
-// Few tokens (up to 16 MT per workgroup): the weights' bytes count, and every
+// Up to 16 tokens: the weights' bytes count, and every
 // wave of the chip has to read some. A workgroup takes 16 weight rows (SILU: 8
 // gate and their 8 up rows) and its eight waves split K; nothing is staged, a
 // wave streams both operands' MFMA 16x16x64 fragments from memory (64
 // contiguous bytes of each of 16 rows per load) with the next group in
 // flight, and the eight partial sums, exact integers, meet in LDS.
 constexpr int kSkinnyWaves = 8;
-template <int MT, bool SILU>
+template <bool SILU>
 __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8Args g) {
-  constexpr int U = MT == 4 ? 2 : 4;  // 64-byte steps of a group
-  __shared__ int sums[kSkinnyWaves][MT][16][17];  // [wave][subtile][token][weight row], padded against conflicts
+  constexpr int U = 4;                        // 64-byte steps of a group
+  __shared__ int sums[kSkinnyWaves][16][17];  // [wave][token][weight row], padded against conflicts
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, kq = (lane >> 4) * 16;
-  const int m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * (SILU ? 8 : 16), half = g.N / 2;
+  const int n0 = blockIdx.x * (SILU ? 8 : 16), half = g.N / 2;
   const int row = SILU ? (i < 8 ? n0 + i : half + n0 + i - 8) : min(n0 + i, g.N - 1);
   const int steps = (g.K + 63) / 64;
   const int per = ((steps + kSkinnyWaves - 1) / kSkinnyWaves + 1) & ~1;  // whole 128-byte lines per wave
   const int s0 = wave * per, s1 = min(s0 + per, steps);
   const int8_t* pb = g.b + (size_t)row * g.K;
-  const int8_t* pa[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) pa[j] = g.a + (size_t)min(m0 + 16 * j + i, g.M - 1) * g.K;
-  int4v acc[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) acc[j] = int4v{0, 0, 0, 0};
-  int4v fa[2][U][MT], fb[2][U];
-  auto load = [&](int s, int4v (&a)[U][MT], int4v (&b)[U]) {
+  const int8_t* pa = g.a + (size_t)min(i, g.M - 1) * g.K;
+  int4v acc = int4v{0, 0, 0, 0};
+  int4v fa[2][U], fb[2][U];
+  auto load = [&](int s, int4v (&a)[U], int4v (&b)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // past this wave's share or the row: some bytes of the row again, and
@@ -546,15 +547,12 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8A
       const int k = (s + u) * 64 + kq, at = min(k, g.K - 16);
       const int4v w = *reinterpret_cast<const int4v*>(pb + at);
       b[u] = s + u < s1 && k < g.K ? w : int4v{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < MT; ++j) a[u][j] = *reinterpret_cast<const int4v*>(pa[j] + at);
+      a[u] = *reinterpret_cast<const int4v*>(pa + at);
     }
   };
-  auto multiply = [&](const int4v (&a)[U][MT], const int4v (&b)[U]) {
+  auto multiply = [&](const int4v (&a)[U], const int4v (&b)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[u], a[u][j], acc[j], 0, 0, 0);
+    for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[u], a[u], acc, 0, 0, 0);
   };
   if (s0 < s1) load(s0, fa[0], fb[0]);
   for (int s = s0; s < s1; s += 2 * U) {
@@ -564,29 +562,25 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8A
     if (s + 2 * U < s1) load(s + 2 * U, fa[0], fb[0]);
     multiply(fa[1], fb[1]);
   }
-  // lane: token i of a subtile, weight rows 4 (lane / 16) + 0..3
+  // lane: token i, weight rows 4 (lane / 16) + 0..3
 #pragma unroll
-  for (int j = 0; j < MT; ++j)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) sums[wave][j][i][4 * (lane >> 4) + v] = acc[j][v];
+  for (int v = 0; v < 4; ++v) sums[wave][i][4 * (lane >> 4) + v] = acc[v];
   __syncthreads();
   constexpr int COLS = SILU ? 8 : 16;
-  for (int at = threadIdx.x; at < MT * 16 * COLS; at += 64 * kSkinnyWaves) {
-    const int c = at % COLS, tok = at / COLS, m = m0 + tok, n = n0 + c;
-    if (m >= g.M || n >= g.n_out) continue;
-    int s = 0, u = 0;
+  const int c = threadIdx.x % COLS, m = threadIdx.x / COLS, n = n0 + c;
+  if (m >= g.M || n >= g.n_out) return;  // g.M <= 16
+  int s = 0, u = 0;
 #pragma unroll
-    for (int w = 0; w < kSkinnyWaves; ++w) {
-      s += sums[w][tok >> 4][tok & 15][c];
-      if (SILU) u += sums[w][tok >> 4][tok & 15][c + 8];
-    }
-    const float as = g.a_s[m];
-    float o = (float)s * (as * g.b_s[n]);
-    if (SILU) o = silu_mul(o, (float)u * (as * g.b_s[half + n]));
-    const size_t d = (size_t)m * g.n_out + n;
-    if (g.add) o += bf16_to_f32(g.add[d]);
-    g.d[d] = (uint16_t)f32_to_bf16(o);
+  for (int w = 0; w < kSkinnyWaves; ++w) {
+    s += sums[w][m][c];
+    if (SILU) u += sums[w][m][c + 8];
   }
+  const float as = g.a_s[m];
+  float o = (float)s * (as * g.b_s[n]);
+  if (SILU) o = silu_mul(o, (float)u * (as * g.b_s[half + n]));
+  const size_t d = (size_t)m * g.n_out + n;
+  if (g.add) o += bf16_to_f32(g.add[d]);
+  g.d[d] = (uint16_t)f32_to_bf16(o);
 }
 
 }  // namespace nvfp4
@@ -633,11 +627,10 @@ static int launch_int8_tile(const Int8Args& g, hipStream_t stream) {
   return NVFP4_OK;
 }
 
-template <int MT, bool SILU>
+template <bool SILU>
 static int launch_int8_skinny(const Int8Args& g, hipStream_t stream) {
   const int cols = SILU ? 8 : 16;
-  hipLaunchKernelGGL((int8_skinny_kernel<MT, SILU>), dim3((g.n_out + cols - 1) / cols, (g.M + 16 * MT - 1) / (16 * MT)),
-                     dim3(64 * kSkinnyWaves), 0, stream, g);
+  hipLaunchKernelGGL(int8_skinny_kernel<SILU>, dim3((g.n_out + cols - 1) / cols), dim3(64 * kSkinnyWaves), 0, stream, g);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
 }
@@ -675,7 +668,7 @@ static int launch_int8(const Int8Args& g, hipStream_t stream) {
     NVFP4_CHECK_LAUNCH();
     return NVFP4_OK;
   }
-  if (g.M <= kSkinnyM) return launch_int8_skinny<1, SILU>(g, stream);
+  if (g.M <= kSkinnyM) return launch_int8_skinny<SILU>(g, stream);
   // the largest tile that still gives most of the 256 CUs one
   const auto tiles = [&](int bm, int bn) { return (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
   if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, 64, OUT>(g, stream);

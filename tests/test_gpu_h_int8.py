@@ -48,8 +48,8 @@ def test_rows(nv, M, K, kind, dtype):
 
 
 SHAPES = [(1, 8, 16), (1, 7168, 2048), (2, 16, 32), (5, 1000, 1040), (16, 4096, 7168), (17, 264, 7168), (33, 40, 144),
-          (64, 4096, 7168), (63, 7168, 2048), (33, 72, 4112), (100, 1096, 7168), (65, 128, 128), (128, 256, 65536), (333, 1000, 1040), (500, 520, 272),
-          (1030, 2056, 1168), (2048, 2048, 256), (2049, 4104, 400), (4100, 1536, 128)]
+          (64, 4096, 7168), (63, 7168, 2048), (33, 72, 4112), (100, 1096, 7168), (65, 128, 128), (128, 256, 65536),
+          (333, 1000, 1040), (500, 520, 272), (1030, 2056, 1168), (2048, 2048, 256), (2049, 4104, 400), (4100, 1536, 128)]
 
 
 def operands(M, N, K, seed):
@@ -100,7 +100,8 @@ def test_product_silu(nv, M, N, K, with_add):
     assert (np.abs(got - ref) <= tol).all(), float(np.max(np.abs(got - ref) / np.maximum(tol, 1e-30)))
 
 
-@pytest.mark.parametrize("T,H,I", [(1, 7168, 2048), (3, 64, 16), (40, 4112, 2064), (70, 5120, 80), (64, 1040, 528), (200, 512, 256), (1100, 1024, 512)])
+@pytest.mark.parametrize("T,H,I", [(1, 7168, 2048), (3, 64, 16), (40, 4112, 2064), (70, 5120, 80), (64, 1040, 528),
+                                   (200, 512, 256), (1100, 1024, 512)])
 def test_dense_expert_is_its_steps(nv, T, H, I):
     """The forward equals its public steps bit for bit (each checked above), on a dirty workspace."""
     g = torch.Generator(device=DEV).manual_seed(T)
@@ -127,6 +128,25 @@ def test_dense_expert_is_its_steps(nv, T, H, I):
     full = (torch.nn.functional.silu(x.float() @ wg.T) * (x.float() @ wu.T)) @ wd.T + add.float()
     cos = torch.nn.functional.cosine_similarity(full.flatten(), ref.float().flatten(), 0)
     assert cos > 0.999
+
+
+@pytest.mark.parametrize("H,I", [(4352, 2176), (1040, 528)])
+def test_token_by_itself(nv, H, I):
+    """A token's outputs have the same bits whatever else the call holds, though other kernels compute them."""
+    T = 2300
+    g = torch.Generator(device=DEV).manual_seed(H)
+    w = nv.prepare_int8_weights(*(torch.randn(s, device=DEV, generator=g) * 0.03 for s in ((I, H), (I, H), (H, I))))
+    x, add = (torch.randn(T, H, device=DEV, generator=g).bfloat16() for _ in range(2))
+    q, s = nv.int8_quantize_rows(x)
+    add_h = torch.randn(T, I, device=DEV, generator=g).bfloat16()
+    whole = nv.int8_ffn_forward(w, x, add=add)
+    whole_h = nv.int8_gemm(q, s, w.w1_q, w.w1_scale, nv.EPI_SILU_MUL, add=add_h)
+    add_up = torch.randn(T, 2 * I, device=DEV, generator=g).bfloat16()
+    whole_up = nv.int8_gemm(q, s, w.w1_q, w.w1_scale, add=add_up)
+    for n in (1, 16, 17, 130, 500, 1200):
+        assert torch.equal(nv.int8_ffn_forward(w, x[:n], add=add[:n]), whole[:n])
+        assert torch.equal(nv.int8_gemm(q[:n], s[:n], w.w1_q, w.w1_scale, nv.EPI_SILU_MUL, add=add_h[:n]), whole_h[:n])
+        assert torch.equal(nv.int8_gemm(q[:n], s[:n], w.w1_q, w.w1_scale, add=add_up[:n]), whole_up[:n])
 
 
 def test_empty(nv):
