@@ -5,6 +5,7 @@
 // The sum is exact in int32 (K <= 65536: |sum| <= 2^30), so neither the order
 // of K nor its split can change a result; the scales are applied to it in
 // float32 and the output is rounded once.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -517,29 +518,37 @@ __global__ __launch_bounds__(256) void int8_join_rows_kernel(Int8Args g, int8_t*
   }
 }
 
-// Up to 16 tokens: the weights' bytes count, and every
-// wave of the chip has to read some. A workgroup takes 16 weight rows (SILU: 8
-// gate and their 8 up rows) and its eight waves split K; nothing is staged, a
-// wave streams both operands' MFMA 16x16x64 fragments from memory (64
-// contiguous bytes of each of 16 rows per load) with the next group in
-// flight, and the eight partial sums, exact integers, meet in LDS.
+// Few tokens: the weights' bytes count, and every wave of the chip has to read
+// some. A workgroup takes 16 weight rows (SILU: 8 gate and their 8 up rows) and
+// 16 MT tokens; its eight waves split K; nothing is staged, a wave streams both
+// operands' MFMA 16x16x64 fragments from memory (64 contiguous bytes of each of
+// 16 rows per load) with the next group in flight, and the eight partial sums,
+// exact integers, meet in LDS. Groups of two steps, one 128-byte line of each
+// row: with four, 1 x 4096 x 7168 took 10.7 us, not 8.7 (3.4 TB/s; 1 x 16384 x
+// 8192: 29.9, not 26.4: 5.1 TB/s), with one 10.4. What is left at small sizes
+// is the launch (2 us) and the latency of a few dependent loads.
 constexpr int kSkinnyWaves = 8;
-template <bool SILU>
+template <int MT, bool SILU>
 __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8Args g) {
-  constexpr int U = 4;                        // 64-byte steps of a group
-  __shared__ int sums[kSkinnyWaves][16][17];  // [wave][token][weight row], padded against conflicts
+  constexpr int U = 2;                            // 64-byte steps of a group
+  __shared__ int sums[kSkinnyWaves][MT][16][17];  // [wave][subtile][token][weight row], padded against conflicts
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, kq = (lane >> 4) * 16;
-  const int n0 = blockIdx.x * (SILU ? 8 : 16), half = g.N / 2;
+  const int m0 = blockIdx.y * 16 * MT, n0 = blockIdx.x * (SILU ? 8 : 16), half = g.N / 2;
   const int row = SILU ? (i < 8 ? n0 + i : half + n0 + i - 8) : min(n0 + i, g.N - 1);
   const int steps = (g.K + 63) / 64;
   const int per = ((steps + kSkinnyWaves - 1) / kSkinnyWaves + 1) & ~1;  // whole 128-byte lines per wave
   const int s0 = wave * per, s1 = min(s0 + per, steps);
   const int8_t* pb = g.b + (size_t)row * g.K;
-  const int8_t* pa = g.a + (size_t)min(i, g.M - 1) * g.K;
-  int4v acc = int4v{0, 0, 0, 0};
-  int4v fa[2][U], fb[2][U];
-  auto load = [&](int s, int4v (&a)[U], int4v (&b)[U]) {
+  const int8_t* pa[MT];
+  int4v acc[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    pa[j] = g.a + (size_t)min(m0 + 16 * j + i, g.M - 1) * g.K;
+    acc[j] = int4v{0, 0, 0, 0};
+  }
+  int4v fa[2][U][MT], fb[2][U];
+  auto load = [&](int s, int4v (&a)[U][MT], int4v (&b)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // past this wave's share or the row: some bytes of the row again, and
@@ -547,12 +556,15 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8A
       const int k = (s + u) * 64 + kq, at = min(k, g.K - 16);
       const int4v w = *reinterpret_cast<const int4v*>(pb + at);
       b[u] = s + u < s1 && k < g.K ? w : int4v{0, 0, 0, 0};
-      a[u] = *reinterpret_cast<const int4v*>(pa + at);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) a[u][j] = *reinterpret_cast<const int4v*>(pa[j] + at);
     }
   };
-  auto multiply = [&](const int4v (&a)[U], const int4v (&b)[U]) {
+  auto multiply = [&](const int4v (&a)[U][MT], const int4v (&b)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[u], a[u], acc, 0, 0, 0);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[u], a[u][j], acc[j], 0, 0, 0);
   };
   if (s0 < s1) load(s0, fa[0], fb[0]);
   for (int s = s0; s < s1; s += 2 * U) {
@@ -562,18 +574,21 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8A
     if (s + 2 * U < s1) load(s + 2 * U, fa[0], fb[0]);
     multiply(fa[1], fb[1]);
   }
-  // lane: token i, weight rows 4 (lane / 16) + 0..3
+  // lane: token i of a subtile, weight rows 4 (lane / 16) + 0..3
 #pragma unroll
-  for (int v = 0; v < 4; ++v) sums[wave][i][4 * (lane >> 4) + v] = acc[v];
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sums[wave][j][i][4 * (lane >> 4) + v] = acc[j][v];
   __syncthreads();
   constexpr int COLS = SILU ? 8 : 16;
-  const int c = threadIdx.x % COLS, m = threadIdx.x / COLS, n = n0 + c;
-  if (m >= g.M || n >= g.n_out) return;  // g.M <= 16
+  static_assert(MT * 16 * COLS <= 64 * kSkinnyWaves, "an output per thread");
+  const int c = threadIdx.x % COLS, tok = threadIdx.x / COLS, m = m0 + tok, n = n0 + c;
+  if (tok >= 16 * MT || m >= g.M || n >= g.n_out) return;
   int s = 0, u = 0;
 #pragma unroll
   for (int w = 0; w < kSkinnyWaves; ++w) {
-    s += sums[w][m][c];
-    if (SILU) u += sums[w][m][c + 8];
+    s += sums[w][tok >> 4][tok & 15][c];
+    if (SILU) u += sums[w][tok >> 4][tok & 15][c + 8];
   }
   const float as = g.a_s[m];
   float o = (float)s * (as * g.b_s[n]);
@@ -604,7 +619,7 @@ extern "C" int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int
     return NVFP4_OK;
   };
   constexpr std::integral_constant<int, 2> two;
-  constexpr std::integral_constant<int, 8> eight;  // rows past 2048 chunks
+  constexpr std::integral_constant<int, 8> eight;  // rows of more than 1024 threads' two chunks
   if (x_dtype == NVFP4_DT_BF16) return K <= 16384 ? go(uint16_t(), two) : go(uint16_t(), eight);
   return K <= 16384 ? go(float(), two) : go(float(), eight);
 }
@@ -627,35 +642,41 @@ static int launch_int8_tile(const Int8Args& g, hipStream_t stream) {
   return NVFP4_OK;
 }
 
-template <bool SILU>
+template <int MT, bool SILU>
 static int launch_int8_skinny(const Int8Args& g, hipStream_t stream) {
-  const int cols = SILU ? 8 : 16;
-  hipLaunchKernelGGL(int8_skinny_kernel<SILU>, dim3((g.n_out + cols - 1) / cols), dim3(64 * kSkinnyWaves), 0, stream, g);
+  const dim3 grid((g.N + 15) / 16, (g.M + 16 * MT - 1) / (16 * MT));
+  hipLaunchKernelGGL((int8_skinny_kernel<MT, SILU>), grid, dim3(64 * kSkinnyWaves), 0, stream, g);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
 }
 
-// Parts of K for a product: 1, or as many as bring 64 x 128 tiles to about one
-// per CU, each of at least kMinSplit bytes.
-constexpr int kSkinnyM = 16, kMinSplit = 512;
-static int int8_splits(int64_t M, int64_t N, int64_t K) {
-  if (M <= kSkinnyM) return 1;
-  const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
-  int64_t s = 256 / tiles;
-  if (s > K / kMinSplit) s = K / kMinSplit;
-  return s < 2 || K < 4096 ? 1 : (int)s;
+// Which kernel a product takes (us, weights from memory, the other side in
+// brackets). The few-token kernel up to 16 tokens (16 x 4096 x 7168: 9.9 [tiles
+// 14.9], 16 x 16384 x 8192: 36 [36]), and where its workgroups of 32 tokens by
+// 16 rows do not outnumber the CUs (24 x 4096 x 7168: 11.9 [15.2]; 128 x 1024 x
+// 1040: 3.5 [5.5]; with 448 of them, 32 x 7168 x 2048, it loses: 8.7 [7.2]),
+// unless a long K meets too few of them (128 x 64 x 7168: 11.5 [9.3]).
+constexpr int kSkinnyM = 16, kLongK = 4096;
+static bool int8_few(int64_t M, int64_t N, int64_t K) {
+  return M <= kSkinnyM || (((M + 31) / 32) * ((N + 15) / 16) <= 256 && (K < kLongK || N >= 4096));
 }
+// Parts of K for tiles: as many as bring 64 x 128 tiles to about one per CU,
+// each of at least 512 bytes (33 x 4096 x 7168: 15.6 [undivided 27], 192: 21.5
+// [29]), or one: with a short K the join costs more than it saves (32 x 7168 x
+// 2048: 7.3 [divided 10.4]).
+static int int8_parts(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
+  const int64_t s = std::min<int64_t>(256 / tiles, K / 512);
+  return s < 2 || K < kLongK ? 1 : (int)s;
+}
+static int int8_splits(int64_t M, int64_t N, int64_t K) { return int8_few(M, N, K) ? 1 : int8_parts(M, N, K); }
 static Int8Args int8_args(const int8_t* a_q, const float* a_s, const int8_t* b_q, const float* b_s, int M, int N, int K,
-                          bool silu, const void* add, void* d, void* ws) {
-  const int want = int8_splits(M, N, K);
+                          int want, bool silu, const void* add, void* d, void* ws) {
   const int per = ((K + want - 1) / want + 127) / 128 * 128;
   return {a_q, a_s, b_q, b_s, reinterpret_cast<const uint16_t*>(add), reinterpret_cast<uint16_t*>(d), M, N, K,
           silu ? N / 2 : N, (K + per - 1) / per, per, reinterpret_cast<int32_t*>(ws)};
 }
-static size_t int8_part_bytes(int64_t M, int64_t N, int64_t K) {
-  const int s = int8_splits(M, N, K);
-  return s > 1 ? (size_t)s * M * N * 4 : 0;
-}
+static size_t int8_part_bytes(int64_t M, int64_t N, int splits) { return splits > 1 ? (size_t)splits * M * N * 4 : 0; }
 
 template <bool SILU>
 static int launch_int8(const Int8Args& g, hipStream_t stream) {
@@ -668,8 +689,12 @@ static int launch_int8(const Int8Args& g, hipStream_t stream) {
     NVFP4_CHECK_LAUNCH();
     return NVFP4_OK;
   }
-  if (g.M <= kSkinnyM) return launch_int8_skinny<SILU>(g, stream);
-  // the largest tile that still gives most of the 256 CUs one
+  if (g.M <= kSkinnyM) return launch_int8_skinny<1, SILU>(g, stream);
+  if (int8_few(g.M, g.N, g.K)) return launch_int8_skinny<2, SILU>(g, stream);
+  // The largest tile that still gives most of the 256 CUs one: 4096 x 4096 x
+  // 7168 takes 115 us by 256 x 256 [161 by 128 x 128], 1024 x 7168 x 2048 takes
+  // 24.6 by 128 x 128 [30.5 by 256, 30.3 by 64], 512 x 4096 x 7168 takes 29 by
+  // 64 x 128 [47 by 128].
   const auto tiles = [&](int bm, int bn) { return (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
   if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, 64, OUT>(g, stream);
   if (tiles(128, 128) >= 192) return launch_int8_tile<128, 128, 2, 2, 64, OUT>(g, stream);
@@ -678,7 +703,7 @@ static int launch_int8(const Int8Args& g, hipStream_t stream) {
 
 extern "C" size_t int8_gemm_ws_bytes(int32_t M, int32_t N, int32_t K) {
   if (int8_gemm_check(M, N, K, NVFP4_EPI_BF16)) return 0;
-  return int8_part_bytes(M, N, K);
+  return int8_part_bytes(M, N, int8_splits(M, N, K));
 }
 
 extern "C" int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int32_t M,
@@ -687,19 +712,25 @@ extern "C" int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* 
   const int st = int8_gemm_check(M, N, K, epilogue);
   if (st) return st;
   if (M == 0) return NVFP4_OK;
-  const size_t need = int8_part_bytes(M, N, K);
+  const int splits = int8_splits(M, N, K);
+  const size_t need = int8_part_bytes(M, N, splits);
   if (!a_q || !a_scale || !b_q || !b_scale || !d_bf16 || (need && !ws)) return NVFP4_ERR_NULL;
   if (!nvfp4_aligned16(a_q) || !nvfp4_aligned16(a_scale) || !nvfp4_aligned16(b_q) || !nvfp4_aligned16(b_scale) ||
       !nvfp4_aligned16(add_bf16) || !nvfp4_aligned16(d_bf16) || !nvfp4_aligned16(ws))
     return NVFP4_ERR_ALIGN;
   if (ws_bytes < need) return NVFP4_ERR_WORKSPACE;
   const bool silu = epilogue == NVFP4_EPI_SILU_MUL;
-  const Int8Args g = int8_args(a_q, a_scale, b_q, b_scale, M, N, K, silu, add_bf16, d_bf16, ws);
+  const Int8Args g = int8_args(a_q, a_scale, b_q, b_scale, M, N, K, splits, silu, add_bf16, d_bf16, ws);
   return silu ? launch_int8<true>(g, (hipStream_t)stream) : launch_int8<false>(g, (hipStream_t)stream);
 }
 
 // ------------------------------------------------------------- dense expert
 
+// Parts of K of the up product. Past 16 tokens the join that a divided K needs
+// quantizes h on the way, which is worth more than the few-token kernel.
+static int int8_up_splits(int64_t T, int64_t hidden, int64_t inter) {
+  return T <= kSkinnyM ? 1 : int8_parts(T, 2 * inter, hidden);
+}
 struct Int8FfnWs {
   size_t x_q, x_s, h, h_q, h_s, part, end;
 };
@@ -716,7 +747,8 @@ static Int8FfnWs int8_ffn_layout(int64_t T, int64_t hidden, int64_t inter) {
   w.h = put((size_t)T * inter * 2);
   w.h_q = put((size_t)T * inter);
   w.h_s = put((size_t)T * 4);
-  const size_t p1 = int8_part_bytes(T, 2 * inter, hidden), p2 = int8_part_bytes(T, hidden, inter);
+  const size_t p1 = int8_part_bytes(T, 2 * inter, int8_up_splits(T, hidden, inter));
+  const size_t p2 = int8_part_bytes(T, hidden, int8_splits(T, hidden, inter));
   w.part = put(p1 > p2 ? p1 : p2);
   w.end = p;
   return w;
@@ -751,7 +783,8 @@ extern "C" int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const
   float* h_s = reinterpret_cast<float*>(base + l.h_s);
   st = int8_quantize_rows(x_bf16, NVFP4_DT_BF16, T, hidden, x_q, x_s, stream);
   if (st) return st;
-  const Int8Args up = int8_args(x_q, x_s, w1_q, w1_scale, T, 2 * inter, hidden, true, nullptr, base + l.h, base + l.part);
+  const Int8Args up = int8_args(x_q, x_s, w1_q, w1_scale, T, 2 * inter, hidden, int8_up_splits(T, hidden, inter), true,
+                                nullptr, base + l.h, base + l.part);
   if (up.splits > 1) {  // the join quantizes h as well
     st = launch_int8_tile<64, 128, 2, 2, 128, kInt8Part>(up, (hipStream_t)stream);
     if (st) return st;
@@ -763,6 +796,7 @@ extern "C" int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const
     st = int8_quantize_rows(base + l.h, NVFP4_DT_BF16, T, inter, h_q, h_s, stream);
     if (st) return st;
   }
-  return launch_int8<false>(int8_args(h_q, h_s, w2_q, w2_scale, T, hidden, inter, false, add_bf16, out_bf16,
-                                      base + l.part), (hipStream_t)stream);
+  const Int8Args down = int8_args(h_q, h_s, w2_q, w2_scale, T, hidden, inter, int8_splits(T, hidden, inter), false,
+                                  add_bf16, out_bf16, base + l.part);
+  return launch_int8<false>(down, (hipStream_t)stream);
 }
