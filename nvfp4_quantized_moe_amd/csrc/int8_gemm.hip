@@ -198,7 +198,7 @@ struct OutVec<4> {
   typedef uint32_t type __attribute__((ext_vector_type(2)));
 };
 template <int W>
-__device__ __forceinline__ typename OutVec<W>::type add_and_round(const float (&o)[8], typename OutVec<W>::type add) {
+__device__ __forceinline__ typename OutVec<W>::type add_and_round(const float* o, typename OutVec<W>::type add) {
   typename OutVec<W>::type r;
 #pragma unroll
   for (int e = 0; e < W / 2; ++e)
@@ -437,85 +437,75 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(Int8Args g, int
   }
 }
 
-// Joins the parts of K: eight outputs (and their sums' columns) of row m from n on.
+// Joins the parts of K: four outputs of row m from n on. Eight parts are in
+// flight at once: they come from other XCDs' workgroups, through memory.
 template <bool SILU>
-__device__ __forceinline__ void join8(const Int8Args& g, int m, int n, float (&o)[8]) {
+__device__ __forceinline__ void join4(const Int8Args& g, int m, int n, float (&o)[4]) {
   const int half = g.N / 2;
-  int4v s[2] = {int4v{0, 0, 0, 0}, int4v{0, 0, 0, 0}}, u[2] = {int4v{0, 0, 0, 0}, int4v{0, 0, 0, 0}};
+  int4v s = int4v{0, 0, 0, 0}, u = int4v{0, 0, 0, 0};
   const int32_t* p = g.part + (size_t)m * g.N + n;
   const size_t step = (size_t)g.M * g.N;
-  for (int i = 0; i < g.splits; i += 4) {  // four parts in flight
-    int4v vs[4][2], vu[4][2];
+  for (int i = 0; i < g.splits; i += 8) {
+    int4v vs[8], vu[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j) {
+      const int32_t* at = p + (size_t)min(i + j, g.splits - 1) * step;
+      vs[j] = *reinterpret_cast<const int4v*>(at);
+      if (SILU) vu[j] = *reinterpret_cast<const int4v*>(at + half);
+    }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int32_t* at = p + (size_t)min(i + j, g.splits - 1) * step + 4 * h;
-        vs[j][h] = *reinterpret_cast<const int4v*>(at);
-        if (SILU) vu[j][h] = *reinterpret_cast<const int4v*>(at + half);
-      }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       if (i + j < g.splits) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[h] += vs[j][h];
-          if (SILU) u[h] += vu[j][h];
-        }
+        s += vs[j];
+        if (SILU) u += vu[j];
       }
   }
   const float as = g.a_s[m];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    o[e] = (float)s[e >> 2][e & 3] * (as * g.b_s[n + e]);
-    if (SILU) o[e] = silu_mul(o[e], (float)u[e >> 2][e & 3] * (as * g.b_s[half + n + e]));
+  for (int e = 0; e < 4; ++e) {
+    o[e] = (float)s[e] * (as * g.b_s[n + e]);
+    if (SILU) o[e] = silu_mul(o[e], (float)u[e] * (as * g.b_s[half + n + e]));
   }
 }
 
 template <bool SILU>
 __global__ __launch_bounds__(256) void int8_join_kernel(Int8Args g) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  typedef OutVec<4>::type vec_t;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (at >= (int64_t)g.M * g.n_out) return;
   const int m = (int)(at / g.n_out), n = (int)(at - (int64_t)m * g.n_out);
-  float o[8];
-  join8<SILU>(g, m, n, o);
-  typename OutVec<8>::type add = OutVec<8>::type(0u);
-  if (g.add) add = *reinterpret_cast<const OutVec<8>::type*>(g.add + at);
-  *reinterpret_cast<OutVec<8>::type*>(g.d + at) = add_and_round<8>(o, add);
+  vec_t add = vec_t(0u);
+  if (g.add) add = *reinterpret_cast<const vec_t*>(g.add + at);
+  float o[4];
+  join4<SILU>(g, m, n, o);
+  *reinterpret_cast<vec_t*>(g.d + at) = add_and_round<4>(o, add);
 }
 
 // The same for the dense expert's h, quantized in the same pass: workgroup m
-// joins row m, writes it as BF16 to d, and its codes and scale as
-// int8_rows_kernel would from there.
-__global__ __launch_bounds__(256) void int8_join_rows_kernel(Int8Args g, int8_t* __restrict__ q,
-                                                             float* __restrict__ scale) {
-  __shared__ float red[4];
-  const int m = blockIdx.x;
-  uint16_t* h = g.d + (size_t)m * g.n_out;
-  float top = 0.0f;
-  for (int n = threadIdx.x * 8; n < g.n_out; n += 2048) {
-    float o[8];
-    join8<true>(g, m, n, o);
-    const OutVec<8>::type v = add_and_round<8>(o, OutVec<8>::type(0u));
-    *reinterpret_cast<OutVec<8>::type*>(h + n) = v;
+// joins row m of up to kJoinRows outputs, four to a thread, rounds them to BF16
+// and writes their codes and scale as int8_rows_kernel would from there.
+// (64 x 2 x 2048 of 8 parts: 5.3 us; with four parts of eight values in flight
+// and h by way of memory 7.0.)
+constexpr int kJoinRows = 4096;
+__global__ __launch_bounds__(1024) void int8_join_rows_kernel(Int8Args g, int8_t* __restrict__ q,
+                                                              float* __restrict__ scale) {
+  typedef OutVec<4>::type vec_t;
+  __shared__ float red[16];
+  const int m = blockIdx.x, n = threadIdx.x * 4;
+  float f[4], top = 0.0f;
+  join4<true>(g, m, min(n, g.n_out - 4), f);
+  const vec_t h = add_and_round<4>(f, vec_t(0u));
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
+  for (int e = 0; e < 2; ++e) {
+    f[2 * e] = __uint_as_float(h[e] << 16);
+    f[2 * e + 1] = __uint_as_float(h[e] & 0xFFFF0000u);
+    top = fmaxf(top, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
   }
   const RowScale rs = row_scale(top, red);
   if (threadIdx.x == 0) scale[m] = rs.stored;
-  for (int n = threadIdx.x * 8; n < g.n_out; n += 2048) {  // each thread its own values again
-    const OutVec<8>::type v = *reinterpret_cast<const OutVec<8>::type*>(h + n);
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(v[e] << 16);
-      f[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
-    }
-    uint32_t w[2];
-    quantize_codes<8>(f, rs, w);
-    *reinterpret_cast<uint2*>(q + (size_t)m * g.n_out + n) = make_uint2(w[0], w[1]);
-  }
+  uint32_t w;
+  quantize_codes<4>(f, rs, &w);
+  if (n < g.n_out) *reinterpret_cast<uint32_t*>(q + (size_t)m * g.n_out + n) = w;
 }
 
 // Few tokens: the weights' bytes count, and every wave of the chip has to read
@@ -684,7 +674,7 @@ static int launch_int8(const Int8Args& g, hipStream_t stream) {
   if (g.splits > 1) {
     const int st = launch_int8_tile<64, 128, 2, 2, 128, kInt8Part>(g, stream);
     if (st) return st;
-    hipLaunchKernelGGL(int8_join_kernel<SILU>, dim3((unsigned)(((int64_t)g.M * g.n_out / 8 + 255) / 256)), dim3(256), 0,
+    hipLaunchKernelGGL(int8_join_kernel<SILU>, dim3((unsigned)(((int64_t)g.M * g.n_out / 4 + 255) / 256)), dim3(256), 0,
                        stream, g);
     NVFP4_CHECK_LAUNCH();
     return NVFP4_OK;
@@ -785,10 +775,11 @@ extern "C" int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const
   if (st) return st;
   const Int8Args up = int8_args(x_q, x_s, w1_q, w1_scale, T, 2 * inter, hidden, int8_up_splits(T, hidden, inter), true,
                                 nullptr, base + l.h, base + l.part);
-  if (up.splits > 1) {  // the join quantizes h as well
+  if (up.splits > 1 && inter <= kJoinRows) {  // the join quantizes h as well
     st = launch_int8_tile<64, 128, 2, 2, 128, kInt8Part>(up, (hipStream_t)stream);
     if (st) return st;
-    hipLaunchKernelGGL(int8_join_rows_kernel, dim3(T), dim3(256), 0, (hipStream_t)stream, up, h_q, h_s);
+    hipLaunchKernelGGL(int8_join_rows_kernel, dim3(T), dim3((inter / 4 + 63) / 64 * 64), 0, (hipStream_t)stream, up, h_q,
+                       h_s);
     NVFP4_CHECK_LAUNCH();
   } else {
     st = launch_int8<true>(up, (hipStream_t)stream);
