@@ -147,7 +147,9 @@ int moe_route_slots(const int32_t* topk_ids, const float* topk_w, int32_t T, int
 /* -------------------------------------------------------------------- gate
  * The routing gate in front of moe_route_slots: expert ids and weights from
  * router logits [T, E] (row-major, BF16 or float; each finite, or -inf for an
- * expert the token must not use). E <= 1024, 1 <= k <= min(E, 64), T*k < 2^30.
+ * expert the token must not use). E <= 1024, 1 <= k <= min(E, 64), T < 2^26,
+ * T*k < 2^30. In this section and the next outputs and workspaces
+ * overlap neither inputs nor each other, except where it is said.
  *
  *   score  MOE_SCORE_SOFTMAX        s = softmax over the row
  *          MOE_SCORE_SIGMOID        s = 1 / (1 + e^-x)
@@ -332,8 +334,10 @@ int nvfp4_grouped_gemm_silu_nvfp4(const uint8_t* a_q, const uint8_t* a_sf, const
  *   scale[m] = RN_f32(max_k |x[m, k]| * RN_f32(1 / 127))
  *   q[m, k]  = the integer nearest to x[m, k] / scale[m], ties to even (as on
  *              the real quotient), at most 127 in size; 0 where scale is 0.
- * q int8 [M, K]; scale float [M]. For activations a row is a token, for
- * weights [N, K] an output channel. K % 16 == 0, 0 < K <= 65536. One launch.
+ * x finite; q int8 [M, K]; scale float [M]. For activations a row is a token,
+ * for weights [N, K] an output channel. K % 16 == 0, 0 < K <= 65536,
+ * M <= 64 * 65535. One launch. In this section outputs and
+ * workspaces overlap neither inputs nor each other, except where it is said.
  */
 int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int32_t K, int8_t* q, float* scale, void* stream);
 
@@ -346,7 +350,8 @@ int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int32_t K, int
  * add: BF16 of d's shape, or NULL; may be d itself. K % 16 == 0, K <= 65536,
  * M <= 64 * 65535. ws: at least int8_gemm_ws_bytes(M, N, K) bytes (the sums of
  * the parts of K where few tokens split it; 0 otherwise, then ws may be NULL).
- * One launch, or two with parts.
+ * A token's outputs have the same bits whichever other tokens M holds. One
+ * launch, or two with parts.
  */
 size_t int8_gemm_ws_bytes(int32_t M, int32_t N, int32_t K);
 int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int32_t M, int32_t N,
@@ -360,6 +365,7 @@ int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const 
  * [H, I] with w2_scale [H]; x, out BF16 [T, H]; add BF16 [T, H] (such as the
  * output of nvfp4_moe_forward; may be out) or NULL. H % 16 == 0, I % 16 == 0,
  * both <= 65536, T <= 64 * 65535. ws: at least int8_ffn_ws_bytes(T, H, I).
+ * Exactly what the functions above give in sequence. Four or five launches.
  */
 size_t int8_ffn_ws_bytes(int32_t T, int32_t hidden, int32_t inter);
 int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const int8_t* w2_q, const float* w2_scale,

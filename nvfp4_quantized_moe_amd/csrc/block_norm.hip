@@ -9,8 +9,10 @@
 // i + blockDim.x, ... (16-byte loads). It walks the rows of its share with the
 // next row's loads in flight and its columns' weights in registers: read
 // again for every row, the three float32 vectors would be as many bytes from
-// L2 as the row is from memory. Sums are float32: the lanes of a wave by DPP,
+// L2 as the row is from memory (8192 x 7168 BF16: 93 us, 5.05 TB/s, weights
+// read again 108; backward 150 and 197). Sums are float32: the lanes of a wave by DPP,
 // then the waves through LDS in wave order, so results repeat bit for bit.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
@@ -22,6 +24,7 @@ namespace nvfp4 {
 
 constexpr int kNormMaxH = 16384;
 constexpr int kNormMaxWaves = 16;
+constexpr unsigned kGradThreads = 768;  // of a backward workgroup, at one chunk per thread
 
 template <typename T>
 struct Vec8;  // eight elements as loaded
@@ -238,8 +241,8 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
       if constexpr (QUANT) {
         // a 16-element block is the chunks of two neighbouring lanes (an even
         // number of chunks in a row): the even lane takes the odd one's words
-        const uint4 next = make_uint4((uint32_t)dpp_i32<kDppXor1>((int)bits.x), (uint32_t)dpp_i32<kDppXor1>((int)bits.y),
-                                      (uint32_t)dpp_i32<kDppXor1>((int)bits.z), (uint32_t)dpp_i32<kDppXor1>((int)bits.w));
+        const auto swap = [](uint32_t v) { return (uint32_t)dpp_i32<kDppXor1>((int)v); };
+        const uint4 next = make_uint4(swap(bits.x), swap(bits.y), swap(bits.z), swap(bits.w));
         if (ch < nchunk && (threadIdx.x & 1) == 0) {
           const uint32_t w[8] = {bits.x, bits.y, bits.z, bits.w, next.x, next.y, next.z, next.w};
           uint2 packed;
@@ -284,10 +287,9 @@ struct NormGradRow {
 };
 
 template <typename X, typename R, int CH>
-__global__ __launch_bounds__(CH == 1 ? 768 : 512) void block_norm_backward_kernel(const X* d_y, const R* d_res_out, const X* x,
-                                                                  const R* res_out, NormArgs a, int row_threads,
-                                                                  X* d_x, R* d_res, float* d_gate_tokens,
-                                                                  float* partial) {
+__global__ __launch_bounds__(CH == 1 ? kGradThreads : 512) void block_norm_backward_kernel(
+    const X* d_y, const R* d_res_out, const X* x, const R* res_out, NormArgs a, int row_threads, X* d_x, R* d_res,
+    float* d_gate_tokens, float* partial) {
   constexpr bool KEEP = CH <= 2;
   extern __shared__ float columns[];  // [3][H], with more than one row group
   __shared__ float scratch_a[2][kNormMaxWaves][3];
@@ -419,7 +421,7 @@ __global__ __launch_bounds__(CH == 1 ? 768 : 512) void block_norm_backward_kerne
 // Column sums over the workgroups' partial rows: workgroup (b, s) adds 64
 // columns of sum s. Its 16 waves take every 16th row, eight loads in flight,
 // and are added in wave order (with 4 waves and one load in flight this took
-// 20 us for 256 rows of 3 x 7168, now 6).
+// 20 us for 256 rows of 3 x 7168, now 5.4).
 constexpr int kColumnWaves = 16;
 __global__ __launch_bounds__(64 * kColumnWaves) void norm_columns_kernel(const float* __restrict__ partial, int rows,
                                                                          int H, float* d_pre, float* d_post,
@@ -467,16 +469,27 @@ static int norm_check(int32_t T, int32_t H, int32_t x_dtype, int32_t res_dtype, 
 
 // Threads for rows of H elements at CH chunks of 8 per thread: at most 512.
 static unsigned norm_threads(int32_t H, int ch) { return (unsigned)(((H / 8 + ch - 1) / ch + 63) / 64 * 64); }
-// Workgroups that walk T rows: as many per CU as give it about `waves` waves.
-static unsigned norm_grid(int32_t T, unsigned threads, int waves) {
-  int per_cu = waves / (int)(threads / 64);
-  if (per_cu < 1) per_cu = 1;
-  return (unsigned)(T < kNormCus * per_cu ? T : kNormCus * per_cu);
+// Workgroups that walk T rows: as many per CU as give it up to 16 waves. (More
+// bring nothing where bytes count, 8192 x 7168: 93 us with 16 or 28, 98 with a
+// workgroup per row; 4096 x 5120: 26.8, 29.6, 28.9; 2047 x 2888 float: 17.0,
+// 19.5, 19.2. Small rows by themselves would be a little faster, 16384 x 2048:
+// 43.3, 43.7, 40.6, larger ones not, 16384 x 4096: 102, 104, 125.)
+static unsigned norm_grid(int32_t T, unsigned threads) {
+  const int per_cu = std::max(1, 16 / (int)(threads / 64));
+  return (unsigned)std::min(T, kNormCus * per_cu);
+}
+// Chunks per thread: the fewest that 512 threads hold. Backward, one chunk only
+// where two rows still share a workgroup of 768 threads: each thread's sums and
+// weights of a second chunk cost less than a CU with a single row (16384 x
+// 4096: 159 us instead of 180; 2047 x 2888 float: one chunk 32.9, two 34.5).
+static int norm_chunks(int32_t H) { return H <= 4096 ? 1 : H <= 8192 ? 2 : 4; }
+static int norm_grad_chunks(int32_t H) {
+  return H <= 4096 && 2 * norm_threads(H, 1) > kGradThreads ? 2 : norm_chunks(H);
 }
 template <typename Fn>
-static int norm_by_width(int32_t H, Fn fn) {
-  if (H <= 4096) return fn(std::integral_constant<int, 1>());
-  if (H <= 8192) return fn(std::integral_constant<int, 2>());
+static int norm_by_chunks(int chunks, Fn fn) {
+  if (chunks == 1) return fn(std::integral_constant<int, 1>());
+  if (chunks == 2) return fn(std::integral_constant<int, 2>());
   return fn(std::integral_constant<int, 4>());
 }
 
@@ -509,14 +522,15 @@ extern "C" int moe_block_norm(const void* x, int32_t x_dtype, const void* residu
     auto go = [&](auto ch, auto quant) -> int {
       constexpr int CH = decltype(ch)::value;
       const unsigned threads = norm_threads(H, CH);
-      hipLaunchKernelGGL((block_norm_kernel<X, R, CH, decltype(quant)::value>), dim3(norm_grid(T, threads, 28)),
-                         dim3(threads), 0, (hipStream_t)stream, reinterpret_cast<const X*>(x), reinterpret_cast<const R*>(residual), a,
-                         reinterpret_cast<R*>(residual_out), reinterpret_cast<X*>(y), gs_in, y_q, y_sf);
+      hipLaunchKernelGGL((block_norm_kernel<X, R, CH, decltype(quant)::value>), dim3(norm_grid(T, threads)),
+                         dim3(threads), 0, (hipStream_t)stream, reinterpret_cast<const X*>(x),
+                         reinterpret_cast<const R*>(residual), a, reinterpret_cast<R*>(residual_out),
+                         reinterpret_cast<X*>(y), gs_in, y_q, y_sf);
       NVFP4_CHECK_LAUNCH();
       return NVFP4_OK;
     };
     auto by_width = [&](auto quant) -> int {
-      return norm_by_width(H, [&](auto ch) { return go(ch, quant); });
+      return norm_by_chunks(norm_chunks(H), [&](auto ch) { return go(ch, quant); });
     };
     if constexpr (std::is_same<X, uint16_t>::value)
       if (gs_in) return by_width(std::true_type());
@@ -525,16 +539,16 @@ extern "C" int moe_block_norm(const void* x, int32_t x_dtype, const void* residu
 }
 
 // One workgroup per CU, of as many row groups as give it 12 waves (8 with two
-// chunks per thread, whose registers allow no more), fewer where the rows run
-// out.
+// chunks per thread, whose registers allow no more; 16384 x 2048 with 8 also at
+// one chunk: 91 us instead of 84), fewer where the rows run out.
 struct NormGradShape {
   unsigned row_threads, groups, grid;
 };
 static NormGradShape norm_grad_shape(int32_t T, int32_t H) {
-  const int ch = H <= 4096 ? 1 : H <= 8192 ? 2 : 4;
+  const int ch = norm_grad_chunks(H);
   NormGradShape s;
   s.row_threads = norm_threads(H, ch);
-  s.groups = (ch == 1 ? 768 : 512) / s.row_threads;
+  s.groups = (ch == 1 ? kGradThreads : 512) / s.row_threads;
   const unsigned rows = T < 1 ? 1 : (unsigned)T, want = (rows + kNormCus - 1) / kNormCus;
   if (s.groups > want) s.groups = want;
   if (s.groups < 1) s.groups = 1;
@@ -586,7 +600,7 @@ extern "C" int moe_block_norm_backward(const void* d_y, const void* d_residual_o
         NVFP4_CHECK_LAUNCH();
         return NVFP4_OK;
       };
-      return norm_by_width(H, go);
+      return norm_by_chunks(norm_grad_chunks(H), go);
     });
     if (r) return r;
   }

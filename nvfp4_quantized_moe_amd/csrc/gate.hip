@@ -270,13 +270,14 @@ __device__ __forceinline__ void pick_by_rounds(F (&key)[VPT], int want, int* id,
   }
 }
 
-// The `want` highest float keys, want <= 16, without a chain of wave maxima.
+// The `want` highest float keys for k <= 16, without a chain of wave maxima.
 // The wave's lanes fall into `groups` >= k runs; the lowest of the runs' maxima
 // is at most the groups-th highest key, so the keys from it on (about 17 of
 // 384 for 8 runs) hold the k highest. They are compacted in expert order, one
 // per lane, and each counts those before it. Returns false, having done
 // nothing, when more than 64 remain (many equal keys); *all tells whether the
-// want-th is among them.
+// want-th is among them. (16384 x 384 and k = 8: 28 us, by rounds 36; k = 16:
+// 32 and 44; k = 2: 7.6 and 7.3. Past 16 the runs would be single lanes.)
 constexpr int kFastK = 16;
 template <int VPT>
 __device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, int want, uint2* lds, int* id, float* at,
@@ -701,9 +702,8 @@ __global__ __launch_bounds__(64 * WAVES) void balance_join_kernel(const int32_t*
   }
 }
 
-// The two losses from the sequences' terms, one workgroup. (In the join
-// itself, by the workgroup that finishes last, it took longer: the release
-// that this needs writes back each L2.)
+// The two losses from the sequences' terms, one workgroup: 2.2 us for 24
+// sequences of 384 experts, nearly all of it the launch.
 constexpr int kLossWaves = 4;
 __global__ __launch_bounds__(64 * kLossWaves) void balance_loss_kernel(BalanceShape g, BalanceWs ws, int cols,
                                                                        int32_t* __restrict__ tokens,
@@ -891,7 +891,7 @@ using namespace nvfp4;
 
 static int gate_check(const void* logits, int32_t dtype, int32_t T, int32_t E, int32_t k, int32_t score) {
   if (T < 0 || E < 1 || E > kGateMaxExperts || k < 1 || k > kGateMaxK || k > E) return NVFP4_ERR_SHAPE;
-  if ((int64_t)T * k >= (1ll << 30)) return NVFP4_ERR_SHAPE;
+  if ((int64_t)T * k >= (1ll << 30) || T >= (1 << 26)) return NVFP4_ERR_SHAPE;  // 64 threads a token: a grid's limit
   if (dtype != NVFP4_DT_BF16 && dtype != NVFP4_DT_F32) return NVFP4_ERR_ARG;
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SQRT_SOFTPLUS)
     return NVFP4_ERR_ARG;
@@ -943,12 +943,13 @@ extern "C" int moe_gate_topk(const void* logits, int32_t logits_dtype, const flo
   });
 }
 
-// Tokens of one partial sum: 16, and more for batches of over 16384 tokens, so
+// Tokens of one partial sum: 8, and more for batches of over 8192 tokens, so
 // that the partial rows (8 E bytes each) stay a small part of the logits'
-// bytes. (32 tokens at 16384, half as many waves: 16.6 instead of 10 us.)
+// bytes. (The whole call, 2048 x 384: 8 tokens 10.9 us, 16 11.6, 32 13.6;
+// 16384 x 384 in 4 sequences: 16 tokens 16.2, 32 16.7.)
 static int balance_chunk(int32_t T) {
   const int per = ((T + 1023) / 1024 + kGateWaves - 1) / kGateWaves * kGateWaves;
-  return per < 16 ? 16 : per;
+  return per < 8 ? 8 : per;
 }
 static size_t balance_layout(int32_t T, int32_t E, int32_t B, BalanceShape* g, char* base, BalanceWs* ws) {
   const int chunk = balance_chunk(T);
@@ -1009,7 +1010,9 @@ extern "C" int moe_balance_loss(const void* logits, int32_t logits_dtype, const 
                          (hipStream_t)stream, reinterpret_cast<const uint16_t*>(logits), topk_ids, token_mask,
                          cu_seqlens, g, w);
     NVFP4_CHECK_LAUNCH();
-    // long sequences: more workgroups and waves over the same chunks
+    // Long sequences: more workgroups and waves over the same chunks (the whole
+    // call, 16384 x 384: one sequence 17.3 us [otherwise 29.5], 4 sequences 16.1
+    // [18.0]; short ones lose, 24 sequences: 21.5 [15.3]).
     const bool tall = T / B >= 64 * g.chunk;
     const int cols = tall ? (E + 15) / 16 : (E + 63) / 64;
     if (tall)

@@ -23,6 +23,7 @@ typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
 
 constexpr int kInt8MaxK = 65536;
+constexpr int kInt8MaxM = 64 * 65535;  // by 1024 threads still within a grid
 
 // ------------------------------------------------------------- row quantizer
 
@@ -594,7 +595,7 @@ using namespace nvfp4;
 
 extern "C" int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int32_t K, int8_t* q, float* scale,
                                   void* stream) {
-  if (M < 0 || K <= 0 || K % 16 != 0 || K > kInt8MaxK) return NVFP4_ERR_SHAPE;
+  if (M < 0 || M > kInt8MaxM || K <= 0 || K % 16 != 0 || K > kInt8MaxK) return NVFP4_ERR_SHAPE;
   if (x_dtype != NVFP4_DT_BF16 && x_dtype != NVFP4_DT_F32) return NVFP4_ERR_ARG;
   if (M == 0) return NVFP4_OK;
   if (!x || !q || !scale) return NVFP4_ERR_NULL;
@@ -618,14 +619,14 @@ static int int8_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue) {
   if (epilogue != NVFP4_EPI_BF16 && epilogue != NVFP4_EPI_SILU_MUL) return NVFP4_ERR_ARG;
   if (M < 0 || N <= 0 || K <= 0 || K % 16 != 0 || K > kInt8MaxK) return NVFP4_ERR_SHAPE;
   if (N % (epilogue == NVFP4_EPI_SILU_MUL ? 16 : 8) != 0) return NVFP4_ERR_SHAPE;
-  if ((M + 63) / 64 > 65535) return NVFP4_ERR_SHAPE;
+  if (M > kInt8MaxM) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 
 template <int BM, int BN, int WM, int WN, int BK, int OUT>
 static int launch_int8_tile(const Int8Args& g, hipStream_t stream) {
   const int mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN;
-  if ((int64_t)mt * nt >= (1ll << 31)) return NVFP4_ERR_SHAPE;
+  if ((int64_t)mt * nt * (64 * WM * WN) >= (1ll << 32)) return NVFP4_ERR_SHAPE;  // threads of a grid
   hipLaunchKernelGGL((int8_tile_kernel<BM, BN, WM, WN, BK, OUT>), dim3((unsigned)mt * nt, g.splits),
                      dim3(64 * WM * WN), 0, stream, g, mt, nt);
   NVFP4_CHECK_LAUNCH();
@@ -745,7 +746,7 @@ static Int8FfnWs int8_ffn_layout(int64_t T, int64_t hidden, int64_t inter) {
 }
 static int int8_ffn_check(int32_t T, int32_t hidden, int32_t inter) {
   if (T < 0 || hidden <= 0 || inter <= 0 || hidden % 16 != 0 || inter % 16 != 0 || hidden > kInt8MaxK ||
-      inter > kInt8MaxK || T > 64 * 65535)
+      inter > kInt8MaxK || T > kInt8MaxM)
     return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
