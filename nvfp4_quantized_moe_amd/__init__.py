@@ -23,7 +23,8 @@ __all__ = [
     "nvfp4_moe_ws_bytes", "nvfp4_moe_ws_layout", "nvfp4_moe_tile_m", "MoEWeights", "prepare_weights",
     "ws_view", "SCORE_SOFTMAX", "SCORE_SIGMOID", "SCORE_SQRT_SOFTPLUS", "moe_gate_topk", "moe_balance_loss",
     "moe_balance_loss_ws_bytes", "moe_gate_backward", "moe_block_norm", "moe_block_norm_backward",
-    "moe_block_norm_backward_ws_bytes", "int8_quantize_rows", "int8_gemm", "int8_gemm_ws_bytes", "int8_ffn_forward", "int8_ffn_ws_bytes",
+    "moe_block_norm_backward_ws_bytes", "int8_quantize_rows", "int8_gemm", "int8_gemm_ws_bytes", "int8_ffn_forward",
+    "int8_ffn_ws_bytes",
     "Int8FFNWeights", "prepare_int8_weights",
 ]
 
@@ -128,7 +129,7 @@ def _stream():
 def _dev(t, dtype, name):
     """t must be a contiguous tensor of dtype on the current device (the
     device whose current stream the call is issued on)."""
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+    if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor, got {t.dtype} on {t.device}")
     if t.get_device() != _current_device():
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_current_device()}")
@@ -147,7 +148,7 @@ def _buf(t, dtype, numel, name):
 
 
 def _shape(t, shape, name):
-    if t.shape != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -256,15 +257,18 @@ def moe_route_slots(topk_ids, topk_w, expert_start, num_local, tile_m):
 
 # -------------------------------------------------------------------------- gate
 
+# (Where the smallest calls are bound by the host: torch.empty with its sizes as
+# separate arguments takes 0.35 us less than with a tuple.)
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
 def _float_dev(t, name):
     """t as _dev, BF16 or float32; returns its NVFP4_DT_* code."""
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name}: expected BF16 or float32, got {t.dtype}")
-    _dev(t, t.dtype, name)
-    return _DTYPES[t.dtype]
+    dtype = t.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"{name}: expected BF16 or float32, got {dtype}")
+    _dev(t, dtype, name)
+    return _DTYPES[dtype]
 
 
 def _matrix(t, name):
@@ -291,9 +295,9 @@ def moe_gate_topk(logits, k, score=SCORE_SOFTMAX, bias=None, token_mask=None, n_
     dev = logits.device
     _opt(bias, torch.float32, (E,), "bias")
     _opt(token_mask, torch.uint8, (T,), "token_mask")
-    topk_ids = (torch.empty((T, k), dtype=torch.int32, device=dev) if topk_ids is None
+    topk_ids = (torch.empty(T, k, dtype=torch.int32, device=dev) if topk_ids is None
                 else _buf(topk_ids, torch.int32, T * k, "topk_ids"))
-    topk_w = (torch.empty((T, k), dtype=torch.float32, device=dev) if topk_w is None
+    topk_w = (torch.empty(T, k, dtype=torch.float32, device=dev) if topk_w is None
               else _buf(topk_w, torch.float32, T * k, "topk_w"))
     _check(_gate_topk(_ptr(logits), dt, _ptr(bias), _ptr(token_mask), T, E, k, score, n_group, topk_group,
                       int(renormalize), scale, _ptr(topk_ids), _ptr(topk_w), _stream()), "moe_gate_topk")
@@ -327,7 +331,7 @@ def moe_balance_loss(logits, topk_ids, score=SCORE_SOFTMAX, token_mask=None, cu_
     dev = logits.device
     _opt(token_mask, torch.uint8, (T,), "token_mask")
     loss = torch.empty(2, dtype=torch.float32, device=dev) if loss is None else _buf(loss, torch.float32, 2, "loss")
-    counts = (torch.empty((B, E), dtype=torch.int32, device=dev) if counts is None
+    counts = (torch.empty(B, E, dtype=torch.int32, device=dev) if counts is None
               else _buf(counts, torch.int32, B * E, "counts"))
     tokens = (torch.empty(B + 2, dtype=torch.int32, device=dev) if tokens is None
               else _buf(tokens, torch.int32, B + 2, "tokens"))
@@ -400,15 +404,15 @@ def moe_block_norm(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0, e
     _opt(w_pre, torch.float32, (H,), "w_pre")
     _opt(w_post, torch.float32, (H,), "w_post")
     mode = _gate_mode(gate, T, H)
-    residual_out = (torch.empty((T, H), dtype=rtype, device=dev) if residual_out is None
+    residual_out = (torch.empty(T, H, dtype=rtype, device=dev) if residual_out is None
                     else _buf(residual_out, rtype, T * H, "residual_out"))
     if w_pre is not None:
-        y = torch.empty((T, H), dtype=x.dtype, device=dev) if y is None else _buf(y, x.dtype, T * H, "y")
+        y = torch.empty(T, H, dtype=x.dtype, device=dev) if y is None else _buf(y, x.dtype, T * H, "y")
     if gs is not None:
         _opt(gs, torch.float32, (1,), "gs")
-        y_q = (torch.empty((T, H // 2), dtype=torch.uint8, device=dev) if y_q is None
+        y_q = (torch.empty(T, H // 2, dtype=torch.uint8, device=dev) if y_q is None
                else _buf(y_q, torch.uint8, T * H // 2, "y_q"))
-        y_sf = (torch.empty((T, H // 16), dtype=torch.uint8, device=dev) if y_sf is None
+        y_sf = (torch.empty(T, H // 16, dtype=torch.uint8, device=dev) if y_sf is None
                 else _buf(y_sf, torch.uint8, T * H // 16, "y_sf"))
     _check(_block_norm(_ptr(x), dt, _ptr(residual), rdt, T, H, _ptr(w_pre), _ptr(w_post), _ptr(gate), mode, scale, eps,
                        _ptr(residual_out), _ptr(y), _ptr(gs), _ptr(y_q), _ptr(y_sf), _stream()), "moe_block_norm")
@@ -574,7 +578,7 @@ def int8_quantize_rows(x, q=None, scale=None):
     """x BF16 or float32 [M, K] -> (q int8 [M, K], scale float32 [M] = row amax * (1 / 127))."""
     dt = _float_dev(x, "x")
     M, K = _matrix(x, "x")
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device) if q is None else _buf(q, torch.int8, M * K, "q")
+    q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else _buf(q, torch.int8, M * K, "q")
     scale = (torch.empty(M, dtype=torch.float32, device=x.device) if scale is None
              else _buf(scale, torch.float32, M, "scale"))
     _check(_int8_rows(_ptr(x), dt, M, K, _ptr(q), _ptr(scale), _stream()), "int8_quantize_rows")
@@ -597,7 +601,7 @@ def int8_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, d=None, w
     _opt(b_scale, torch.float32, (N,), "b_scale")
     n_out = N // 2 if epilogue == EPI_SILU_MUL else N
     _opt(add, torch.bfloat16, (M, n_out), "add")
-    d = (torch.empty((M, n_out), dtype=torch.bfloat16, device=a_q.device) if d is None
+    d = (torch.empty(M, n_out, dtype=torch.bfloat16, device=a_q.device) if d is None
          else _buf(d, torch.bfloat16, M * n_out, "d"))
     need = _int8_gemm_ws(M, N, K) if ws is None else 0
     ws = (_alloc_ws(need, a_q.device) if need else None) if ws is None else _buf(ws, torch.uint8, 0, "ws")
@@ -643,7 +647,7 @@ def int8_ffn_forward(weights: Int8FFNWeights, x, add=None, out=None, ws=None):
     _shape(x, (T, w.hidden), "x")
     _dev(w.w1_q, torch.int8, "weights.w1_q")
     _opt(add, torch.bfloat16, (T, w.hidden), "add")
-    out = (torch.empty((T, w.hidden), dtype=torch.bfloat16, device=x.device) if out is None
+    out = (torch.empty(T, w.hidden, dtype=torch.bfloat16, device=x.device) if out is None
            else _buf(out, torch.bfloat16, T * w.hidden, "out"))
     ws = (_alloc_ws(int8_ffn_ws_bytes(T, w.hidden, w.inter), x.device) if ws is None
           else _buf(ws, torch.uint8, 0, "ws"))
