@@ -32,6 +32,10 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run `python __graft_entry__.py` (build()) first")
 lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _native  # the calls of the operators around the expert FFN (csrc/binding.cpp)
+except ImportError as e:
+    raise ImportError(f"the native calls are not built ({e}); run `python __graft_entry__.py` (build()) first") from e
 
 EPI_BF16, EPI_SILU_MUL, EPI_SILU_MUL_DUAL = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRT_SOFTPLUS = 0, 1, 2
@@ -82,6 +86,7 @@ _forward_stages = _sig("nvfp4_moe_forward_stage_events", ctypes.c_int, ctypes.PO
                        _vp, _i32, _i32, _vp, _vp, _sz, ctypes.POINTER(_vp), _vp)
 _forward_static = _sig("nvfp4_moe_forward_static", ctypes.c_int, ctypes.POINTER(_Weights), _vp, _i32, _vp, _vp,
                        _i32, _i32, _vp, _vp, _vp, _sz, _vp)
+# the C entry points behind _native, which checks their arguments and calls them itself
 _gate_topk = _sig("moe_gate_topk", ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
                   _vp, _vp, _vp)
 _balance_ws = _sig("moe_balance_loss_ws_bytes", _sz, _i32, _i32, _i32)
@@ -124,6 +129,9 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _stream():
     return _raw_stream(_current_device())
+
+
+_native.set_up(_current_device, _raw_stream, NVFP4Error)
 
 
 def _dev(t, dtype, name):
@@ -257,64 +265,16 @@ def moe_route_slots(topk_ids, topk_w, expert_start, num_local, tile_m):
 
 # -------------------------------------------------------------------------- gate
 
-# (Where the smallest calls are bound by the host: torch.empty with its sizes as
-# separate arguments takes 0.35 us less than with a tuple.)
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
-
-
-def _float_dev(t, name):
-    """t as _dev, BF16 or float32; returns its NVFP4_DT_* code."""
-    dtype = t.dtype
-    if dtype not in _DTYPES:
-        raise ValueError(f"{name}: expected BF16 or float32, got {dtype}")
-    _dev(t, dtype, name)
-    return _DTYPES[dtype]
-
-
-def _matrix(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
-    return t.shape
-
-
-def _opt(t, dtype, shape, name):
-    """An optional input tensor of exactly this shape."""
-    if t is None:
-        return None
-    _dev(t, dtype, name)
-    return _shape(t, shape, name)
-
-
 def moe_gate_topk(logits, k, score=SCORE_SOFTMAX, bias=None, token_mask=None, n_group=1, topk_group=1,
                   renormalize=True, scale=1.0, topk_ids=None, topk_w=None):
     """Router logits BF16 or float32 [T, E] -> (topk_ids int32 [T, k], topk_w float32 [T, k]), as moe_route_slots
     and nvfp4_moe_forward take them. bias: float32 [E], added to the scores for the choice alone; token_mask: uint8
     [T], 0 for padding (ids -1, weights 0); n_group / topk_group: choose within the best groups of experts."""
-    dt = _float_dev(logits, "logits")
-    T, E = _matrix(logits, "logits")
-    dev = logits.device
-    _opt(bias, torch.float32, (E,), "bias")
-    _opt(token_mask, torch.uint8, (T,), "token_mask")
-    topk_ids = (torch.empty(T, k, dtype=torch.int32, device=dev) if topk_ids is None
-                else _buf(topk_ids, torch.int32, T * k, "topk_ids"))
-    topk_w = (torch.empty(T, k, dtype=torch.float32, device=dev) if topk_w is None
-              else _buf(topk_w, torch.float32, T * k, "topk_w"))
-    _check(_gate_topk(_ptr(logits), dt, _ptr(bias), _ptr(token_mask), T, E, k, score, n_group, topk_group,
-                      int(renormalize), scale, _ptr(topk_ids), _ptr(topk_w), _stream()), "moe_gate_topk")
-    return topk_ids, topk_w
+    return _native.gate_topk(logits, k, score, bias, token_mask, n_group, topk_group, renormalize, scale, topk_ids, topk_w)
 
 
 def moe_balance_loss_ws_bytes(T, E, B) -> int:
     return int(_balance_ws(T, E, B))
-
-
-def _num_seqs(cu_seqlens):
-    if cu_seqlens is None:
-        return 1
-    _dev(cu_seqlens, torch.int32, "cu_seqlens")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-        raise ValueError(f"cu_seqlens: expected [B + 1] with B >= 1, got shape {tuple(cu_seqlens.shape)}")
-    return cu_seqlens.numel() - 1
 
 
 def moe_balance_loss(logits, topk_ids, score=SCORE_SOFTMAX, token_mask=None, cu_seqlens=None, loss=None, counts=None,
@@ -322,23 +282,7 @@ def moe_balance_loss(logits, topk_ids, score=SCORE_SOFTMAX, token_mask=None, cu_
     """Balance loss and mean squared log-sum of the logits over the gate's choices -> (loss float32 [2], counts
     int32 [B, E], tokens int32 [B + 2]); counts and tokens are what moe_gate_backward takes. cu_seqlens: int32
     [B + 1] sequence bounds (None: all tokens are one sequence)."""
-    dt = _float_dev(logits, "logits")
-    T, E = _matrix(logits, "logits")
-    _dev(topk_ids, torch.int32, "topk_ids")
-    _shape(topk_ids, (T, _matrix(topk_ids, "topk_ids")[1]), "topk_ids")
-    k = topk_ids.shape[1]
-    B = _num_seqs(cu_seqlens)
-    dev = logits.device
-    _opt(token_mask, torch.uint8, (T,), "token_mask")
-    loss = torch.empty(2, dtype=torch.float32, device=dev) if loss is None else _buf(loss, torch.float32, 2, "loss")
-    counts = (torch.empty(B, E, dtype=torch.int32, device=dev) if counts is None
-              else _buf(counts, torch.int32, B * E, "counts"))
-    tokens = (torch.empty(B + 2, dtype=torch.int32, device=dev) if tokens is None
-              else _buf(tokens, torch.int32, B + 2, "tokens"))
-    ws = _alloc_ws(moe_balance_loss_ws_bytes(T, E, B), dev) if ws is None else _buf(ws, torch.uint8, 0, "ws")
-    _check(_balance(_ptr(logits), dt, _ptr(topk_ids), _ptr(token_mask), _ptr(cu_seqlens), B, T, E, k, score,
-                    _ptr(loss), _ptr(counts), _ptr(tokens), _ptr(ws), ws.numel(), _stream()), "moe_balance_loss")
-    return loss, counts, tokens
+    return _native.balance_loss(logits, topk_ids, score, token_mask, cu_seqlens, loss, counts, tokens, ws)
 
 
 def moe_gate_backward(logits, topk_ids, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, token_mask=None,
@@ -346,41 +290,11 @@ def moe_gate_backward(logits, topk_ids, score=SCORE_SOFTMAX, renormalize=True, s
     """Gradient of the logits (their type and shape): through the weights when d_topk_w (float32 [T, k]) is given
     (score, renormalize and scale as in moe_gate_topk), of the losses when d_loss (float32 [2]) is given (counts
     and tokens from moe_balance_loss, the same cu_seqlens), or the sum of both."""
-    dt = _float_dev(logits, "logits")
-    T, E = _matrix(logits, "logits")
-    _dev(topk_ids, torch.int32, "topk_ids")
-    k = _matrix(topk_ids, "topk_ids")[1]
-    _shape(topk_ids, (T, k), "topk_ids")
-    _opt(token_mask, torch.uint8, (T,), "token_mask")
-    _opt(d_topk_w, torch.float32, (T, k), "d_topk_w")
-    B = 1
-    if d_loss is not None:
-        B = _num_seqs(cu_seqlens)
-        _opt(d_loss, torch.float32, (2,), "d_loss")
-        if counts is None or tokens is None:
-            raise ValueError("d_loss needs counts and tokens of moe_balance_loss")
-        _buf(counts, torch.int32, B * E, "counts")
-        _buf(tokens, torch.int32, B + 2, "tokens")
-    d_logits = torch.empty_like(logits) if d_logits is None else _buf(d_logits, logits.dtype, T * E, "d_logits")
-    _check(_gate_backward(_ptr(logits), dt, _ptr(topk_ids), _ptr(token_mask), T, E, k, score, int(renormalize), scale,
-                          _ptr(d_topk_w), _ptr(d_loss), _ptr(counts), _ptr(tokens), _ptr(cu_seqlens), B,
-                          _ptr(d_logits), _stream()), "moe_gate_backward")
-    return d_logits
+    return _native.gate_backward(logits, topk_ids, score, renormalize, scale, token_mask, d_topk_w, d_loss, counts, tokens,
+                                 cu_seqlens, d_logits)
 
 
 # ------------------------------------------------------------ norms of the block
-
-def _gate_mode(gate, T, H):
-    """MOE_GATE_* of a gate float32 [H] (channels) or [T, 1] (tokens)."""
-    if gate is None:
-        return 0
-    _dev(gate, torch.float32, "gate")
-    if tuple(gate.shape) == (H,):
-        return 1
-    if tuple(gate.shape) == (T, 1):
-        return 2
-    raise ValueError(f"gate: expected shape ({H},) or ({T}, 1), got {tuple(gate.shape)}")
-
 
 def moe_block_norm(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0, eps=1e-6, gs=None, residual_out=None,
                    y=None, y_q=None, y_sf=None):
@@ -389,38 +303,14 @@ def moe_block_norm(x, residual, w_pre=None, w_post=None, gate=None, scale=1.0, e
     without w_pre. x, residual: BF16 or float32 [T, H] (residual None: zeros, of x's type); w_pre, w_post: float32
     [H]; gate: float32 [H] or [T, 1]. With gs (float32 [1], device) also y as NVFP4 with that fixed global scale:
     (residual_out, y, y_q, y_sf)."""
-    dt = _float_dev(x, "x")
-    T, H = _matrix(x, "x")
-    dev = x.device
-    rdt = dt
-    rtype = x.dtype
-    if residual is not None:
-        rdt = _float_dev(residual, "residual")
-        rtype = residual.dtype
-        _shape(residual, (T, H), "residual")
-    elif residual_out is not None:
-        rdt = _float_dev(residual_out, "residual_out")
-        rtype = residual_out.dtype
-    _opt(w_pre, torch.float32, (H,), "w_pre")
-    _opt(w_post, torch.float32, (H,), "w_post")
-    mode = _gate_mode(gate, T, H)
-    residual_out = (torch.empty(T, H, dtype=rtype, device=dev) if residual_out is None
-                    else _buf(residual_out, rtype, T * H, "residual_out"))
-    if w_pre is not None:
-        y = torch.empty(T, H, dtype=x.dtype, device=dev) if y is None else _buf(y, x.dtype, T * H, "y")
-    if gs is not None:
-        _opt(gs, torch.float32, (1,), "gs")
-        y_q = (torch.empty(T, H // 2, dtype=torch.uint8, device=dev) if y_q is None
-               else _buf(y_q, torch.uint8, T * H // 2, "y_q"))
-        y_sf = (torch.empty(T, H // 16, dtype=torch.uint8, device=dev) if y_sf is None
-                else _buf(y_sf, torch.uint8, T * H // 16, "y_sf"))
-    _check(_block_norm(_ptr(x), dt, _ptr(residual), rdt, T, H, _ptr(w_pre), _ptr(w_post), _ptr(gate), mode, scale, eps,
-                       _ptr(residual_out), _ptr(y), _ptr(gs), _ptr(y_q), _ptr(y_sf), _stream()), "moe_block_norm")
-    return (residual_out, y) if gs is None else (residual_out, y, y_q, y_sf)
+    return _native.block_norm(x, residual, w_pre, w_post, gate, scale, eps, gs, residual_out, y, y_q, y_sf)
 
 
 def moe_block_norm_backward_ws_bytes(T, H) -> int:
     return int(_block_norm_ws(T, H))
+
+
+_NORM_GRADIENTS = ("d_x", "d_residual", "d_w_pre", "d_w_post", "d_gate")
 
 
 def moe_block_norm_backward(d_y, d_residual_out, x, residual_out, w_pre=None, w_post=None, gate=None, scale=1.0,
@@ -428,32 +318,9 @@ def moe_block_norm_backward(d_y, d_residual_out, x, residual_out, w_pre=None, w_
     """Gradients of moe_block_norm from d_y (None without w_pre) and d_residual_out (None: zeros), with the x and the
     residual_out of the forward call -> dict of d_x, d_residual, d_w_pre, d_w_post, d_gate (None where there is no
     such input)."""
-    dt = _float_dev(x, "x")
-    T, H = _matrix(x, "x")
-    rdt = _float_dev(residual_out, "residual_out")
-    _shape(residual_out, (T, H), "residual_out")
-    _opt(d_y, x.dtype, (T, H), "d_y")
-    _opt(d_residual_out, residual_out.dtype, (T, H), "d_residual_out")
-    _opt(w_pre, torch.float32, (H,), "w_pre")
-    _opt(w_post, torch.float32, (H,), "w_post")
-    mode = _gate_mode(gate, T, H)
-    f32 = dict(dtype=torch.float32, device=x.device)
-    d_x = torch.empty_like(x) if d_x is None else _buf(d_x, x.dtype, T * H, "d_x")
-    d_residual = (torch.empty_like(residual_out) if d_residual is None
-                  else _buf(d_residual, residual_out.dtype, T * H, "d_residual"))
-
-    def grad(buf, of, name):
-        if of is None:
-            return None
-        return torch.empty(of.shape, **f32) if buf is None else _buf(buf, torch.float32, of.numel(), name)
-    d_w_pre, d_w_post = grad(d_w_pre, w_pre, "d_w_pre"), grad(d_w_post, w_post, "d_w_post")
-    d_gate = grad(d_gate, gate, "d_gate")
-    ws = _alloc_ws(moe_block_norm_backward_ws_bytes(T, H), x.device) if ws is None else _buf(ws, torch.uint8, 0, "ws")
-    _check(_block_norm_backward(_ptr(d_y), _ptr(d_residual_out), _ptr(x), dt, _ptr(residual_out), rdt, T, H,
-                                _ptr(w_pre), _ptr(w_post), _ptr(gate), mode, scale, eps, _ptr(d_x), _ptr(d_residual),
-                                _ptr(d_w_pre), _ptr(d_w_post), _ptr(d_gate), _ptr(ws), ws.numel(), _stream()),
-           "moe_block_norm_backward")
-    return dict(d_x=d_x, d_residual=d_residual, d_w_pre=d_w_pre, d_w_post=d_w_post, d_gate=d_gate)
+    return dict(zip(_NORM_GRADIENTS, _native.block_norm_backward(
+        d_y, d_residual_out, x, residual_out, w_pre, w_post, gate, scale, eps, d_x, d_residual, d_w_pre, d_w_post, d_gate,
+        ws)))
 
 
 # ------------------------------------------------------------------ grouped GEMM
@@ -576,13 +443,7 @@ def nvfp4_fold_scales(w1_sf, gs_gate, gs_up, gs1=None):
 
 def int8_quantize_rows(x, q=None, scale=None):
     """x BF16 or float32 [M, K] -> (q int8 [M, K], scale float32 [M] = row amax * (1 / 127))."""
-    dt = _float_dev(x, "x")
-    M, K = _matrix(x, "x")
-    q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else _buf(q, torch.int8, M * K, "q")
-    scale = (torch.empty(M, dtype=torch.float32, device=x.device) if scale is None
-             else _buf(scale, torch.float32, M, "scale"))
-    _check(_int8_rows(_ptr(x), dt, M, K, _ptr(q), _ptr(scale), _stream()), "int8_quantize_rows")
-    return q, scale
+    return _native.quantize_rows(x, q, scale)
 
 
 def int8_gemm_ws_bytes(M, N, K) -> int:
@@ -592,22 +453,13 @@ def int8_gemm_ws_bytes(M, N, K) -> int:
 def int8_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, d=None, ws=None):
     """a_q int8 [M, K], a_scale float32 [M], b_q int8 [N, K], b_scale float32 [N] -> BF16 [M, N] (EPI_BF16), or
     [M, N / 2] of silu(gate) * up with the gate rows of b_q first (EPI_SILU_MUL); add: BF16 of that shape."""
-    _dev(a_q, torch.int8, "a_q")
-    _dev(b_q, torch.int8, "b_q")
-    M, K = _matrix(a_q, "a_q")
-    N = _matrix(b_q, "b_q")[0]
-    _shape(b_q, (N, K), "b_q")
-    _opt(a_scale, torch.float32, (M,), "a_scale")
-    _opt(b_scale, torch.float32, (N,), "b_scale")
-    n_out = N // 2 if epilogue == EPI_SILU_MUL else N
-    _opt(add, torch.bfloat16, (M, n_out), "add")
-    d = (torch.empty(M, n_out, dtype=torch.bfloat16, device=a_q.device) if d is None
-         else _buf(d, torch.bfloat16, M * n_out, "d"))
-    need = _int8_gemm_ws(M, N, K) if ws is None else 0
-    ws = (_alloc_ws(need, a_q.device) if need else None) if ws is None else _buf(ws, torch.uint8, 0, "ws")
-    _check(_int8_gemm(_ptr(a_q), _ptr(a_scale), _ptr(b_q), _ptr(b_scale), M, N, K, epilogue, _ptr(add), _ptr(d),
-                      _ptr(ws), 0 if ws is None else ws.numel(), _stream()), "int8_gemm")
-    return d
+    return _native.gemm(a_q, a_scale, b_q, b_scale, epilogue, add, d, ws)
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 class Int8FFNWeights:
@@ -622,8 +474,8 @@ class Int8FFNWeights:
         _shape(w2_q, (self.hidden, self.inter), "w2_q")
         if two_i % 2:
             raise ValueError(f"w1_q: an even number of rows (gate and up), got {two_i}")
-        _opt(w1_scale, torch.float32, (two_i,), "w1_scale")
-        _opt(w2_scale, torch.float32, (self.hidden,), "w2_scale")
+        for scale, rows, name in ((w1_scale, two_i, "w1_scale"), (w2_scale, self.hidden, "w2_scale")):
+            _shape(_dev(scale, torch.float32, name), (rows,), name)
         self.w1_q, self.w1_scale, self.w2_q, self.w2_scale = w1_q, w1_scale, w2_q, w2_scale
 
 
@@ -642,18 +494,7 @@ def int8_ffn_forward(weights: Int8FFNWeights, x, add=None, out=None, ws=None):
     """Dense expert FFN of x BF16 [T, H] in 8-bit integers -> BF16 [T, H], plus add (BF16 [T, H], such as the routed
     experts' output; may be out) when given."""
     w = weights
-    _dev(x, torch.bfloat16, "x")
-    T = _matrix(x, "x")[0]
-    _shape(x, (T, w.hidden), "x")
-    _dev(w.w1_q, torch.int8, "weights.w1_q")
-    _opt(add, torch.bfloat16, (T, w.hidden), "add")
-    out = (torch.empty(T, w.hidden, dtype=torch.bfloat16, device=x.device) if out is None
-           else _buf(out, torch.bfloat16, T * w.hidden, "out"))
-    ws = (_alloc_ws(int8_ffn_ws_bytes(T, w.hidden, w.inter), x.device) if ws is None
-          else _buf(ws, torch.uint8, 0, "ws"))
-    _check(_int8_ffn(_ptr(w.w1_q), _ptr(w.w1_scale), _ptr(w.w2_q), _ptr(w.w2_scale), _ptr(x), T, w.hidden, w.inter,
-                     _ptr(add), _ptr(out), _ptr(ws), ws.numel(), _stream()), "int8_ffn_forward")
-    return out
+    return _native.ffn(w.w1_q, w.w1_scale, w.w2_q, w.w2_scale, x, add, out, ws)
 
 
 # --------------------------------------------------------------------- the layer

@@ -150,3 +150,29 @@ def test_int8(nv):
     for bad in ("w1", "s1", "w2", "s2", "x", "out", "ws"):
         assert ffn(**{bad: None}) == NULL and ffn(**{bad: ODD}) == ALIGN, bad
     assert ffn(add=ODD) == ALIGN and ffn(n=need - 1) == WORKSPACE and ffn(T=0, x=None, out=None) == 0
+
+
+def test_sizes_past_a_grid(nv):
+    assert nv._gate_topk(P, 1, None, None, 1 << 26, 4, 1, 0, 1, 1, 1, 1.0, P, P, None) == SHAPE
+    assert nv._balance(P, 1, P, None, None, 1, 1 << 26, 4, 1, 0, P, P, P, P, 1 << 40, None) == SHAPE
+    assert nv._gate_backward(P, 1, P, None, 1 << 26, 4, 1, 0, 1, 1.0, P, None, None, None, None, 1, P, None) == SHAPE
+    assert nv._int8_rows(P, 0, 64 * 65535 + 1, 64, P, P, None) == SHAPE
+
+
+def test_calls_refuse_what_is_no_gpu_tensor(nv):
+    """The Python calls look at their tensors first: nothing here needs a device."""
+    import torch
+    x, ids = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32)
+    q, s = torch.zeros(4, 16, dtype=torch.int8), torch.zeros(4)
+    calls = [lambda: nv.moe_gate_topk(x, 2), lambda: nv.moe_balance_loss(x, ids),
+             lambda: nv.moe_gate_backward(x, ids, d_topk_w=x), lambda: nv.moe_block_norm(x, x),
+             lambda: nv.moe_block_norm_backward(None, x, x, x), lambda: nv.int8_quantize_rows(x),
+             lambda: nv.int8_gemm(q, s, q, s), lambda: nv.prepare_int8_weights(x, x, x.t()),
+             lambda: nv.moe_gate_topk(x.half(), 2), lambda: nv.int8_gemm(q, None, q, s), lambda: nv.int8_gemm(None, s, q, s)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    for call in (lambda: nv.moe_gate_topk([[1.0]], 1), lambda: nv.moe_block_norm("x", x), lambda: nv._native.gemm(q)):
+        with pytest.raises(TypeError):
+            call()
