@@ -114,14 +114,6 @@ __device__ __forceinline__ float near_exp(float x) {
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e * kLn2, rest, e);
 }
-// Score for a key (see gate_topk_kernel for what float keys may be off by).
-__device__ __forceinline__ float key_score(float x, int score) {
-  return score == MOE_SCORE_SIGMOID ? __builtin_amdgcn_rcpf(1.0f + near_exp(-x)) : fast_sqrt_softplus<false>(x, nullptr);
-}
-__device__ __forceinline__ double key_score(double x, int score) { return pointwise_score(x, score); }
-__device__ __forceinline__ float key_exp(float x) { return near_exp(x); }
-__device__ __forceinline__ double key_exp(double x) { return exp(x); }
-
 // Bits of a key in the order of unsigned integers (-0 as 0).
 __device__ __forceinline__ uint32_t order_bits(float key) {
   const uint32_t bits = __float_as_uint(key + 0.0f);
@@ -135,66 +127,86 @@ struct GateShape {
   float scale;
 };
 
-// Key of every logit of the lane, in F (float or double): the logits
-// themselves when the order of scores is theirs (no bias, one group).
-// *bmax: the lane's largest |bias|.
-template <typename F, int VPT>
-__device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bias, const GateShape& g, F (&key)[VPT],
-                                          float* bmax) {
+// Float key of every logit of the lane: the logits themselves when the order
+// of scores is theirs (no bias, one group). *bmax: the lane's largest |bias|.
+template <int VPT>
+__device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bias, const GateShape& g,
+                                          float (&key)[VPT], float* bmax) {
   const int lane = threadIdx.x & 63;
   *bmax = 0.0f;
-  const F inf = (F)kInf;
   if (!bias && g.n_group == 1) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) key[v] = (F)x[v];
+    for (int v = 0; v < VPT; ++v) key[v] = x[v];
     return;
   }
   if (g.score == MOE_SCORE_SOFTMAX) {
-    F top = -inf, sum = 0;
+    float top = -kInf, sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) top = (F)x[v] > top ? (F)x[v] : top;
+    for (int v = 0; v < VPT; ++v) top = fmaxf(top, x[v]);
     top = wave_all_max(top);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      key[v] = x[v] > -kInf ? key_exp((F)x[v] - top) : (F)0;
+      key[v] = x[v] > -kInf ? near_exp(x[v] - top) : 0.0f;
       sum += key[v];
     }
-    sum = (F)1 / wave_all_sum(sum);
+    sum = 1.0f / wave_all_sum(sum);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) key[v] *= sum;
+  } else if (g.score == MOE_SCORE_SIGMOID) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) key[v] = __builtin_amdgcn_rcpf(1.0f + near_exp(-x[v]));
   } else {
-    if (g.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) key[v] = key_score((F)x[v], MOE_SCORE_SIGMOID);
-    } else {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) key[v] = key_score((F)x[v], MOE_SCORE_SQRT_SOFTPLUS);
-    }
+    for (int v = 0; v < VPT; ++v) key[v] = fast_sqrt_softplus<false>(x[v], nullptr);
   }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     if (bias) {
       const float b = bias[min(v * 64 + lane, g.E - 1)];
       *bmax = fmaxf(*bmax, fabsf(b));
-      key[v] += (F)b;
+      key[v] += b;
     }
-    if (!(x[v] > -kInf)) key[v] = -inf;
+    if (!(x[v] > -kInf)) key[v] = -kInf;
   }
 }
 
-// Drops the experts of the groups that are not kept: a group's value is the
-// sum of its two highest keys; the topk_group highest values stay, ties to the
-// lower group. Returns how far apart the last kept and the first dropped value
-// are, relative to their size (float keys: whether float64 could decide
-// otherwise), in *gap and *size. keys: LDS, E of them, this wave's own.
-template <typename F, int VPT>
-__device__ __forceinline__ void keep_groups(F (&key)[VPT], const GateShape& g, F* keys, F* gap, F* size) {
+// The same in float64, one logit at a time. For softmax, of a row whose
+// highest logit and 1 / (sum of e^(x - highest)) are given.
+struct ExactRow {
+  double top, inv;
+};
+template <typename L>
+__device__ __forceinline__ ExactRow exact_row(const L* logits, size_t row, const GateShape& g) {
+  ExactRow r = {0.0, 0.0};
+  if (g.score != MOE_SCORE_SOFTMAX) return r;
+  const int lane = threadIdx.x & 63;
+  float top = -kInf;
+#pragma unroll 1
+  for (int e = lane; e < g.E; e += 64) top = fmaxf(top, load_logit(logits, row + e));
+  r.top = wave_all_max(top);
+  double sum = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < g.E; e += 64) {
+    const float x = load_logit(logits, row + e);
+    sum += x > -kInf ? exp((double)x - r.top) : 0.0;
+  }
+  r.inv = 1.0 / wave_all_sum(sum);
+  return r;
+}
+__device__ __forceinline__ double exact_key(float x, float bias, const ExactRow& r, int score) {
+  const double s = score == MOE_SCORE_SOFTMAX ? exp((double)x - r.top) * r.inv : pointwise_score((double)x, score);
+  return x > -kInf ? s + (double)bias : (double)-kInf;
+}
+
+// Which groups stay: a group's value is the sum of its two highest keys; the
+// topk_group highest values stay, ties to the lower group. Bit per * i of
+// *stays is group i's. Tells how far apart the last kept and the first dropped
+// value are, and their size, in *gap and *size (float keys: whether float64
+// could decide otherwise). keys: LDS, E of them, this wave's own.
+template <typename F>
+__device__ __forceinline__ int choose_groups(const F* keys, const GateShape& g, uint64_t* stays, F* gap, F* size) {
   const int lane = threadIdx.x & 63;
   const F inf = (F)kInf;
-#pragma unroll
-  for (int v = 0; v < VPT; ++v)
-    if (v * 64 + lane < g.E) keys[v * 64 + lane] = key[v];
-  wave_lds_fence();
   int per = 64;  // lanes per group: a power of two, per * n_group <= 64
   while (per * g.n_group > 64) per >>= 1;
   const int mine = lane / per, sub = lane % per;
@@ -225,36 +237,72 @@ __device__ __forceinline__ void keep_groups(F (&key)[VPT], const GateShape& g, F
       rank += (o > value || (o == value && j < mine)) ? 1 : 0;
     }
   }
-  const bool kept = mine < g.n_group && rank < g.topk_group;
-  const F lowest = -wave_all_max(kept ? -value : -inf);
-  const F highest = wave_all_max(mine < g.n_group && !kept ? value : -inf);
+  const bool there = mine < g.n_group;
+  *stays = __ballot(there && rank < g.topk_group);
+  // the lanes of the last kept and the first dropped group (the latter is there if any is)
+  const uint64_t last = __ballot(there && rank == g.topk_group - 1), first = __ballot(there && rank == g.topk_group);
+  const F lowest = lane_value(value, __ffsll((unsigned long long)last) - 1);
+  const F highest = first ? lane_value(value, __ffsll((unsigned long long)first) - 1) : -inf;
   *gap = lowest - highest;
   *size = fmax(fabs(lowest), fabs(highest));
-  const uint64_t stays = __ballot(kept);
+  return per;
+}
+
+// The whole row's float64 keys, in LDS (E of them, this wave's own).
+template <typename L>
+__device__ __forceinline__ void exact_keys(const L* logits, size_t row, const float* bias, const GateShape& g,
+                                           double* keys) {
+  const ExactRow r = exact_row(logits, row, g);
+#pragma unroll 1
+  for (int e = threadIdx.x & 63; e < g.E; e += 64)
+    keys[e] = exact_key(load_logit(logits, row + e), bias ? bias[e] : 0.0f, r, g.score);
+  wave_lds_fence();
+}
+
+// Drops the float keys of the groups that do not stay, by float64 keys where
+// the last kept and the first dropped value are too close: a value is a sum of
+// two keys, each score + bias, |bias| <= bmax.
+template <typename L, int VPT>
+__device__ __forceinline__ void keep_groups(const L* logits, size_t row, const float* bias, float (&key)[VPT],
+                                            const GateShape& g, float tol, float bmax, double* lds) {
+  const int lane = threadIdx.x & 63;
+  float* const keys = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+    if (v * 64 + lane < g.E) keys[v * 64 + lane] = key[v];
+  wave_lds_fence();
+  uint64_t stays;
+  float gap, size;
+  const uint32_t per = choose_groups(keys, g, &stays, &gap, &size);
+  if (g.topk_group < g.n_group && !(gap > 4.0f * tol * (size + 2.0f * wave_all_max(bmax)))) {
+    double gap64, size64;
+    wave_lds_fence();
+    exact_keys(logits, row, bias, g, lds);
+    choose_groups(lds, g, &stays, &gap64, &size64);
+  }
   const uint32_t magic = ((1u << 20) + (uint32_t)g.group_size - 1u) / (uint32_t)g.group_size;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     // e / group_size: exact for e, group_size <= 1024
     const uint32_t grp = ((uint32_t)(v * 64 + lane) * magic) >> 20;
-    if (!((stays >> ((grp * (uint32_t)per) & 63u)) & 1u)) key[v] = -inf;
+    if (!((stays >> ((grp * per) & 63u)) & 1u)) key[v] = -kInf;
   }
   wave_lds_fence();
 }
 
 // The `want` highest keys, one wave maximum at a time, ties to the lowest
 // expert: lane j < want gets the j-th (id -1 when none is left).
-template <typename F, int VPT>
-__device__ __forceinline__ void pick_by_rounds(F (&key)[VPT], int want, int* id, F* at) {
+template <int VPT>
+__device__ __forceinline__ void pick_by_rounds(float (&key)[VPT], int want, int* id, float* at) {
   const int lane = threadIdx.x & 63;
-  const F inf = (F)kInf;
   *id = -1;
-  *at = -inf;
+  *at = -kInf;
   for (int r = 0; r < want; ++r) {
-    F top = -inf;
+    float top = -kInf;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) top = fmax(top, key[v]);
+    for (int v = 0; v < VPT; ++v) top = fmaxf(top, key[v]);
     top = wave_all_max(top);
-    if (!(top > -inf)) break;
+    if (!(top > -kInf)) break;
     int e = 0x7FFFFFFF;
 #pragma unroll
     for (int v = VPT - 1; v >= 0; --v)
@@ -262,7 +310,7 @@ __device__ __forceinline__ void pick_by_rounds(F (&key)[VPT], int want, int* id,
     e = wave_all_min_i32(e);
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      if (v * 64 + lane == e) key[v] = -inf;
+      if (v * 64 + lane == e) key[v] = -kInf;
     if (lane == r) {
       *id = e;
       *at = top;
@@ -270,22 +318,21 @@ __device__ __forceinline__ void pick_by_rounds(F (&key)[VPT], int want, int* id,
   }
 }
 
-// The `want` highest float keys for k <= 16, without a chain of wave maxima.
-// The wave's lanes fall into `groups` >= k runs; the lowest of the runs' maxima
-// is at most the groups-th highest key, so the keys from it on (about 17 of
-// 384 for 8 runs) hold the k highest. They are compacted in expert order, one
-// per lane, and each counts those before it. Returns false, having done
-// nothing, when more than 64 remain (many equal keys); *all tells whether the
-// want-th is among them. (16384 x 384 and k = 8: 28 us, by rounds 36; k = 16:
-// 32 and 44; k = 2: 7.6 and 7.3. Past 16 the runs would be single lanes.)
+// The `want` highest keys for k <= 16, without a chain of wave maxima. The
+// wave's lanes fall into `groups` >= k runs; the lowest of the runs' maxima is
+// at most the groups-th highest key, so the keys from it on (about 17 of 384
+// for 8 runs) hold the k highest. They are compacted in expert order, one per
+// lane, and each counts those before it. Returns false, having done nothing,
+// when more than 64 remain (many equal keys); *all tells whether the want-th is
+// among them. (16384 x 384 and k = 8: 20.7 us, by rounds 29; k = 16: 26 and
+// 37; k = 2: 7.3 and 7.1. Past 16 the runs would be single lanes.)
 constexpr int kFastK = 16;
-template <int VPT>
-__device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, int want, uint2* lds, int* id, float* at,
-                                              bool* all) {
-  const int lane = threadIdx.x & 63;
-  float m = key[0];
-#pragma unroll
-  for (int v = 1; v < VPT; ++v) m = fmaxf(m, key[v]);
+struct Picked {  // a compacted key with its expert
+  float key;
+  int32_t id;
+};
+// The lowest of the runs' maxima, from each lane's maximum m.
+__device__ __forceinline__ float lowest_run(float m, int k) {
   const auto up = [](float a, float b) { return fmaxf(a, b); };
   const auto down = [](float a, float b) { return fminf(a, b); };
   // steps 1, 2, 4, 8, 16, 32 of the reduction: maxima inside a run, then minima over the runs
@@ -297,7 +344,40 @@ __device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, in
   u32x2_t r = rows16(__float_as_uint(m));
   m = k <= 2 ? up(__uint_as_float(r[0]), __uint_as_float(r[1])) : down(__uint_as_float(r[0]), __uint_as_float(r[1]));
   r = rows32(__float_as_uint(m));
-  m = k <= 1 ? up(__uint_as_float(r[0]), __uint_as_float(r[1])) : down(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  return k <= 1 ? up(__uint_as_float(r[0]), __uint_as_float(r[1]))
+                : down(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+// How many of the n lanes' keys come before this lane's: a higher key, or the
+// same in a lower lane.
+__device__ __forceinline__ int rank_of(float key, int n) {
+  const int lane = threadIdx.x & 63;
+  // one comparison, of the key's bits (in an order of integers) above the place
+  const uint32_t order = order_bits(key);
+  const uint64_t mine = ((uint64_t)order << 32) | (uint32_t)(63 - lane);
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)order, j) << 32) | (uint32_t)(63 - j);
+    rank += other > mine ? 1 : 0;
+  }
+  return rank;
+}
+__device__ __forceinline__ int rank_of(double key, int n) {
+  const int lane = threadIdx.x & 63;
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double other = lane_value(key, j);
+    rank += other > key || (other == key && j < lane) ? 1 : 0;
+  }
+  return rank;
+}
+template <int VPT>
+__device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, int want, Picked* lds, int* id, float* at,
+                                              bool* all) {
+  const int lane = threadIdx.x & 63;
+  float m = key[0];
+#pragma unroll
+  for (int v = 1; v < VPT; ++v) m = fmaxf(m, key[v]);
+  m = lowest_run(m, k);
   uint64_t mine[VPT];
   int n = 0;
 #pragma unroll
@@ -309,40 +389,88 @@ __device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, in
   int before = 0;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    if ((mine[v] >> lane) & 1u)
-      lds[before + __popcll(mine[v] & ((1ull << lane) - 1ull))] = make_uint2(__float_as_uint(key[v]), v * 64 + lane);
+    if ((mine[v] >> lane) & 1u) lds[before + __popcll(mine[v] & ((1ull << lane) - 1ull))] = {key[v], v * 64 + lane};
     before += __popcll(mine[v]);
   }
   wave_lds_fence();
-  const uint2 c = lds[lane];  // past n: left over, never counted
-  // higher key first, then the lower place: one comparison of the key's bits
-  // (in an order of integers) above the place
-  const uint32_t order = order_bits(__uint_as_float(c.x));
-  const uint64_t mine64 = ((uint64_t)order << 32) | (uint32_t)(63 - lane);
-  int rank = 0;
-  for (int j = 0; j < n; ++j) {
-    const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)order, j) << 32) | (uint32_t)(63 - j);
-    rank += other > mine64 ? 1 : 0;
-  }
+  const Picked c = lds[lane];  // past n: left over, never counted
+  const int rank = rank_of(c.key, n);
   wave_lds_fence();
   if (lane < n && rank < want) lds[rank] = c;
   wave_lds_fence();
   const int have = min(n, want);
-  const uint2 got = lds[lane];
-  *id = lane < have ? (int)got.y : -1;
-  *at = lane < have ? __uint_as_float(got.x) : -kInf;
+  const Picked got = lds[lane];
+  *id = lane < have ? got.id : -1;
+  *at = lane < have ? got.key : -kInf;
   *all = n >= want;
   wave_lds_fence();
   return true;
 }
 
-// The weights of the choices (lane j < k: expert id) and the stores.
+// The k highest by float64 keys, where the k highest float keys (lane j: the
+// j-th, expert *id) are within `slack` of keys that may belong before them:
+// the experts down to the k-th key - slack, one exact key per lane; or, if
+// these are more than 64, the whole row's keys in LDS, one maximum at a time.
 template <typename L, int VPT>
-__device__ __forceinline__ void write_choices(const L* logits, size_t row, const float (&x)[VPT], const GateShape& g,
-                                              int id, size_t t, int32_t* ids, float* w) {
+__device__ __forceinline__ void pick_exact(const L* logits, size_t row, const float* bias, const GateShape& g,
+                                           const float (&key)[VPT], float at, float slack, Picked* picked,
+                                           double* keys, int* id) {
+  const int lane = threadIdx.x & 63;
+  const float from = lane_value(at, g.k - 1) - slack;  // of -inf: all there are
+  int n = 0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) n += __popcll(__ballot(key[v] >= from && key[v] > -kInf));
+  if (n <= 64) {
+    int before = 0;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const uint64_t mine = __ballot(key[v] >= from && key[v] > -kInf);
+      if ((mine >> lane) & 1u) picked[before + __popcll(mine & ((1ull << lane) - 1ull))].id = v * 64 + lane;
+      before += __popcll(mine);
+    }
+    wave_lds_fence();
+    const int e = lane < n ? picked[lane].id : 0;
+    const double key64 =
+        exact_key(load_logit(logits, row + e), bias ? bias[e] : 0.0f, exact_row(logits, row, g), g.score);
+    const int rank = rank_of(key64, n);
+    wave_lds_fence();
+    if (lane < n && rank < g.k) picked[rank].id = e;
+    wave_lds_fence();
+    *id = lane < min(n, g.k) ? picked[lane].id : -1;
+    return;
+  }
+  exact_keys(logits, row, bias, g, keys);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)  // the dropped groups
+    if (v * 64 + lane < g.E && !(key[v] > -kInf)) keys[v * 64 + lane] = -kInf;
+  *id = -1;
+#pragma unroll 1
+  for (int j = 0; j < g.k; ++j) {
+    double top = -kInf;
+    int first = 0x7FFFFFFF;  // this lane's first expert with its highest key
+#pragma unroll 1
+    for (int e = lane; e < g.E; e += 64) {  // each lane reads and writes its own
+      const double k64 = keys[e];
+      if (k64 > top) {
+        top = k64;
+        first = e;
+      }
+    }
+    const double best = wave_all_max(top);
+    if (!(best > (double)-kInf)) break;
+    const int e = wave_all_min_i32(top == best ? first : 0x7FFFFFFF);
+    if (lane == j) *id = e;
+    if (lane == (e & 63)) keys[e] = -kInf;
+  }
+}
+
+// The weights of the choices (lane j < k: expert id, its logit xl) and the stores.
+template <int VPT>
+__device__ __forceinline__ void write_choices(const float (&x)[VPT], const GateShape& g, int id, float xl, size_t t,
+                                              int32_t* ids, float* w) {
   const int lane = threadIdx.x & 63;
   const bool on = lane < g.k && id >= 0;
-  const float xl = on ? load_logit(logits, row + (on ? id : 0)) : -kInf;
+  if (!on) xl = -kInf;
   float s;
   if (g.score == MOE_SCORE_SOFTMAX) {
     if (g.renormalize) {  // the softmax over the choices alone: nothing of the row's sum is left in it
@@ -375,16 +503,24 @@ __device__ __forceinline__ void write_choices(const L* logits, size_t row, const
 // float64; float32 keys decide it wherever two neighbours are further apart
 // than their rounding (2^-20 of the scores for the sigmoid; 2^-17 for softmax,
 // whose argument x - max is rounded first, and for sqrt-softplus, from the
-// hardware's logarithm) or are the same sum of the same numbers, and the row
-// is done again in float64 where they are not (0.4 % of the rows at 16384 x 256
-// with a bias and groups).
+// hardware's logarithm) or are the same sum of the same numbers. Where they are
+// not, float64 keys decide: those of the candidates, one per lane (of every
+// expert, 16384 x 384 by sqrt-softplus took 33 us instead of 20.7, and the
+// registers that this needed left six waves on a SIMD).
+//
+// Bound by the instructions of choosing: 16384 x 256 BF16 with bias and 8
+// groups takes 20.5 us, 570 vector instructions a token, 70 % of the time
+// issuing them (its 8 MB take 1.8 us); 16384 x 256 by the logits alone 7.3.
+// Eight waves on a SIMD (64 registers; the float64 paths spill a few there):
+// 8192 x 384 8.0 us, with seven 8.9; 16384 x 384 20, with four 26. With 16
+// logits per lane five fit: 16384 x 1024 38 us, with four 41.
 template <typename L, int VPT>
-__global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __restrict__ logits,
+__global__ __launch_bounds__(64 * kGateWaves, VPT <= 8 ? 8 : 5) void gate_topk_kernel(const L* __restrict__ logits,
                                                                     const float* __restrict__ bias,
                                                                     const uint8_t* __restrict__ mask, GateShape g,
                                                                     int32_t* __restrict__ ids, float* __restrict__ w) {
-  extern __shared__ double lds[];
-  __shared__ uint2 picked[kGateWaves][64];
+  extern __shared__ double lds[];  // unless the keys are the logits: [kGateWaves][E]
+  __shared__ Picked picked[kGateWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
   if (t >= g.T) return;
@@ -405,37 +541,38 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_topk_kernel(const L* __r
   float at;
   float bmax;
   gate_keys(x, bias, g, key, &bmax);
-  bool doubt = false;
+  double* const keys = lds + (size_t)wave * g.E;
   const float tol = g.score == MOE_SCORE_SIGMOID ? 0x1p-20f : 0x1p-17f;
-  if (g.n_group > 1) {
-    float gap, size;
-    keep_groups(key, g, reinterpret_cast<float*>(lds + (size_t)wave * g.E), &gap, &size);
-    // a value is a sum of two keys, each score + bias, |bias| <= bmax
-    bmax = wave_all_max(bmax);
-    doubt = !(gap > 4.0f * tol * (size + 2.0f * bmax));
-    if (g.topk_group == g.n_group) doubt = false;
-  }
+  if (g.n_group > 1) keep_groups(logits, row, bias, key, g, tol, bmax, keys);
   const int want = by_logit ? g.k : min(g.k + 1, 64);
   bool all = true;
-  if (g.k > kFastK || !pick_by_count(key, g.k, want, picked[wave], &id, &at, &all)) pick_by_rounds(key, want, &id, &at);
+  const bool counted = g.k <= kFastK && pick_by_count(key, g.k, want, picked[wave], &id, &at, &all);
+  if (!counted) pick_by_rounds(key, want, &id, &at);
+  float xl = at;
   if (!by_logit) {
-    const float xl = id >= 0 ? load_logit(logits, row + id) : -kInf;
-    const float bl = id >= 0 && bias ? bias[id] : 0.0f;
+    xl = load_logit(logits, row + max(id, 0));
+    const float bl = bias ? bias[max(id, 0)] : 0.0f;
     const float next = __shfl_down(at, 1, 64), xn = __shfl_down(xl, 1, 64), bn = __shfl_down(bl, 1, 64);
     const int idn = __shfl_down(id, 1, 64);
     const bool same = xl == xn && bl == bn;
     const float size = fabsf(at) + fabsf(next) + fabsf(bl) + fabsf(bn);
     const bool close = lane + 1 < want && idn >= 0 && !same && !(at - next > 2.0f * tol * size);
-    doubt = doubt || __ballot(close) != 0 || want == g.k || !all;  // !all: the first key left out is unknown
+    if (__ballot(close) != 0 || want == g.k || !all) {  // !all: the first key left out is unknown
+      if (!counted) {  // the rounds took the picked keys out
+        for (int j = 0; j < want; ++j) {
+          const int e = __builtin_amdgcn_readlane(id, j);
+          const float k32 = lane_value(at, j);
+#pragma unroll
+          for (int v = 0; v < VPT; ++v)
+            if (v * 64 + lane == e) key[v] = k32;
+        }
+      }
+      const float kth = lane_value(at, g.k - 1), slack = 4.0f * tol * (fabsf(kth) + 2.0f * wave_all_max(bmax));
+      pick_exact(logits, row, bias, g, key, at, slack, picked[wave], keys, &id);
+      xl = load_logit(logits, row + max(id, 0));
+    }
   }
-  if (doubt) {
-    double key64[VPT], gap, size, at64;
-    gate_keys(x, bias, g, key64, &bmax);
-    if (g.n_group > 1) keep_groups(key64, g, lds + (size_t)wave * g.E, &gap, &size);
-    pick_by_rounds(key64, g.k, &id, &at64);
-  }
-  if (lane >= g.k) id = -1;
-  write_choices(logits, row, x, g, id, (size_t)t, ids, w);
+  write_choices(x, g, id, xl, (size_t)t, ids, w);
 }
 
 // ---------------------------------------------------------------- balance loss
@@ -546,6 +683,10 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
   return true;
 }
 
+// A wave's tokens one after the other, their scores summed in its registers,
+// then the waves' in LDS; choices counted by LDS atomics on whole numbers.
+// (16384 x 384 float: 12.4 us, 2 TB/s; about half of it issues the 200 vector
+// instructions a token, the rest is the launch and the first row's latency.)
 template <typename L, int VPT>
 __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const L* __restrict__ logits,
                                                                           const int32_t* __restrict__ ids,
@@ -567,11 +708,21 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
   for (int v = 0; v < VPT; ++v) acc[v] = 0.0f;
   double z = 0.0;
   int n = 0;
-  for (int t = span.begin + wave; t < span.end; t += kGateWaves) {
-    if (mask && mask[t] == 0) continue;
+  float next[VPT];
+  int next_id = -1, next_on = 0;
+  const auto load = [&](int t) {
+    load_row(logits, (size_t)t * g.E, g.E, next);
+    next_id = ids[(size_t)t * g.k + min(lane, g.k - 1)];
+    next_on = mask ? mask[t] : 1;
+  };
+  if (span.begin + wave < span.end) load(span.begin + wave);
+  for (int t = span.begin + wave; t < span.end; t += kGateWaves) {  // with the next row's loads in flight
     float x[VPT], q[VPT], p[VPT], unused[VPT];
-    load_row(logits, (size_t)t * g.E, g.E, x);
-    const int id = lane < g.k ? ids[(size_t)t * g.k + lane] : -1;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) x[v] = next[v];
+    const int id = lane < g.k ? next_id : -1, on = next_on;
+    load(min(t + kGateWaves, span.end - 1));
+    if (!on) continue;
     RowSums r;
     if (!row_scores<false>(x, g.score, q, p, unused, &r)) continue;
     if (id >= 0 && id < g.E) atomicAdd(&hist[id], 1);
@@ -758,6 +909,8 @@ __global__ __launch_bounds__(64 * kLossWaves) void balance_loss_kernel(BalanceSh
 //   balance  dq_e = g0 E counts_be / (B' N_b^2 k), then ds_e = (dq_e - sum dq q) / sum s
 //   z        2 g1 lse p_e / N
 // and dx_e = s'(x_e) ds_e, or p_e (ds_e - sum ds p) for softmax.
+// (16384 x 384 float, both losses: 16 us, 3.1 TB/s of logits and gradients;
+// three quarters of it issue the 420 vector instructions a token.)
 struct GateGradArgs {
   const int32_t* ids;
   const float* d_w;      // NULL: no gradient through the weights
@@ -928,7 +1081,7 @@ extern "C" int moe_gate_topk(const void* logits, int32_t logits_dtype, const flo
     return NVFP4_ERR_ALIGN;
   const GateShape g = {T, E, k, score, n_group, topk_group, E / n_group, renormalize, scale};
   const unsigned grid = (unsigned)((T + kGateWaves - 1) / kGateWaves);
-  const size_t lds = n_group > 1 ? (size_t)kGateWaves * E * sizeof(double) : 0;
+  const size_t lds = n_group > 1 || bias ? (size_t)kGateWaves * E * sizeof(double) : 0;
   return gate_by_width(E, [&](auto vpt) -> int {
     constexpr int VPT = decltype(vpt)::value;
     if (logits_dtype == NVFP4_DT_F32)

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle.gate as G
-from _block_cases import DEV, EPS32, HALF_BF16, gate_logits, grad_bound, guarded, to_dev, torch_dtype
+from _block_cases import DEV, EPS32, HALF_BF16, as_stored, gate_logits, grad_bound, guarded, to_dev, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +78,28 @@ def test_choices_and_weights(nv, c):
     span = np.minimum(200.0, np.abs(fin).max(1, keepdims=True) * 2) if c["score"] == G.SOFTMAX else 0.0
     tol = (16 + k + span) * EPS32 * ref_w + 2.5 * 2.0 ** -126
     assert (np.abs(got - ref_w) <= tol).all(), float(np.max(np.abs(got - ref_w) / np.maximum(ref_w, 1e-30)))
+
+
+@pytest.mark.parametrize("E,k,score,groups,top", [
+    (384, 8, G.SIGMOID, 1, 1), (40, 8, G.SIGMOID, 1, 1), (384, 20, G.SIGMOID, 1, 1), (1000, 16, G.SQRT_SOFTPLUS, 1, 1),
+    (63, 5, G.SQRT_SOFTPLUS, 1, 1), (256, 8, G.SIGMOID, 8, 4), (96, 5, G.SOFTMAX, 32, 7), (64, 4, G.SOFTMAX, 1, 1),
+    (512, 16, G.SOFTMAX, 4, 2), (300, 64, G.SIGMOID, 1, 1)])
+def test_crowded_keys(nv, E, k, score, groups, top):
+    """Rows whose keys lie closer together than float32 can tell apart: all of them, or a crowd around the k-th. The
+    logits differ by steps of 2^-24, the biases by about as much; float64 separates them by far more than its own
+    rounding."""
+    T = 34
+    rng = np.random.default_rng(E + k)
+    x = (0.5 + rng.integers(0, 400, (T, E)) * 2.0 ** -24)
+    x[::2] += np.where(rng.random((T // 2, E)) < 0.5, 0.0, -1.0)                 # half of the row out of question
+    x[::4, : k // 2] += 1.0                                                       # the first choices clear
+    x[1::4, ::3] = -np.inf
+    x = as_stored(x, "f32")
+    bias = (rng.standard_normal(E) * 1e-7).astype(np.float32)
+    ref_ids, _ = G.gate_topk(x, k, score, bias, None, groups, top, True, 1.0)
+    ids, _ = nv.moe_gate_topk(to_dev(x.astype(np.float32)), k, score=score, bias=to_dev(bias), n_group=groups,
+                              topk_group=top)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
 
 
 def seq_of(T, cu):
