@@ -166,6 +166,10 @@ constexpr int kNormCus = 256;
 template <typename X, typename R, int CH, bool QUANT>
 __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* residual, NormArgs a, R* residual_out,
                                                          X* y, const float* gs_in, uint8_t* y_q, uint8_t* y_sf) {
+  // Every rounding as the formulas have it (one of g and g_row is 1), so that a
+  // BF16 residual rounds as it does where they are computed step by step; a
+  // float y made from it would show each that went the other way.
+#pragma clang fp contract(off)
   constexpr bool KEEP = CH <= 2;
   __shared__ float scratch[4][kNormMaxWaves][1];
   __shared__ uint4 lut[QUANT ? kLutWords / 4 : 1];
@@ -201,10 +205,11 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
         }
       }
     }
-    float sig = a.scale * ((a.gate && a.gate_tokens) ? a.gate[t] : 1.0f);
+    const float g_row = (a.gate && a.gate_tokens) ? a.gate[t] : 1.0f;
+    float sig = 1.0f;
     if (a.w_post) {
       group_sums(at, s, scratch[parity]);
-      sig *= rsqrtf(s[0] * inv_h + a.eps);
+      sig = rsqrtf(s[0] * inv_h + a.eps);
     }
     s[0] = 0.0f;
 #pragma unroll
@@ -216,8 +221,8 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
         gate.get(at, c, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          f[c][i] = f[c][i] * sig * (w[i] * g[i]);
-          if (residual) f[c][i] += now.r[c].get(i);
+          f[c][i] = a.scale * (f[c][i] * sig * w[i] * (g[i] * g_row));
+          if (residual) f[c][i] = now.r[c].get(i) + f[c][i];
         }
         store8(residual_out + row + ch * 8, f[c]);
 #pragma unroll
