@@ -619,7 +619,7 @@ static int int8_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue) {
   if (epilogue != NVFP4_EPI_BF16 && epilogue != NVFP4_EPI_SILU_MUL) return NVFP4_ERR_ARG;
   if (M < 0 || N <= 0 || K <= 0 || K % 16 != 0 || K > kInt8MaxK) return NVFP4_ERR_SHAPE;
   if (N % (epilogue == NVFP4_EPI_SILU_MUL ? 16 : 8) != 0) return NVFP4_ERR_SHAPE;
-  if (M > kInt8MaxM) return NVFP4_ERR_SHAPE;
+  if (M > kInt8MaxM || N >= (1 << 27)) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 

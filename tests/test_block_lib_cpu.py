@@ -157,6 +157,8 @@ def test_sizes_past_a_grid(nv):
     assert nv._balance(P, 1, P, None, None, 1, 1 << 26, 4, 1, 0, P, P, P, P, 1 << 40, None) == SHAPE
     assert nv._gate_backward(P, 1, P, None, 1 << 26, 4, 1, 0, 1, 1.0, P, None, None, None, None, 1, P, None) == SHAPE
     assert nv._int8_rows(P, 0, 64 * 65535 + 1, 64, P, P, None) == SHAPE
+    assert nv._int8_gemm(P, P, P, P, 1, 1 << 27, 16, 0, None, P, None, 0, None) == SHAPE
+    assert nv._int8_gemm(P, P, P, P, 64 * 65535, 1 << 26, 16, 0, None, P, None, 0, None) == SHAPE
 
 
 def test_calls_refuse_what_is_no_gpu_tensor(nv):
