@@ -980,9 +980,8 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
         float ds = c;
         if (a.renormalize) {
           const float sum = wave_all_sum(s);
-          const float is = sum > 0.0f ? 1.0f / sum : 0.0f;
-          const float dot = wave_all_sum(c * s) * is;
-          ds = some ? (c - dot) * is : 0.0f;
+          const float dot = wave_all_sum(c * s) / sum;
+          ds = some && sum > 0.0f ? (c - dot) / sum : 0.0f;
         }
         if (softmax) {
           d = s * ds;
