@@ -685,7 +685,7 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
 
 // A wave's tokens one after the other, their scores summed in its registers,
 // then the waves' in LDS; choices counted by LDS atomics on whole numbers.
-// (16384 x 384 float: 12.4 us, 2 TB/s; about half of it issues the 200 vector
+// (16384 x 384 float: 12.4 us, 2 TB/s; about half of it issues the 220 vector
 // instructions a token, the rest is the launch and the first row's latency.)
 template <typename L, int VPT>
 __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const L* __restrict__ logits,
