@@ -331,21 +331,19 @@ struct Picked {  // a compacted key with its expert
   float key;
   int32_t id;
 };
-// The lowest of the runs' maxima, from each lane's maximum m.
-__device__ __forceinline__ float lowest_run(float m, int k) {
-  const auto up = [](float a, float b) { return fmaxf(a, b); };
-  const auto down = [](float a, float b) { return fminf(a, b); };
+// The lowest of the runs' maxima, from each lane's maximum.
+__device__ __forceinline__ float lowest_run(float highest, int k) {
   // steps 1, 2, 4, 8, 16, 32 of the reduction: maxima inside a run, then minima over the runs
-  const auto step = [&](bool inside, float other) { return inside ? up(m, other) : down(m, other); };
-  m = step(true, dpp_f32<kDppXor1>(m));
-  m = step(true, dpp_f32<kDppXor2>(m));
-  m = step(k <= 8, dpp_f32<kDppHalfMirror>(m));
-  m = step(k <= 4, dpp_f32<kDppMirror>(m));
-  u32x2_t r = rows16(__float_as_uint(m));
-  m = k <= 2 ? up(__uint_as_float(r[0]), __uint_as_float(r[1])) : down(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  r = rows32(__float_as_uint(m));
-  return k <= 1 ? up(__uint_as_float(r[0]), __uint_as_float(r[1]))
-                : down(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const auto step = [](bool inside, int a, int b) { return inside ? max(a, b) : min(a, b); };
+  int m = ordered(highest);
+  m = max(m, dpp_i32<kDppXor1>(m));
+  m = max(m, dpp_i32<kDppXor2>(m));
+  m = step(k <= 8, m, dpp_i32<kDppHalfMirror>(m));
+  m = step(k <= 4, m, dpp_i32<kDppMirror>(m));
+  u32x2_t r = rows16((uint32_t)m);
+  m = step(k <= 2, (int)r[0], (int)r[1]);
+  r = rows32((uint32_t)m);
+  return from_ordered(step(k <= 1, (int)r[0], (int)r[1]));
 }
 // How many of the n lanes' keys come before this lane's: a higher key, or the
 // same in a lower lane.

@@ -44,21 +44,32 @@ __device__ __forceinline__ float wave_all_f32(float v, Op op) {
 __device__ __forceinline__ float wave_all_sum(float v) {
   return wave_all_f32(v, [](float a, float b) { return a + b; });
 }
-__device__ __forceinline__ float wave_all_max(float v) {
-  return wave_all_f32(v, [](float a, float b) { return fmaxf(a, b); });
-}
-__device__ __forceinline__ float wave_all_min(float v) {
-  return wave_all_f32(v, [](float a, float b) { return fminf(a, b); });
+template <typename Op>
+__device__ __forceinline__ int wave_all_i32(int v, Op op) {
+  v = op(v, dpp_i32<kDppXor1>(v));
+  v = op(v, dpp_i32<kDppXor2>(v));
+  v = op(v, dpp_i32<kDppHalfMirror>(v));
+  v = op(v, dpp_i32<kDppMirror>(v));
+  u32x2_t r = rows16((uint32_t)v);
+  v = op((int)r[0], (int)r[1]);
+  r = rows32((uint32_t)v);
+  return op((int)r[0], (int)r[1]);
 }
 __device__ __forceinline__ int wave_all_min_i32(int v) {
-  v = min(v, dpp_i32<kDppXor1>(v));
-  v = min(v, dpp_i32<kDppXor2>(v));
-  v = min(v, dpp_i32<kDppHalfMirror>(v));
-  v = min(v, dpp_i32<kDppMirror>(v));
-  u32x2_t r = rows16((uint32_t)v);
-  v = min((int)r[0], (int)r[1]);
-  r = rows32((uint32_t)v);
-  return min((int)r[0], (int)r[1]);
+  return wave_all_i32(v, [](int a, int b) { return min(a, b); });
+}
+// A float's bits in the order of signed integers; its own inverse. Maxima and
+// minima of these take one instruction a step, with the lane move in it; those
+// of floats three (the move and a quieting of its result apart).
+__device__ __forceinline__ int ordered(float v) {
+  const int b = __builtin_bit_cast(int, v);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_ordered(int o) {
+  return __builtin_bit_cast(float, o ^ ((o >> 31) & 0x7FFFFFFF));
+}
+__device__ __forceinline__ float wave_all_max(float v) {
+  return from_ordered(wave_all_i32(ordered(v), [](int a, int b) { return max(a, b); }));
 }
 __device__ __forceinline__ double wave_all_max(double v) {
   for (int o = 1; o < 64; o <<= 1) v = fmax(v, __shfl_xor(v, o, 64));
