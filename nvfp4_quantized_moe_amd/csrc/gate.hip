@@ -248,6 +248,10 @@ __device__ __forceinline__ int choose_groups(const F* keys, const GateShape& g, 
   return per;
 }
 
+// Doubles of a wave's part of LDS: E float64 keys, or a float per lane and
+// register (64 VPT <= 2 E, but for E < 32).
+__host__ __device__ __forceinline__ int gate_keys_stride(int E) { return E < 32 ? 32 : E; }
+
 // The whole row's float64 keys, in LDS (E of them, this wave's own).
 template <typename L>
 __device__ __forceinline__ void exact_keys(const L* logits, size_t row, const float* bias, const GateShape& g,
@@ -268,8 +272,7 @@ __device__ __forceinline__ void keep_groups(const L* logits, size_t row, const f
   const int lane = threadIdx.x & 63;
   float* const keys = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int v = 0; v < VPT; ++v)
-    if (v * 64 + lane < g.E) keys[v * 64 + lane] = key[v];
+  for (int v = 0; v < VPT; ++v) keys[v * 64 + lane] = key[v];  // the wave's part holds 64 VPT floats
   wave_lds_fence();
   uint64_t stays;
   float gap, size;
@@ -349,13 +352,17 @@ __device__ __forceinline__ float lowest_run(float highest, int k) {
 // same in a lower lane.
 __device__ __forceinline__ int rank_of(float key, int n) {
   const int lane = threadIdx.x & 63;
-  // one comparison, of the key's bits (in an order of integers) above the place
-  const uint32_t order = order_bits(key);
+  // one comparison, of the key's bits (in an order of integers; 0 past n, before
+  // none) above the place; four lanes a turn
+  const uint32_t order = lane < n ? order_bits(key) : 0u;
   const uint64_t mine = ((uint64_t)order << 32) | (uint32_t)(63 - lane);
   int rank = 0;
-  for (int j = 0; j < n; ++j) {
-    const uint64_t other = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)order, j) << 32) | (uint32_t)(63 - j);
-    rank += other > mine ? 1 : 0;
+  for (int j = 0; j < n; j += 4) {  // n <= 64
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)order, j + u);
+      rank += (((uint64_t)o << 32) | (uint32_t)(63 - j - u)) > mine ? 1 : 0;
+    }
   }
   return rank;
 }
@@ -517,7 +524,7 @@ __global__ __launch_bounds__(64 * kGateWaves, VPT <= 8 ? 8 : 5) void gate_topk_k
                                                                     const float* __restrict__ bias,
                                                                     const uint8_t* __restrict__ mask, GateShape g,
                                                                     int32_t* __restrict__ ids, float* __restrict__ w) {
-  extern __shared__ double lds[];  // unless the keys are the logits: [kGateWaves][E]
+  extern __shared__ double lds[];  // unless the keys are the logits: [kGateWaves][gate_keys_stride(E)]
   __shared__ Picked picked[kGateWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kGateWaves + wave;
@@ -539,7 +546,7 @@ __global__ __launch_bounds__(64 * kGateWaves, VPT <= 8 ? 8 : 5) void gate_topk_k
   float at;
   float bmax;
   gate_keys(x, bias, g, key, &bmax);
-  double* const keys = lds + (size_t)wave * g.E;
+  double* const keys = lds + (size_t)wave * gate_keys_stride(g.E);
   const float tol = g.score == MOE_SCORE_SIGMOID ? 0x1p-20f : 0x1p-17f;
   if (g.n_group > 1) keep_groups(logits, row, bias, key, g, tol, bmax, keys);
   const int want = by_logit ? g.k : min(g.k + 1, 64);
@@ -1078,7 +1085,7 @@ extern "C" int moe_gate_topk(const void* logits, int32_t logits_dtype, const flo
     return NVFP4_ERR_ALIGN;
   const GateShape g = {T, E, k, score, n_group, topk_group, E / n_group, renormalize, scale};
   const unsigned grid = (unsigned)((T + kGateWaves - 1) / kGateWaves);
-  const size_t lds = n_group > 1 || bias ? (size_t)kGateWaves * E * sizeof(double) : 0;
+  const size_t lds = n_group > 1 || bias ? (size_t)kGateWaves * gate_keys_stride(E) * sizeof(double) : 0;
   return gate_by_width(E, [&](auto vpt) -> int {
     constexpr int VPT = decltype(vpt)::value;
     if (logits_dtype == NVFP4_DT_F32)
