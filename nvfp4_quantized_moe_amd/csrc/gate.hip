@@ -212,10 +212,16 @@ __device__ __forceinline__ int choose_groups(const F* keys, const GateShape& g, 
   const int mine = lane / per, sub = lane % per;
   F a = -inf, b = -inf;  // the two highest of this lane's share, a >= b
   if (mine < g.n_group)
-    for (int i = sub; i < g.group_size; i += per) {
-      const F v = keys[mine * g.group_size + i];
-      b = fmax(b, fmin(a, v));
-      a = fmax(a, v);
+    for (int i = sub; i < g.group_size; i += 4 * per) {  // four reads in flight
+      F v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = keys[mine * g.group_size + min(i + u * per, g.group_size - 1)];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const F w = i + u * per < g.group_size ? v[u] : -inf;
+        b = fmax(b, fmin(a, w));
+        a = fmax(a, w);
+      }
     }
   for (int o = 1; o < per; o <<= 1) {
     const F a2 = __shfl_xor(a, o, 64), b2 = __shfl_xor(b, o, 64);
