@@ -171,10 +171,17 @@ __device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bi
 }
 
 // The same in float64, one logit at a time. For softmax, of a row whose
-// highest logit and 1 / (sum of e^(x - highest)) are given.
+// highest logit and 1 / (sum of e^(x - highest)) are given. (Not inlined: the
+// constants of three float64 functions would take registers of the whole
+// kernel, which hardly ever calls them; 16384 x 512 in groups took 49 us
+// instead of 24.)
 struct ExactRow {
   double top, inv;
 };
+static __device__ __attribute__((noinline)) double exact_key(float x, float bias, ExactRow r, int score) {
+  const double s = score == MOE_SCORE_SOFTMAX ? exp((double)x - r.top) * r.inv : pointwise_score((double)x, score);
+  return x > -kInf ? s + (double)bias : (double)-kInf;
+}
 template <typename L>
 __device__ __forceinline__ ExactRow exact_row(const L* logits, size_t row, const GateShape& g) {
   ExactRow r = {0.0, 0.0};
@@ -186,16 +193,10 @@ __device__ __forceinline__ ExactRow exact_row(const L* logits, size_t row, const
   r.top = wave_all_max(top);
   double sum = 0.0;
 #pragma unroll 1
-  for (int e = lane; e < g.E; e += 64) {
-    const float x = load_logit(logits, row + e);
-    sum += x > -kInf ? exp((double)x - r.top) : 0.0;
-  }
+  for (int e = lane; e < g.E; e += 64)
+    sum += fmax(exact_key(load_logit(logits, row + e), 0.0f, {r.top, 1.0}, MOE_SCORE_SOFTMAX), 0.0);  // 0 at -inf
   r.inv = 1.0 / wave_all_sum(sum);
   return r;
-}
-__device__ __forceinline__ double exact_key(float x, float bias, const ExactRow& r, int score) {
-  const double s = score == MOE_SCORE_SOFTMAX ? exp((double)x - r.top) * r.inv : pointwise_score((double)x, score);
-  return x > -kInf ? s + (double)bias : (double)-kInf;
 }
 
 // Which groups stay: a group's value is the sum of its two highest keys; the
@@ -333,8 +334,8 @@ __device__ __forceinline__ void pick_by_rounds(float (&key)[VPT], int want, int*
 // for 8 runs) hold the k highest. They are compacted in expert order, one per
 // lane, and each counts those before it. Returns false, having done nothing,
 // when more than 64 remain (many equal keys); *all tells whether the want-th is
-// among them. (16384 x 384 and k = 8: 20.7 us, by rounds 29; k = 16: 26 and
-// 37; k = 2: 7.3 and 7.1. Past 16 the runs would be single lanes.)
+// among them. (16384 x 384 and k = 8: 20 us, by rounds 29; k = 16: 25 and
+// 37; k = 2: 7.1 and 7.1. Past 16 the runs would be single lanes.)
 constexpr int kFastK = 16;
 struct Picked {  // a compacted key with its expert
   float key;
@@ -516,17 +517,17 @@ __device__ __forceinline__ void write_choices(const float (&x)[VPT], const GateS
 // whose argument x - max is rounded first, and for sqrt-softplus, from the
 // hardware's logarithm) or are the same sum of the same numbers. Where they are
 // not, float64 keys decide: those of the candidates, one per lane (of every
-// expert, 16384 x 384 by sqrt-softplus took 33 us instead of 20.7, and the
-// registers that this needed left six waves on a SIMD).
+// expert, 16384 x 384 by sqrt-softplus took 33 us instead of 20).
 //
 // Bound by the instructions of choosing: 16384 x 256 BF16 with bias and 8
-// groups takes 20.5 us, 570 vector instructions a token, 70 % of the time
-// issuing them (its 8 MB take 1.8 us); 16384 x 256 by the logits alone 7.3.
-// Eight waves on a SIMD (64 registers; the float64 paths spill a few there):
-// 8192 x 384 8.0 us, with seven 8.9; 16384 x 384 20, with four 26. With 16
-// logits per lane five fit: 16384 x 1024 38 us, with four 41.
+// groups takes 18.6 us, 550 vector instructions a token, 70 % of the time
+// issuing them (its 8 MB take 1.8 us); 16384 x 384 by the logits alone 11.4.
+// Waves on a SIMD, as many as the registers of the common path allow: eight
+// (8192 x 256 in groups 11.5 us, with seven 12.3; 16384 x 384 19.6, with six
+// 20.6), six with 8 logits per lane (16384 x 512 by the logits 12.7, with eight
+// 13.2), four with 16 (16384 x 1024 32.1, with five 32.6).
 template <typename L, int VPT>
-__global__ __launch_bounds__(64 * kGateWaves, VPT <= 8 ? 8 : 5) void gate_topk_kernel(const L* __restrict__ logits,
+__global__ __launch_bounds__(64 * kGateWaves, VPT <= 6 ? 8 : VPT <= 8 ? 6 : 4) void gate_topk_kernel(const L* __restrict__ logits,
                                                                     const float* __restrict__ bias,
                                                                     const uint8_t* __restrict__ mask, GateShape g,
                                                                     int32_t* __restrict__ ids, float* __restrict__ w) {
