@@ -682,14 +682,21 @@ static int launch_int8(const Int8Args& g, hipStream_t stream) {
   }
   if (g.M <= kSkinnyM) return launch_int8_skinny<1, SILU>(g, stream);
   if (int8_few(g.M, g.N, g.K)) return launch_int8_skinny<2, SILU>(g, stream);
-  // The largest tile that still gives most of the 256 CUs one: 4096 x 4096 x
-  // 7168 takes 115 us by 256 x 256 [161 by 128 x 128], 1024 x 7168 x 2048 takes
-  // 24.6 by 128 x 128 [30.5 by 256, 30.3 by 64], 512 x 4096 x 7168 takes 29 by
-  // 64 x 128 [47 by 128].
-  const auto tiles = [&](int bm, int bn) { return (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return launch_int8_tile<256, 256, 2, 4, 64, OUT>(g, stream);
-  if (tiles(128, 128) >= 192) return launch_int8_tile<128, 128, 2, 2, 64, OUT>(g, stream);
-  return launch_int8_tile<64, SILU ? 128 : 64, 2, 2, 128, OUT>(g, stream);
+  // The tile whose rounds over the 256 CUs take least, by what one of each size
+  // took at K = 7168 (us, in proportion to K): alone on its CU, or each of more.
+  // (By the largest tile that still gives 192 CUs one, 2100 x 4096 x 7168 took
+  // 100 us, not 83; 1536 x 7168 x 2048 34.8, not 31.7; 2900 x 3000 x 4096 58,
+  // not 50.)
+  const auto cost = [&](int bm, int bn, double alone, double each) {
+    const int64_t tiles = (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn);
+    return tiles <= 256 ? alone : each * (double)((tiles + 255) / 256);
+  };
+  constexpr int BN = SILU ? 128 : 64;
+  const double large = cost(256, 256, 96.0, 96.0), middle = cost(128, 128, 49.0, 41.0);
+  const double small = SILU ? cost(64, 128, 29.0, 26.0) : cost(64, 64, 24.0, 16.5);
+  if (large <= middle && large <= small) return launch_int8_tile<256, 256, 2, 4, 64, OUT>(g, stream);
+  if (middle <= small) return launch_int8_tile<128, 128, 2, 2, 64, OUT>(g, stream);
+  return launch_int8_tile<64, BN, 2, 2, 128, OUT>(g, stream);
 }
 
 extern "C" size_t int8_gemm_ws_bytes(int32_t M, int32_t N, int32_t K) {
