@@ -268,11 +268,9 @@ __global__ __launch_bounds__(512) void block_norm_kernel(const X* x, const R* re
 //   d_x = sig (db' w_post - xn mean(db' w_post xn)),  or db' without w_post
 // Two reductions per row (the second needs the first's result). The column
 // sums d_w_pre, d_w_post, d_gate stay in registers over all rows of the
-// thread; the workgroup's row groups add theirs in LDS, halving their number
-// each time, and it leaves one row of partial sums, which norm_columns_kernel
-// adds in workgroup order. (With a workgroup for each row group, twice the
-// partial rows: 2047 x 2888 took 36 us. One group after the other: 8192 x 128
-// 17.0 us, not 14.6.)
+// thread; the workgroup's row groups add theirs in LDS, and it leaves one row
+// of partial sums, which norm_columns_kernel adds in workgroup order. (With a
+// workgroup for each row group, twice the partial rows: 2047 x 2888 took 36 us.)
 template <typename X, typename R, int CH>
 struct NormGradRow {
   Vec8<X> x[CH], y[CH];
@@ -396,37 +394,69 @@ __global__ __launch_bounds__(CH == 1 ? kGradThreads : 512) void block_norm_backw
     }
     if (!KEEP && t0 + step < a.T) in.load(at, x, py, res_out, d_res_out, (size_t)next * a.H, nchunk);
   }
-  // The row groups' column sums: the upper half of the groups leaves its own in
-  // LDS, the lower half adds them, until one is left, which writes the
-  // workgroup's partial sums, [workgroup][3][H].
-  const auto each = [&](auto fn) {  // fn(place in [3][H], the eight sums there)
+  // The row groups' column sums end in one group, which writes the workgroup's
+  // partial sums, [workgroup][3][H]. Of up to twelve groups (one chunk per
+  // thread) the upper half leaves its own in LDS and the lower half adds them,
+  // again and again (8192 x 128: one group after the other 17.1 us, so 14.5);
+  // of one or two the last adds the first's, which keeps the loop above as fast
+  // as it is without (8192 x 7168: 151, in halves 154).
+  if constexpr (CH == 1) {
+    const auto each = [&](auto fn) {  // fn(place in [3][H], the eight sums there)
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int ch = at.tid + c * at.threads;
-      if (ch < nchunk) {
-        fn(ch * 8, c_pre[c]);
-        fn(a.H + ch * 8, c_post[c]);
-        fn(2 * a.H + ch * 8, c_gate[c]);
+      for (int c = 0; c < CH; ++c) {
+        const int ch = at.tid + c * at.threads;
+        if (ch < nchunk) {
+          fn(ch * 8, c_pre[c]);
+          fn(a.H + ch * 8, c_post[c]);
+          fn(2 * a.H + ch * 8, c_gate[c]);
+        }
       }
-    }
-  };
-  for (int n = groups; n > 1;) {
-    const int keep = (n + 1) / 2;  // group keep + i adds to group i
-    if (at.group >= keep && at.group < n)
-      each([&](int place, float(&v)[8]) { store8(columns + (size_t)(at.group - keep) * 3 * a.H + place, v); });
-    __syncthreads();
-    if (at.group < n - keep)
-      each([&](int place, float(&v)[8]) {
-        Vec8<float> other;
-        other.load(columns + (size_t)at.group * 3 * a.H + place);
+    };
+    for (int n = groups; n > 1;) {
+      const int keep = (n + 1) / 2;  // group keep + i adds to group i
+      if (at.group >= keep && at.group < n)
+        each([&](int place, float(&v)[8]) { store8(columns + (size_t)(at.group - keep) * 3 * a.H + place, v); });
+      __syncthreads();
+      if (at.group < n - keep)
+        each([&](int place, float(&v)[8]) {
+          Vec8<float> other;
+          other.load(columns + (size_t)at.group * 3 * a.H + place);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += other.get(e);
-      });
-    __syncthreads();
-    n = keep;
+          for (int e = 0; e < 8; ++e) v[e] += other.get(e);
+        });
+      __syncthreads();
+      n = keep;
+    }
+    if (at.group == 0)
+      each([&](int place, float(&v)[8]) { store8(partial + (size_t)blockIdx.x * 3 * a.H + place, v); });
+  } else {
+    for (int g = 0; g < groups; ++g) {
+      const bool last = g + 1 == groups;
+      if (at.group == g) {
+        // the last group writes the workgroup's partial sums: [workgroup][3][H]
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int ch = at.tid + c * at.threads;
+          if (ch < nchunk) {
+            float* out = partial + (size_t)blockIdx.x * 3 * a.H + ch * 8;
+            float(*v[3])[8] = {&c_pre[c], &c_post[c], &c_gate[c]};
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              float* sum = columns + (size_t)i * a.H + ch * 8;
+              if (g > 0) {
+                Vec8<float> was;
+                was.load(sum);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) (*v[i])[e] += was.get(e);
+              }
+              store8(last ? out + (size_t)i * a.H : sum, *v[i]);
+            }
+          }
+        }
+      }
+      if (!last) __syncthreads();
+    }
   }
-  if (at.group == 0)
-    each([&](int place, float(&v)[8]) { store8(partial + (size_t)blockIdx.x * 3 * a.H + place, v); });
 }
 
 // Column sums over the workgroups' partial rows: workgroup (b, s) adds 64
