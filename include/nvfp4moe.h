@@ -365,7 +365,7 @@ int int8_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const 
  * [H, I] with w2_scale [H]; x, out BF16 [T, H]; add BF16 [T, H] (such as the
  * output of nvfp4_moe_forward; may be out) or NULL. H % 16 == 0, I % 16 == 0,
  * both <= 65536, T <= 64 * 65535. ws: at least int8_ffn_ws_bytes(T, H, I).
- * Exactly what the functions above give in sequence. Four or five launches.
+ * Exactly what the functions above give in sequence. Four to six launches.
  */
 size_t int8_ffn_ws_bytes(int32_t T, int32_t hidden, int32_t inter);
 int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const int8_t* w2_q, const float* w2_scale,
