@@ -128,7 +128,8 @@ struct GateShape {
 };
 
 // Float key of every logit of the lane: the logits themselves when the order
-// of scores is theirs (no bias, one group). *bmax: the lane's largest |bias|.
+// of scores is theirs (no bias, one group). *bmax: the lane's largest |bias| of
+// an expert that can be chosen.
 template <int VPT>
 __device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bias, const GateShape& g,
                                           float (&key)[VPT], float* bmax) {
@@ -161,12 +162,9 @@ __device__ __forceinline__ void gate_keys(const float (&x)[VPT], const float* bi
   }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    if (bias) {
-      const float b = bias[min(v * 64 + lane, g.E - 1)];
-      *bmax = fmaxf(*bmax, fabsf(b));
-      key[v] += b;
-    }
-    if (!(x[v] > -kInf)) key[v] = -kInf;
+    const float b = bias ? bias[min(v * 64 + lane, g.E - 1)] : 0.0f;
+    key[v] = x[v] > -kInf ? key[v] + b : -kInf;
+    *bmax = fmaxf(*bmax, key[v] > -kInf ? fabsf(b) : 0.0f);
   }
 }
 
@@ -568,20 +566,30 @@ __global__ __launch_bounds__(64 * kGateWaves, VPT <= 6 ? 8 : VPT <= 8 ? 6 : 4) v
     const int idn = __shfl_down(id, 1, 64);
     const bool same = xl == xn && bl == bn;
     const float size = fabsf(at) + fabsf(next) + fabsf(bl) + fabsf(bn);
-    const bool close = lane + 1 < want && idn >= 0 && !same && !(at - next > 2.0f * tol * size);
-    if (__ballot(close) != 0 || want == g.k || !all) {  // !all: the first key left out is unknown
-      if (!counted) {  // the rounds took the picked keys out
-        for (int j = 0; j < want; ++j) {
-          const int e = __builtin_amdgcn_readlane(id, j);
-          const float k32 = lane_value(at, j);
+    const bool close = lane + 1 < g.k && idn >= 0 && !same && !(at - next > 2.0f * tol * size);
+    // Between the last choice and what is left out the largest bias counts, not
+    // those of the two neighbours: further down lie keys whose biases have
+    // cancelled large scores. (Every lane asks with its own largest.)
+    const float kth = lane_value(at, g.k - 1), left = lane_value(at, min(g.k, 63));
+    const bool last = left > -kInf && !(kth - left > 4.0f * tol * (fabsf(kth) + 2.0f * bmax));
+    const bool doubt = __ballot(close) != 0 || want == g.k || !all;  // !all: the first key left out is unknown
+    if (doubt || __ballot(last) != 0) {
+      const float slack = 4.0f * tol * (fabsf(kth) + 2.0f * wave_all_max(bmax));
+      // copies of one logit and bias on both sides of the border: the lower ids were taken
+      const bool copies = (__ballot(same) >> (g.k - 1)) & 1u;
+      if (doubt || !copies) {
+        if (!counted) {  // the rounds took the picked keys out
+          for (int j = 0; j < want; ++j) {
+            const int e = __builtin_amdgcn_readlane(id, j);
+            const float k32 = lane_value(at, j);
 #pragma unroll
-          for (int v = 0; v < VPT; ++v)
-            if (v * 64 + lane == e) key[v] = k32;
+            for (int v = 0; v < VPT; ++v)
+              if (v * 64 + lane == e) key[v] = k32;
+          }
         }
+        pick_exact(logits, row, bias, g, key, at, slack, picked[wave], keys, &id);
+        xl = load_logit(logits, row + max(id, 0));
       }
-      const float kth = lane_value(at, g.k - 1), slack = 4.0f * tol * (fabsf(kth) + 2.0f * wave_all_max(bmax));
-      pick_exact(logits, row, bias, g, key, at, slack, picked[wave], keys, &id);
-      xl = load_logit(logits, row + max(id, 0));
     }
   }
   write_choices(x, g, id, xl, (size_t)t, ids, w);

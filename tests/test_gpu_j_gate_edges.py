@@ -1,0 +1,48 @@
+"""The gate, the balance loss and their gradient where float32 keys, sums or scores run out: against the float64
+oracle, with the tolerances of test_gpu_f_gate.py."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.gate as G
+from _block_cases import DEV, as_stored, to_dev, torch_dtype
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def nv():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import nvfp4_quantized_moe_amd as nv
+    return nv
+
+
+def choices(nv, x, k, score, bias=None, groups=1, top=1, dtype="f32"):
+    """ids of the kernel and of the oracle."""
+    ids, _ = nv.moe_gate_topk(to_dev(x.astype(np.float32), torch_dtype(dtype)), k, score=score,
+                              bias=None if bias is None else to_dev(bias), n_group=groups, topk_group=top)
+    return ids.cpu().numpy(), G.gate_topk(x, k, score, bias, None, groups, top)[0]
+
+
+def wrong_rows(got, ref):
+    return int((got != ref).any(1).sum())
+
+
+@pytest.mark.parametrize("k", [2, 7, 20])
+def test_a_bias_that_cancels_its_score(nv, k):
+    """k - 1 clear choices, then scores of 2e-8 and 1e-8 without a bias, and further down an expert whose bias is the
+    negative of its rounded score: what is left of its key is the rounding, often more than 2e-8."""
+    E, low = 64, 32
+    rng = np.random.default_rng(k)
+    for _ in range(10):
+        bias = np.zeros(E, np.float32)
+        at = rng.uniform(1.5, 3.0, E).astype(np.float32)
+        bias[low + 2:] = -(1.0 / (1.0 + np.exp(-at[low + 2:].astype(np.float64)))).astype(np.float32)
+        x = np.full((E - low - 2, E), -np.inf)
+        x[:, :k - 1] = rng.uniform(2.0, 6.0, (len(x), k - 1))
+        x[:, low - 1] = np.log(2e-8)
+        x[:, low] = np.log(1e-8)
+        for t in range(len(x)):
+            x[t, low + 2 + t] = at[low + 2 + t]
+        got, ref = choices(nv, as_stored(x, "f32"), k, G.SIGMOID, bias)
+        assert wrong_rows(got, ref) == 0
