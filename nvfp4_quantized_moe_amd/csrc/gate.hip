@@ -417,6 +417,20 @@ __device__ __forceinline__ bool pick_by_count(const float (&key)[VPT], int k, in
   return true;
 }
 
+// Whether some key is within slack of `key0` that is not of the logit x0 and the bias b0.
+template <int VPT>
+__device__ __forceinline__ bool others_near(const float (&x)[VPT], const float (&key)[VPT], const float* bias, int E,
+                                            float key0, float slack, float x0, float b0) {
+  const int lane = threadIdx.x & 63;
+  bool found = false;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const float b = bias ? bias[min(v * 64 + lane, E - 1)] : 0.0f;
+    found |= fabsf(key[v] - key0) <= slack && !(x[v] == x0 && b == b0);
+  }
+  return __ballot(found) != 0;
+}
+
 // The k highest by float64 keys, where the k highest float keys (lane j: the
 // j-th, expert *id) are within `slack` of keys that may belong before them:
 // the experts down to the k-th key - slack, one exact key per lane; or, if
@@ -575,9 +589,10 @@ __global__ __launch_bounds__(64 * kGateWaves, VPT <= 6 ? 8 : VPT <= 8 ? 6 : 4) v
     const bool doubt = __ballot(close) != 0 || want == g.k || !all;  // !all: the first key left out is unknown
     if (doubt || __ballot(last) != 0) {
       const float slack = 4.0f * tol * (fabsf(kth) + 2.0f * wave_all_max(bmax));
-      // copies of one logit and bias on both sides of the border: the lower ids were taken
+      // Copies of one logit and bias on both sides of the border: the lower ids
+      // were taken, unless some other key is as near.
       const bool copies = (__ballot(same) >> (g.k - 1)) & 1u;
-      if (doubt || !copies) {
+      if (doubt || !copies || others_near(x, key, bias, g.E, kth, slack, lane_value(xl, g.k - 1), lane_value(bl, g.k - 1))) {
         if (!counted) {  // the rounds took the picked keys out
           for (int j = 0; j < want; ++j) {
             const int e = __builtin_amdgcn_readlane(id, j);

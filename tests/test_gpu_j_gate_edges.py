@@ -46,3 +46,31 @@ def test_a_bias_that_cancels_its_score(nv, k):
             x[t, low + 2 + t] = at[low + 2 + t]
         got, ref = choices(nv, as_stored(x, "f32"), k, G.SIGMOID, bias)
         assert wrong_rows(got, ref) == 0
+
+
+@pytest.mark.parametrize("score,k,row,expected", [
+    (G.SIGMOID, 1, [20, 20, 21, 0, 0, 0, 0, 0], [2]),                # 1 in float32, all three of the highest
+    (G.SIGMOID, 2, [20, 19, 20, 21, 0, 0, 0, 0], [3, 0]),
+    (G.SOFTMAX, 2, [200, 1, 1, 2, 0, 0, 0, 0], [0, 3]),              # 0 in float32, all but the first
+    (G.SQRT_SOFTPLUS, 1, [-200, -200, -190, -300, -300, -300, -300, -300], [2]),
+])
+def test_copies_at_the_last_choice(nv, score, k, row, expected):
+    """The k-th and the next key are copies of one logit, and float32 cannot tell a higher one from them."""
+    x, bias = np.array([row], np.float64), np.zeros(len(row), np.float32)
+    got, ref = choices(nv, x, k, score, bias)
+    assert got.tolist() == ref.tolist() == [expected]
+
+
+@pytest.mark.parametrize("k", [1, 2, 6, 20])
+@pytest.mark.parametrize("E,score,scale,groups,top,biased", [
+    (256, G.SIGMOID, 8, 1, 1, True), (256, G.SIGMOID, 8, 8, 4, False), (384, G.SIGMOID, 12, 8, 3, False),
+    (60, G.SOFTMAX, 40, 1, 1, True), (256, G.SOFTMAX, 40, 8, 4, False), (96, G.SQRT_SOFTPLUS, 60, 4, 2, False),
+    (300, G.SQRT_SOFTPLUS, 60, 1, 1, True)])
+def test_saturated_rows_of_few_values(nv, E, score, scale, groups, top, biased, k):
+    """BF16 logits of a wide range: many equal ones, many whose scores float32 rounds to the same, and no bias (or
+    one of zeros) to tell them apart."""
+    rng = np.random.default_rng(E + k)
+    x = as_stored(rng.standard_normal((400, E)) * scale, "bf16")
+    x[::4] = np.round(x[::4])
+    got, ref = choices(nv, x, k, score, np.zeros(E, np.float32) if biased else None, groups, top, "bf16")
+    assert wrong_rows(got, ref) == 0
