@@ -669,11 +669,13 @@ __device__ Span find_chunk(const int32_t* cu, const BalanceShape& g, int i) {
 }
 
 // Normalized scores of a row (lane l: experts l, l + 64, ...). Returns false
-// for a row without a logit above -inf. sum: of the scores, lse: log of the
-// sum of e^x; e[v] = e^(x - lse).
+// for a row without a logit above -inf. top: the highest logit, part: 1 / sum of
+// e^(x - top), lse: log of the sum of e^x, inv: 1 / sum of the scores, 0 for 0;
+// p[v] = e^(x - top) part, which a common offset of a row's logits leaves as it
+// is (e^(x - lse) would take on the rounding of lse at the offset's size).
 // slope[v]: of the pointwise scores, with SLOPE.
 struct RowSums {
-  float sum, inv, lse;  // inv = 1 / sum, 0 for 0
+  float top, part, lse, inv;
 };
 template <bool SLOPE, int VPT>
 __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, float (&q)[VPT], float (&p)[VPT],
@@ -691,11 +693,12 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
   }
   es = wave_all_sum(es);
   r->lse = top + __builtin_amdgcn_logf(es) * kLn2;
-  const float inv = __builtin_amdgcn_rcpf(es);
+  r->top = top;
+  r->part = __builtin_amdgcn_rcpf(es);
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) p[v] *= inv;
+  for (int v = 0; v < VPT; ++v) p[v] *= r->part;
   if (score == MOE_SCORE_SOFTMAX) {
-    r->sum = r->inv = 1.0f;
+    r->inv = 1.0f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) q[v] = p[v];
     return true;
@@ -711,7 +714,6 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
 #pragma unroll
   for (int v = 0; v < VPT; ++v) sum += q[v];
   sum = wave_all_sum(sum);
-  r->sum = sum;
   r->inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) q[v] *= r->inv;
@@ -988,7 +990,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
     }
     bool in_loss = seq >= 0;
     float q[VPT], p[VPT], slope[VPT];
-    RowSums r = {1.0f, 1.0f, 0.0f};
+    RowSums r = {0.0f, 1.0f, 0.0f, 1.0f};
     int32_t chosen[VPT];
     if (in_loss) {
 #pragma unroll
@@ -1011,7 +1013,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
         e = e / fmaxf(wave_all_sum(e), 1.0f);  // the largest is e^0; 1 also where nothing is chosen
         d = e * (c - wave_all_sum(c * e));
       } else {
-        const float s = !some ? 0.0f : softmax ? expf(xl - r.lse) : pointwise_score(xl, a.score);
+        const float s = !some ? 0.0f : softmax ? expf(xl - r.top) * r.part : pointwise_score(xl, a.score);
         float ds = c;
         if (a.renormalize) {
           const float sum = wave_all_sum(s);

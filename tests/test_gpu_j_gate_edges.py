@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle.gate as G
-from _block_cases import DEV, as_stored, to_dev, torch_dtype
+from _block_cases import DEV, as_stored, grad_bound, to_dev, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,20 @@ def test_saturated_rows_of_few_values(nv, E, score, scale, groups, top, biased, 
     x[::4] = np.round(x[::4])
     got, ref = choices(nv, x, k, score, np.zeros(E, np.float32) if biased else None, groups, top, "bf16")
     assert wrong_rows(got, ref) == 0
+
+
+@pytest.mark.parametrize("offset", [0.0, 1000.0, -30000.0])
+def test_softmax_gradient_of_shifted_rows(nv, offset):
+    """Softmax does not see a common offset of a row's logits; neither does the gradient through weights that are not
+    renormalized. (Logits in steps of 2^-8, so that float32 holds them with the offset.)"""
+    T, E, k = 200, 90, 6
+    rng = np.random.default_rng(4)
+    x = np.round(rng.standard_normal((T, E)) * 1.5 * 256) / 256 + offset
+    assert np.array_equal(as_stored(x, "f32"), x)
+    ids, _ = G.gate_topk(x, k, G.SOFTMAX)
+    d_w = rng.standard_normal((T, k)).astype(np.float32)
+    got = nv.moe_gate_backward(to_dev(x.astype(np.float32)), to_dev(ids), G.SOFTMAX, False, 1.5, d_topk_w=to_dev(d_w))
+    ref = G.gate_backward(x, ids, G.SOFTMAX, False, 1.5, d_w=d_w)
+    tol = grad_bound(x, ids, 1.5 * d_w, G.SOFTMAX, False, None, None, None, None, np.full(T, -1)) + 2.0 ** -120
+    worst = float(np.max(np.abs(got.double().cpu().numpy() - ref) / tol))
+    assert worst <= 1
