@@ -1016,8 +1016,9 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
         const float s = !some ? 0.0f : softmax ? expf(xl - r.top) * r.part : pointwise_score(xl, a.score);
         float ds = c;
         if (a.renormalize) {
+          // by the weights' quotients s / sum: of a single choice exactly 1, and its gradient 0
           const float sum = wave_all_sum(s);
-          const float dot = wave_all_sum(c * s) / sum;
+          const float dot = wave_all_sum(c * (s / sum));
           ds = some && sum > 0.0f ? (c - dot) / sum : 0.0f;
         }
         if (softmax) {

@@ -91,3 +91,21 @@ def test_softmax_gradient_of_shifted_rows(nv, offset):
     tol = grad_bound(x, ids, 1.5 * d_w, G.SOFTMAX, False, None, None, None, None, np.full(T, -1)) + 2.0 ** -120
     worst = float(np.max(np.abs(got.double().cpu().numpy() - ref) / tol))
     assert worst <= 1
+
+
+@pytest.mark.parametrize("score", [G.SOFTMAX, G.SIGMOID, G.SQRT_SOFTPLUS])
+@pytest.mark.parametrize("k", [1, 4])
+def test_a_single_renormalized_choice_has_no_gradient(nv, k, score):
+    """Its weight is the scale whatever its logit: k = 1, or one expert that the token may use."""
+    T, E = 300, 40
+    rng = np.random.default_rng(k)
+    x = as_stored(rng.standard_normal((T, E)) * 3, "f32")
+    if k > 1:
+        keep = x[np.arange(T), np.arange(T) % E]
+        x[:] = -np.inf
+        x[np.arange(T), np.arange(T) % E] = keep
+    ids, w = nv.moe_gate_topk(to_dev(x.astype(np.float32)), k, score, scale=2.5)
+    assert (ids[:, 1:] == -1).all()
+    d_w = to_dev(rng.standard_normal((T, k)).astype(np.float32))
+    d = nv.moe_gate_backward(to_dev(x.astype(np.float32)), ids, score, True, 2.5, d_topk_w=d_w)
+    assert not d.any()
