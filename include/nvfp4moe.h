@@ -164,6 +164,9 @@ int moe_route_slots(const int32_t* topk_ids, const float* topk_w, int32_t T, int
  *            topk_ids int32 [T, k],
  *            topk_w   float [T, k] = scale * s, or with renormalize = 1
  *                     scale * s / (sum of the k scores), 0 if that sum is 0.
+ *          A score that is divided by a sum of scores, here and in the balance
+ *          loss, may lie far below float32's range; where all logits of the sum
+ *          are under -708, about where float64 ends, it counts as 0.
  * Where fewer than k experts can be chosen the rest is id -1, weight 0 (and
  * dropped by moe_route_slots). token_mask (uint8 [T] or NULL): tokens with
  * mask 0 get ids -1 and weights 0, and their logits are not used (any bits).

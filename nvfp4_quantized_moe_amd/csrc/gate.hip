@@ -75,6 +75,16 @@ __device__ __forceinline__ float score_slope(float x, float s, int score) {
   return x < -20.0f ? 0.5f * s : 0.5f * sigmoid_score(x) / s;
 }
 
+// Far below 0 a score is e^(x tail_power) to float32's last bit, and soon leaves
+// float32. Scores that are divided by their sum, a sum that shows all of them to
+// lie there, are taken relative to the largest instead; down to where float64
+// ends (below, they count as 0).
+__device__ __forceinline__ float tail_power(int score) { return score == MOE_SCORE_SIGMOID ? 1.0f : 0.5f; }
+__device__ __forceinline__ bool in_tail(float sum, int score) {  // every logit below -19: e^-19 < 2^-27
+  return sum < (score == MOE_SCORE_SIGMOID ? 0x1p-28f : 0x1p-14f);
+}
+constexpr float kTailEnd = -708.0f;
+
 // The same scores where they are summed or multiplied into a gradient rather
 // than compared: hardware exponential, logarithm and reciprocal, each within
 // one or two float32 steps, e^x through 2^(x log2 e) with |x| half steps more.
@@ -514,8 +524,13 @@ __device__ __forceinline__ void write_choices(const float (&x)[VPT], const GateS
     s = on ? pointwise_score(xl, g.score) : 0.0f;
   }
   if (g.renormalize) {
-    const float sum = wave_all_sum(s);
-    s = sum > 0x1p-100f ? s * __builtin_amdgcn_rcpf(sum) : sum > 0.0f ? s / sum : 0.0f;
+    float sum = wave_all_sum(s);
+    if (in_tail(sum, g.score)) {
+      const float top = wave_all_max(xl);
+      s = on && top >= kTailEnd ? near_exp(tail_power(g.score) * (xl - top)) : 0.0f;
+      sum = wave_all_sum(s);
+    }
+    s = sum > 0.0f ? s * __builtin_amdgcn_rcpf(sum) : 0.0f;
   }
   if (lane < g.k) {
     ids[t * g.k + lane] = on ? id : -1;
@@ -714,6 +729,17 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
 #pragma unroll
   for (int v = 0; v < VPT; ++v) sum += q[v];
   sum = wave_all_sum(sum);
+  if (in_tail(sum, score)) {
+    sum = 0.0f;
+    const float power = tail_power(score);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      q[v] = top >= kTailEnd ? fast_exp(power * (x[v] - top)) : 0.0f;
+      if (SLOPE) slope[v] = power * q[v];
+      sum += q[v];
+    }
+    sum = wave_all_sum(sum);
+  }
   r->inv = sum > 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) q[v] *= r->inv;
@@ -1013,11 +1039,17 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
         e = e / fmaxf(wave_all_sum(e), 1.0f);  // the largest is e^0; 1 also where nothing is chosen
         d = e * (c - wave_all_sum(c * e));
       } else {
-        const float s = !some ? 0.0f : softmax ? expf(xl - r.top) * r.part : pointwise_score(xl, a.score);
-        float ds = c;
+        float s = !some ? 0.0f : softmax ? expf(xl - r.top) * r.part : pointwise_score(xl, a.score);
+        float ds = c, slope_l = some && !softmax ? score_slope(xl, s, a.score) : 0.0f;
         if (a.renormalize) {
+          float sum = wave_all_sum(s);
+          if (in_tail(sum, a.score)) {
+            const float top = wave_all_max(some ? xl : -kInf), power = tail_power(a.score);
+            s = some && top >= kTailEnd ? expf(power * (xl - top)) : 0.0f;
+            slope_l = power * s;
+            sum = wave_all_sum(s);
+          }
           // by the weights' quotients s / sum: of a single choice exactly 1, and its gradient 0
-          const float sum = wave_all_sum(s);
           const float dot = wave_all_sum(c * (s / sum));
           ds = some && sum > 0.0f ? (c - dot) / sum : 0.0f;
         }
@@ -1025,7 +1057,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void gate_backward_kernel(const L*
           d = s * ds;
           inner = wave_all_sum(d);
         } else {
-          d = some ? ds * score_slope(xl, s, a.score) : 0.0f;
+          d = some ? ds * slope_l : 0.0f;
         }
       }
       // an expert listed twice gets both gradients: every lane of it holds the sum

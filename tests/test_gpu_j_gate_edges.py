@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle.gate as G
-from _block_cases import DEV, as_stored, grad_bound, to_dev, torch_dtype
+from _block_cases import DEV, EPS32, as_stored, grad_bound, to_dev, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,36 @@ def test_a_single_renormalized_choice_has_no_gradient(nv, k, score):
     d_w = to_dev(rng.standard_normal((T, k)).astype(np.float32))
     d = nv.moe_gate_backward(to_dev(x.astype(np.float32)), ids, score, True, 2.5, d_topk_w=d_w)
     assert not d.any()
+
+
+@pytest.mark.parametrize("score", [G.SIGMOID, G.SQRT_SOFTPLUS])
+@pytest.mark.parametrize("level", [-15.0, -25.0, -88.0, -110.0, -180.0, -400.0])
+def test_rows_far_below_zero(nv, level, score):
+    """Scores that are divided by their sum depend on their ratios alone, also where float32 cannot hold them."""
+    T, E, k = 90, 70, 5
+    rng = np.random.default_rng(int(-level))
+    x = as_stored(level + rng.standard_normal((T, E)) * 4, "f32")
+    x[::3, 7:] = -np.inf
+    dev = to_dev(x.astype(np.float32))
+    bias = rng.standard_normal(E).astype(np.float32)   # float64 keys of such scores would be those of the bias
+    ids, w = nv.moe_gate_topk(dev, k, score, bias=to_dev(bias), scale=2.5)
+    ref_ids, ref_w = G.gate_topk(x, k, score, bias, scale=2.5)
+    assert wrong_rows(ids.cpu().numpy(), ref_ids) == 0
+    # exp within 2 steps, k additions and 6 other roundings, and |x - max| half steps of an exponential's argument;
+    # beside a sum of at least 2^-28 scores under 2^-126 may be lost
+    fin = np.where(x > -np.inf, x, np.nan)
+    span = np.nanmax(fin, 1) - np.nanmin(fin, 1)
+    tol = (16 + k + 2 * span[:, None]) * EPS32 * ref_w + 2.5 * 2.0 ** -98
+    assert float(np.max(np.abs(w.double().cpu().numpy() - ref_w) / tol)) <= 1
+    d_w, d_loss = rng.standard_normal((T, k)).astype(np.float32), np.array([0.9, 0.0], np.float32)
+    loss, counts, tokens = nv.moe_balance_loss(dev, ids, score)
+    ref_loss, ref_counts, ref_tokens = G.balance_loss(x, ref_ids, score)
+    assert abs(float(loss[0]) - ref_loss[0]) <= (110 + 2 * span.max()) * EPS32 * ref_loss[0]
+    for use_w, use_loss in ((True, False), (False, True)):
+        got = nv.moe_gate_backward(dev, ids, score, True, 1.5, d_topk_w=to_dev(d_w) if use_w else None,
+                                   d_loss=to_dev(d_loss) if use_loss else None, counts=counts, tokens=tokens)
+        args = dict(d_w=d_w if use_w else None, d_loss=d_loss if use_loss else None)
+        ref = G.gate_backward(x, ref_ids, score, True, 1.5, counts=ref_counts, tokens=ref_tokens, **args)
+        tol = grad_bound(x, ref_ids, 1.5 * d_w if use_w else None, score, True, None, args["d_loss"], ref_counts,
+                         ref_tokens, np.zeros(T, int)) + 2.0 ** -98
+        assert float(np.max(np.abs(got.double().cpu().numpy() - ref) / tol)) <= 1, (use_w, use_loss)
