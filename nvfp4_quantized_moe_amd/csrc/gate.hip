@@ -746,8 +746,10 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
   return true;
 }
 
-// A wave's tokens one after the other, their scores summed in its registers,
-// then the waves' in LDS; choices counted by LDS atomics on whole numbers.
+// A wave's tokens one after the other, their scores summed in its registers in
+// float32, 64 tokens at most in a row, then in LDS in float64 (a chunk of the
+// largest batches gives a wave 16384 tokens); choices counted by LDS atomics on
+// whole numbers.
 // (16384 x 384 float: 12.4 us, 2 TB/s; about half of it issues the 220 vector
 // instructions a token, the rest is the launch and the first row's latency.)
 template <typename L, int VPT>
@@ -757,7 +759,7 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
                                                                           const int32_t* __restrict__ cu,
                                                                           BalanceShape g, BalanceWs ws) {
   extern __shared__ double lds[];
-  float* q_sh = reinterpret_cast<float*>(lds);                    // [kGateWaves][E]
+  double* q_sh = lds;                                                   // [kGateWaves][E]
   int32_t* hist = reinterpret_cast<int32_t*>(q_sh + kGateWaves * g.E);  // [E]
   __shared__ double z_sh[kGateWaves];
   __shared__ int n_sh[kGateWaves];
@@ -779,24 +781,33 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
     next_on = mask ? mask[t] : 1;
   };
   if (span.begin + wave < span.end) load(span.begin + wave);
-  for (int t = span.begin + wave; t < span.end; t += kGateWaves) {  // with the next row's loads in flight
-    float x[VPT], q[VPT], p[VPT], unused[VPT];
+  constexpr int kRun = 64 * kGateWaves;
+  for (int from = span.begin; from < span.end; from += kRun) {
+    const int to = min(from + kRun, span.end);
+    for (int t = from + wave; t < to; t += kGateWaves) {  // with the next row's loads in flight
+      float x[VPT], q[VPT], p[VPT], unused[VPT];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) x[v] = next[v];
-    const int id = lane < g.k ? next_id : -1, on = next_on;
-    load(min(t + kGateWaves, span.end - 1));
-    if (!on) continue;
-    RowSums r;
-    if (!row_scores<false>(x, g.score, q, p, unused, &r)) continue;
-    if (id >= 0 && id < g.E) atomicAdd(&hist[id], 1);
+      for (int v = 0; v < VPT; ++v) x[v] = next[v];
+      const int id = lane < g.k ? next_id : -1, on = next_on;
+      load(min(t + kGateWaves, span.end - 1));
+      if (!on) continue;
+      RowSums r;
+      if (!row_scores<false>(x, g.score, q, p, unused, &r)) continue;
+      if (id >= 0 && id < g.E) atomicAdd(&hist[id], 1);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) acc[v] += q[v];
-    z += (double)r.lse * (double)r.lse;
-    ++n;
+      for (int v = 0; v < VPT; ++v) acc[v] += q[v];
+      z += (double)r.lse * (double)r.lse;
+      ++n;
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (v * 64 + lane < g.E) {  // this lane's alone until the barrier
+        double* const sum = q_sh + wave * g.E + v * 64 + lane;
+        *sum = from > span.begin ? *sum + (double)acc[v] : (double)acc[v];
+      }
+      acc[v] = 0.0f;
+    }
   }
-#pragma unroll
-  for (int v = 0; v < VPT; ++v)
-    if (v * 64 + lane < g.E) q_sh[wave * g.E + v * 64 + lane] = acc[v];
   if (lane == 0) {
     z_sh[wave] = z;
     n_sh[wave] = n;
@@ -804,9 +815,9 @@ __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const 
   __syncthreads();
   const size_t at = (size_t)blockIdx.x * g.E;
   for (int e = threadIdx.x; e < g.E; e += blockDim.x) {
-    float s = q_sh[e];
+    double s = q_sh[e];
     for (int w = 1; w < kGateWaves; ++w) s += q_sh[w * g.E + e];
-    ws.q[at + e] = s;
+    ws.q[at + e] = (float)s;
     ws.counts[at + e] = hist[e];
   }
   if (threadIdx.x == 0) {
@@ -1220,7 +1231,7 @@ extern "C" int moe_balance_loss(const void* logits, int32_t logits_dtype, const 
   BalanceShape g = {T, E, k, B, score, 0, 0};
   BalanceWs w;
   if (ws_bytes < balance_layout(T, E, B, &g, reinterpret_cast<char*>(ws), &w)) return NVFP4_ERR_WORKSPACE;
-  const size_t lds = (size_t)(kGateWaves + 1) * E * 4;
+  const size_t lds = (size_t)(kGateWaves * 8 + 4) * E;
   return gate_by_width(E, [&](auto vpt) -> int {
     constexpr int VPT = decltype(vpt)::value;
     if (logits_dtype == NVFP4_DT_F32)

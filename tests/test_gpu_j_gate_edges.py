@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle.gate as G
-from _block_cases import DEV, EPS32, as_stored, grad_bound, to_dev, torch_dtype
+from _block_cases import DEV, EPS32, HALF_BF16, as_stored, grad_bound, to_dev, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +142,52 @@ def test_rows_far_below_zero(nv, level, score):
         tol = grad_bound(x, ref_ids, 1.5 * d_w if use_w else None, score, True, None, args["d_loss"], ref_counts,
                          ref_tokens, np.zeros(T, int)) + 2.0 ** -98
         assert float(np.max(np.abs(got.double().cpu().numpy() - ref) / tol)) <= 1, (use_w, use_loss)
+
+
+@pytest.mark.parametrize("score,row", [(G.SIGMOID, [1.1, 0.0]), (G.SIGMOID, [-1.3, 0.4]), (G.SOFTMAX, [0.7, 0.1]),
+                                       (G.SQRT_SOFTPLUS, [2.0, -0.5])])
+def test_sums_over_very_many_tokens(nv, score, row):
+    """Equal rows, so that additions that are rounded all round the same way: 2^25 tokens give a wave 8192 of them."""
+    T, E = (1 << 25) + 77, 2
+    x = as_stored(np.array([row]), "f32")
+    dev = to_dev(x.astype(np.float32)).expand(T, E).contiguous()
+    ids = torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    loss, counts, tokens = nv.moe_balance_loss(dev, ids, score)
+    assert counts.tolist() == [[T, 0]] and tokens.tolist() == [T, T, 1]
+    s = G.scores(x, score)[0]
+    ref = E * s[0] / s.sum()
+    # as in test_balance_loss_and_gradient: a share within its own roundings, at most 64 float32 additions in a row
+    assert abs(float(loss[0]) - ref) <= (110 + 2 * np.abs(x).max()) * EPS32 * ref
+    lse = np.log(np.exp(x).sum())
+    assert abs(float(loss[1]) - lse ** 2) <= 16 * EPS32 * (abs(lse) + 2 * np.abs(x).max() + 1) ** 2
+
+
+@pytest.mark.parametrize("cu", [None, [0, 11000, 11000, 11003, 11100, 11900, 12010]], ids=["one", "one-long"])
+@pytest.mark.parametrize("T,E,k,score,dtype", [(12011, 24, 3, G.SIGMOID, "f32"), (33000, 10, 2, G.SOFTMAX, "bf16"),
+                                               (20000, 70, 1, G.SQRT_SOFTPLUS, "f32")])
+def test_balance_loss_of_large_batches(nv, T, E, k, score, dtype, cu):
+    """More than eight tokens to a partial sum; a long sequence beside short ones."""
+    rng = np.random.default_rng(T)
+    x = as_stored(rng.standard_normal((T, E)) * 1.5 + rng.standard_normal(E), dtype)
+    ids = np.argsort(-x, 1, kind="stable")[:, :k].astype(np.int32)
+    mask = (rng.random(T) > 0.1).astype(np.uint8)
+    cu = None if cu is None else np.array(cu, np.int32)
+    dev = to_dev(x.astype(np.float32), torch_dtype(dtype))
+    loss, counts, tokens = nv.moe_balance_loss(dev, to_dev(ids), score, to_dev(mask), None if cu is None else to_dev(cu))
+    ref_loss, ref_counts, ref_tokens = G.balance_loss(x, ids, score, mask, cu)
+    assert np.array_equal(counts.cpu().numpy(), ref_counts) and np.array_equal(tokens.cpu().numpy(), ref_tokens)
+    span = 2 * np.abs(x).max()
+    got = loss.double().cpu().numpy()
+    assert abs(got[0] - ref_loss[0]) <= (110 + span) * EPS32 * ref_loss[0]
+    assert abs(got[1] - ref_loss[1]) <= 16 * EPS32 * (np.sqrt(ref_loss[1]) + span + 1) ** 2
+    d_loss = np.array([0.9, 0.02], np.float32)
+    d = nv.moe_gate_backward(dev, to_dev(ids), score, token_mask=to_dev(mask), d_loss=to_dev(d_loss), counts=counts,
+                             tokens=tokens, cu_seqlens=None if cu is None else to_dev(cu))
+    ref = G.gate_backward(x, ids, score, mask=mask, d_loss=d_loss, counts=ref_counts, tokens=ref_tokens, cu=cu)
+    seq = np.full(T, -1)
+    for b, (lo, hi) in enumerate(G.spans(T, cu)):
+        seq[lo:hi] = b
+    tol = grad_bound(x, ids, None, score, True, mask, d_loss, ref_counts, ref_tokens, seq) + 2.0 ** -120
+    if dtype == "bf16":
+        tol = tol * (1 + HALF_BF16) + HALF_BF16 * np.abs(ref)
+    assert (np.abs(d.double().cpu().numpy() - ref) <= tol).all()
