@@ -585,7 +585,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves, 2) void int8_skinny_kernel(Int8A
   float o = (float)s * (as * g.b_s[n]);
   if (SILU) o = silu_mul(o, (float)u * (as * g.b_s[half + n]));
   const size_t d = (size_t)m * g.n_out + n;
-  if (g.add) o += bf16_to_f32(g.add[d]);
+  o += g.add ? bf16_to_f32(g.add[d]) : 0.0f;  // 0 too, as the tiles do: it makes a -0 of the product 0
   g.d[d] = (uint16_t)f32_to_bf16(o);
 }
 
