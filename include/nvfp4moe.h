@@ -351,7 +351,7 @@ int int8_quantize_rows(const void* x, int32_t x_dtype, int32_t M, int32_t K, int
  * epilogue NVFP4_EPI_SILU_MUL: gate rows [0, I), up rows [I, 2I) of b_q, N = 2I:
  *   d BF16 [M, I], d = RN_bf16(silu(G[m, n]) * G[m, I + n] [+ add]); I % 8 == 0
  * add: BF16 of d's shape, or NULL; may be d itself. K % 16 == 0, K <= 65536,
- * M <= 64 * 65535, N < 2^27. ws: at least int8_gemm_ws_bytes(M, N, K) bytes (the sums of
+ * M <= 64 * 65535, N <= 2^27 - 16. ws: at least int8_gemm_ws_bytes(M, N, K) bytes (the sums of
  * the parts of K where few tokens split it; 0 otherwise, then ws may be NULL).
  * A token's outputs have the same bits whichever other tokens M holds. One
  * launch, or two with parts.

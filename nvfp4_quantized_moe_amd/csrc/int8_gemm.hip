@@ -23,7 +23,8 @@ typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
 
 constexpr int kInt8MaxK = 65536;
-constexpr int kInt8MaxM = 64 * 65535;  // by 1024 threads still within a grid
+constexpr int kInt8MaxM = 64 * 65535;        // by 1024 threads still within a grid
+constexpr int kInt8MaxN = (1 << 27) - 16;    // by 512 threads for 16 columns: fewer than 2^32
 
 // ------------------------------------------------------------- row quantizer
 
@@ -619,7 +620,7 @@ static int int8_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue) {
   if (epilogue != NVFP4_EPI_BF16 && epilogue != NVFP4_EPI_SILU_MUL) return NVFP4_ERR_ARG;
   if (M < 0 || N <= 0 || K <= 0 || K % 16 != 0 || K > kInt8MaxK) return NVFP4_ERR_SHAPE;
   if (N % (epilogue == NVFP4_EPI_SILU_MUL ? 16 : 8) != 0) return NVFP4_ERR_SHAPE;
-  if (M > kInt8MaxM || N >= (1 << 27)) return NVFP4_ERR_SHAPE;
+  if (M > kInt8MaxM || N > kInt8MaxN) return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 
