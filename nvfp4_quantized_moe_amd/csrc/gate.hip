@@ -137,6 +137,10 @@ struct GateShape {
   float scale;
 };
 
+// What a float key may be off by beside its relative error: scores below 2^-126
+// become 0 (a sum of two of them, or with a bias, then loses its order).
+constexpr float kLostScore = 0x1p-120f;
+
 // Float key of every logit of the lane: the logits themselves when the order
 // of scores is theirs (no bias, one group). *bmax: the lane's largest |bias| of
 // an expert that can be chosen.
@@ -292,7 +296,7 @@ __device__ __forceinline__ void keep_groups(const L* logits, size_t row, const f
   uint64_t stays;
   float gap, size;
   const uint32_t per = choose_groups(keys, g, &stays, &gap, &size);
-  if (g.topk_group < g.n_group && !(gap > 4.0f * tol * (size + 2.0f * wave_all_max(bmax)))) {
+  if (g.topk_group < g.n_group && !(gap > 4.0f * tol * (size + 2.0f * wave_all_max(bmax)) + kLostScore)) {
     double gap64, size64;
     wave_lds_fence();
     exact_keys(logits, row, bias, g, lds);
@@ -595,15 +599,15 @@ __global__ __launch_bounds__(64 * kGateWaves, VPT <= 6 ? 8 : VPT <= 8 ? 6 : 4) v
     const int idn = __shfl_down(id, 1, 64);
     const bool same = xl == xn && bl == bn;
     const float size = fabsf(at) + fabsf(next) + fabsf(bl) + fabsf(bn);
-    const bool close = lane + 1 < g.k && idn >= 0 && !same && !(at - next > 2.0f * tol * size);
+    const bool close = lane + 1 < g.k && idn >= 0 && !same && !(at - next > 2.0f * tol * size + kLostScore);
     // Between the last choice and what is left out the largest bias counts, not
     // those of the two neighbours: further down lie keys whose biases have
     // cancelled large scores. (Every lane asks with its own largest.)
     const float kth = lane_value(at, g.k - 1), left = lane_value(at, min(g.k, 63));
-    const bool last = left > -kInf && !(kth - left > 4.0f * tol * (fabsf(kth) + 2.0f * bmax));
+    const bool last = left > -kInf && !(kth - left > 4.0f * tol * (fabsf(kth) + 2.0f * bmax) + kLostScore);
     const bool doubt = __ballot(close) != 0 || want == g.k || !all;  // !all: the first key left out is unknown
     if (doubt || __ballot(last) != 0) {
-      const float slack = 4.0f * tol * (fabsf(kth) + 2.0f * wave_all_max(bmax));
+      const float slack = 4.0f * tol * (fabsf(kth) + 2.0f * wave_all_max(bmax)) + kLostScore;
       // Copies of one logit and bias on both sides of the border: the lower ids
       // were taken, unless some other key is as near.
       const bool copies = (__ballot(same) >> (g.k - 1)) & 1u;

@@ -191,3 +191,20 @@ def test_balance_loss_of_large_batches(nv, T, E, k, score, dtype, cu):
     if dtype == "bf16":
         tol = tol * (1 + HALF_BF16) + HALF_BF16 * np.abs(ref)
     assert (np.abs(d.double().cpu().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("score,level,bias_size", [(G.SIGMOID, -87.35, 0.0), (G.SQRT_SOFTPLUS, -174.7, 0.0),
+                                                   (G.SOFTMAX, -87.35, 0.0), (G.SIGMOID, -87.35, 1e-38)])
+def test_scores_at_the_end_of_float32(nv, score, level, bias_size):
+    """Scores about 2^-126: a sum (of a group's two highest, or with a bias) of what float32 keeps of one and loses of
+    another does not have the order of the sums."""
+    T, E = 600, 64
+    rng = np.random.default_rng(9)
+    x = level + rng.uniform(-0.15, 0.15, (T, E))
+    if score == G.SOFTMAX:
+        x[:, 0] = 0.0
+    x = as_stored(x, "f32")
+    bias = (rng.uniform(-1, 1, E) * bias_size).astype(np.float32) if bias_size else None
+    for groups, top in ((1, 1), (16, 5)) if bias_size else ((16, 5), (32, 3)):
+        got, ref = choices(nv, x, 3, score, bias, groups, top)
+        assert wrong_rows(got, ref) == 0, groups
