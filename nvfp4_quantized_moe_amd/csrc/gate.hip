@@ -52,7 +52,10 @@ __device__ __forceinline__ void load_row(const L* logits, size_t row, int E, flo
 
 // Scores that depend on one logit alone (x = -inf gives 0).
 __device__ __forceinline__ float sigmoid_score(float x) { return 1.0f / (1.0f + expf(-x)); }
-__device__ __forceinline__ double sigmoid_score(double x) { return 1.0 / (1.0 + exp(-x)); }
+__device__ __forceinline__ double sigmoid_score(double x) {  // e^-x itself would end at x = -709, not -745
+  const double e = exp(-fabs(x));
+  return (x < 0.0 ? e : 1.0) / (1.0 + e);
+}
 // sqrt(log(1 + e^x)) with the large term outside the logarithm. Far below 0
 // it equals e^(x/2) to the last bit, and e^x itself would underflow first.
 __device__ __forceinline__ float sqrt_softplus(float x) {

@@ -208,3 +208,17 @@ def test_scores_at_the_end_of_float32(nv, score, level, bias_size):
     for groups, top in ((1, 1), (16, 5)) if bias_size else ((16, 5), (32, 3)):
         got, ref = choices(nv, x, 3, score, bias, groups, top)
         assert wrong_rows(got, ref) == 0, groups
+
+
+@pytest.mark.parametrize("score,level", [(G.SIGMOID, -500.0), (G.SIGMOID, -712.0), (G.SIGMOID, -722.0),
+                                         (G.SQRT_SOFTPLUS, -650.0), (G.SOFTMAX, -722.0)])
+@pytest.mark.parametrize("groups,top", [(1, 1), (4, 2)])
+def test_keys_of_float64_down_to_its_end(nv, score, level, groups, top):
+    """Scores that float64 still tells apart (steps of 1/4 of the logit, its last digits above 2^-1074)."""
+    T, E = 300, 40
+    rng = np.random.default_rng(int(-level))
+    x = level + rng.integers(-20, 21, (T, E)) / 4.0
+    if score == G.SOFTMAX:
+        x[:, ::10] = 0.0
+    got, ref = choices(nv, x, 7, score, np.zeros(E, np.float32), groups, top)
+    assert wrong_rows(got, ref) == 0
