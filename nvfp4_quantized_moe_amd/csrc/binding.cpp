@@ -410,12 +410,16 @@ PyObject* gemm(PyObject* const* a) {
   return d.take();
 }
 
-PyObject* ffn(PyObject* const* a) {  // weights (checked when they were made), x, add, out, ws
+PyObject* ffn(PyObject* const* a) {  // weights (whose attributes may have been set since they were made), x, add, out, ws
   Call call("int8_ffn_forward");
   const at::Tensor& w1 = call.here(needed(a[0], "weights.w1_q"), kI8, "weights.w1_q");
-  const at::Tensor& w2 = needed(a[2], "weights.w2_q");
-  const at::Tensor &w1_scale = needed(a[1], "weights.w1_scale"), &w2_scale = needed(a[3], "weights.w2_scale");
-  const int64_t H = w2.size(0), I = w2.size(1);
+  const at::Tensor& w2 = call.here(needed(a[2], "weights.w2_q"), kI8, "weights.w2_q");
+  const auto [H, I] = matrix(w2, "weights.w2_q");
+  call.shaped(w1, {2 * I, H}, "weights.w1_q");
+  needed(a[1], "weights.w1_scale");
+  needed(a[3], "weights.w2_scale");
+  const float* w1_scale = call.input<float>(a[1], kF32, {2 * I}, "weights.w1_scale");
+  const float* w2_scale = call.input<float>(a[3], kF32, {H}, "weights.w2_scale");
   const at::Tensor& x = call.here(needed(a[4], "x"), kBf16, "x");
   const int64_t T = matrix(x, "x").rows;
   call.shaped(x, {T, H}, "x");
@@ -423,9 +427,9 @@ PyObject* ffn(PyObject* const* a) {  // weights (checked when they were made), x
   const Out out(call, a[6], {T, H}, kBf16, "out");
   const Out ws = workspace(call, a[7], int8_ffn_ws_bytes((int32_t)T, (int32_t)H, (int32_t)I));
   call.run([&, T = (int32_t)T, H = (int32_t)H, I = (int32_t)I](void* stream) {
-    return int8_ffn_forward(static_cast<const int8_t*>(w1.data_ptr()), static_cast<const float*>(w1_scale.data_ptr()),
-                            static_cast<const int8_t*>(w2.data_ptr()), static_cast<const float*>(w2_scale.data_ptr()),
-                            x.data_ptr(), T, H, I, add, out.at<void>(), ws.at<void>(), ws.bytes(), stream);
+    return int8_ffn_forward(static_cast<const int8_t*>(w1.data_ptr()), w1_scale,
+                            static_cast<const int8_t*>(w2.data_ptr()), w2_scale, x.data_ptr(), T, H, I, add,
+                            out.at<void>(), ws.at<void>(), ws.bytes(), stream);
   });
   return out.take();
 }
