@@ -4,6 +4,11 @@ Argument marshalling only: every step runs in the library's HIP kernels;
 torch provides device memory and the current stream. The functions carry the
 names of the C entry points declared in include/nvfp4moe.h.
 
+No call takes part in autograd: outputs come back without a history, also from
+tensors that require a gradient. Gradients are calls of their own
+(moe_gate_backward, moe_block_norm_backward), for a user's autograd function to
+call; the expert layer and the dense expert have none.
+
 Importing this module loads the built library and fails loudly when it is
 missing; there is no CPU fallback.
 """
@@ -86,7 +91,8 @@ _forward_stages = _sig("nvfp4_moe_forward_stage_events", ctypes.c_int, ctypes.PO
                        _vp, _i32, _i32, _vp, _vp, _sz, ctypes.POINTER(_vp), _vp)
 _forward_static = _sig("nvfp4_moe_forward_static", ctypes.c_int, ctypes.POINTER(_Weights), _vp, _i32, _vp, _vp,
                        _i32, _i32, _vp, _vp, _vp, _sz, _vp)
-# the C entry points behind _native, which checks their arguments and calls them itself
+# the C entry points behind _native, which checks their arguments and calls them itself; declared here for callers
+# who bring pointers of their own
 _gate_topk = _sig("moe_gate_topk", ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
                   _vp, _vp, _vp)
 _balance_ws = _sig("moe_balance_loss_ws_bytes", _sz, _i32, _i32, _i32)

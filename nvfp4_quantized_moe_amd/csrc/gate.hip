@@ -89,8 +89,10 @@ __device__ __forceinline__ bool in_tail(float sum, int score) {  // every logit 
 constexpr float kTailEnd = -708.0f;
 
 // The same scores where they are summed or multiplied into a gradient rather
-// than compared: hardware exponential, logarithm and reciprocal, each within
-// one or two float32 steps, e^x through 2^(x log2 e) with |x| half steps more.
+// than compared: hardware exponential, logarithm, root and reciprocal, each
+// within one or two float32 steps of what it is given: e^x through 2^(x log2 e)
+// has |x| half steps more, log(1 + t) the rounding of 1 + t (64 half steps of the
+// result at t = 2^-6, fewer above).
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 __device__ __forceinline__ float fast_log1p(float t) {  // t >= 0
@@ -554,12 +556,16 @@ __device__ __forceinline__ void write_choices(const float (&x)[VPT], const GateS
 // expert, 16384 x 384 by sqrt-softplus took 33 us instead of 20).
 //
 // Bound by the instructions of choosing: 16384 x 256 BF16 with bias and 8
-// groups takes 18.6 us, 550 vector instructions a token, 70 % of the time
-// issuing them (its 8 MB take 1.8 us); 16384 x 384 by the logits alone 11.4.
+// groups takes 19.1 us, 570 vector instructions a token, waiting for 38 % of
+// its waves' cycles (its 8 MB take 1.8 us); 16384 x 384 by the logits alone 10.9.
 // Waves on a SIMD, as many as the registers of the common path allow: eight
-// (8192 x 256 in groups 11.5 us, with seven 12.3; 16384 x 384 19.6, with six
-// 20.6), six with 8 logits per lane (16384 x 512 by the logits 12.7, with eight
-// 13.2), four with 16 (16384 x 1024 32.1, with five 32.6).
+// (8192 x 256 in groups 12.0 us, with seven 12.3; 16384 x 384 by sqrt-softplus
+// with bias 19.5, 20.0), six with 8 logits per lane (16384 x 512 by the logits
+// 12.5, with eight 15.7), four with 16 (16384 x 1024 by the sigmoid with bias
+// 32.5, with five 52).
+// k of one or two with a bias or groups: the threshold of k runs often passes
+// fewer than k + 1 keys, and such rows take the float64 keys (16384 x 384 by
+// sqrt-softplus with bias: k = 1 23.0 us, 2 22.1, 4 19.6, 8 20.4).
 template <typename L, int VPT>
 __global__ __launch_bounds__(64 * kGateWaves, VPT <= 6 ? 8 : VPT <= 8 ? 6 : 4) void gate_topk_kernel(const L* __restrict__ logits,
                                                                     const float* __restrict__ bias,
@@ -757,7 +763,7 @@ __device__ __forceinline__ bool row_scores(const float (&x)[VPT], int score, flo
 // float32, 64 tokens at most in a row, then in LDS in float64 (a chunk of the
 // largest batches gives a wave 16384 tokens); choices counted by LDS atomics on
 // whole numbers.
-// (16384 x 384 float: 12.4 us, 2 TB/s; about half of it issues the 220 vector
+// (16384 x 384 float: 12.6 us, 2 TB/s; about half of it issues the 230 vector
 // instructions a token, the rest is the launch and the first row's latency.)
 template <typename L, int VPT>
 __global__ __launch_bounds__(64 * kGateWaves) void balance_partial_kernel(const L* __restrict__ logits,
@@ -1252,7 +1258,9 @@ extern "C" int moe_balance_loss(const void* logits, int32_t logits_dtype, const 
     NVFP4_CHECK_LAUNCH();
     // Long sequences: more workgroups and waves over the same chunks (the whole
     // call, 16384 x 384: one sequence 17.3 us [otherwise 29.5], 4 sequences 16.1
-    // [18.0]; short ones lose, 24 sequences: 21.5 [15.3]).
+    // [18.0]; short ones lose, 24 sequences: 21.5 [15.3]). By the mean length, as
+    // the lengths are on the device: one sequence of 16016 tokens beside 23 of 16
+    // takes 32.6 us, alone 19.9 (logits from memory).
     const bool tall = T / B >= 64 * g.chunk;
     const int cols = tall ? (E + 15) / 16 : (E + 63) / 64;
     if (tall)
