@@ -25,7 +25,7 @@ def score_slopes(x, score):
     """d score / d x of the scores that depend on one logit alone."""
     s = scores(x, score)
     if score == SIGMOID:
-        return s * (1.0 - s)
+        return s * scores(-np.asarray(x, np.float64), SIGMOID)  # 1 - s would have lost its digits where s is near 1
     low = np.maximum(np.where(np.isfinite(x), x, -1e9), -700.0)
     full = scores(low, SIGMOID) / (2.0 * scores(low, score))
     return np.where(np.isfinite(x), full, 0.0)
