@@ -1,0 +1,484 @@
+"""Operators beside the NVFP4 layer, as cases that can be timed and compared.
+
+Microscaled 4-bit floating point (E2M1 elements, one power of two for each 32 of them): quantisation along rows, along
+columns or both, and the product of two such matrices, which is what a projection, a dense expert and the three products
+of a training step need. The whole expert layer for a few tokens, on the NVFP4 weights the layer keeps anyway. Layer norm
+with the residual update in front of it, and its gradients.
+
+With `own` false, `run` computes them from elementary torch operations; with `own` true it calls this package.
+`exact` gives the same results in 64 bits: the forward formulas written a second time, the gradients from
+differentiating them.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+FLOOR, CEIL = 0, 1  # the block's scale: the largest power of two below amax / 4, or the smallest that clips nothing
+EPS = 1e-5
+
+
+def listed():
+    return [
+        # activations of one decode step, quantised along the row for the next product
+        dict(name="mx_quant_decode", kind="mx_quant", M=64, K=7168, dtype="bf16", way="rows", rule=FLOOR),
+        # gradients of a training step, for both products that read them: along the rows and along the columns
+        dict(name="mx_quant_train", kind="mx_quant", M=8192, K=7168, dtype="bf16", way="both", rule=CEIL),
+        # one projection of one token: its weights are read once
+        dict(name="mx_linear_token", kind="mx_linear", T=1, N=4096, K=7168, silu=False, add=False, rule=FLOOR),
+        # a projection of a ragged chunk, added to a residual
+        dict(name="mx_linear_ragged", kind="mx_linear", T=333, N=1000, K=1040, silu=False, add=True, rule=FLOOR),
+        # the gate and up product of a dense expert over a prefill batch
+        dict(name="mx_linear_prefill", kind="mx_linear", T=8192, N=4096, K=7168, silu=True, add=False, rule=FLOOR),
+        # a projection's training step: its output, the gradient of its input and the one of its weights
+        dict(name="mx_train", kind="mx_train", T=4096, N=4096, K=7168, rule=CEIL),
+        # the expert layer of a small model for five tokens: latency
+        dict(name="few_small", kind="few", T=5, k=4, E=64, local=16, start=16, H=512, I=384, add=False, masked=False),
+        # one token through its eight experts, all of them on this GPU, added to the dense expert's output
+        dict(name="few_token", kind="few", T=1, k=8, E=32, local=32, start=0, H=7168, I=2048, add=True, masked=False),
+        # a decode step of a serving batch with padding, on one rank's share of the experts
+        dict(name="few_batch", kind="few", T=64, k=8, E=384, local=48, start=96, H=7168, I=2048, add=False, masked=True),
+        # the norm of a decode step, behind its residual update
+        dict(name="norm_decode", kind="norm", T=64, H=7168, x="bf16", res="bf16"),
+        # the same for a prefill batch
+        dict(name="norm_prefill", kind="norm", T=8192, H=7168, x="bf16", res="bf16"),
+        # its backward pass: float32 residual stream, ragged width, an odd number of tokens
+        dict(name="norm_train", kind="norm_backward", T=8191, H=2888, x="bf16", res="f32"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    kind = rng.choice(["mx_quant", "mx_linear", "mx_linear", "mx_train", "few", "few", "norm", "norm_backward"])
+    rule = rng.choice([FLOOR, CEIL])
+    if kind == "mx_quant":
+        return dict(kind=kind, M=_log_int(rng, 1, 8192), K=8 * _log_int(rng, 4, 896), dtype=rng.choice(["bf16", "f32"]),
+                    way=rng.choice(["rows", "columns", "both"]), rule=rule)
+    if kind == "mx_linear":
+        silu = rng.random() < 0.4
+        return dict(kind=kind, T=_log_int(rng, 1, 8192), N=16 * _log_int(rng, 4, 256), K=8 * _log_int(rng, 8, 896),
+                    silu=silu, add=rng.random() < 0.5, rule=rule)
+    if kind == "mx_train":
+        return dict(kind=kind, T=_log_int(rng, 1, 4096), N=8 * _log_int(rng, 8, 512), K=8 * _log_int(rng, 8, 896),
+                    rule=rule)
+    if kind == "few":
+        local = _log_int(rng, 1, 48)
+        E = local * rng.choice([1, 1, 2, 8])
+        return dict(kind=kind, T=_log_int(rng, 1, 64), k=rng.randint(1, min(8, E)), E=E, local=local,
+                    start=rng.randrange(0, E - local + 1), H=128 * _log_int(rng, 1, 56), I=128 * _log_int(rng, 1, 16),
+                    add=rng.random() < 0.5, masked=rng.random() < 0.5)
+    return dict(kind=kind, T=_log_int(rng, 1, 8192), H=8 * _log_int(rng, 16, 896), x=rng.choice(["bf16", "f32"]),
+                res=rng.choice(["none", "bf16", "f32"]))
+
+
+# ------------------------------------------------------------------------------------------------------ inputs
+
+MIDPOINTS = (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)  # between neighbouring magnitudes; a tie goes to the even index
+
+
+def _e2m1_index(a):
+    """Index of the magnitude nearest to a >= 0 among 0, .5, 1, 1.5, 2, 3, 4, 6."""
+    i = torch.zeros_like(a, dtype=torch.uint8)
+    for j, mid in enumerate(MIDPOINTS):
+        i += (a >= mid) if j % 2 else (a > mid)
+    return i
+
+
+def _pack(index, negative):
+    nib = index | (negative.to(torch.uint8) << 3)
+    return nib[..., 0::2] | (nib[..., 1::2] << 4)
+
+
+def _padded(n):
+    return (n + 127) // 128 * 128
+
+
+def _power_of_two(field):
+    """2^(field - 127) float32, field int32 in [0, 254]: its exponent bits, or the subnormal 2^-127."""
+    return torch.where(field == 0, 0x400000, field << 23).to(torch.int32).view(torch.float32)
+
+
+def _mx_codes(x, rule):
+    """(index uint8, negative, exponent code uint8) of x [M, K] float32, zeros behind K up to a multiple of 128."""
+    M, K = x.shape
+    by = torch.nn.functional.pad(x, (0, _padded(K) - K)).view(M, -1, 32)
+    bits = by.abs().amax(2).contiguous().view(torch.int32)
+    code = (bits >> 23) - 2
+    if rule == CEIL:
+        code = code + ((bits & 0x7FFFFF) > 0x400000)
+    code = code.clamp(min=0)
+    index = _e2m1_index(by.abs() * _power_of_two(254 - code)[..., None])
+    return index.view(M, -1), (by < 0).view(M, -1), code.to(torch.uint8)
+
+
+def _mx_value(index, negative, code):
+    values = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=index.device)
+    v = values[index.long()]
+    v = torch.where(negative, -v, v)
+    return (v.view(*code.shape, 32) * _power_of_two(code.int())[..., None]).view(v.shape)
+
+
+def _mx(x, rule):
+    """The values that x [M, K] has after quantisation, float32 [M, K padded]."""
+    return _mx_value(*_mx_codes(x.float(), rule))
+
+
+def _nvfp4_codes(w):
+    """NVFP4 of w [N, K] float32: packed codes, E4M3 scales of blocks of 16, the global scale."""
+    N, K = w.shape
+    gs = w.abs().amax() / (6.0 * 448.0)
+    by = w.view(N, K // 16, 16)
+    sf = (by.abs().amax(2) / (6.0 * gs)).to(torch.float8_e4m3fn)
+    index = _e2m1_index(by.abs() / (sf.float() * gs).clamp(min=1e-30)[..., None])
+    return _pack(index.view(N, K), w < 0), sf.view(torch.uint8), gs
+
+
+def _nvfp4_value(q, sf, gs):
+    values = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=q.device)
+    values = torch.cat([values, -values])
+    v = torch.stack([values[(q & 15).long()], values[(q >> 4).long()]], dim=-1).view(*sf.shape, 16)
+    return (v * (sf.view(torch.float8_e4m3fn).float() * gs)[..., None]).view(*q.shape[:-1], -1)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(int(seed))
+
+    def randn(*shape, dtype=torch.float32, scale=1.0):
+        return (torch.randn(*shape, device="cuda", generator=g) * scale).to(dtype)
+
+    def rand(*shape):
+        return torch.rand(*shape, device="cuda", generator=g)
+
+    def activations(rows, cols, dtype):
+        # a size of each channel and, here and there, an outlier: what shared scales have to live with
+        size = torch.exp(randn(cols, scale=0.5))
+        x = randn(rows, cols) * size
+        return torch.where(rand(rows, cols) < 1e-3, x * 20.0, x).to(dtype)
+
+    s = {"case": case, "kind": case["kind"]}
+    kind = case["kind"]
+    if kind == "mx_quant":
+        s["x"] = activations(case["M"], case["K"], DTYPES[case["dtype"]])
+    elif kind == "mx_linear":
+        T, N, K = case["T"], case["N"], case["K"]
+        s["x"] = activations(T, K, torch.bfloat16)
+        index, negative, code = _mx_codes(randn(N, K, scale=0.02), case["rule"])  # offline, kept as codes
+        s["w_q"], s["w_scale"] = _pack(index, negative), code
+        s["add"] = randn(T, N // 2 if case["silu"] else N, dtype=torch.bfloat16) if case["add"] else None
+    elif kind == "mx_train":
+        T, N, K = case["T"], case["N"], case["K"]
+        s["x"] = activations(T, K, torch.bfloat16)
+        s["w"] = randn(N, K, dtype=torch.bfloat16, scale=0.02)
+        s["d_y"] = randn(T, N, dtype=torch.bfloat16, scale=0.01)
+    elif kind == "few":
+        T, k, E, L, H, I = (case[n] for n in ("T", "k", "E", "local", "H", "I"))
+        w = {n: [] for n in ("w1_q", "w1_sf", "w1_gs", "w2_q", "w2_sf", "w2_gs")}
+        for _ in range(L):
+            for n, rows, cols in (("w1", 2 * I, H), ("w2", H, I)):
+                for m, t in zip(("_q", "_sf", "_gs"), _nvfp4_codes(randn(rows, cols, scale=0.02))):
+                    w[n + m].append(t)
+        w = {n: torch.stack(t) for n, t in w.items()}
+        if own:
+            import nvfp4_quantized_moe_amd as nv
+            s["weights"] = nv.MoEWeights(nv.nvfp4_pack_weights(w["w1_q"], w["w1_sf"]), w["w1_gs"],
+                                         nv.nvfp4_pack_weights(w["w2_q"], w["w2_sf"]), w["w2_gs"])
+        else:
+            s.update(w)
+        s["x"] = randn(T, H, dtype=torch.bfloat16)
+        top = torch.topk(randn(E, scale=0.5)[None] + randn(T, E), k, dim=1)
+        s["ids"] = top.indices.to(torch.int32)
+        s["w"] = torch.softmax(top.values, dim=1)
+        if case["masked"]:  # padding tokens choose nothing
+            dead = rand(T, 1) < 0.1
+            s["ids"], s["w"] = s["ids"].masked_fill(dead, -1), s["w"].masked_fill(dead, 0.0)
+        s["ids"], s["w"] = s["ids"].contiguous(), s["w"].contiguous()
+        s["add"] = randn(T, H, dtype=torch.bfloat16) if case["add"] else None
+    else:
+        T, H, xt = case["T"], case["H"], DTYPES[case["x"]]
+        rt = None if case["res"] == "none" else DTYPES[case["res"]]
+        s["x"] = (randn(T, H, scale=0.7) + 0.3).to(xt)
+        s["residual"] = None if rt is None else (randn(T, H, scale=2.0) + randn(T, 1)).to(rt)
+        s["w_ln"], s["b_ln"] = 1.0 + randn(H, scale=0.1), randn(H, scale=0.1)
+        s["scale"] = 1.0 if rt is None else 0.75
+        if kind == "norm_backward":
+            s["d_y"] = randn(T, H, dtype=xt, scale=0.02)
+            s["d_res"] = None if rt is None else randn(T, H, dtype=rt, scale=0.02)
+    return s
+
+
+# -------------------------------------------------------------------------------------------------- plain forms
+
+def _plain_mx_quant(s):
+    c, x = s["case"], s["x"]
+    out = []
+    if c["way"] != "columns":
+        out.append(_mx(x, c["rule"])[:, :c["K"]].to(x.dtype))
+    if c["way"] != "rows":
+        out.append(_mx(x.t().contiguous(), c["rule"])[:, :c["M"]].to(x.dtype))
+    return out
+
+
+def _plain_mx_linear(s):
+    c = s["case"]
+    q = s["w_q"]
+    nib = torch.stack([q & 15, q >> 4], dim=-1).view(q.shape[0], -1)
+    w = _mx_value(nib & 7, nib > 7, s["w_scale"])
+    y = _mx(s["x"], c["rule"]) @ w.t()
+    if c["silu"]:
+        g, u = y[:, :c["N"] // 2], y[:, c["N"] // 2:]
+        y = g / (1.0 + torch.exp(-g)) * u
+    if s["add"] is not None:
+        y = y + s["add"].float()
+    return y.to(torch.bfloat16)
+
+
+def _plain_mx_train(s):
+    rule, T, K, N = (s["case"][n] for n in ("rule", "T", "K", "N"))
+    x, w, dy = s["x"], s["w"], s["d_y"]
+    y = _mx(x, rule) @ _mx(w, rule).t()
+    d_x = _mx(dy, rule) @ _mx(w.t().contiguous(), rule).t()
+    d_w = _mx(dy.t().contiguous(), rule) @ _mx(x.t().contiguous(), rule).t()
+    return {"y": y.to(torch.bfloat16), "d_x": d_x.to(torch.bfloat16), "d_w": d_w}
+
+
+def _plain_few(s):
+    c = s["case"]
+    T, k, L, I = c["T"], c["k"], c["local"], c["I"]
+    x = s["x"].float()
+    out = torch.zeros(T, c["H"], device=x.device) if s["add"] is None else s["add"].float()
+    local = s["ids"] - c["start"]
+    mine = (local >= 0) & (local < L)
+
+    def expert(rows, w1, w2):
+        gu = rows @ w1.t()
+        g, u = gu[:, :I], gu[:, I:]
+        h = (g / (1.0 + torch.exp(-g)) * u).to(torch.bfloat16)  # the second product's input is kept in BF16
+        return h.float() @ w2.t()
+
+    if T * k < L:  # by choices: the weights of each
+        at = local.clamp(0, L - 1).long()
+        for t in range(T):
+            for j in range(k):
+                e = at[t, j:j + 1]
+                w1, w2 = (_nvfp4_value(*(s[n + m].index_select(0, e)[0] for m in ("_q", "_sf", "_gs")))
+                          for n in ("w1", "w2"))
+                out[t] += expert(x[t:t + 1], w1, w2)[0] * (s["w"][t, j] * mine[t, j])
+    else:  # by experts: every token, those that did not choose it with weight 0
+        for e in range(L):
+            w1, w2 = (_nvfp4_value(*(s[n + m][e] for m in ("_q", "_sf", "_gs"))) for n in ("w1", "w2"))
+            weight = (s["w"] * (local == e)).sum(1, keepdim=True)
+            out = out + expert(x, w1, w2) * weight
+    return out.to(torch.bfloat16)
+
+
+def _plain_norm(s):
+    r = s["x"]
+    if s["residual"] is not None:
+        r = (s["residual"].float() + s["scale"] * s["x"].float()).to(s["residual"].dtype)
+    f = r.float()  # the norm reads the residual stream as it is kept
+    d = f - f.mean(1, keepdim=True)
+    y = (d * torch.rsqrt((d * d).mean(1, keepdim=True) + EPS) * s["w_ln"] + s["b_ln"]).to(s["x"].dtype)
+    return (y,) if s["residual"] is None else (r, y)
+
+
+def _plain_norm_grad(s):
+    # `residual` is the stream behind the update, as the forward pass left it
+    r = (s["x"] if s["residual"] is None else s["residual"]).float()
+    dy = s["d_y"].float()
+    d = r - r.mean(1, keepdim=True)
+    rho = torch.rsqrt((d * d).mean(1, keepdim=True) + EPS)
+    n = d * rho
+    dn = dy * s["w_ln"]
+    dr = rho * (dn - dn.mean(1, keepdim=True) - n * (dn * n).mean(1, keepdim=True))
+    out = {"d_w": (dy * n).sum(0), "d_b": dy.sum(0)}
+    if s["residual"] is not None:
+        dr = dr + s["d_res"].float()
+        out["d_residual"] = dr.to(s["residual"].dtype)
+    out["d_x"] = (s["scale"] * dr).to(s["x"].dtype)
+    return out
+
+
+# ------------------------------------------------------------------------------------------------------- a pass
+
+def run(s):
+    kind, c = s["kind"], s["case"]
+    if own:
+        import nvfp4_quantized_moe_amd as nv
+        if kind == "mx_quant":
+            x = s["x"]
+            if c["way"] != "both":
+                way = nv.MX_ROWS if c["way"] == "rows" else nv.MX_COLUMNS
+                q, sc = nv.mxfp4_quantize(x, way, rule=c["rule"])
+                return [nv.mxfp4_dequantize(q, sc, x.dtype, cols=c["K"] if c["way"] == "rows" else c["M"])]
+            q, sc, q_t, sc_t = nv.mxfp4_quantize(x, nv.MX_BOTH, rule=c["rule"])
+            return [nv.mxfp4_dequantize(q, sc, x.dtype, cols=c["K"]),
+                    nv.mxfp4_dequantize(q_t, sc_t, x.dtype, cols=c["M"])]
+        if kind == "mx_linear":
+            q, sc = nv.mxfp4_quantize(s["x"], rule=c["rule"])
+            return nv.mxfp4_gemm(q, sc, s["w_q"], s["w_scale"],
+                                 epilogue=nv.EPI_SILU_MUL if c["silu"] else nv.EPI_BF16, add=s["add"])
+        if kind == "mx_train":
+            x, x_s, x_t, x_ts = nv.mxfp4_quantize(s["x"], nv.MX_BOTH, rule=c["rule"])
+            w, w_s, w_t, w_ts = nv.mxfp4_quantize(s["w"], nv.MX_BOTH, rule=c["rule"])
+            dy, dy_s, dy_t, dy_ts = nv.mxfp4_quantize(s["d_y"], nv.MX_BOTH, rule=c["rule"])
+            return {"y": nv.mxfp4_gemm(x, x_s, w, w_s), "d_x": nv.mxfp4_gemm(dy, dy_s, w_t, w_ts),
+                    "d_w": nv.mxfp4_gemm(dy_t, dy_ts, x_t, x_ts, dtype=torch.float32)}
+        if kind == "few":
+            return nv.nvfp4_moe_forward_few(s["weights"], s["x"], s["ids"], s["w"], c["start"], add=s["add"])
+        if kind == "norm":
+            r, y = nv.moe_layer_norm(s["x"], s["residual"], s["w_ln"], s["b_ln"], scale=s["scale"], eps=EPS)
+            return (y,) if s["residual"] is None else (r, y)
+        d = nv.moe_layer_norm_backward(s["d_y"], s["d_res"], s["x"] if s["residual"] is None else s["residual"],
+                                       s["w_ln"], s["b_ln"], scale=s["scale"], eps=EPS,
+                                       residual=s["residual"] is not None)
+        return {n: v for n, v in d.items() if v is not None}
+    if kind == "mx_quant":
+        return _plain_mx_quant(s)
+    if kind == "mx_linear":
+        return _plain_mx_linear(s)
+    if kind == "mx_train":
+        return _plain_mx_train(s)
+    if kind == "few":
+        return _plain_few(s)
+    return _plain_norm(s) if kind == "norm" else _plain_norm_grad(s)
+
+
+def work(case):
+    kind = case["kind"]
+    size = {"bf16": 2, "f32": 4, "none": 0}
+    if kind == "mx_quant":
+        each = case["M"] * case["K"] * size[case["dtype"]]
+        ways = 2 if case["way"] == "both" else 1
+        return {"bytes": (1 + ways) * each, "flops": 8 * ways * case["M"] * case["K"]}
+    if kind == "mx_linear":
+        T, N, K = case["T"], case["N"], case["K"]
+        n_out = N // 2 if case["silu"] else N
+        return {"bytes": N * K * 17 // 32 + 2 * T * K + 2 * T * n_out * (1 + case["add"]), "flops": 2 * T * N * K}
+    if kind == "mx_train":
+        T, N, K = case["T"], case["N"], case["K"]
+        return {"bytes": 2 * (T * K + N * K + T * N) + 2 * T * (N + K) + 4 * N * K, "flops": 6 * T * N * K}
+    if kind == "few":
+        T, k, H, I = case["T"], case["k"], case["H"], case["I"]
+        share = case["local"] / case["E"]
+        pairs = T * k * share
+        experts = case["local"] * (1.0 - (1.0 - k / case["E"]) ** T)  # those that some token chose, on average
+        return {"bytes": int(experts * 3 * H * I * 9 / 16) + 2 * T * H * (2 + case["add"]) + 8 * T * k,
+                "flops": int(6 * pairs * H * I)}
+    T, H, x, r = case["T"], case["H"], size[case["x"]], size[case["res"]]
+    if kind == "norm":
+        return {"bytes": 2 * T * H * (x + r) + 8 * H, "flops": 8 * T * H}
+    return {"bytes": T * H * (2 * x + (3 * r if r else x)) + 16 * H, "flops": 16 * T * H}
+
+
+# ------------------------------------------------------------------------------------------------ 64-bit results
+
+def _exact_mx(x, rule):
+    """Values of x [M, K] float64 after quantisation along its rows."""
+    M, K = x.shape
+    pad = -K % 32
+    by = torch.cat([x, x.new_zeros(M, pad)], dim=1).view(M, -1, 32)
+    amax = by.abs().max(dim=2, keepdim=True).values
+    m, e = torch.frexp(amax)  # amax = m 2^e, m in [1/2, 1)
+    power = e - 3 + (m > 0.75) if rule == CEIL else e - 3
+    power = torch.where(amax > 0, power, -127).clamp(min=-127)
+    unit = ((power.long() + 1023) << 52).view(torch.float64)
+    v = by / unit
+    a = v.abs()
+    step = torch.where(a < 2.0, 0.5, torch.where(a < 4.0, 1.0, 2.0))
+    near = (torch.round(a / step) * step).clamp(max=6.0)  # torch.round takes halves to the even neighbour
+    return (torch.copysign(near, v) * unit).view(M, -1)[:, :K]
+
+
+def _exact_product(a, b):
+    return torch.matmul(a, b.t().contiguous())
+
+
+def _exact_few(s, weights):
+    c = s["case"]
+    x, I = s["x"].double(), c["I"]
+    out = torch.zeros(c["T"], c["H"], dtype=torch.float64, device=x.device)
+    if s["add"] is not None:
+        out += s["add"].double()
+    ids = s["ids"].cpu() - c["start"]
+    table = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64,
+                         device=x.device)
+
+    def matrix(n, e):
+        q = weights[n + "_q"][e].long()
+        v = torch.empty(q.shape[0], 2 * q.shape[1], dtype=torch.float64, device=q.device)
+        v[:, 0::2], v[:, 1::2] = table[q % 16], table[torch.div(q, 16, rounding_mode="floor")]
+        sf = weights[n + "_sf"][e].view(torch.float8_e4m3fn).double() * weights[n + "_gs"][e].double()
+        return v * sf.repeat_interleave(16, dim=1)
+
+    for e in sorted(set(ids.flatten().tolist())):
+        if not 0 <= e < c["local"]:
+            continue
+        t, j = (ids == e).nonzero(as_tuple=True)
+        gu = _exact_product(x[t], matrix("w1", e))
+        h = (torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]).to(torch.bfloat16).double()
+        y = _exact_product(h, matrix("w2", e)) * s["w"].double()[t, j][:, None]
+        out.index_add_(0, t.to(out.device), y)
+    return out
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False  # the codes, whichever form the package keeps its weights in
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = was
+    kind = s["kind"]
+    if kind == "mx_quant":
+        x, way = s["x"].double(), case["way"]
+        out = [] if way == "columns" else [_exact_mx(x, case["rule"])]
+        return out if way == "rows" else out + [_exact_mx(x.t().contiguous(), case["rule"])]
+    if kind == "mx_linear":
+        q, K, rule = s["w_q"].long(), case["K"], case["rule"]
+        nib = torch.empty(q.shape[0], 2 * q.shape[1], dtype=torch.long, device=q.device)
+        nib[:, 0::2], nib[:, 1::2] = q % 16, torch.div(q, 16, rounding_mode="floor")
+        i = (nib % 8).double()
+        mag = torch.where(i < 4, i / 2, torch.where(i < 6, i - 2, 2 * i - 8))
+        unit = ((s["w_scale"].long() + 1023 - 127) << 52).view(torch.float64)
+        w = torch.where(nib < 8, mag, -mag) * unit.repeat_interleave(32, dim=1)
+        y = _exact_product(_exact_mx(s["x"].double(), rule), w[:, :K])
+        if case["silu"]:
+            g, u = y.chunk(2, dim=1)
+            y = torch.nn.functional.silu(g) * u
+        return y if s["add"] is None else y + s["add"].double()
+    if kind == "mx_train":
+        rule = case["rule"]
+        x, w, dy = (s[n].double() for n in ("x", "w", "d_y"))
+        cols = [_exact_mx(t.t().contiguous(), rule) for t in (x, w, dy)]
+        return {"y": _exact_product(_exact_mx(x, rule), _exact_mx(w, rule)),
+                "d_x": _exact_product(_exact_mx(dy, rule), cols[1]), "d_w": _exact_product(cols[2], cols[0])}
+    if kind == "few":
+        return _exact_few(s, s)
+    leaves = [None if s[n] is None else s[n].double() for n in ("x", "residual", "w_ln", "b_ln")]
+    x, residual, w, b = leaves
+
+    def ln(r, w, b):
+        centred = r - r.sum(1, keepdim=True) / r.shape[1]
+        return centred / torch.sqrt(centred.square().sum(1, keepdim=True) / r.shape[1] + EPS) * w + b
+
+    if kind == "norm":
+        if residual is None:
+            return (ln(x, w, b),)
+        r = residual + s["scale"] * x
+        return r, ln(r.to(s["residual"].dtype).double(), w, b)
+    r = (x if residual is None else residual).requires_grad_(True)
+    w.requires_grad_(True)
+    b.requires_grad_(True)
+    (ln(r, w, b) * s["d_y"].double()).sum().backward()
+    out = {"d_w": w.grad, "d_b": b.grad}
+    d_r = r.grad
+    if residual is not None:
+        d_r = d_r + s["d_res"].double()
+        out["d_residual"] = d_r
+    out["d_x"] = s["scale"] * d_r
+    return out
