@@ -169,6 +169,8 @@ def prepare(case, seed):
         s["x"] = activations(T, K, torch.bfloat16)
         index, negative, code = _mx_codes(randn(N, K, scale=0.02), case["rule"])  # offline, kept as codes
         s["w_q"], s["w_scale"] = _pack(index, negative), code
+        if own:  # a row's four scales of 128 elements side by side, then the rows
+            s["w_scale"] = code.view(N, -1, 4).permute(1, 0, 2).contiguous()
         s["add"] = randn(T, N // 2 if case["silu"] else N, dtype=torch.bfloat16) if case["add"] else None
     elif kind == "mx_train":
         T, N, K = case["T"], case["N"], case["K"]
