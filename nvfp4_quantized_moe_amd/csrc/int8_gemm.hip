@@ -10,6 +10,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "tile.h"
 #include "wave.h"
 
 // Every rounding as it is written (the fmas below are explicit): a token's
@@ -19,7 +20,6 @@
 
 namespace nvfp4 {
 
-typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
 
 constexpr int kInt8MaxK = 65536;
@@ -158,57 +158,6 @@ struct Int8Args {
 };
 enum { kInt8Bf16, kInt8Silu, kInt8Part };  // what a tile writes
 
-// silu(g) u = g u / (1 + e^-g), by e^-|g|: e^-g itself would leave the range
-// of float32 below g = -88 and take the result with it
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  const float e = expf(-fabsf(g));
-  return (g < 0.0f ? g * e : g) / (1.0f + e) * u;
-}
-
-// Tiles in runs of kTileGroup row tiles by all column tiles, so that the
-// workgroups that run at one time share both operands' tiles; consecutive
-// tiles go to one XCD (own L2). Returns (row tile, column tile).
-constexpr int kTileGroup = 8;
-__device__ __forceinline__ int2 tile_of_block(int bid, int mt, int nt) {
-  const int total = mt * nt, whole = total / kXcds * kXcds;
-  const int t = bid < whole ? (bid % kXcds) * (whole / kXcds) + bid / kXcds : bid;
-  const int per = kTileGroup * nt, grp = t / per, rem = t - grp * per;
-  const int rows = min(kTileGroup, mt - grp * kTileGroup);
-  return make_int2(grp * kTileGroup + rem % rows, rem / rows);
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t int8_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
-}
-constexpr int kInt8Out = (int)0x80000000u;  // a buffer offset past every range: such loads give zeros
-
-// 16 bytes per lane from memory to LDS, the lanes' side by side from `to` (the
-// same for the whole wave) on.
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, int4v* to, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, voff, soff, 0, 0);
-}
-
-// W = 8 or 4 outputs of one row, with the BF16 values to be added.
-template <int W>
-struct OutVec;
-template <>
-struct OutVec<8> {
-  typedef uint32_t type __attribute__((ext_vector_type(4)));
-};
-template <>
-struct OutVec<4> {
-  typedef uint32_t type __attribute__((ext_vector_type(2)));
-};
-template <int W>
-__device__ __forceinline__ typename OutVec<W>::type add_and_round(const float* o, typename OutVec<W>::type add) {
-  typename OutVec<W>::type r;
-#pragma unroll
-  for (int e = 0; e < W / 2; ++e)
-    r[e] = f32x2_to_bf16x2(o[2 * e] + __uint_as_float(add[e] << 16),
-                           o[2 * e + 1] + __uint_as_float(add[e] & 0xFFFF0000u));
-  return r;
-}
-
 // Workgroup tile BM x BN of WM x WN waves; MFMA 32x32x32 with the weights as
 // its first operand, so a lane holds runs of four output columns of one token.
 //
@@ -247,9 +196,9 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(Int8Args g, int
   static_assert(!SILU || RPI == 32 || RPI % 64 == 0, "the rows of a load of a wave lie in one half");
   const int a_rows = min(BM, g.M - m0), b_rows = min(SILU ? BN / 2 : BN, (SILU ? half : g.N) - n0);
   const bool up_wave = SILU && RPI != 32 && (wave * (64 / CPR) / 32) % 2 == 1;
-  const __amdgpu_buffer_rsrc_t ra = int8_rsrc(g.a + (size_t)m0 * g.K, (uint32_t)(a_rows * g.K));
-  const __amdgpu_buffer_rsrc_t rb = int8_rsrc(g.b + (size_t)(n0 + (up_wave ? half : 0)) * g.K, (uint32_t)(b_rows * g.K));
-  const __amdgpu_buffer_rsrc_t ru = int8_rsrc(g.b + (size_t)(n0 + half) * g.K, (uint32_t)(b_rows * g.K));
+  const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(g.a + (size_t)m0 * g.K, (uint32_t)(a_rows * g.K));
+  const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(g.b + (size_t)(n0 + (up_wave ? half : 0)) * g.K, (uint32_t)(b_rows * g.K));
+  const __amdgpu_buffer_rsrc_t ru = buffer_rsrc(g.b + (size_t)(n0 + half) * g.K, (uint32_t)(b_rows * g.K));
   int va[PA], vb[PB];
 #pragma unroll
   for (int i = 0; i < PA; ++i) va[i] = min(trow + i * RPI, a_rows - 1) * g.K + tk;
@@ -265,11 +214,11 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(Int8Args g, int
     const int ks = k0 < k_end ? k0 : 0;  // the scalar offset stays inside the range
 #pragma unroll
     for (int i = 0; i < PA; ++i)
-      load_lds16(ra, to + wave * 64 + i * TH, in ? va[i] : kInt8Out, ks);
+      load_lds16(ra, to + wave * 64 + i * TH, in ? va[i] : kOutOfRange, ks);
 #pragma unroll
     for (int i = 0; i < PB; ++i)
       load_lds16(SILU && RPI == 32 && i % 2 == 1 ? ru : rb, to + BM * CPR + wave * 64 + i * TH,
-                 in ? vb[i] : kInt8Out, ks);
+                 in ? vb[i] : kOutOfRange, ks);
   };
   int16v acc[SN][SM];
 #pragma unroll
@@ -305,19 +254,6 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(Int8Args g, int
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks & 1][i], fa[ks & 1][j], acc[i][j], 0, 0, 0);
     }
   };
-  // Waits until at most `left` of this wave's loads are in flight, then for
-  // all waves. The loads of a wave complete in order.
-  auto wait = [](auto left) {
-    constexpr int n = decltype(left)::value;
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 7 << 4);  // vmcnt(n), lgkmcnt(0), no export count
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  constexpr std::integral_constant<int, 0> none;
-  constexpr std::integral_constant<int, 2 * PL> two_stages;
   const int stages = (k_end - k_begin + BK - 1) / BK;
   fetch(k_begin, l0);
   fetch(k_begin + BK, l1);
@@ -327,7 +263,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(Int8Args g, int
   // inside the loop: around the stages it leaves the compiler unsure which
   // buffer a load fills, and it waits for all of them before it reads any.
   auto stage = [&](int s, const int4v* cur, int4v* next) {
-    wait(two_stages);
+    wait_stage<2 * PL>();
     fetch(k_begin + (s + 3) * BK, next);
     compute(cur);
   };
@@ -345,7 +281,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tile_kernel(Int8Args g, int
       if (s + 2 < stages) stage(s + 2, l2, l1);
     }
   }
-  wait(none);
+  wait_stage<0>();
 
   // Epilogue, each wave by itself: 32 tokens x 32 SN columns of sums through
   // LDS, so that a lane takes eight neighbouring columns of a token (four for
