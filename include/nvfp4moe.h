@@ -375,6 +375,59 @@ int int8_ffn_forward(const int8_t* w1_q, const float* w1_scale, const int8_t* w2
                      const void* x_bf16, int32_t T, int32_t hidden, int32_t inter, const void* add_bf16,
                      void* out_bf16, void* ws, size_t ws_bytes, void* stream);
 
+/* --------------------------------------- microscaled 4-bit floats (MXFP4)
+ * E2M1 codes, two to a byte (the first in the low nibble), and for each 32
+ * elements of a row one power of two, a byte holding its exponent + 127 (0xFF:
+ * the block's values are NaN). A matrix [R, C] is kept with C padded to
+ * Cp = mxfp4_padded(C), whole groups of 128, with codes and scales of 0:
+ *   q uint8 [R, Cp/2];  scale uint8 [Cp/128, R, 4], scale[c, r, i] that of the
+ *   elements [128c + 32i, +32) of row r
+ * (row-major scales uint8 [R, Cp/32] are their view [R, Cp/128, 4] with the first
+ * two axes exchanged).
+ */
+enum { MX_SCALE_FLOOR = 0, MX_SCALE_CEIL = 1 };
+int32_t mxfp4_padded(int32_t n);  /* -1 outside [0, 262144] */
+
+/* Quantizer of x [M, K] (BF16 or float, row-major), along its rows (q, scale:
+ * [M, Kp/2], [Kp/128, M, 4]), along its columns (q_t, scale_t: the transposed
+ * matrix, [K, Mp/2], [Mp/128, K, 4]), or both from one read; the pair that is not
+ * wanted is NULL. Of a block with largest magnitude a > 0:
+ *   MX_SCALE_FLOOR: e = floor(log2 a) - 2; values above 6 * 2^e become 6 * 2^e
+ *   MX_SCALE_CEIL:  the smallest e with a <= 6 * 2^e
+ * but at least -127 (also for a = 0); q = E2M1 nearest to x / 2^e, ties to the
+ * even code, both exactly. A block with an infinity or NaN gets the scale 0xFF.
+ * K % 8 == 0, 0 < K <= 262144; M <= 64 * 65535, along the columns <= 262144.
+ * One launch.
+ */
+int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t K, int32_t rule, uint8_t* q, uint8_t* scale,
+                   uint8_t* q_t, uint8_t* scale_t, void* stream);
+
+/* out [R, cols] (BF16 or float) = the values of the first cols columns of q
+ * [R, K/2], scale [K/128, R, 4]. Every one of them has its value in BF16 except
+ * those past its range, which become infinite. K % 128 == 0, cols <= K. One launch.
+ */
+int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int32_t R, int32_t K, int32_t cols, int32_t out_dtype,
+                     void* out, void* stream);
+
+/* G[m, n] = sum_k A[m, k] B[n, k] of the values of a_q [M, K/2], a_scale
+ * [K/128, M, 4] and b_q [N, K/2], b_scale [K/128, N, 4]; products exact, sums in
+ * float32.
+ * epilogue NVFP4_EPI_BF16:     d [M, N] of d_dtype, d = RN(G [+ add]); N % 8 == 0
+ * epilogue NVFP4_EPI_SILU_MUL: gate rows [0, I), up rows [I, 2I) of B, N = 2I:
+ *   d BF16 [M, I], d = RN(silu(G[m, n]) * G[m, I + n] [+ add]); I % 8 == 0
+ * add: of d's type and shape, or NULL; may be d itself. K % 128 == 0, K <= 262144
+ * (K = 0: d = add, or 0), M <= 64 * 65535, N <= 2^27 - 16, M * K and N * K below
+ * 2^36. ws: at least mxfp4_gemm_ws_bytes(M, N, K) bytes (sums of the parts of K
+ * where few tokens split it; 0 otherwise, then ws may be NULL). The order of a
+ * sum depends on M, N and K alone, so calls repeat bit for bit. One launch, or
+ * two with parts. Outputs and workspaces overlap neither inputs nor each other,
+ * except where it is said.
+ */
+size_t mxfp4_gemm_ws_bytes(int32_t M, int32_t N, int32_t K);
+int mxfp4_gemm(const uint8_t* a_q, const uint8_t* a_scale, const uint8_t* b_q, const uint8_t* b_scale, int32_t M,
+               int32_t N, int32_t K, int32_t epilogue, const void* add, int32_t d_dtype, void* d, void* ws,
+               size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------- weighted scatter
  * out[t, :] = RN_bf16( sum over j = 0..k-1 with token_slot[t*k+j] >= 0 of
  *                      topk_w[t, j] * y[token_slot[t*k+j], :] ), float32, increasing j;

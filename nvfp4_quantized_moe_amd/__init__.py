@@ -30,7 +30,8 @@ __all__ = [
     "moe_balance_loss_ws_bytes", "moe_gate_backward", "moe_block_norm", "moe_block_norm_backward",
     "moe_block_norm_backward_ws_bytes", "int8_quantize_rows", "int8_gemm", "int8_gemm_ws_bytes", "int8_ffn_forward",
     "int8_ffn_ws_bytes",
-    "Int8FFNWeights", "prepare_int8_weights",
+    "Int8FFNWeights", "prepare_int8_weights", "MX_ROWS", "MX_COLUMNS", "MX_BOTH", "MX_SCALE_FLOOR", "MX_SCALE_CEIL",
+    "mxfp4_padded", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_gemm_ws_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
@@ -44,6 +45,8 @@ except ImportError as e:
 
 EPI_BF16, EPI_SILU_MUL, EPI_SILU_MUL_DUAL = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID, SCORE_SQRT_SOFTPLUS = 0, 1, 2
+MX_ROWS, MX_COLUMNS, MX_BOTH = 1, 2, 3
+MX_SCALE_FLOOR, MX_SCALE_CEIL = 0, 1
 WS_REGIONS = ["x_q", "x_sf", "scalars", "counts", "offsets", "slot_token", "slot_expert", "slot_weight",
               "token_slot", "tiles", "route_scratch", "h", "h_q", "h_sf", "y", "quant_scratch", "end"]
 
@@ -110,6 +113,11 @@ _int8_gemm_ws = _sig("int8_gemm_ws_bytes", _sz, _i32, _i32, _i32)
 _int8_gemm = _sig("int8_gemm", ctypes.c_int, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp)
 _int8_ffn_ws = _sig("int8_ffn_ws_bytes", _sz, _i32, _i32, _i32)
 _int8_ffn = _sig("int8_ffn_forward", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp)
+_mx_padded = _sig("mxfp4_padded", _i32, _i32)
+_mx_quantize = _sig("mxfp4_quantize", ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp)
+_mx_dequantize = _sig("mxfp4_dequantize", ctypes.c_int, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp)
+_mx_gemm_ws = _sig("mxfp4_gemm_ws_bytes", _sz, _i32, _i32, _i32)
+_mx_gemm = _sig("mxfp4_gemm", ctypes.c_int, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _sz, _vp)
 
 
 class NVFP4Error(RuntimeError):
@@ -501,6 +509,48 @@ def int8_ffn_forward(weights: Int8FFNWeights, x, add=None, out=None, ws=None):
     experts' output; may be out) when given."""
     w = weights
     return _native.ffn(w.w1_q, w.w1_scale, w.w2_q, w.w2_scale, x, add, out, ws)
+
+
+# ------------------------------------------- microscaled 4-bit floats (MXFP4)
+
+def mxfp4_padded(n) -> int:
+    """Columns that a matrix of n columns is padded to: whole groups of 128."""
+    p = int(_mx_padded(n))
+    if p < 0:
+        raise ValueError(f"n: expected 0 to 262144, got {n}")
+    return p
+
+
+def mxfp4_quantize(x, direction=MX_ROWS, rule=MX_SCALE_FLOOR, q=None, scale=None, q_t=None, scale_t=None):
+    """x BF16 or float32 [M, K] -> MXFP4 along its rows (MX_ROWS: q uint8 [M, Kp/2], scale uint8 [Kp/128, M, 4]), along
+    its columns (MX_COLUMNS: q_t [K, Mp/2], scale_t [Mp/128, K, 4], the transposed matrix) or both (MX_BOTH: all
+    four), Kp = mxfp4_padded(K). rule: MX_SCALE_FLOOR (the largest values of a block may saturate) or MX_SCALE_CEIL
+    (none does). Scales in rows, [M, Kp/32], are scale.permute(1, 0, 2).reshape(M, -1)."""
+    return _native.mx_quantize(x, direction, rule, q, scale, q_t, scale_t)
+
+
+def _mx_type(dtype):
+    if dtype is torch.bfloat16:
+        return 0
+    if dtype is torch.float32:
+        return 1
+    raise ValueError(f"dtype: expected torch.bfloat16 or torch.float32, got {dtype}")
+
+
+def mxfp4_dequantize(q, scale, dtype=torch.bfloat16, cols=None, out=None):
+    """The values of MXFP4 codes, [R, cols] (None: all the padded columns), BF16 (exact) or float32."""
+    return _native.mx_dequantize(q, scale, _mx_type(dtype), cols, out)
+
+
+def mxfp4_gemm_ws_bytes(M, N, K) -> int:
+    return int(_mx_gemm_ws(M, N, K))
+
+
+def mxfp4_gemm(a_q, a_scale, b_q, b_scale, epilogue=EPI_BF16, add=None, dtype=torch.bfloat16, d=None, ws=None):
+    """The product A B^T of MXFP4 matrices [M, K] and [N, K], as mxfp4_quantize makes them -> [M, N] (EPI_BF16) of
+    dtype, or BF16 [M, N / 2] of silu(gate) * up with the gate rows of b_q first (EPI_SILU_MUL); add: of that type
+    and shape (such as a residual, or a weight's gradient so far), may be d."""
+    return _native.mx_gemm(a_q, a_scale, b_q, b_scale, epilogue, add, _mx_type(dtype), d, ws)
 
 
 # --------------------------------------------------------------------- the layer

@@ -434,6 +434,84 @@ PyObject* ffn(PyObject* const* a) {  // weights (whose attributes may have been 
   return out.take();
 }
 
+// Codes and scales of an MXFP4 matrix of R rows of C elements, as outputs.
+struct MxOut {
+  Out q, scale;
+  MxOut(Call& call, PyObject* q_o, PyObject* scale_o, int64_t R, int64_t C, const char* q_name, const char* scale_name)
+      : q(call, q_o, {R, C / 2}, kU8, q_name), scale(call, scale_o, {C / 128, R, 4}, kU8, scale_name) {}
+};
+int64_t mx_padded(int64_t n, const char* name) {
+  const int32_t p = mxfp4_padded(to_i32(n, name));
+  if (p < 0) refuse(name, std::to_string(n) + " elements along a row of codes are more than 262144");
+  return p;
+}
+
+PyObject* mx_quantize(PyObject* const* a) {  // x, direction (1 rows, 2 columns, 3 both), rule, q, scale, q_t, scale_t
+  Call call("mxfp4_quantize");
+  const at::Tensor& x = call.floats(needed(a[0], "x"), "x");
+  const auto [M, K] = matrix(x, "x");
+  const int32_t direction = py_i32(a[1], "direction"), rule = py_i32(a[2], "rule");
+  if (direction < 1 || direction > 3) refuse("direction", "expected MX_ROWS, MX_COLUMNS or MX_BOTH, got " + std::to_string(direction));
+  std::optional<MxOut> rows, cols;
+  if (direction & 1) rows.emplace(call, a[3], a[4], M, mx_padded(K, "x"), "q", "scale");
+  if (direction & 2) cols.emplace(call, a[5], a[6], K, mx_padded(M, "x"), "q_t", "scale_t");
+  call.run([&, M = (int32_t)M, K = (int32_t)K](void* stream) {
+    return mxfp4_quantize(x.data_ptr(), code(x), M, K, rule, rows ? rows->q.at<uint8_t>() : nullptr,
+                          rows ? rows->scale.at<uint8_t>() : nullptr, cols ? cols->q.at<uint8_t>() : nullptr,
+                          cols ? cols->scale.at<uint8_t>() : nullptr, stream);
+  });
+  if (direction == 3) return tuple({rows->q.take(), rows->scale.take(), cols->q.take(), cols->scale.take()});
+  MxOut& one = rows ? *rows : *cols;
+  return tuple({one.q.take(), one.scale.take()});
+}
+
+// q uint8 [R, C / 2] and scale uint8 [C / 128, R, 4] as inputs
+struct Mx {
+  const uint8_t *q, *scale;
+  int64_t R, C;
+};
+Mx mx_input(Call& call, PyObject* q_o, PyObject* scale_o, const char* q_name, const char* scale_name) {
+  const at::Tensor& q = call.here(needed(q_o, q_name), kU8, q_name);
+  const auto [R, half] = matrix(q, q_name);
+  if (half % 64 != 0 || half > INT_MAX / 2)
+    refuse(q_name, "expected rows of whole groups of 128 codes (64 bytes), got shape " + text(q.sizes()));
+  needed(scale_o, scale_name);
+  const uint8_t* s = call.input<uint8_t>(scale_o, kU8, {half / 64, R, 4}, scale_name);
+  return {static_cast<const uint8_t*>(q.data_ptr()), s, R, half * 2};
+}
+
+PyObject* mx_dequantize(PyObject* const* a) {  // q, scale, type, cols (None: all), out
+  Call call("mxfp4_dequantize");
+  const Mx m = mx_input(call, a[0], a[1], "q", "scale");
+  const int32_t type = py_i32(a[2], "dtype");
+  const int32_t cols = a[3] == Py_None ? (int32_t)m.C : py_i32(a[3], "cols");
+  if (cols < 0 || cols > m.C) refuse("cols", "expected 0 to " + std::to_string(m.C) + ", got " + std::to_string(cols));
+  const Out out(call, a[4], {m.R, cols}, type == NVFP4_DT_F32 ? kF32 : kBf16, "out");
+  call.run([&](void* stream) {
+    return mxfp4_dequantize(m.q, m.scale, (int32_t)m.R, (int32_t)m.C, cols, type, out.at<void>(), stream);
+  });
+  return out.take();
+}
+
+PyObject* mx_gemm(PyObject* const* a) {  // a_q, a_scale, b_q, b_scale, epilogue, add, type, d, ws
+  Call call("mxfp4_gemm");
+  const Mx A = mx_input(call, a[0], a[1], "a_q", "a_scale"), B = mx_input(call, a[2], a[3], "b_q", "b_scale");
+  if (A.C != B.C) refuse("b_q", "expected " + std::to_string(A.C / 2) + " bytes a row, as a_q, got " + std::to_string(B.C / 2));
+  const int32_t epilogue = py_i32(a[4], "epilogue"), type = py_i32(a[6], "dtype");
+  const int64_t n_out = epilogue == NVFP4_EPI_SILU_MUL ? B.R / 2 : B.R;
+  const at::ScalarType d_type = type == NVFP4_DT_F32 ? kF32 : kBf16;
+  const void* add = call.input<void>(a[5], d_type, {A.R, n_out}, "add");
+  const Out d(call, a[7], {A.R, n_out}, d_type, "d");
+  std::optional<Out> ws;
+  const size_t need = a[8] == Py_None ? mxfp4_gemm_ws_bytes((int32_t)A.R, (int32_t)B.R, (int32_t)A.C) : 1;
+  if (need) ws = workspace(call, a[8], need);
+  call.run([&](void* stream) {
+    return mxfp4_gemm(A.q, A.scale, B.q, B.scale, (int32_t)A.R, (int32_t)B.R, (int32_t)A.C, epilogue, add, type,
+                      d.at<void>(), ws ? ws->at<void>() : nullptr, ws ? ws->bytes() : 0, stream);
+  });
+  return d.take();
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -473,6 +551,9 @@ PyMethodDef g_methods[] = {
     method<entry<quantize_rows, 3>>("quantize_rows"),
     method<entry<gemm, 8>>("gemm"),
     method<entry<ffn, 8>>("ffn"),
+    method<entry<mx_quantize, 7>>("mx_quantize"),
+    method<entry<mx_dequantize, 5>>("mx_dequantize"),
+    method<entry<mx_gemm, 9>>("mx_gemm"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,98 @@
+// Microscaled 4-bit floats (MXFP4): E2M1 codes, two to a byte with the first in
+// the low nibble, and for each 32 of them a power of two, held as its exponent
+// + 127 in a byte (0xFF: every value of the block is NaN).
+//
+//   scale of a block  e = floor(log2 amax) - 2 (MX_SCALE_FLOOR: values in
+//                     (6, 8) 2^e saturate) or the smallest e with amax <= 6 2^e
+//                     (MX_SCALE_CEIL), at least -127
+//   code              E2M1 nearest to x 2^-e, ties to the even code
+//
+// Both are exact: e comes from the maximum's exponent bits, and gfx950's
+// conversions divide by the power of two and round once (all BF16 values at 12
+// scales compared, the subnormal scale 2^-127 and saturation among them).
+#pragma once
+#include "common.h"
+
+namespace nvfp4 {
+
+constexpr int kMxBlock = 32;     // elements that share a scale
+constexpr int kMxGroup = 128;    // rows of codes end on whole groups: four scales, one word
+constexpr int kMxMaxK = 262144;  // elements along a row of codes
+
+__device__ __forceinline__ int mx_padded(int n) { return (n + kMxGroup - 1) & ~(kMxGroup - 1); }
+
+// Code of a block's scale from the float32 bits of its largest magnitude.
+__device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax, bool ceil) {
+  const uint32_t f = amax >> 23;
+  int c = (int)f - 2 + (ceil && (amax & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+  c = c < 0 ? 0 : c;
+  return f == 255u ? 255u : (uint32_t)c;  // infinities and NaN: no scale can hold them
+}
+// The scale as the conversions take it: they read the exponent bits alone, 0 as
+// 2^-127 and 255 as NaN.
+__device__ __forceinline__ float mx_scale(uint32_t code) { return __uint_as_float(code << 23); }
+
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+// Larger magnitude, in each half, of two pairs of BF16 magnitudes.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
+
+// Two values to the byte SEL of a word of codes.
+template <int SEL>
+__device__ __forceinline__ uint32_t mx_encode2(uint32_t old, uint32_t bf16_pair, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2_t, bf16_pair), scale, SEL);
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t mx_encode2(uint32_t old, float a, float b, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, SEL);
+}
+
+// Eight values of a row as they are loaded: their largest magnitude (as float32
+// bits) and their codes.
+template <typename T>
+struct MxVec8;
+template <>
+struct MxVec8<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t amax() const {
+    constexpr uint32_t m = 0x7FFF7FFFu;
+    const uint32_t a = max_u16x2(max_u16x2(v.x & m, v.y & m), max_u16x2(v.z & m, v.w & m));
+    const uint32_t lo = a << 16, hi = a & 0xFFFF0000u;
+    return lo > hi ? lo : hi;
+  }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t w = mx_encode2<0>(0u, v.x, s);
+    w = mx_encode2<1>(w, v.y, s);
+    w = mx_encode2<2>(w, v.z, s);
+    return mx_encode2<3>(w, v.w, s);
+  }
+};
+template <>
+struct MxVec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m = max(m, __float_as_uint((&a.x)[i]) & 0x7FFFFFFFu);
+      m = max(m, __float_as_uint((&b.x)[i]) & 0x7FFFFFFFu);
+    }
+    return m;
+  }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t w = mx_encode2<0>(0u, a.x, a.y, s);
+    w = mx_encode2<1>(w, a.z, a.w, s);
+    w = mx_encode2<2>(w, b.x, b.y, s);
+    return mx_encode2<3>(w, b.z, b.w, s);
+  }
+};
+
+}  // namespace nvfp4
