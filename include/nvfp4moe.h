@@ -542,6 +542,26 @@ int nvfp4_moe_forward_static(const nvfp4_moe_weights* w, const void* x_bf16, int
                              const int32_t* topk_ids, const float* topk_w, int32_t k, int32_t expert_start,
                              const float* gs_in, void* out_bf16, void* ws, size_t ws_bytes, void* stream);
 
+/* The layer for at most nvfp4_moe_few_max_tokens() = 64 tokens, in two launches
+ * on the same weights, with activations as they are (BF16, not quantized):
+ *   h_e    = RN_bf16(silu(G) * U), G and U = w1_gs[e] (gate and up) times the
+ *            products of x[t] with the gate and up rows of W1_e
+ *   out[t] = RN_bf16(sum over the experts e of token t on this rank of
+ *            topk_w[t, e] * w2_gs[e] * W2_e h_e [+ add[t]])
+ * sums in float32, each expert with the sum of its weights where a token lists
+ * it twice. add BF16 [T, H] (such as the dense expert's output; may be out) or
+ * NULL. Ids outside [expert_start, expert_start + L) take no part. The order of
+ * the sums depends on what the tokens chose, so a call repeats bit for bit, but
+ * a token's last bits may differ with the others in the batch.
+ * ws: at least nvfp4_moe_few_ws_bytes(...) bytes (h). k <= 64, L <= 4096,
+ * H % 128 == 0, I % 128 == 0, 2I*H*9/16 below 2^31.
+ */
+int32_t nvfp4_moe_few_max_tokens(void);
+size_t nvfp4_moe_few_ws_bytes(int32_t T, int32_t k, int32_t hidden, int32_t inter, int32_t num_local);
+int nvfp4_moe_forward_few(const nvfp4_moe_weights* w, const void* x_bf16, int32_t T, const int32_t* topk_ids,
+                          const float* topk_w, int32_t k, int32_t expert_start, const void* add_bf16, void* out_bf16,
+                          void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

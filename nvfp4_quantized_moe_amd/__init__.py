@@ -32,6 +32,7 @@ __all__ = [
     "int8_ffn_ws_bytes",
     "Int8FFNWeights", "prepare_int8_weights", "MX_ROWS", "MX_COLUMNS", "MX_BOTH", "MX_SCALE_FLOOR", "MX_SCALE_CEIL",
     "mxfp4_padded", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_gemm_ws_bytes",
+    "nvfp4_moe_forward_few", "nvfp4_moe_few_ws_bytes", "nvfp4_moe_few_max_tokens",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
@@ -118,6 +119,10 @@ _mx_quantize = _sig("mxfp4_quantize", ctypes.c_int, _vp, _i32, _i32, _i32, _i32,
 _mx_dequantize = _sig("mxfp4_dequantize", ctypes.c_int, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp)
 _mx_gemm_ws = _sig("mxfp4_gemm_ws_bytes", _sz, _i32, _i32, _i32)
 _mx_gemm = _sig("mxfp4_gemm", ctypes.c_int, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _sz, _vp)
+_few_max = _sig("nvfp4_moe_few_max_tokens", _i32)
+_few_ws = _sig("nvfp4_moe_few_ws_bytes", _sz, _i32, _i32, _i32, _i32, _i32)
+_few = _sig("nvfp4_moe_forward_few", ctypes.c_int, ctypes.POINTER(_Weights), _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp,
+            _vp, _sz, _vp)
 
 
 class NVFP4Error(RuntimeError):
@@ -704,3 +709,19 @@ def calibrate_static_gs(weights: MoEWeights, x, topk_ids, topk_w, expert_start):
     lay = nvfp4_moe_ws_layout(T, k, weights.hidden, weights.inter, weights.num_local)
     sc = ws_view(ws, lay, "scalars", torch.float32, (4,))
     return torch.stack([sc[0], sc[2]]).contiguous()
+
+
+def nvfp4_moe_few_max_tokens() -> int:
+    return int(_few_max())
+
+
+def nvfp4_moe_few_ws_bytes(T, k, hidden, inter, num_local) -> int:
+    return int(_few_ws(T, k, hidden, inter, num_local))
+
+
+def nvfp4_moe_forward_few(weights: MoEWeights, x, topk_ids, topk_w, expert_start, add=None, out=None, ws=None):
+    """One rank's partial output BF16 [T, H] of the expert FFN for at most 64 tokens, in two launches on the same
+    weights, with BF16 activations (nvfp4_moe_forward quantizes them), plus add (BF16 [T, H], such as the dense
+    expert's output; may be out) when given."""
+    w = weights
+    return _native.moe_few(w.w1, w.w1_gs, w.w2, w.w2_gs, x, topk_ids, topk_w, expert_start, add, out, ws)

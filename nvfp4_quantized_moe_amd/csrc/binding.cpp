@@ -512,6 +512,49 @@ PyObject* mx_gemm(PyObject* const* a) {  // a_q, a_scale, b_q, b_scale, epilogue
   return d.take();
 }
 
+// (L, N, K) of packed weights uint8 [L, N/32, K/128, 2304]
+struct Packed {
+  const uint8_t* at;
+  int32_t L, N, K;
+};
+Packed packed(Call& call, PyObject* o, const char* name) {
+  const at::Tensor& t = call.here(needed(o, name), kU8, name);
+  if (t.dim() != 4 || t.size(3) != 2304)
+    refuse(name, "expected packed weights [L, N/32, K/128, 2304], got " + text(t.sizes()));
+  return {static_cast<const uint8_t*>(t.data_ptr()), to_i32(t.size(0), name), to_i32(t.size(1) * 32, name),
+          to_i32(t.size(2) * 128, name)};
+}
+PyObject* moe_few(PyObject* const* a) {  // w1, w1_gs, w2, w2_gs, x, topk_ids, topk_w, expert_start, add, out, ws
+  Call call("nvfp4_moe_forward_few");
+  const Packed w1 = packed(call, a[0], "weights.w1"), w2 = packed(call, a[2], "weights.w2");
+  const int32_t L = w1.L, H = w1.K, I = w1.N / 2;
+  if (w2.L != L || w2.N != H || w2.K != I || w1.N % 2 != 0)
+    refuse("weights.w2", "expected " + text({L, H, I}) + " as weights.w1 has it, got " + text({w2.L, w2.N, w2.K}));
+  const at::Tensor& gs1 = call.here(needed(a[1], "weights.w1_gs"), kF32, "weights.w1_gs");
+  const bool dual = gs1.dim() == 2;
+  if (dual) call.shaped(gs1, {L, 2}, "weights.w1_gs"); else call.shaped(gs1, {L}, "weights.w1_gs");
+  needed(a[3], "weights.w2_gs");
+  const float* gs2 = call.input<float>(a[3], kF32, {L}, "weights.w2_gs");
+  const at::Tensor& x = call.here(needed(a[4], "x"), kBf16, "x");
+  const int64_t T = matrix(x, "x").rows;
+  call.shaped(x, {T, H}, "x");
+  const at::Tensor& ids = call.here(needed(a[5], "topk_ids"), kI32, "topk_ids");
+  const int64_t k = matrix(ids, "topk_ids").cols;
+  call.shaped(ids, {T, k}, "topk_ids");
+  needed(a[6], "topk_w");
+  const float* weight = call.input<float>(a[6], kF32, {T, k}, "topk_w");
+  const int32_t start = py_i32(a[7], "expert_start");
+  const void* add = call.input<void>(a[8], kBf16, {T, H}, "add");
+  const Out out(call, a[9], {T, H}, kBf16, "out");
+  const Out ws = workspace(call, a[10], nvfp4_moe_few_ws_bytes((int32_t)T, (int32_t)k, H, I, L));
+  const nvfp4_moe_weights w = {L, H, I, w1.at, static_cast<const float*>(gs1.data_ptr()), w2.at, gs2, dual ? 1 : 0};
+  call.run([&](void* stream) {
+    return nvfp4_moe_forward_few(&w, x.data_ptr(), (int32_t)T, static_cast<const int32_t*>(ids.data_ptr()), weight,
+                                 (int32_t)k, start, add, out.at<void>(), ws.at<void>(), ws.bytes(), stream);
+  });
+  return out.take();
+}
+
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -554,6 +597,7 @@ PyMethodDef g_methods[] = {
     method<entry<mx_quantize, 7>>("mx_quantize"),
     method<entry<mx_dequantize, 5>>("mx_dequantize"),
     method<entry<mx_gemm, 9>>("mx_gemm"),
+    method<entry<moe_few, 11>>("moe_few"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
