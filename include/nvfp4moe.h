@@ -255,6 +255,39 @@ int moe_block_norm_backward(const void* d_y, const void* d_residual_out, const v
                             void* d_x, void* d_residual, float* d_w_pre, float* d_w_post, float* d_gate, void* ws,
                             size_t ws_bytes, void* stream);
 
+/* Layer norm with the residual update in front of it, for blocks that centre:
+ *   r' = residual + scale * x                        -> residual_out, rounded once
+ *   y  = (r' - mean r') * rsqrt(var r' + eps) * w + b    -> y, from r' as stored
+ * x, y [T, H] of x_dtype; residual, residual_out [T, H] of res_dtype (any
+ * combination); w, b float [H] (NULL: 1, 0). residual NULL: r' = x, which is not
+ * written (residual_out NULL, scale 1, res_dtype x_dtype). residual_out may be
+ * residual, y may be x. var is the mean squared deviation; sums in float32, of
+ * deviations from the mean, so rows far from 0 keep their digits.
+ * y_q, y_scale (both or neither) take y as MXFP4 too, exactly what mxfp4_quantize
+ * makes of the stored y by `rule` (MX_SCALE_*): [T, Hp/2], [Hp/128, T, 4], Hp =
+ * mxfp4_padded(H); y may then be NULL (its values are those it would have). An
+ * infinity or NaN in a row makes all of its y NaN.
+ * Requires T >= 0, 0 < H <= 16384, H % 8 == 0. One launch.
+ */
+int moe_layer_norm(const void* x, int32_t x_dtype, const void* residual, int32_t res_dtype, int32_t T, int32_t H,
+                   const float* w, const float* b, float scale, float eps, void* residual_out, void* y, int32_t rule,
+                   uint8_t* y_q, uint8_t* y_scale, void* stream);
+
+/* Its gradients. d_y [T, H] of x_dtype; r [T, H] of res_dtype, the r' that was
+ * normalized; d_residual_out [T, H] of res_dtype (the gradient of r' from
+ * elsewhere; NULL: zeros). The rounding of r' counts as the identity.
+ *   d_residual [T, H] of res_dtype, d_x = scale * d_residual [T, H] of x_dtype
+ *   (may be d_residual_out and d_y where the types agree); without a residual
+ *   d_residual is NULL, and scale and types as there
+ *   float d_w [H], d_b [H]; NULL where not wanted
+ * ws: at least moe_layer_norm_backward_ws_bytes(T, H) bytes. Sums over tokens
+ * have a fixed order. Two launches.
+ */
+size_t moe_layer_norm_backward_ws_bytes(int32_t T, int32_t H);
+int moe_layer_norm_backward(const void* d_y, int32_t x_dtype, const void* d_residual_out, const void* r,
+                            int32_t res_dtype, int32_t T, int32_t H, const float* w, float scale, float eps, void* d_x,
+                            void* d_residual, float* d_w, float* d_b, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------- weight packing
  * Offline weight preparation, step three (after quantize and fold): the
  * grouped GEMM reads weights in a packed order that matches its MFMA operand

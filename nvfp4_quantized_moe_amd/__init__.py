@@ -6,7 +6,7 @@ names of the C entry points declared in include/nvfp4moe.h.
 
 No call takes part in autograd: outputs come back without a history, also from
 tensors that require a gradient. Gradients are calls of their own
-(moe_gate_backward, moe_block_norm_backward), for a user's autograd function to
+(moe_gate_backward, moe_block_norm_backward, moe_layer_norm_backward), for a user's autograd function to
 call; the expert layer and the dense expert have none.
 
 Importing this module loads the built library and fails loudly when it is
@@ -32,7 +32,8 @@ __all__ = [
     "int8_ffn_ws_bytes",
     "Int8FFNWeights", "prepare_int8_weights", "MX_ROWS", "MX_COLUMNS", "MX_BOTH", "MX_SCALE_FLOOR", "MX_SCALE_CEIL",
     "mxfp4_padded", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "mxfp4_gemm_ws_bytes",
-    "nvfp4_moe_forward_few", "nvfp4_moe_few_ws_bytes", "nvfp4_moe_few_max_tokens",
+    "nvfp4_moe_forward_few", "nvfp4_moe_few_ws_bytes", "nvfp4_moe_few_max_tokens", "moe_layer_norm",
+    "moe_layer_norm_backward", "moe_layer_norm_backward_ws_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4moe.so")
@@ -123,6 +124,11 @@ _few_max = _sig("nvfp4_moe_few_max_tokens", _i32)
 _few_ws = _sig("nvfp4_moe_few_ws_bytes", _sz, _i32, _i32, _i32, _i32, _i32)
 _few = _sig("nvfp4_moe_forward_few", ctypes.c_int, ctypes.POINTER(_Weights), _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp,
             _vp, _sz, _vp)
+_layer_norm = _sig("moe_layer_norm", ctypes.c_int, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _vp, _f32, _f32, _vp, _vp, _i32,
+                   _vp, _vp, _vp)
+_layer_norm_ws = _sig("moe_layer_norm_backward_ws_bytes", _sz, _i32, _i32)
+_layer_norm_backward = _sig("moe_layer_norm_backward", ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _f32,
+                            _f32, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
 
 
 class NVFP4Error(RuntimeError):
@@ -340,6 +346,31 @@ def moe_block_norm_backward(d_y, d_residual_out, x, residual_out, w_pre=None, w_
     return dict(zip(_NORM_GRADIENTS, _native.block_norm_backward(
         d_y, d_residual_out, x, residual_out, w_pre, w_post, gate, scale, eps, d_x, d_residual, d_w_pre, d_w_post, d_gate,
         ws)))
+
+
+def moe_layer_norm(x, residual=None, w=None, b=None, scale=1.0, eps=1e-5, mx_rule=None, residual_out=None, y=None,
+                   y_q=None, y_scale=None):
+    """Layer norm behind the residual update: residual_out = residual + scale * x, y = (residual_out - mean) *
+    rsqrt(var + eps) * w + b -> (residual_out, y). x: BF16 or float32 [T, H], residual of either type (None: x itself
+    is normalized and comes back in its place); w, b: float32 [H] or None. With mx_rule (MX_SCALE_FLOOR or
+    MX_SCALE_CEIL) also y as MXFP4: (residual_out, y, y_q, y_scale), for mxfp4_gemm."""
+    return _native.layer_norm(x, residual, w, b, scale, eps, mx_rule, residual_out, y, y_q, y_scale)
+
+
+def moe_layer_norm_backward_ws_bytes(T, H) -> int:
+    return int(_layer_norm_ws(T, H))
+
+
+_LAYER_NORM_GRADIENTS = ("d_x", "d_residual", "d_w", "d_b")
+
+
+def moe_layer_norm_backward(d_y, d_residual_out, residual_out, w=None, b=None, scale=1.0, eps=1e-5, residual=True,
+                            d_x=None, d_residual=None, d_w=None, d_b=None, ws=None):
+    """Gradients of moe_layer_norm from d_y and d_residual_out (None: zeros), with the residual_out of the forward call
+    -> dict of d_x, d_residual, d_w, d_b (None where there is no such input). residual False: the forward call had no
+    residual, and residual_out is the x it normalized."""
+    return dict(zip(_LAYER_NORM_GRADIENTS, _native.layer_norm_backward(
+        d_y, d_residual_out, residual_out, w, b, scale, eps, residual, d_x, d_residual, d_w, d_b, ws)))
 
 
 # ------------------------------------------------------------------ grouped GEMM

@@ -465,6 +465,72 @@ PyObject* mx_quantize(PyObject* const* a) {  // x, direction (1 rows, 2 columns,
   return tuple({one.q.take(), one.scale.take()});
 }
 
+PyObject* layer_norm(PyObject* const* a) {  // x, residual, w, b, scale, eps, rule (None: no codes), residual_out, y, y_q, y_scale
+  Call call("moe_layer_norm");
+  const at::Tensor& x = call.floats(needed(a[0], "x"), "x");
+  const auto [T, H] = matrix(x, "x");
+  const at::Tensor* residual = given(a[1], "residual");
+  if (residual) {
+    call.floats(*residual, "residual");
+    call.shaped(*residual, {T, H}, "residual");
+  } else if (a[7] != Py_None) {
+    refuse("residual_out", "given without a residual");
+  }
+  const at::ScalarType res_type = residual ? residual->scalar_type() : x.scalar_type();
+  const float* w = call.input<float>(a[2], kF32, {H}, "w");
+  const float* b = call.input<float>(a[3], kF32, {H}, "b");
+  const float scale = py_float(a[4]), eps = py_float(a[5]);
+  if (!residual && scale != 1.0f) refuse("scale", "1 without a residual, got " + std::to_string(scale));
+  const bool quant = a[6] != Py_None;
+  const int32_t rule = quant ? py_i32(a[6], "mx_rule") : 0;
+  std::optional<Out> residual_out;
+  if (residual) residual_out.emplace(call, a[7], at::IntArrayRef({T, H}), res_type, "residual_out");
+  const Out y(call, a[8], {T, H}, x.scalar_type(), "y");
+  std::optional<MxOut> codes;
+  if (quant) codes.emplace(call, a[9], a[10], T, mx_padded(H, "x"), "y_q", "y_scale");
+  call.run([&, T = (int32_t)T, H = (int32_t)H](void* stream) {
+    return moe_layer_norm(x.data_ptr(), code(x), residual ? residual->data_ptr() : nullptr,
+                          res_type == kBf16 ? NVFP4_DT_BF16 : NVFP4_DT_F32, T, H, w, b, scale, eps,
+                          residual ? residual_out->at<void>() : nullptr, y.at<void>(), rule,
+                          quant ? codes->q.at<uint8_t>() : nullptr, quant ? codes->scale.at<uint8_t>() : nullptr, stream);
+  });
+  PyObject* first = a[0];
+  if (residual) first = residual_out->take(); else Py_INCREF(first);
+  if (!quant) return tuple({first, y.take()});
+  return tuple({first, y.take(), codes->q.take(), codes->scale.take()});
+}
+
+PyObject* layer_norm_backward(PyObject* const* a) {  // d_y, d_residual_out, r, w, b, scale, eps, residual, d_x, d_residual, d_w, d_b, ws
+  Call call("moe_layer_norm_backward");
+  const at::Tensor& d_y = call.floats(needed(a[0], "d_y"), "d_y");
+  const auto [T, H] = matrix(d_y, "d_y");
+  const at::Tensor& r = call.floats(needed(a[2], "residual_out"), "residual_out");
+  call.shaped(r, {T, H}, "residual_out");
+  const at::ScalarType x_type = d_y.scalar_type(), res_type = r.scalar_type();
+  const void* d_res_out = call.input<void>(a[1], res_type, {T, H}, "d_residual_out");
+  const float* w = call.input<float>(a[3], kF32, {H}, "w");
+  const float* b = call.input<float>(a[4], kF32, {H}, "b");
+  const float scale = py_float(a[5]), eps = py_float(a[6]);
+  const bool residual = PyObject_IsTrue(a[7]) == 1;
+  if (!residual && (scale != 1.0f || res_type != x_type))
+    refuse("residual", "without one, scale is 1 and residual_out (the x that was normalized) of d_y's type");
+  if (!residual && a[9] != Py_None) refuse("d_residual", "given without a residual");
+  const Out d_x(call, a[8], {T, H}, x_type, "d_x");
+  std::optional<Out> d_residual, d_w, d_b;
+  if (residual) d_residual.emplace(call, a[9], at::IntArrayRef({T, H}), res_type, "d_residual");
+  if (w) d_w.emplace(call, a[10], at::IntArrayRef({H}), kF32, "d_w");
+  if (b) d_b.emplace(call, a[11], at::IntArrayRef({H}), kF32, "d_b");
+  const Out ws = workspace(call, a[12], moe_layer_norm_backward_ws_bytes((int32_t)T, (int32_t)H));
+  call.run([&, T = (int32_t)T, H = (int32_t)H](void* stream) {
+    return moe_layer_norm_backward(d_y.data_ptr(), code(d_y), d_res_out, r.data_ptr(), code(r), T, H, w, scale, eps,
+                                   d_x.at<void>(), residual ? d_residual->at<void>() : nullptr,
+                                   d_w ? d_w->at<float>() : nullptr, d_b ? d_b->at<float>() : nullptr, ws.at<void>(),
+                                   ws.bytes(), stream);
+  });
+  const auto grad = [](const std::optional<Out>& o) { return o ? o->take() : none(); };
+  return tuple({d_x.take(), grad(d_residual), grad(d_w), grad(d_b)});
+}
+
 // q uint8 [R, C / 2] and scale uint8 [C / 128, R, 4] as inputs
 struct Mx {
   const uint8_t *q, *scale;
@@ -598,6 +664,8 @@ PyMethodDef g_methods[] = {
     method<entry<mx_dequantize, 5>>("mx_dequantize"),
     method<entry<mx_gemm, 9>>("mx_gemm"),
     method<entry<moe_few, 11>>("moe_few"),
+    method<entry<layer_norm, 11>>("layer_norm"),
+    method<entry<layer_norm_backward, 13>>("layer_norm_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
