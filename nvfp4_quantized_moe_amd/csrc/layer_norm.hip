@@ -126,11 +126,11 @@ __global__ __launch_bounds__(512) void layer_norm_kernel(const X* x, const R* re
         int top = (int)v.amax();
         top = max(top, dpp_i32<kDppXor1>(top));
         top = max(top, dpp_i32<kDppXor2>(top));
-        const uint32_t code = mx_scale_code((uint32_t)top, a.ceil);
-        const uint32_t codes = v.codes(mx_scale(code));
+        const uint32_t scale = mx_scale_bits((uint32_t)top, a.ceil ? MxVec8<X>::kUp : 0u);
+        const uint32_t codes = v.codes(__uint_as_float(scale));
         if (ch * 8 < Hp) {
           *reinterpret_cast<uint32_t*>(a.q + (size_t)t * (Hp / 2) + ch * 4) = codes;
-          if ((ch & 3) == 0) a.s[((size_t)(ch / 16) * a.T + t) * 4 + (ch / 4) % 4] = (uint8_t)code;
+          if ((ch & 3) == 0) a.s[((size_t)(ch / 16) * a.T + t) * 4 + (ch / 4) % 4] = (uint8_t)(scale >> 23);
         }
       }
     }

@@ -21,16 +21,16 @@ constexpr int kMxMaxK = 262144;  // elements along a row of codes
 
 __device__ __forceinline__ int mx_padded(int n) { return (n + kMxGroup - 1) & ~(kMxGroup - 1); }
 
-// Code of a block's scale from the float32 bits of its largest magnitude.
-__device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax, bool ceil) {
-  const uint32_t f = amax >> 23;
-  int c = (int)f - 2 + (ceil && (amax & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-  c = c < 0 ? 0 : c;
-  return f == 255u ? 255u : (uint32_t)c;  // infinities and NaN: no scale can hold them
+// A block's scale, as float32 bits, from those of its largest magnitude: the
+// exponent field less 2, or one more where the fraction is above 1/2 (MX_SCALE_CEIL:
+// `up` carries into the exponent there). Of BF16 values the low halves of `amax`
+// may hold anything. The conversions read the exponent bits alone, 0 as 2^-127 and
+// 255 as NaN; the field is the scale's code. Infinities and NaN: no scale holds them.
+constexpr uint32_t kMxUpF32 = 0x3FFFFFu, kMxUpBf16 = 0x3F0000u;
+__device__ __forceinline__ uint32_t mx_scale_bits(uint32_t amax, uint32_t up) {
+  const int e = (int)((amax + up) & 0x7F800000u) - 0x01000000;
+  return amax >= 0x7F800000u ? 0x7F800000u : (uint32_t)(e > 0 ? e : 0);
 }
-// The scale as the conversions take it: they read the exponent bits alone, 0 as
-// 2^-127 and 255 as NaN.
-__device__ __forceinline__ float mx_scale(uint32_t code) { return __uint_as_float(code << 23); }
 
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 // Larger magnitude, in each half, of two pairs of BF16 magnitudes.
@@ -48,20 +48,20 @@ __device__ __forceinline__ uint32_t mx_encode2(uint32_t old, float a, float b, f
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, SEL);
 }
 
-// Eight values of a row as they are loaded: their largest magnitude (as float32
-// bits) and their codes.
+// Eight values of a row as they are loaded: their largest magnitude (float32
+// bits, the low half open for BF16) and their codes.
 template <typename T>
 struct MxVec8;
 template <>
 struct MxVec8<uint16_t> {
+  static constexpr uint32_t kUp = kMxUpBf16;
   uint4 v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ uint32_t amax() const {
     constexpr uint32_t m = 0x7FFF7FFFu;
     const uint32_t a = max_u16x2(max_u16x2(v.x & m, v.y & m), max_u16x2(v.z & m, v.w & m));
-    const uint32_t lo = a << 16, hi = a & 0xFFFF0000u;
-    return lo > hi ? lo : hi;
+    return max(a, a << 16);
   }
   __device__ __forceinline__ uint32_t codes(float s) const {
     uint32_t w = mx_encode2<0>(0u, v.x, s);
@@ -72,6 +72,7 @@ struct MxVec8<uint16_t> {
 };
 template <>
 struct MxVec8<float> {
+  static constexpr uint32_t kUp = kMxUpF32;
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];

@@ -28,28 +28,35 @@ struct MxArgs {
 };
 
 // Along rows: a wave takes 512 columns of R rows, all R loads in flight; lane l
-// holds columns 8 l .. 8 l + 7 of each, so four lanes share a scale.
+// holds columns 8 l .. 8 l + 7 of each, so four lanes share a scale. Of four rows'
+// scales each of them keeps one, so that all lanes store together: a byte store
+// takes as long for 16 lanes as for 64.
 template <typename T, int R>
 __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, MxArgs g) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int Kp = mx_padded(g.K), c = blockIdx.y * 512 + lane * 8;
-  const int r0 = (blockIdx.x * 4 + wave) * R;
+  const int Kp = mx_padded(g.K), across = (g.K + 511) / 512;
+  const int c = (int)(blockIdx.x % across) * 512 + lane * 8, r0 = ((int)(blockIdx.x / across) * 4 + wave) * R;
   MxVec8<T> v[R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
     v[i].load(x + (size_t)min(r0 + i, g.M - 1) * g.K + min(c, g.K - 8));
+  const uint32_t up = g.ceil ? MxVec8<T>::kUp : 0u;
+  uint32_t keep = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (c >= g.K) v[i].zero();
     int m = (int)v[i].amax();
     m = max(m, dpp_i32<kDppXor1>(m));
     m = max(m, dpp_i32<kDppXor2>(m));
-    const uint32_t code = mx_scale_code((uint32_t)m, g.ceil);
-    const uint32_t w = v[i].codes(mx_scale(code));
+    const uint32_t scale = mx_scale_bits((uint32_t)m, up);
+    const uint32_t w = v[i].codes(__uint_as_float(scale));
     const int r = r0 + i;
-    if (r < g.M && c < Kp) {
-      *reinterpret_cast<uint32_t*>(g.q + (size_t)r * (Kp / 2) + c / 2) = w;
-      if ((lane & 3) == 0) g.s[((size_t)(c / kMxGroup) * g.M + r) * 4 + (c / kMxBlock) % 4] = (uint8_t)code;
+    if (r < g.M && c < Kp) *reinterpret_cast<uint32_t*>(g.q + (size_t)r * (Kp / 2) + c / 2) = w;
+    keep = (lane & 3) == (i & 3) ? scale : keep;
+    if ((i & 3) == 3 || i == R - 1) {
+      const int from = r0 + (i & ~3) + (lane & 3);
+      if ((lane & 3) <= (i & 3) && from < g.M && c < Kp)
+        g.s[((size_t)(c / kMxGroup) * g.M + from) * 4 + (c / kMxBlock) % 4] = (uint8_t)(keep >> 23);
     }
   }
 }
@@ -59,13 +66,13 @@ template <typename T>
 struct MxVec4;
 template <>
 struct MxVec4<uint16_t> {
+  static constexpr uint32_t kUp = kMxUpBf16;
   uint2 v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint2*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
   __device__ __forceinline__ uint32_t amax() const {
     const uint32_t a = max_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
-    const uint32_t lo = a << 16, hi = a & 0xFFFF0000u;
-    return lo > hi ? lo : hi;
+    return max(a, a << 16);
   }
   __device__ __forceinline__ uint32_t codes(float s) const { return mx_encode2<1>(mx_encode2<0>(0u, v.x, s), v.y, s); }
   // largest magnitudes of the four columns, running
@@ -89,6 +96,7 @@ struct MxVec4<uint16_t> {
 };
 template <>
 struct MxVec4<float> {
+  static constexpr uint32_t kUp = kMxUpF32;
   float4 v;
   __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
@@ -115,96 +123,141 @@ struct MxVec4<float> {
   }
 };
 
-// Along columns (ROWS: and along rows, from the same registers): a wave holds 32
-// rows of 256 columns, four columns to a lane, so that a lane has whole blocks
-// of its columns. Four waves take the 128 rows of a group.
+// Along columns (ROWS: and along rows, from the same registers): a workgroup takes
+// 128 rows of 128 columns, a wave 32 of the rows, lane half h its rows 16 h ..
+// 16 h + 15 and four columns to a lane, so that two lanes have whole blocks of
+// their columns and eight share a block of a row. Codes and scales of the tile
+// meet in LDS and leave in whole 64-byte runs: stored from the registers, 8 bytes
+// here and there in 64 lines, the address unit was busy 84 % of the time
+// (8192 x 7168 both ways: 48.5 us).
+constexpr int kMxColPitch = 80;  // of a column's 64 bytes of codes in LDS, against bank conflicts
 template <typename T, bool ROWS>
 __global__ __launch_bounds__(256) void mx_columns_kernel(const T* __restrict__ x, MxArgs g) {
+  constexpr int N = kMxBlock / 2;
+  __shared__ __attribute__((aligned(16))) uint8_t cols[128 * kMxColPitch];  // [32 (c % 4) + c / 4][64 bytes]
+  __shared__ __attribute__((aligned(16))) uint8_t rows[ROWS ? 128 * 64 : 16];
+  __shared__ __attribute__((aligned(4))) uint8_t scales[2][128][4];         // of the columns, of the rows
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 256 + lane * 4, r0 = blockIdx.y * kMxGroup + wave * kMxBlock;
-  MxVec4<T> v[kMxBlock];
+  const int c0 = blockIdx.x * 128, m0 = blockIdx.y * kMxGroup;
+  const int cl = (lane & 31) * 4, rl = wave * kMxBlock + (lane >> 5) * N, c = c0 + cl, r0 = m0 + rl;
+  MxVec4<T> v[N];
+  const T* from = x + min(c, g.K - 4);
 #pragma unroll
-  for (int i = 0; i < kMxBlock; ++i)
-    v[i].load(x + (size_t)min(r0 + i, g.M - 1) * g.K + min(c, g.K - 4));
+  for (int i = 0; i < N; ++i) v[i].load(from + (size_t)min(r0 + i, g.M - 1) * g.K);
+  if (c0 + 128 > g.K || m0 + kMxGroup > g.M) {  // the same for the workgroup
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c >= g.K || r0 + i >= g.M) v[i].zero();
+  }
+  const uint32_t up = g.ceil ? MxVec4<T>::kUp : 0u;
   typename MxVec4<T>::Max top;
 #pragma unroll
-  for (int i = 0; i < kMxBlock; ++i) {
-    if (c >= g.K || r0 + i >= g.M) v[i].zero();
-    top.add(v[i]);
-  }
-  if (c < g.K) {
-    const size_t pitch = (size_t)(mx_padded(g.M) / 2);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t code = mx_scale_code(top.get(j), g.ceil);
-      const float s = mx_scale(code);
-      uint32_t w[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const MxVec4<T>* at = v + 8 * p;
-        w[p] = MxVec4<T>::template pair<0>(0u, at[0], at[1], j, s);
-        w[p] = MxVec4<T>::template pair<1>(w[p], at[2], at[3], j, s);
-        w[p] = MxVec4<T>::template pair<2>(w[p], at[4], at[5], j, s);
-        w[p] = MxVec4<T>::template pair<3>(w[p], at[6], at[7], j, s);
-      }
-      *reinterpret_cast<uint4*>(g.qt + (size_t)(c + j) * pitch + r0 / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-      g.st[((size_t)blockIdx.y * g.K + c + j) * 4 + wave] = (uint8_t)code;
-    }
-  }
+  for (int i = 0; i < N; ++i) top.add(v[i]);
   if constexpr (ROWS) {
-    const int Kp = mx_padded(g.K);
+    uint32_t keep = 0;  // of eight rows' scales each of a block's lanes keeps one
 #pragma unroll
-    for (int i = 0; i < kMxBlock; ++i) {
-      int m = (int)v[i].amax();  // eight lanes share a block of the row
+    for (int i = 0; i < N; ++i) {
+      int m = (int)v[i].amax();
       m = max(m, dpp_i32<kDppXor1>(m));
       m = max(m, dpp_i32<kDppXor2>(m));
       m = max(m, dpp_i32<kDppHalfMirror>(m));
-      const uint32_t code = mx_scale_code((uint32_t)m, g.ceil);
-      const uint32_t w = v[i].codes(mx_scale(code));
-      const int r = r0 + i;
-      if (r < g.M && c < Kp) {
-        *reinterpret_cast<uint16_t*>(g.q + (size_t)r * (Kp / 2) + c / 2) = (uint16_t)w;
-        if ((lane & 7) == 0) g.s[((size_t)(c / kMxGroup) * g.M + r) * 4 + (c / kMxBlock) % 4] = (uint8_t)code;
-      }
+      const uint32_t scale = mx_scale_bits((uint32_t)m, up);
+      *reinterpret_cast<uint16_t*>(rows + (rl + i) * 64 + cl / 2) = (uint16_t)v[i].codes(__uint_as_float(scale));
+      keep = (lane & 7) == (i & 7) ? scale : keep;
+      if ((i & 7) == 7) scales[1][rl + i - 7 + (lane & 7)][(lane >> 3) & 3] = (uint8_t)(keep >> 23);
     }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const u32x2_t halves = rows32(top.get(j));  // this lane's and that of the lane 32 on or back
+    const uint32_t scale = mx_scale_bits(max(halves[0], halves[1]), up);
+    const float s = __uint_as_float(scale);
+    uint32_t w[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const MxVec4<T>* at = v + 8 * p;
+      w[p] = MxVec4<T>::template pair<0>(0u, at[0], at[1], j, s);
+      w[p] = MxVec4<T>::template pair<1>(w[p], at[2], at[3], j, s);
+      w[p] = MxVec4<T>::template pair<2>(w[p], at[4], at[5], j, s);
+      w[p] = MxVec4<T>::template pair<3>(w[p], at[6], at[7], j, s);
+    }
+    *reinterpret_cast<uint2*>(cols + (32 * j + (lane & 31)) * kMxColPitch + rl / 2) = make_uint2(w[0], w[1]);
+    if (lane < 32) scales[0][cl + j][wave] = (uint8_t)(scale >> 23);
+  }
+  __syncthreads();
+  const int t = threadIdx.x, part = (t & 3) * 16;
+  const size_t col_pitch = (size_t)(mx_padded(g.M) / 2), row_pitch = (size_t)(mx_padded(g.K) / 2);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = t / 4 + 64 * i;
+    if (c0 + at < g.K)
+      *reinterpret_cast<uint4*>(g.qt + (c0 + at) * col_pitch + m0 / 2 + part) =
+          *reinterpret_cast<const uint4*>(cols + (32 * (at & 3) + at / 4) * kMxColPitch + part);
+    if (ROWS && m0 + at < g.M)
+      *reinterpret_cast<uint4*>(g.q + (m0 + at) * row_pitch + c0 / 2 + part) =
+          *reinterpret_cast<const uint4*>(rows + at * 64 + part);
+  }
+  if (t < 128) {
+    if (c0 + t < g.K)
+      reinterpret_cast<uint32_t*>(g.st)[(size_t)blockIdx.y * g.K + c0 + t] = *reinterpret_cast<const uint32_t*>(scales[0][t]);
+  } else if (ROWS && m0 + t - 128 < g.M) {
+    reinterpret_cast<uint32_t*>(g.s)[(size_t)blockIdx.x * g.M + m0 + t - 128] =
+        *reinterpret_cast<const uint32_t*>(scales[1][t - 128]);
   }
 }
 
-// Values of the codes, [R, cols] of the Kp columns: a thread takes eight of a
-// row. Rows of any length: the store is 16 bytes at the type's own alignment.
+// Values of the codes, [R, cols] of the Kp columns: a lane takes 16 bytes of
+// values (eight or four columns) of N rows. Rows of any length: the store is 16
+// bytes at the type's own alignment. (Eight float32 values to a lane, in two
+// stores of every other 16 bytes, 8192 x 7168 took 70 us.)
 template <typename T>
-struct __attribute__((packed, aligned(sizeof(T)))) Loose8 {
-  uint32_t w[2 * sizeof(T)];
+struct __attribute__((packed, aligned(sizeof(T)))) Loose16 {
+  uint32_t w[4];
 };
-template <typename T>
+template <typename T, int N>
 __global__ __launch_bounds__(256) void mx_values_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                         int R, int Kp, int cols, T* __restrict__ out) {
-  const int c = (blockIdx.y * 64 + (threadIdx.x & 63)) * 8, r = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= R || c >= cols) return;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(q + (size_t)r * (Kp / 2) + c / 2);
-  const float s = mx_scale(scale[((size_t)(c / kMxGroup) * R + r) * 4 + (c / kMxBlock) % 4]);
-  Loose8<T> o;
-  if constexpr (sizeof(T) == 2) {
-    o.w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-    o.w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-    o.w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-    o.w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-  } else {
-    const float2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 1);
-    const float2_t v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, 3);
-    const float f[8] = {v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+  constexpr int E = 16 / sizeof(T);
+  const int across = (cols + 64 * E - 1) / (64 * E);
+  const int c = ((int)(blockIdx.x % across) * 64 + (int)(threadIdx.x & 63)) * E;
+  const int r0 = ((int)(blockIdx.x / across) * 4 + (int)(threadIdx.x >> 6)) * N;
+  if (c >= cols) return;
+  uint32_t w[N], code[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.w[i] = __float_as_uint(f[i]);
+  for (int i = 0; i < N; ++i) {
+    const int r = min(r0 + i, R - 1);
+    const uint8_t* from = q + (size_t)r * (Kp / 2) + c / 2;
+    w[i] = E == 8 ? *reinterpret_cast<const uint32_t*>(from) : *reinterpret_cast<const uint16_t*>(from);
+    code[i] = scale[((size_t)(c / kMxGroup) * R + r) * 4 + (c / kMxBlock) % 4];
   }
-  T* to = out + (size_t)r * cols + c;
-  if (c + 8 <= cols) {
-    *reinterpret_cast<Loose8<T>*>(to) = o;
-  } else {
-    for (int i = 0; i < cols - c; ++i) {
-      if constexpr (sizeof(T) == 2)
-        to[i] = (uint16_t)(o.w[i >> 1] >> (16 * (i & 1)));
-      else
-        to[i] = __uint_as_float(o.w[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (r0 + i >= R) return;
+    const float s = __uint_as_float(code[i] << 23);  // 0 is 2^-127, 255 NaN
+    Loose16<T> o;
+    if constexpr (sizeof(T) == 2) {
+      o.w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 0));
+      o.w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 1));
+      o.w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 2));
+      o.w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], s, 3));
+    } else {
+      const float2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 0), hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 1);
+      const float f[4] = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o.w[j] = __float_as_uint(f[j]);
+    }
+    T* to = out + (size_t)(r0 + i) * cols + c;
+    if (c + E <= cols) {
+      *reinterpret_cast<Loose16<T>*>(to) = o;
+    } else {
+#pragma unroll
+      for (int j = 0; j < E - 1; ++j) {
+        if (c + j >= cols) break;
+        if constexpr (sizeof(T) == 2)
+          to[j] = (uint16_t)(o.w[j >> 1] >> (16 * (j & 1)));
+        else
+          to[j] = __uint_as_float(o.w[j]);
+      }
     }
   }
 }
@@ -226,6 +279,7 @@ extern "C" int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t
       !nvfp4_aligned16(scale_t))
     return NVFP4_ERR_ALIGN;
   if (q_t && M > kMxMaxK) return NVFP4_ERR_SHAPE;  // along the columns, M is the length of a row of codes
+  if ((int64_t)((M + 31) / 32) * ((K + 511) / 512) >= (1 << 24)) return NVFP4_ERR_SHAPE;  // threads of a grid
   const MxArgs g = {M, K, q, scale, q_t, scale_t, rule == MX_SCALE_CEIL};
   const auto go = [&](auto xt) -> int {
     using T = decltype(xt);
@@ -233,11 +287,11 @@ extern "C" int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t
     if (!q_t) {
       const int cols = (K + 511) / 512;
       if ((int64_t)M * cols <= 8192)
-        hipLaunchKernelGGL((mx_rows_kernel<T, 1>), dim3((M + 3) / 4, cols), dim3(256), 0, (hipStream_t)stream, at, g);
+        hipLaunchKernelGGL((mx_rows_kernel<T, 1>), dim3((unsigned)((M + 3) / 4) * cols), dim3(256), 0, (hipStream_t)stream, at, g);
       else
-        hipLaunchKernelGGL((mx_rows_kernel<T, 8>), dim3((M + 31) / 32, cols), dim3(256), 0, (hipStream_t)stream, at, g);
+        hipLaunchKernelGGL((mx_rows_kernel<T, 8>), dim3((unsigned)((M + 31) / 32) * cols), dim3(256), 0, (hipStream_t)stream, at, g);
     } else {
-      const dim3 grid((K + 255) / 256, (M + kMxGroup - 1) / kMxGroup);
+      const dim3 grid((K + 127) / 128, (M + kMxGroup - 1) / kMxGroup);
       if (q)
         hipLaunchKernelGGL((mx_columns_kernel<T, true>), grid, dim3(256), 0, (hipStream_t)stream, at, g);
       else
@@ -253,16 +307,24 @@ extern "C" int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int32_t 
                                 int32_t out_dtype, void* out, void* stream) {
   if (R < 0 || R > kMxMaxM || K < 0 || K > kMxMaxK || K % kMxGroup != 0 || cols < 0 || cols > K) return NVFP4_ERR_SHAPE;
   if (out_dtype != NVFP4_DT_BF16 && out_dtype != NVFP4_DT_F32) return NVFP4_ERR_ARG;
+  if ((int64_t)((R + 31) / 32) * ((K + 255) / 256) >= (1 << 24)) return NVFP4_ERR_SHAPE;  // threads of a grid
   if (R == 0 || cols == 0) return NVFP4_OK;
   if (!q || !scale || !out) return NVFP4_ERR_NULL;
   if (!nvfp4_aligned16(q) || !nvfp4_aligned16(scale) || !nvfp4_aligned16(out)) return NVFP4_ERR_ALIGN;
-  const dim3 grid((R + 3) / 4, (cols + 511) / 512);
+  const auto by_size = [&](auto t) {
+    using T = decltype(t);
+    const unsigned across = (cols * sizeof(T) + 1023) / 1024;
+    if ((int64_t)R * across <= 8192)  // few waves: one row each
+      hipLaunchKernelGGL((mx_values_kernel<T, 1>), dim3((R + 3) / 4 * across), dim3(256), 0, (hipStream_t)stream, q, scale,
+                         R, K, cols, reinterpret_cast<T*>(out));
+    else
+      hipLaunchKernelGGL((mx_values_kernel<T, 8>), dim3((R + 31) / 32 * across), dim3(256), 0, (hipStream_t)stream, q,
+                         scale, R, K, cols, reinterpret_cast<T*>(out));
+  };
   if (out_dtype == NVFP4_DT_BF16)
-    hipLaunchKernelGGL(mx_values_kernel<uint16_t>, grid, dim3(256), 0, (hipStream_t)stream, q, scale, R, K, cols,
-                       reinterpret_cast<uint16_t*>(out));
+    by_size(uint16_t());
   else
-    hipLaunchKernelGGL(mx_values_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream, q, scale, R, K, cols,
-                       reinterpret_cast<float*>(out));
+    by_size(float());
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
 }
