@@ -7,6 +7,7 @@
 // the scales cost one word per row and 128 elements and nothing is decoded. A
 // byte does what it does in the 8-bit integer product, on twice the elements.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.h"
@@ -38,6 +39,14 @@ __device__ __forceinline__ int8v mx_operand(int4v v) { return int8v{v[0], v[1], 
 template <int BYTE>
 __device__ __forceinline__ float16_t mx_mfma32(int4v a, int a_s, int4v b, int b_s, float16_t c) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx_operand(a), mx_operand(b), c, 4, 4, BYTE, a_s, BYTE, b_s);
+}
+
+// silu(g) u by the hardware's power of two and reciprocal, each within one step:
+// in the epilogue of 256 x 128 outputs the division and the exact exponential
+// took 8 us of a tile's 70.
+__device__ __forceinline__ float mx_silu_mul(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(g));
+  return (g < 0.0f ? g * e : g) * __builtin_amdgcn_rcpf(1.0f + e) * u;
 }
 
 // One word per lane from memory to LDS, side by side from `to` on.
@@ -79,8 +88,15 @@ struct MxOut<kMxF32> {
 // stages of BK bytes through four LDS buffers, filled straight from memory three
 // stages ahead; the wait before a stage leaves the two younger stages in flight.
 // A row's 16-byte chunks are permuted by its number, which spreads the rows that
-// eight lanes of a fragment read touch over all banks. Behind a buffer's codes
-// lie the stage's scales, one word per row and 64 bytes of codes.
+// sixteen lanes of a fragment read touch over all 64 banks (permuted for eight
+// lanes and 32 banks, 43 % of the LDS cycles were conflicts). Behind a buffer's
+// codes lie the stage's scales, one word per row and 64 bytes of codes.
+//
+// What bounds the large tile is power: on random codes the clock falls to 1.7 GHz
+// (8192 x 4096 x 7168: 118 us, 4.1 PFLOP/s; zeros, at the same number of cycles,
+// 90 us), where the matrix unit by itself does 6.0. Four waves of 128 x 128, with
+// a third less to read from LDS, took 125; reads kept strictly ahead of a step's
+// products 129.
 //
 // SILU: the tile's weight rows alternate in runs of 32 between gate (row n)
 // and up (row I + n), so that a wave holds both halves of an output.
@@ -107,7 +123,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
   // row of the matrix again where there is none: its results are not stored),
   // K bytes tk of a stage. SILU: the rows of one load of a wave lie in one half,
   // by the wave (RPI a multiple of 64) or by the load (RPI 32).
-  const auto swizzle = [](int row, int chunk) { return CPR == 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3); };
+  const auto swizzle = [](int row, int chunk) { return CPR == 8 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3); };
   const int trow = threadIdx.x / CPR, tk = swizzle(trow, threadIdx.x % CPR) * 16;
   static_assert(!SILU || RPI == 32 || RPI % 64 == 0, "the rows of a load of a wave lie in one half");
   const int a_rows = min(BM, g.M - m0), b_rows = min(SILU ? BN / 2 : BN, (SILU ? half : g.N) - n0);
@@ -176,60 +192,82 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
     fb_at[ks] = (BM + wn * 32 * SN + r) * CPR + c;
   }
   const int sa_at = wm * 32 * SM + r, sb_at = BM + wn * 32 * SN + r;
-  auto compute = [&](const int4v* at) {
-    int4v fa[2][SM], fb[2][SN];
-    int wa[DW][SM], wb[DW][SN];  // scales of this lane's blocks: ks in byte 2 (ks % 2) of word ks / 2
-    auto read = [&](int ks) {
+  int4v fa[2][SM], fb[2][SN];
+  int wa[DW][SM], wb[DW][SN];  // scales of this lane's blocks: step ks in byte 2 (ks % 2) of word ks / 2
+  auto read = [&](const int4v* at, int ks) {
 #pragma unroll
-      for (int j = 0; j < SM; ++j) fa[ks & 1][j] = at[fa_at[ks] + j * 32 * CPR];
+    for (int j = 0; j < SM; ++j) fa[ks & 1][j] = at[fa_at[ks] + j * 32 * CPR];
 #pragma unroll
-      for (int i = 0; i < SN; ++i) fb[ks & 1][i] = at[fb_at[ks] + i * 32 * CPR];
-    };
+    for (int i = 0; i < SN; ++i) fb[ks & 1][i] = at[fb_at[ks] + i * 32 * CPR];
+  };
+  int na[DW][SM], nb[DW][SN];  // the next stage's, as read
+  auto read_scales = [&](const int4v* at) {
     const int* s = reinterpret_cast<const int*>(at + BUF);
 #pragma unroll
     for (int d = 0; d < DW; ++d) {
 #pragma unroll
-      for (int j = 0; j < SM; ++j) wa[d][j] = (int)((uint32_t)s[d * (BM + BN) + sa_at + j * 32] >> (8 * hi));
+      for (int j = 0; j < SM; ++j) na[d][j] = s[d * (BM + BN) + sa_at + j * 32];
 #pragma unroll
-      for (int i = 0; i < SN; ++i) wb[d][i] = (int)((uint32_t)s[d * (BM + BN) + sb_at + i * 32] >> (8 * hi));
+      for (int i = 0; i < SN; ++i) nb[d][i] = s[d * (BM + BN) + sb_at + i * 32];
     }
-    read(0);
+  };
+  auto take_scales = [&]() {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      if (ks + 1 < KS) read(ks + 1);
+    for (int d = 0; d < DW; ++d) {
 #pragma unroll
-      for (int i = 0; i < SN; ++i)
+      for (int j = 0; j < SM; ++j) wa[d][j] = (int)((uint32_t)na[d][j] >> (8 * hi));
 #pragma unroll
-        for (int j = 0; j < SM; ++j)
-          acc[i][j] = ks & 1 ? mx_mfma32<2>(fb[1][i], wb[ks / 2][i], fa[1][j], wa[ks / 2][j], acc[i][j])
-                             : mx_mfma32<0>(fb[0][i], wb[ks / 2][i], fa[0][j], wa[ks / 2][j], acc[i][j]);
+      for (int i = 0; i < SN; ++i) wb[d][i] = (int)((uint32_t)nb[d][i] >> (8 * hi));
     }
+  };
+  auto multiply = [&](int ks) {
+#pragma unroll
+    for (int i = 0; i < SN; ++i)
+#pragma unroll
+      for (int j = 0; j < SM; ++j)
+        acc[i][j] = ks & 1 ? mx_mfma32<2>(fb[1][i], wb[ks / 2][i], fa[1][j], wa[ks / 2][j], acc[i][j])
+                           : mx_mfma32<0>(fb[0][i], wb[ks / 2][i], fa[0][j], wa[ks / 2][j], acc[i][j]);
   };
   const int stages = (k_end - k_begin + BK - 1) / BK;
   fetch(k_begin, l0);
   fetch(k_begin + BK, l1);
   fetch(k_begin + 2 * BK, l2);
-  // Stage s: its own loads have arrived; every wave is past stage s - 1, whose
-  // buffer takes the loads of stage s + 3 (zeros past the end of K). No branch
-  // inside the loop: around the stages it leaves the compiler unsure which
-  // buffer a load fills, and it waits for all of them before it reads any.
-  auto stage = [&](int s, const int4v* cur, int4v* next) {
-    wait_stage<2 * PL>();
-    fetch(k_begin + (s + 3) * BK, next);
-    compute(cur);
+  wait_stage<2 * PL>();
+  read_scales(l0);
+  read(l0, 0);
+  // Stage s, whose first fragments are on their way: each step reads the next
+  // one's, the last those of stage s + 1, whose loads have then arrived for every
+  // wave. All waves are past stage s - 1 there, so its buffer takes the loads of
+  // stage s + 3 (zeros past the end of K). No branch inside the loop: around the
+  // stages it leaves the compiler unsure which buffer a load fills, and it waits
+  // for all of them before it reads any.
+  auto stage = [&](int s, const int4v* cur, const int4v* after, int4v* fill) {
+    take_scales();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if (ks + 1 < KS) {
+        read(cur, ks + 1);
+      } else {
+        wait_stage<PL>();
+        fetch(k_begin + (s + 3) * BK, fill);
+        read_scales(after);
+        read(after, 0);
+      }
+      multiply(ks);
+    }
   };
   int s = 0;
   for (; s + 4 <= stages; s += 4) {
-    stage(s, l0, l3);
-    stage(s + 1, l1, l0);
-    stage(s + 2, l2, l1);
-    stage(s + 3, l3, l2);
+    stage(s, l0, l1, l3);
+    stage(s + 1, l1, l2, l0);
+    stage(s + 2, l2, l3, l1);
+    stage(s + 3, l3, l0, l2);
   }
   if (s < stages) {
-    stage(s, l0, l3);
+    stage(s, l0, l1, l3);
     if (s + 1 < stages) {
-      stage(s + 1, l1, l0);
-      if (s + 2 < stages) stage(s + 2, l2, l1);
+      stage(s + 1, l1, l2, l0);
+      if (s + 2 < stages) stage(s + 2, l2, l3, l1);
     }
   }
   wait_stage<0>();
@@ -288,7 +326,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
       }
       if constexpr (SILU) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = silu_mul(o[e], o[4 + e]);
+        for (int e = 0; e < 4; ++e) o[e] = mx_silu_mul(o[e], o[4 + e]);
       }
       if (m >= g.M || !n_ok) continue;
       if constexpr (OUT == kMxPart)
@@ -328,7 +366,7 @@ __global__ __launch_bounds__(256) void mx_join_kernel(MxGemmArgs g) {
   }
   if constexpr (SILU) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = silu_mul(s[e], u[e]);
+    for (int e = 0; e < 4; ++e) s[e] = mx_silu_mul(s[e], u[e]);
   }
   if constexpr (OUT == kMxF32) {
     if (g.add) s += *reinterpret_cast<const float4_t*>(reinterpret_cast<const float*>(g.add) + at);
@@ -352,7 +390,7 @@ constexpr int kMxSkinnyWaves = 8;
 template <int MT, int OUT>
 __global__ __launch_bounds__(64 * kMxSkinnyWaves, 2) void mx_skinny_kernel(MxGemmArgs g) {
   constexpr bool SILU = OUT == kMxSilu;
-  constexpr int U = 2;                                // 64-byte steps of a group
+  constexpr int U = 2;                                // 64-byte steps of a group (1 and 4: the same times)
   __shared__ float sums[kMxSkinnyWaves][MT][16][17];  // [wave][subtile][token][weight row], padded against conflicts
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, kq = lane >> 4;
@@ -426,7 +464,7 @@ __global__ __launch_bounds__(64 * kMxSkinnyWaves, 2) void mx_skinny_kernel(MxGem
     o += sums[w][tok >> 4][tok & 15][c];
     if (SILU) up += sums[w][tok >> 4][tok & 15][c + 8];
   }
-  if (SILU) o = silu_mul(o, up);
+  if (SILU) o = mx_silu_mul(o, up);
   const size_t d = (size_t)m * g.n_out + n;
   if constexpr (OUT == kMxF32) {
     reinterpret_cast<float*>(g.d)[d] = o + (g.add ? reinterpret_cast<const float*>(g.add)[d] : 0.0f);
@@ -470,20 +508,29 @@ static int launch_mx_skinny(const MxGemmArgs& g, hipStream_t stream) {
   return NVFP4_OK;
 }
 
-// Which kernel a product takes: the few-token kernel up to 16 tokens, and where
-// its workgroups of 32 tokens by 16 rows do not outnumber the CUs, unless a long
-// K meets too few of them. KB are bytes.
-constexpr int kMxSkinnyM = 16, kMxLongK = 4096;
-static bool mx_few(int64_t M, int64_t N, int64_t KB) {
-  return M <= kMxSkinnyM || (((M + 31) / 32) * ((N + 15) / 16) <= 256 && (KB < kMxLongK || N >= 4096));
+// Which kernel a product takes (us on the card, operands from memory, the other
+// side in brackets; KB are bytes). Few tokens: one subtile of 16 tokens a
+// workgroup up to 16 tokens (1 x 4096 x 7168: 5.3 [tiles 9.4]; 16 x 16384 x 8192:
+// 16.7 [17.6]) or where that takes at most a workgroup per CU (32 x 1024 x 7168:
+// 5.3 [two subtiles 7.1], 128 x 512 x 8192: 6.2 [parts of K 8.7]), two where that
+// does (32 x 4096 x 7168: 6.8 [9.5], 64 x 2048 x 16384: 13.6 [parts 14.7]), unless
+// a very long K meets few workgroups: their time grows with it.
+constexpr int kMxSkinnyM = 16, kMxSkinnyKB = 8192;
+static int mx_few(int64_t M, int64_t N, int64_t KB) {
+  const int64_t across = (N + 15) / 16, one = (M + 15) / 16 * across, two = (M + 31) / 32 * across;
+  if (M <= kMxSkinnyM) return KB > kMxSkinnyKB && one <= 128 ? 0 : 1;
+  if (KB > kMxSkinnyKB) return 0;
+  return one <= 256 ? 1 : two <= 256 ? 2 : 0;
 }
 // Parts of K for tiles: as many as bring 64 x 128 tiles to about one per CU,
-// each of at least 512 bytes, or one where K is short.
+// each of at least 512 bytes (64 x 4096 x 16384: 11.7 + 3.8 [undivided 26]; 128
+// x 1024 x 16384: 10.2 + 3.8 [18.3]), or one where K is short: the join costs
+// more than it saves (64 x 4096 x 7168: 9.6 undivided).
 static int mx_splits(int64_t M, int64_t N, int64_t KB) {
   if (mx_few(M, N, KB)) return 1;
   const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
   const int64_t s = std::min<int64_t>(256 / tiles, KB / 512);
-  return s < 2 || KB < kMxLongK ? 1 : (int)s;
+  return s < 2 || KB < 4096 ? 1 : (int)s;
 }
 static size_t mx_part_bytes(int64_t M, int64_t N, int splits) { return splits > 1 ? (size_t)splits * M * N * 4 : 0; }
 
@@ -498,20 +545,21 @@ static int launch_mx(const MxGemmArgs& g, hipStream_t stream) {
     NVFP4_CHECK_LAUNCH();
     return NVFP4_OK;
   }
-  if (g.M <= kMxSkinnyM) return launch_mx_skinny<1, OUT>(g, stream);
-  if (mx_few(g.M, g.N, g.KB)) return launch_mx_skinny<2, OUT>(g, stream);
-  // The tile whose rounds over the 256 CUs take least, by what one of each size
-  // takes: alone on its CU, or each of more.
-  const auto cost = [&](int bm, int bn, double alone, double each) {
-    const int64_t tiles = (int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn);
-    return tiles <= 256 ? alone : each * (double)((tiles + 255) / 256);
+  const int few = mx_few(g.M, g.N, g.KB);
+  if (few == 1) return launch_mx_skinny<1, OUT>(g, stream);
+  if (few == 2) return launch_mx_skinny<2, OUT>(g, stream);
+  // The tile that takes least, by what each took at K = 7168 (us, in proportion
+  // to K), with r tiles for each of the 256 CUs: alone on a CU or, where all are
+  // busy and the clock falls, by the tile.
+  const auto rounds = [&](int bm, int bn) {
+    return (double)((int64_t)((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn)) / 256.0;
   };
-  constexpr int BN = SILU ? 128 : 64;
-  const double large = cost(256, 256, 96.0, 96.0), middle = cost(128, 128, 49.0, 41.0);
-  const double small = SILU ? cost(64, 128, 29.0, 26.0) : cost(64, 64, 24.0, 16.5);
+  const double rl = rounds(256, 256), rm = rounds(128, 128), rs = rounds(64, SILU ? 128 : 64);
+  const double large = std::max(41.0 * std::ceil(rl), 61.0 * rl), middle = std::max(16.6 * std::ceil(rm), 1.8 + 19.2 * rm);
+  const double small = SILU ? std::max(14.7 * std::ceil(rs), 15.2 * rs) : rs <= 1.0 ? 9.8 : 2.6 + 6.3 * rs;
   if (large <= middle && large <= small) return launch_mx_tile<256, 256, 2, 4, 64, OUT>(g, stream);
-  if (middle <= small) return launch_mx_tile<128, 128, 2, 2, 64, OUT>(g, stream);
-  return launch_mx_tile<64, BN, 2, 2, 128, OUT>(g, stream);
+  if (middle <= small) return launch_mx_tile<128, 128, 4, 2, 128, OUT>(g, stream);
+  return launch_mx_tile<64, SILU ? 128 : 64, 2, 2, 128, OUT>(g, stream);
 }
 
 extern "C" size_t mxfp4_gemm_ws_bytes(int32_t M, int32_t N, int32_t K) {
