@@ -29,6 +29,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kFewMaxT = 64, kFewMaxK = 64, kFewMaxL = 4096;
 constexpr int kFewChunk = 2304, kFewScales = 2048;  // bytes of 32 rows x 128 columns, and where their scales start
 constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kUpDepth = 3, kDownDepth = 4;
 
 struct FewArgs {
   const uint16_t* x;     // BF16 [T, H]
@@ -106,14 +107,22 @@ __device__ __forceinline__ int choice_of(const FewArgs& g, const int16_t* ids, i
   return first;
 }
 
+// Loads of a wave's stages. `in` says whether the stage exists: where it does
+// not they take an offset out of range, which moves nothing; a branch around
+// them would leave the compiler unsure what is in flight, and it would wait for
+// all of it.
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int voff, int soff) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0);
+}
 // One lane's part of a chunk, and its BF16 operands.
 struct Chunk {
   u32x4_t q[2];
   uint32_t s;
-  __device__ __forceinline__ void load(const uint8_t* p, int lane) {
-    q[0] = *reinterpret_cast<const u32x4_t*>(p + lane * 16);
-    q[1] = *reinterpret_cast<const u32x4_t*>(p + 1024 + lane * 16);
-    s = *reinterpret_cast<const uint32_t*>(p + kFewScales + lane * 4);
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int soff, int lane, bool in) {
+    const int at = in ? lane * 16 : kOutOfRange, scales = in ? lane * 4 : kOutOfRange;
+    q[0] = load16(r, at, soff);
+    q[1] = load16(r, at, soff + 1024);
+    s = __builtin_amdgcn_raw_buffer_load_b32(r, scales, soff + kFewScales, 0);
   }
   template <int STEP>
   __device__ __forceinline__ bf16x8_t operand() const {
@@ -132,9 +141,10 @@ struct Chunk {
 // The tokens' operands of a chunk: eight runs of eight elements.
 struct Tokens {
   u32x4_t v[8];
-  __device__ __forceinline__ void load(const uint16_t* p) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int voff, int soff, bool in) {
+    const int at = in ? voff : kOutOfRange;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4_t*>(p + 8 * i);
+    for (int i = 0; i < 8; ++i) v[i] = load16(r, at + 16 * i, soff);
   }
 };
 template <int STEP = 0>
@@ -158,32 +168,41 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewArgs g) {
   const uint64_t chose = __ballot(j >= 0);
   const int some = __builtin_ctzll(chose) + (item & 1) * 32;  // lanes without a token repeat one
   const int stages = g.H / 128;
-  const uint16_t* x = g.x + (size_t)(j >= 0 ? t : some) * g.H + 64 * (lane >> 5);
-  const uint8_t* w = g.w1 + (size_t)e * (2 * g.I / 32) * stages * kFewChunk + (size_t)sub * stages * kFewChunk;
-  const size_t up = (size_t)pairs * stages * kFewChunk;
+  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(g.x, (uint32_t)(g.T * g.H * 2));
+  const int matrix = 2 * pairs * stages * kFewChunk, from = sub * stages * kFewChunk, up = pairs * stages * kFewChunk;
+  const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(g.w1 + (size_t)e * matrix, (uint32_t)matrix);
+  const int at_x = (j >= 0 ? t : some) * g.H * 2 + 128 * (lane >> 5);
   float16_t acc[2];
 #pragma unroll
   for (int v = 0; v < 16; ++v) acc[0][v] = acc[1][v] = 0.0f;
-  Chunk c[2][2];
-  Tokens tok[2];
-  auto load = [&](int s, int b) {
-    const int at = min(s, stages - 1);
-    c[b][0].load(w + (size_t)at * kFewChunk, lane);
-    c[b][1].load(w + up + (size_t)at * kFewChunk, lane);
-    tok[b].load(x + at * 128);
+  struct Stage {
+    Chunk gate, up;
+    Tokens tok;
+  } st[kUpDepth];
+  auto load = [&](int s, Stage& to) {
+    const bool in = s < stages;
+    const int at = in ? from + s * kFewChunk : 0;
+    to.gate.load(rw, at, lane, in);
+    to.up.load(rw, at + up, lane, in);
+    to.tok.load(rx, at_x, in ? s * 256 : 0, in);
   };
-  auto compute = [&](int b) {
-    multiply(c[b][0], tok[b], acc[0]);
-    multiply(c[b][1], tok[b], acc[1]);
+  auto compute = [&](const Stage& it) {
+    multiply(it.gate, it.tok, acc[0]);
+    multiply(it.up, it.tok, acc[1]);
   };
-  load(wave, 0);
-  for (int s = wave; s < stages; s += 2 * kUpWaves) {
-    load(s + kUpWaves, 1);
-    compute(0);
-    if (s + kUpWaves >= stages) break;
-    load(s + 2 * kUpWaves, 0);
-    compute(1);
+#pragma unroll
+  for (int d = 0; d < kUpDepth - 1; ++d) load(wave + d * kUpWaves, st[d]);
+  int s = wave;
+  for (; s + (kUpDepth - 1) * kUpWaves < stages; s += kUpDepth * kUpWaves) {
+#pragma unroll
+    for (int d = 0; d < kUpDepth; ++d) {
+      load(s + (d + kUpDepth - 1) * kUpWaves, st[(d + kUpDepth - 1) % kUpDepth]);
+      compute(st[d]);
+    }
   }
+#pragma unroll
+  for (int d = 0; d < kUpDepth - 1; ++d)
+    if (s + d * kUpWaves < stages) compute(st[d]);
 #pragma unroll
   for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -224,6 +243,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
   for (int i = threadIdx.x; i < g.T * g.k; i += 64 * kDownWaves) weight[i] = g.weight[i];
   find_items(g, items, ids);
   float* const mine = tiles + wave * g.T * PITCH;
+  const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(g.h, (uint32_t)(g.T * g.k * g.I * 2));
   const int stages = g.I / 128, words = (2 * g.L + 31) / 32;
   const int64_t total = (int64_t)items.before[256] * stages;
   int64_t u = total * wave / kDownWaves;
@@ -237,26 +257,34 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
     const uint64_t chose = __ballot(j >= 0);
     const int first = __builtin_ctzll(chose);
     const int row = j >= 0 ? t * g.k + j : -1, some = __shfl(row, first, 64);
-    const uint16_t* h = g.h + (size_t)(row >= 0 ? row : some) * g.I + 64 * (lane >> 5);
-    const uint8_t* w = g.w2 + ((size_t)e * (g.H / 32) + blockIdx.x) * stages * kFewChunk;
+    const int matrix = (g.H / 32) * stages * kFewChunk, from = (int)blockIdx.x * stages * kFewChunk;
+    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(g.w2 + (size_t)e * matrix, (uint32_t)matrix);
+    const int at_h = (row >= 0 ? row : some) * g.I * 2 + 128 * (lane >> 5);
     float16_t acc;
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
-    Chunk c[2];
-    Tokens tok[2];
-    auto load = [&](int s, int b) {
-      const int at = min(s, s1 - 1);
-      c[b].load(w + (size_t)at * kFewChunk, lane);
-      tok[b].load(h + at * 128);
+    struct Stage {
+      Chunk c;
+      Tokens tok;
+    } st[kDownDepth];
+    auto load = [&](int s, Stage& to) {
+      const bool in = s < s1;
+      to.c.load(rw, in ? from + s * kFewChunk : 0, lane, in);
+      to.tok.load(rh, at_h, in ? s * 256 : 0, in);
     };
-    load(s0, 0);
-    for (int s = s0; s < s1; s += 2) {
-      load(s + 1, 1);
-      multiply(c[0], tok[0], acc);
-      if (s + 1 >= s1) break;
-      load(s + 2, 0);
-      multiply(c[1], tok[1], acc);
+#pragma unroll
+    for (int d = 0; d < kDownDepth - 1; ++d) load(s0 + d, st[d]);
+    int s = s0;
+    for (; s + kDownDepth <= s1; s += kDownDepth) {
+#pragma unroll
+      for (int d = 0; d < kDownDepth; ++d) {
+        load(s + d + kDownDepth - 1, st[(d + kDownDepth - 1) % kDownDepth]);
+        multiply(st[d].c, st[d].tok, acc);
+      }
     }
+#pragma unroll
+    for (int d = 0; d < kDownDepth - 1; ++d)
+      if (s + d < s1) multiply(st[d].c, st[d].tok, acc);
     if (j >= 0) {  // a token that lists an expert twice has both weights
       float wt = 0.0f;
       for (int i = j; i < g.k; ++i) wt += ids[t * g.k + i] == e ? weight[t * g.k + i] : 0.0f;
