@@ -8,13 +8,24 @@
 // its expert in the choices themselves, and every wave streams weight chunks
 // from memory to registers and multiplies them there.
 //
-// E2M1 x E4M3 has at most 6 significant bits, so a weight without its global
-// scale is exact in BF16: two values decode to float32 in one instruction, are
-// multiplied by the block's scale and meet in one word. MFMA 32x32x16 BF16
-// with the weights' 32 rows as first operand and 32 tokens as second; a chunk's
-// lanes hold 64 of 128 K elements each (lane half g the range [64 g, 64 g + 64)),
-// and the tokens' operand is read in the same order.
+// What bounds the rest is instructions and the loads of the tokens, so an item of
+// up to eight tokens (most are, in a decode step) is handled so that each weight
+// costs least. An E2M1 code is exact in BF16, and a block of 16 shares one E4M3
+// scale: a matrix step covers one block, MFMA 32x32x16 BF16 with the tokens as
+// first operand and 32 weight rows as second, from codes turned to BF16 two at a
+// time, and its sums are added to the running ones times the rows' scales. A lane
+// of the result holds one weight row, so one scale, and four tokens: four
+// multiply-adds for what takes 24 instructions where every weight is multiplied
+// by its scale before the step. The tokens' operands come through LDS, by loads
+// that pass no register, one for four tokens: read by every lane from memory they
+// kept the address unit busy for longer than the weights. More tokens are handled
+// by scaled weights and direct loads, as their own multiply-adds would cost more.
+// (64 tokens on 48 x 7168 x 2048: 105 + 82 us that way for all, MEASURED.)
+//
+// A packed chunk's lane halves hold 64 of 128 K elements each. A swap between the
+// halves brings the two words of a block side by side.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "internal.h"
@@ -28,8 +39,8 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kFewMaxT = 64, kFewMaxK = 64, kFewMaxL = 4096;
 constexpr int kFewChunk = 2304, kFewScales = 2048;  // bytes of 32 rows x 128 columns, and where their scales start
-constexpr int kUpWaves = 4, kDownWaves = 8;
-constexpr int kUpDepth = 3, kDownDepth = 4;
+constexpr int kUpWaves = 4, kDownWaves = 8, kDownDepth = 5, kDownPitch = 36;
+constexpr size_t kLdsBytes = 160 * 1024;
 
 struct FewArgs {
   const uint16_t* x;     // BF16 [T, H]
@@ -43,68 +54,108 @@ struct FewArgs {
   int T, k, L, start, H, I, dual;
 };
 
-// An item is an expert and 32 tokens (the lower or the upper half of the batch)
-// of which at least one chose it. Bit 2 e + half of a bitmap in LDS says which
-// there are; they are taken in ascending order.
-struct Items {
-  uint32_t bits[2 * kFewMaxL / 32];
-  int before[2 * kFewMaxL / 32 + 1];  // items in the words before, and in all
-};
 __device__ __forceinline__ int local_expert(const FewArgs& g, int id) {
   const int64_t e = (int64_t)id - g.start;
   return e >= 0 && e < g.L ? (int)e : -1;
 }
-// Fills the bitmap, and ids with the choices as local experts (-1: not here).
-__device__ __forceinline__ void find_items(const FewArgs& g, Items& s, int16_t* ids) {
-  const int words = (2 * g.L + 31) / 32, n = g.T * g.k;
-  for (int i = threadIdx.x; i < words; i += blockDim.x) s.bits[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int e = local_expert(g, g.ids[i]);
-    ids[i] = (int16_t)e;
-    if (e >= 0) {
-      const int b = 2 * e + (i >= 32 * g.k ? 1 : 0);
-      atomicOr(&s.bits[b >> 5], 1u << (b & 31));
+
+// An item is an expert and 32 tokens (the lower or the upper half of the batch)
+// of which at least one chose it. Every workgroup finds the items in the choices
+// by itself: a bitmap in LDS has bit 2 e + half for each, and they are taken in
+// ascending order.
+struct Choices {
+  struct Items {
+    uint32_t bits[2 * kFewMaxL / 32];
+    int before[2 * kFewMaxL / 32 + 1];  // items in the words before, and in all
+  };
+  const Items* s;
+  const int16_t* ids;   // the choices as local experts, -1: not here
+  const float* weights;
+  int k, T, words;
+  __device__ __forceinline__ void find(const FewArgs& g, Items& to, int16_t* local, float* weights_lds) {
+    s = &to;
+    ids = local;
+    weights = weights_lds;
+    k = g.k;
+    T = g.T;
+    words = (2 * g.L + 31) / 32;
+    const int n = T * k;
+    for (int i = threadIdx.x; i < words; i += blockDim.x) to.bits[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int e = local_expert(g, g.ids[i]);
+      local[i] = (int16_t)e;
+      if (weights_lds) weights_lds[i] = g.weight[i];
+      if (e >= 0) {
+        const int b = 2 * e + (i >= 32 * k ? 1 : 0);
+        atomicOr(&to.bits[b >> 5], 1u << (b & 31));
+      }
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < 64) {  // four words to a lane, at most 256
-    int sum = 0, c[4];
+    __syncthreads();
+    if (threadIdx.x < 64) {  // four words to a lane, at most 256
+      int sum = 0, c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = threadIdx.x * 4 + i;
-      c[i] = sum;
-      sum += at < words ? __popc(s.bits[at]) : 0;
-    }
-    int scan = sum;
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(scan, o, 64);
-      if ((int)threadIdx.x >= o) scan += v;
-    }
+      for (int i = 0; i < 4; ++i) {
+        const int at = threadIdx.x * 4 + i;
+        c[i] = sum;
+        sum += at < words ? __popc(to.bits[at]) : 0;
+      }
+      int scan = sum;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(scan, o, 64);
+        if ((int)threadIdx.x >= o) scan += v;
+      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s.before[threadIdx.x * 4 + i] = scan - sum + c[i];
-    if (threadIdx.x == 63) s.before[256] = scan;
+      for (int i = 0; i < 4; ++i) to.before[threadIdx.x * 4 + i] = scan - sum + c[i];
+      if (threadIdx.x == 63) to.before[256] = scan;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-}
-// The a-th item (a < their number): 2 e + half. The same for a whole wave.
-__device__ __forceinline__ int item_at(const Items& s, int a, int words) {
-  int lo = 0, hi = words - 1;  // the last word with before <= a
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.before[mid] <= a) lo = mid; else hi = mid - 1;
+  __device__ __forceinline__ int count() const { return s->before[256]; }
+  __device__ __forceinline__ int item(int a) const {
+    int lo = 0, hi = words - 1;  // the last word with before <= a
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s->before[mid] <= a) lo = mid; else hi = mid - 1;
+    }
+    uint32_t b = s->bits[lo];
+    for (int i = a - s->before[lo]; i > 0; --i) b &= b - 1;
+    return __builtin_amdgcn_readfirstlane(lo * 32 + __ffs((int)b) - 1);
   }
-  uint32_t b = s.bits[lo];
-  for (int i = a - s.before[lo]; i > 0; --i) b &= b - 1;
-  return lo * 32 + __ffs((int)b) - 1;
-}
-// This lane's token of an item (lane % 32 of its half), its first choice that is
-// the expert (-1: none).
-__device__ __forceinline__ int choice_of(const FewArgs& g, const int16_t* ids, int e, int t) {
-  int first = -1;
-  if (t < g.T)
-    for (int j = g.k - 1; j >= 0; --j) first = ids[t * g.k + j] == e ? j : first;
-  return first;
+  // the first choice of token t that is the item's expert (-1: none)
+  __device__ __forceinline__ int choice(int item, int t) const {
+    int first = -1;
+    if (t < T)
+      for (int j = k - 1; j >= 0; --j) first = ids[t * k + j] == item >> 1 ? j : first;
+    return first;
+  }
+  // the weight of token t on it, of which j is the first choice: a token that
+  // lists an expert twice has both weights
+  __device__ __forceinline__ float weight(int item, int t, int j) const {
+    float sum = 0.0f;
+    if (j >= 0)
+      for (int i = j; i < k; ++i) sum += ids[t * k + i] == item >> 1 ? weights[t * k + i] : 0.0f;
+    return sum;
+  }
+};
+
+// An item's tokens in order: lane p (and p + 32) holds the p-th; those from n on
+// the first again, with j = -1.
+struct Mine {
+  int n, t, j;
+};
+__device__ __forceinline__ Mine tokens_of(const Choices& ch, int item) {
+  const int lane = threadIdx.x & 63, t = (item & 1) * 32 + (lane & 31), j = ch.choice(item, t);
+  const uint32_t chose = (uint32_t)__ballot(j >= 0), below = (1u << (lane & 31)) - 1u;
+  Mine m;
+  m.n = __popc(chose);
+  // each lane hands its token to the lane of its rank, those without one behind
+  const int rank = j >= 0 ? __popc(chose & below) : m.n + __popc(~chose & below);
+  const int both = __builtin_amdgcn_ds_permute((rank + (lane & 32)) * 4, t << 8 | (j & 255));
+  const bool there = (lane & 31) < m.n;
+  m.t = (there ? both : __builtin_amdgcn_readfirstlane(both)) >> 8;
+  m.j = there ? both & 255 : -1;
+  return m;
 }
 
 // Loads of a wave's stages. `in` says whether the stage exists: where it does
@@ -114,7 +165,7 @@ __device__ __forceinline__ int choice_of(const FewArgs& g, const int16_t* ids, i
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int voff, int soff) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0);
 }
-// One lane's part of a chunk, and its BF16 operands.
+// One lane's part of a chunk, and (direct) its BF16 operands with their scales.
 struct Chunk {
   u32x4_t q[2];
   uint32_t s;
@@ -133,12 +184,15 @@ struct Chunk {
 
  private:
   template <int SEL>
-  static __device__ __forceinline__ uint32_t pair(uint32_t w, float f) {
+  static __device__ __forceinline__ uint32_t pair(uint32_t w, float f) {  // at most 6 significant bits: exact
     const float2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, SEL);
-    return __builtin_amdgcn_perm(__float_as_uint(v[1] * f), __float_as_uint(v[0] * f), 0x07060302u);  // exact
+    return __builtin_amdgcn_perm(__float_as_uint(v[1] * f), __float_as_uint(v[0] * f), 0x07060302u);
   }
 };
-// The tokens' operands of a chunk: eight runs of eight elements.
+
+// ---- more than eight tokens: direct loads, scaled weights as first operand
+
+// Lane half g holds the elements [64 g, 64 g + 64) of its row, eight to a step.
 struct Tokens {
   u32x4_t v[8];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int voff, int soff, bool in) {
@@ -153,159 +207,313 @@ __device__ __forceinline__ void multiply(const Chunk& c, const Tokens& t, float1
   if constexpr (STEP < 7) multiply<STEP + 1>(c, t, acc);
 }
 
+// ---- up to eight tokens: through LDS, scales behind the step
+
+// A stage's tokens in LDS: 256 bytes each, a token's 16-byte pieces permuted by its
+// number, so that the tokens' pieces of one step lie in different banks.
+struct FewLoad {  // this lane's piece of each load of four tokens
+  int at[2];
+  __device__ __forceinline__ void init(int offset, int n) {  // offset: of the token that lane p holds
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int r = 4 * g + lane / 16, from = __shfl(offset, r, 64);
+      at[g] = r < n ? from + ((lane & 15) ^ r) * 16 : kOutOfRange;
+    }
+  }
+  template <int NG>
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int4v* to, int soff, bool in) const {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) load_lds16(r, to + 64 * g, in ? at[g] : kOutOfRange, soff);
+  }
+};
+// acc += tokens x chunk: register i of a lane is weight row lane % 32 and token
+// 4 (lane / 32) + i.
+__device__ __forceinline__ float16_t block_product(int4v tok, uint32_t codes) {
+  const u32x4_t w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, 1.0f, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, 1.0f, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, 1.0f, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, 1.0f, 3))};
+  float16_t zero;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) zero[v] = 0.0f;
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, tok), __builtin_bit_cast(bf16x8_t, w), zero, 0,
+                                                 0, 0);
+}
+struct FewTokens {
+  int4v lo[4], hi[4];  // pieces of the lower half's blocks and of the upper half's
+  // piece: this lane's token's place in the stage, and its number
+  __device__ __forceinline__ void read(const int4v* stage, int r) {
+    const int half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      lo[b] = stage[r * 16 + ((2 * b + half) ^ r)];
+      hi[b] = stage[r * 16 + ((8 + 2 * b + half) ^ r)];
+    }
+  }
+};
+__device__ __forceinline__ void multiply(const Chunk& c, const FewTokens& t, float4_t& acc) {
+  const u32x2_t s = rows32(c.s);  // scales of the lower half's blocks, and of the upper half's
+  float16_t p[2];
+  const auto add = [&](const float16_t& v, float scale) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(scale, v[i], acc[i]);
+  };
+#define FEW_BLOCK(B)                                                                                             \
+  {                                                                                                              \
+    const u32x2_t w = __builtin_amdgcn_permlane32_swap(c.q[B / 2][2 * (B % 2)], c.q[B / 2][2 * (B % 2) + 1], false, \
+                                                       false);                                                   \
+    const float16_t lo = block_product(t.lo[B], w[0]);                                                           \
+    if (B > 0) add(p[1], __builtin_amdgcn_cvt_f32_fp8((int)s[1], B > 0 ? B - 1 : 0));                            \
+    const float16_t hi = block_product(t.hi[B], w[1]);                                                           \
+    add(lo, __builtin_amdgcn_cvt_f32_fp8((int)s[0], B));                                                         \
+    p[1] = hi;                                                                                                   \
+    __builtin_amdgcn_sched_barrier(0); /* more products at a time would not fit the registers */                 \
+  }
+  FEW_BLOCK(0) FEW_BLOCK(1) FEW_BLOCK(2) FEW_BLOCK(3)
+#undef FEW_BLOCK
+  add(p[1], __builtin_amdgcn_cvt_f32_fp8((int)s[1], 3));
+}
+
 // A workgroup: 32 gate and their 32 up rows of one item's expert. Its waves share
 // out the K stages, and their sums meet in LDS in the waves' order.
 __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewArgs g) {
-  __shared__ Items items;
-  __shared__ float sums[kUpWaves][2][32][36];  // [wave][gate, up][token][row]
+  __shared__ Choices::Items items;
+  __shared__ int4v r0[kUpWaves][128], r1[kUpWaves][128], r2[kUpWaves][128];  // stages' tokens, eight for each wave
+  __shared__ float sums[kUpWaves][2][32][36];                                // [wave][gate, up][token][row]
+  __shared__ int place[32];                                                  // of the item's tokens in h
   extern __shared__ int16_t ids[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  find_items(g, items, ids);
+  Choices ch;
+  ch.find(g, items, ids, nullptr);
   const int pairs = g.I / 32, a = blockIdx.x / pairs, sub = blockIdx.x % pairs;
-  if (a >= items.before[256]) return;
-  const int item = item_at(items, a, (2 * g.L + 31) / 32);
-  const int e = item >> 1, t = (item & 1) * 32 + (lane & 31), j = choice_of(g, ids, e, t);
-  const uint64_t chose = __ballot(j >= 0);
-  const int some = __builtin_ctzll(chose) + (item & 1) * 32;  // lanes without a token repeat one
-  const int stages = g.H / 128;
+  if (a >= ch.count()) return;
+  const int item = ch.item(a), e = item >> 1, stages = g.H / 128;
+  const Mine m = tokens_of(ch, item);
   const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(g.x, (uint32_t)(g.T * g.H * 2));
   const int matrix = 2 * pairs * stages * kFewChunk, from = sub * stages * kFewChunk, up = pairs * stages * kFewChunk;
   const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(g.w1 + (size_t)e * matrix, (uint32_t)matrix);
-  const int at_x = (j >= 0 ? t : some) * g.H * 2 + 128 * (lane >> 5);
-  float16_t acc[2];
-#pragma unroll
-  for (int v = 0; v < 16; ++v) acc[0][v] = acc[1][v] = 0.0f;
-  struct Stage {
-    Chunk gate, up;
-    Tokens tok;
-  } st[kUpDepth];
-  auto load = [&](int s, Stage& to) {
+  constexpr int W = kUpWaves;
+  Chunk gate[3], ups[3];
+  auto load_w = [&](int s, int d) {
     const bool in = s < stages;
     const int at = in ? from + s * kFewChunk : 0;
-    to.gate.load(rw, at, lane, in);
-    to.up.load(rw, at + up, lane, in);
-    to.tok.load(rx, at_x, in ? s * 256 : 0, in);
+    gate[d].load(rw, at, lane, in);
+    ups[d].load(rw, at + up, lane, in);
   };
-  auto compute = [&](const Stage& it) {
-    multiply(it.gate, it.tok, acc[0]);
-    multiply(it.up, it.tok, acc[1]);
-  };
+  const int n = __builtin_amdgcn_readfirstlane(m.n);
+  if (n <= 8) {
+    const auto body = [&](auto ng) {
+      constexpr int NG = decltype(ng)::value;
+      FewLoad tok;
+      tok.init(m.t * g.H * 2, n);
+      const int r = min(lane & 31, n - 1);
+      float4_t acc[2] = {float4_t{0, 0, 0, 0}, float4_t{0, 0, 0, 0}};
+      const auto slot = [&](int d) { return d == 0 ? r0[wave] : d == 1 ? r1[wave] : r2[wave]; };
+      auto load = [&](int s, int d) {
+        tok.template load<NG>(rx, slot(d), s < stages ? s * 256 : 0, s < stages);
+        load_w(s, d);
+      };
+      auto compute = [&](int d) {
+        FewTokens t;
+        t.read(slot(d), r);
+        multiply(gate[d], t, acc[0]);
+        multiply(ups[d], t, acc[1]);
+      };
+      load(wave, 0);
+      load(wave + W, 1);
+      int s = wave;
+      for (; s + 2 * W < stages; s += 3 * W) {
 #pragma unroll
-  for (int d = 0; d < kUpDepth - 1; ++d) load(wave + d * kUpWaves, st[d]);
-  int s = wave;
-  for (; s + (kUpDepth - 1) * kUpWaves < stages; s += kUpDepth * kUpWaves) {
+        for (int d = 0; d < 3; ++d) {
+          load(s + (d + 2) * W, (d + 2) % 3);
+          compute(d);
+        }
+      }
+      if (s < stages) compute(0);
+      if (s + W < stages) compute(1);
 #pragma unroll
-    for (int d = 0; d < kUpDepth; ++d) {
-      load(s + (d + kUpDepth - 1) * kUpWaves, st[(d + kUpDepth - 1) % kUpDepth]);
-      compute(st[d]);
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[wave][p][4 * (lane >> 5) + i][lane & 31] = acc[p][i];
+    };
+    if (n <= 4)
+      body(std::integral_constant<int, 1>());
+    else
+      body(std::integral_constant<int, 2>());
+  } else {
+    const int at_x = m.t * g.H * 2 + 128 * (lane >> 5);
+    Tokens tok[2];
+    float16_t acc[2];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[0][v] = acc[1][v] = 0.0f;
+    auto load_x = [&](int s, int d) { tok[d].load(rx, at_x, s < stages ? s * 256 : 0, s < stages); };
+    auto step = [&](int s, int d) {
+      load_x(s + (d + 1) * W, (d + 1) % 2);
+      load_w(s + (d + 2) * W, (d + 2) % 3);
+      multiply(gate[d % 3], tok[d % 2], acc[0]);
+      multiply(ups[d % 3], tok[d % 2], acc[1]);
+    };
+    load_w(wave, 0);
+    load_x(wave, 0);
+    load_w(wave + W, 1);
+    int s = wave;
+    for (; s + 5 * W < stages; s += 6 * W) {
+#pragma unroll
+      for (int d = 0; d < 6; ++d) step(s, d);
     }
+#pragma unroll
+    for (int d = 0; d < 5; ++d) {
+      if (s + d * W >= stages) break;
+      step(s, d);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4_t*>(&sums[wave][p][lane & 31][8 * q + 4 * (lane >> 5)]) =
+            float4_t{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]};
   }
-#pragma unroll
-  for (int d = 0; d < kUpDepth - 1; ++d)
-    if (s + d * kUpWaves < stages) compute(st[d]);
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<float4_t*>(&sums[wave][p][lane & 31][8 * q + 4 * (lane >> 5)]) =
-          float4_t{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]};
+  if (threadIdx.x < 32) place[threadIdx.x] = m.j >= 0 ? m.t * g.k + m.j : -1;
   __syncthreads();
-  const int token = threadIdx.x >> 3, row = (threadIdx.x & 7) * 4;
-  const int tt = (item & 1) * 32 + token, jj = choice_of(g, ids, e, tt);
-  if (jj < 0) return;
-  float4_t gate = float4_t{0, 0, 0, 0}, ups = float4_t{0, 0, 0, 0};
+  const int token = threadIdx.x >> 3, row = (threadIdx.x & 7) * 4, slot = place[token];
+  if (slot < 0) return;
+  float4_t g4 = float4_t{0, 0, 0, 0}, u4 = float4_t{0, 0, 0, 0};
 #pragma unroll
   for (int v = 0; v < kUpWaves; ++v) {
-    gate += *reinterpret_cast<const float4_t*>(&sums[v][0][token][row]);
-    ups += *reinterpret_cast<const float4_t*>(&sums[v][1][token][row]);
+    g4 += *reinterpret_cast<const float4_t*>(&sums[v][0][token][row]);
+    u4 += *reinterpret_cast<const float4_t*>(&sums[v][1][token][row]);
   }
   const float ag = g.dual ? g.gs1[2 * e] : g.gs1[e], au = g.dual ? g.gs1[2 * e + 1] : ag;
   float o[4];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) o[v] = silu_mul(ag * gate[v], au * ups[v]);
-  *reinterpret_cast<uint2*>(g.h + ((size_t)tt * g.k + jj) * g.I + sub * 32 + row) =
+  for (int v = 0; v < 4; ++v) o[v] = silu_mul(ag * g4[v], au * u4[v]);
+  *reinterpret_cast<uint2*>(g.h + (size_t)slot * g.I + sub * 32 + row) =
       make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
 }
 
 // A workgroup: 32 rows of the down weights of every item. Its waves take equal
 // runs of the (item, K stage) sequence; each adds what its items give, times
 // their weights, to a tile of its own in LDS, and the tiles are added in the
-// waves' order.
+// waves' order. RING: items of up to eight tokens go through LDS (five stages of
+// eight tokens for each wave, where that fits beside the tiles).
+template <bool RING>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
-  __shared__ Items items;
+  constexpr int W = kDownWaves, PITCH = kDownPitch, D = kDownDepth;
+  __shared__ Choices::Items items;
+  __shared__ int4v r0[RING ? W : 1][128], r1[RING ? W : 1][128], r2[RING ? W : 1][128], r3[RING ? W : 1][128], r4[RING ? W : 1][128];
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  constexpr int PITCH = 36;
-  float* const tiles = lds;                                             // [wave][T][PITCH]
-  float* const weight = lds + kDownWaves * g.T * PITCH;                 // [T][k]
-  int16_t* const ids = reinterpret_cast<int16_t*>(weight + g.T * g.k);  // [T][k]
-  for (int i = threadIdx.x; i < kDownWaves * g.T * PITCH; i += 64 * kDownWaves) tiles[i] = 0.0f;
-  for (int i = threadIdx.x; i < g.T * g.k; i += 64 * kDownWaves) weight[i] = g.weight[i];
-  find_items(g, items, ids);
+  float* const tiles = lds;                                              // [wave][T][PITCH]
+  float* const weights = lds + W * g.T * PITCH;                          // [T][k]
+  int16_t* const ids = reinterpret_cast<int16_t*>(weights + g.T * g.k);  // [T][k]
+  for (int i = lane; i < g.T * PITCH; i += 64) tiles[wave * g.T * PITCH + i] = 0.0f;
+  Choices ch;
+  ch.find(g, items, ids, weights);
   float* const mine = tiles + wave * g.T * PITCH;
   const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(g.h, (uint32_t)(g.T * g.k * g.I * 2));
-  const int stages = g.I / 128, words = (2 * g.L + 31) / 32;
-  const int64_t total = (int64_t)items.before[256] * stages;
-  int64_t u = total * wave / kDownWaves;
-  const int64_t end = total * (wave + 1) / kDownWaves;
+  const int stages = g.I / 128, total = ch.count() * stages;  // at most 4096 items of 512 stages
+  const int end = total * (wave + 1) / W;
+  int u = total * wave / W;
   while (u < end) {
-    const int a = (int)(u / stages), s0 = (int)(u - (int64_t)a * stages);
-    const int s1 = (int)min((int64_t)stages, s0 + (end - u));
+    const int a = u / stages, s0 = u - a * stages, s1 = min(stages, s0 + end - u);
     u += s1 - s0;
-    const int item = item_at(items, a, words);
-    const int e = item >> 1, t = (item & 1) * 32 + (lane & 31), j = choice_of(g, ids, e, t);
-    const uint64_t chose = __ballot(j >= 0);
-    const int first = __builtin_ctzll(chose);
-    const int row = j >= 0 ? t * g.k + j : -1, some = __shfl(row, first, 64);
+    const int item = ch.item(a), e = item >> 1;
+    const Mine m = tokens_of(ch, item);
+    const float wt = ch.weight(item, m.t, m.j), gs = g.gs2[e];
+    const int row = m.t * g.k + m.j, first = __builtin_amdgcn_readfirstlane(row);
     const int matrix = (g.H / 32) * stages * kFewChunk, from = (int)blockIdx.x * stages * kFewChunk;
     const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(g.w2 + (size_t)e * matrix, (uint32_t)matrix);
-    const int at_h = (row >= 0 ? row : some) * g.I * 2 + 128 * (lane >> 5);
-    float16_t acc;
+    const int n = __builtin_amdgcn_readfirstlane(m.n);
+    if (RING && n <= 8) {
+      const auto body = [&](auto ng) {
+        constexpr int NG = decltype(ng)::value;
+        FewLoad tok;
+        tok.init(row * g.I * 2, n);
+        const int r = min(lane & 31, n - 1);
+        float4_t acc = float4_t{0, 0, 0, 0};
+        Chunk c[D];
+        const auto slot = [&](int d) { return d == 0 ? r0[wave] : d == 1 ? r1[wave] : d == 2 ? r2[wave] : d == 3 ? r3[wave] : r4[wave]; };
+        auto load = [&](int s, int d) {
+          tok.template load<NG>(rh, slot(d), s < s1 ? s * 256 : 0, s < s1);
+          c[d].load(rw, s < s1 ? from + s * kFewChunk : 0, lane, s < s1);
+        };
+        auto compute = [&](int d) {
+          FewTokens t;
+          t.read(slot(d), r);
+          multiply(c[d], t, acc);
+        };
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
-    struct Stage {
-      Chunk c;
-      Tokens tok;
-    } st[kDownDepth];
-    auto load = [&](int s, Stage& to) {
-      const bool in = s < s1;
-      to.c.load(rw, in ? from + s * kFewChunk : 0, lane, in);
-      to.tok.load(rh, at_h, in ? s * 256 : 0, in);
-    };
+        for (int d = 0; d + 1 < D; ++d) load(s0 + d, d);
+        int s = s0;
+        for (; s + D <= s1; s += D) {
 #pragma unroll
-    for (int d = 0; d < kDownDepth - 1; ++d) load(s0 + d, st[d]);
-    int s = s0;
-    for (; s + kDownDepth <= s1; s += kDownDepth) {
+          for (int d = 0; d < D; ++d) {
+            load(s + d + D - 1, (d + D - 1) % D);
+            compute(d);
+          }
+        }
 #pragma unroll
-      for (int d = 0; d < kDownDepth; ++d) {
-        load(s + d + kDownDepth - 1, st[(d + kDownDepth - 1) % kDownDepth]);
-        multiply(st[d].c, st[d].tok, acc);
+        for (int d = 0; d + 1 < D; ++d)
+          if (s + d < s1) compute(d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = 4 * (lane >> 5) + i;  // the item's p-th token, which lane p knows
+          const float pw = __shfl(wt, p, 64);
+          const int pt = __shfl(m.t, p, 64);
+          if (p < n) mine[pt * PITCH + (lane & 31)] += pw * (gs * acc[i]);
+        }
+      };
+      if (n <= 4)
+        body(std::integral_constant<int, 1>());
+      else
+        body(std::integral_constant<int, 2>());
+    } else {
+      const int at_h = (m.j >= 0 ? row : first) * g.I * 2 + 128 * (lane >> 5);
+      float16_t acc;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+      Chunk c[3];
+      Tokens tok[2];
+      auto load_w = [&](int s, int d) { c[d].load(rw, s < s1 ? from + s * kFewChunk : 0, lane, s < s1); };
+      auto load_h = [&](int s, int d) { tok[d].load(rh, at_h, s < s1 ? s * 256 : 0, s < s1); };
+      auto step = [&](int s, int d) {
+        load_h(s + d + 1, (d + 1) % 2);
+        load_w(s + d + 2, (d + 2) % 3);
+        multiply(c[d % 3], tok[d % 2], acc);
+      };
+      load_w(s0, 0);
+      load_h(s0, 0);
+      load_w(s0 + 1, 1);
+      int s = s0;
+      for (; s + 6 <= s1; s += 6) {
+#pragma unroll
+        for (int d = 0; d < 6; ++d) step(s, d);
       }
-    }
 #pragma unroll
-    for (int d = 0; d < kDownDepth - 1; ++d)
-      if (s + d < s1) multiply(st[d].c, st[d].tok, acc);
-    if (j >= 0) {  // a token that lists an expert twice has both weights
-      float wt = 0.0f;
-      for (int i = j; i < g.k; ++i) wt += ids[t * g.k + i] == e ? weight[t * g.k + i] : 0.0f;
-      const float gs = g.gs2[e];
+      for (int d = 0; d < 5; ++d) {
+        if (s + d >= s1) break;
+        step(s, d);
+      }
+      if (m.j >= 0) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float4_t* at = reinterpret_cast<float4_t*>(mine + t * PITCH + 8 * q + 4 * (lane >> 5));
-        float4_t v = *at;
+        for (int q = 0; q < 4; ++q) {
+          float4_t* at = reinterpret_cast<float4_t*>(mine + m.t * PITCH + 8 * q + 4 * (lane >> 5));
+          float4_t v = *at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += wt * (gs * acc[4 * q + i]);
-        *at = v;
+          for (int i = 0; i < 4; ++i) v[i] += wt * (gs * acc[4 * q + i]);
+          *at = v;
+        }
       }
     }
     wave_lds_fence();
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < g.T * 8; i += 64 * kDownWaves) {
+  for (int i = threadIdx.x; i < g.T * 8; i += 64 * W) {
     const int t = i >> 3, row = (i & 7) * 4;
     float4_t o = float4_t{0, 0, 0, 0};
 #pragma unroll
-    for (int v = 0; v < kDownWaves; ++v) o += *reinterpret_cast<const float4_t*>(tiles + (v * g.T + t) * PITCH + row);
+    for (int v = 0; v < W; ++v) o += *reinterpret_cast<const float4_t*>(tiles + (v * g.T + t) * PITCH + row);
     const size_t at = (size_t)t * g.H + blockIdx.x * 32 + row;
     typedef OutVec<4>::type vec_t;
     vec_t add = vec_t(0u);
@@ -356,8 +564,12 @@ extern "C" int nvfp4_moe_forward_few(const nvfp4_moe_weights* w, const void* x_b
   hipLaunchKernelGGL(few_up_kernel, dim3((unsigned)items * (w->inter / 32)), dim3(64 * kUpWaves),
                      (size_t)(T * k * 2 + 15) / 16 * 16, (hipStream_t)stream, g);
   NVFP4_CHECK_LAUNCH();
-  const size_t lds = (size_t)kDownWaves * T * 36 * 4 + (size_t)T * k * 6;
-  hipLaunchKernelGGL(few_down_kernel, dim3(w->hidden / 32), dim3(64 * kDownWaves), lds, (hipStream_t)stream, g);
+  const dim3 down(w->hidden / 32), threads(64 * kDownWaves);
+  const size_t lds = (size_t)kDownWaves * T * kDownPitch * 4 + (size_t)T * k * 6;
+  if (lds + kDownWaves * kDownDepth * 2048 + sizeof(Choices::Items) <= kLdsBytes)
+    hipLaunchKernelGGL(few_down_kernel<true>, down, threads, lds, (hipStream_t)stream, g);
+  else  // many choices for many tokens
+    hipLaunchKernelGGL(few_down_kernel<false>, down, threads, lds, (hipStream_t)stream, g);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
 }
