@@ -576,7 +576,7 @@ int nvfp4_moe_forward_static(const nvfp4_moe_weights* w, const void* x_bf16, int
                              const float* gs_in, void* out_bf16, void* ws, size_t ws_bytes, void* stream);
 
 /* The layer for at most nvfp4_moe_few_max_tokens() = 64 tokens, in two launches
- * on the same weights, with activations as they are (BF16, not quantized):
+ * (three for narrow layers) on the same weights, with activations as they are (BF16, not quantized):
  *   h_e    = RN_bf16(silu(G) * U), G and U = w1_gs[e] (gate and up) times the
  *            products of x[t] with the gate and up rows of W1_e
  *   out[t] = RN_bf16(sum over the experts e of token t on this rank of
@@ -586,7 +586,8 @@ int nvfp4_moe_forward_static(const nvfp4_moe_weights* w, const void* x_bf16, int
  * NULL. Ids outside [expert_start, expert_start + L) take no part. The order of
  * the sums depends on what the tokens chose, so a call repeats bit for bit, but
  * a token's last bits may differ with the others in the batch.
- * ws: at least nvfp4_moe_few_ws_bytes(...) bytes (h). k <= 64, L <= 4096,
+ * ws: at least nvfp4_moe_few_ws_bytes(...) bytes; h comes first, BF16 [T, k, I],
+ * a row for each choice on this rank (the first of an expert listed twice). k <= 64, L <= 4096,
  * H % 128 == 0, I % 128 == 0, 2I*H*9/16 below 2^31.
  */
 int32_t nvfp4_moe_few_max_tokens(void);

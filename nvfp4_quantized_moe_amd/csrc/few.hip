@@ -1,4 +1,5 @@
-// The expert layer for a few tokens, in two launches over the packed NVFP4
+// The expert layer for a few tokens, in two launches (a third joins parts of the
+// down products where the layer is narrow) over the packed NVFP4
 // weights of the layer (moe_forward's, nvfp4_pack_weights):
 //   h[t, e]  = bf16(silu(gs_g W_gate x[t]) * (gs_u W_up x[t]))  for the experts e of token t on this rank
 //   out[t]   = bf16(sum_e w[t, e] gs_2 W_down h[t, e] [+ add[t]])
@@ -8,8 +9,8 @@
 // its expert in the choices themselves, and every wave streams weight chunks
 // from memory to registers and multiplies them there.
 //
-// What bounds the rest is instructions and the loads of the tokens, so an item of
-// up to eight tokens (most are, in a decode step) is handled so that each weight
+// What bounds the rest is instructions and the loads of the tokens, so an expert
+// with up to eight tokens (most, in a decode step) is handled so that each weight
 // costs least. An E2M1 code is exact in BF16, and a block of 16 shares one E4M3
 // scale: a matrix step covers one block, MFMA 32x32x16 BF16 with the tokens as
 // first operand and 32 weight rows as second, from codes turned to BF16 two at a
@@ -20,7 +21,9 @@
 // that pass no register, one for four tokens: read by every lane from memory they
 // kept the address unit busy for longer than the weights. More tokens are handled
 // by scaled weights and direct loads, as their own multiply-adds would cost more.
-// (64 tokens on 48 x 7168 x 2048: 105 + 82 us that way for all, MEASURED.)
+// (64 tokens on 48 x 7168 x 2048, up and down: 102 + 61 us, all that way 105 + 82;
+// with an expert's tokens in one place, not in those of a half of the batch, whose
+// weights were read again: 79 + 46, 5.0 and 4.4 TB/s.)
 //
 // A packed chunk's lane halves hold 64 of 128 K elements each. A swap between the
 // halves brings the two words of a block side by side.
@@ -39,7 +42,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kFewMaxT = 64, kFewMaxK = 64, kFewMaxL = 4096;
 constexpr int kFewChunk = 2304, kFewScales = 2048;  // bytes of 32 rows x 128 columns, and where their scales start
-constexpr int kUpWaves = 4, kDownWaves = 8, kDownDepth = 5, kDownPitch = 36;
+constexpr int kUpWaves = 4, kDownWaves = 8, kDownPitch = 36;
 constexpr size_t kLdsBytes = 160 * 1024;
 
 struct FewArgs {
@@ -49,36 +52,42 @@ struct FewArgs {
   const uint8_t *w1, *w2;
   const float *gs1, *gs2;
   uint16_t* h;           // BF16 [T * k, I], row t k + j of the first j with that expert
+  float* partial;        // [parts][T, H], with more than one part
   const uint16_t* add;   // BF16 [T, H] or NULL
   uint16_t* out;
-  int T, k, L, start, H, I, dual;
+  int T, k, L, start, H, I, dual, parts;
 };
 
+__device__ __forceinline__ void few_store(const FewArgs& g, size_t at, float4_t o) {
+  typedef OutVec<4>::type vec_t;
+  vec_t add = vec_t(0u);
+  if (g.add) add = *reinterpret_cast<const vec_t*>(g.add + at);
+  const float f[4] = {o[0], o[1], o[2], o[3]};
+  *reinterpret_cast<vec_t*>(g.out + at) = add_and_round<4>(f, add);
+}
 __device__ __forceinline__ int local_expert(const FewArgs& g, int id) {
   const int64_t e = (int64_t)id - g.start;
   return e >= 0 && e < g.L ? (int)e : -1;
 }
 
-// An item is an expert and 32 tokens (the lower or the upper half of the batch)
-// of which at least one chose it. Every workgroup finds the items in the choices
-// by itself: a bitmap in LDS has bit 2 e + half for each, and they are taken in
-// ascending order.
+// The experts that some token chose, as every workgroup finds them in the choices
+// by itself: a bitmap in LDS, taken in ascending order.
 struct Choices {
-  struct Items {
-    uint32_t bits[2 * kFewMaxL / 32];
-    int before[2 * kFewMaxL / 32 + 1];  // items in the words before, and in all
+  struct Found {
+    uint32_t bits[kFewMaxL / 32];
+    int before[kFewMaxL / 32 + 1];  // experts in the words before, and in all
   };
-  const Items* s;
-  const int16_t* ids;   // the choices as local experts, -1: not here
+  const Found* s;
+  const int16_t* ids;  // the choices as local experts, -1: not here
   const float* weights;
   int k, T, words;
-  __device__ __forceinline__ void find(const FewArgs& g, Items& to, int16_t* local, float* weights_lds) {
+  __device__ __forceinline__ void find(const FewArgs& g, Found& to, int16_t* local, float* weights_lds) {
     s = &to;
     ids = local;
     weights = weights_lds;
     k = g.k;
     T = g.T;
-    words = (2 * g.L + 31) / 32;
+    words = (g.L + 31) / 32;
     const int n = T * k;
     for (int i = threadIdx.x; i < words; i += blockDim.x) to.bits[i] = 0;
     __syncthreads();
@@ -86,33 +95,25 @@ struct Choices {
       const int e = local_expert(g, g.ids[i]);
       local[i] = (int16_t)e;
       if (weights_lds) weights_lds[i] = g.weight[i];
-      if (e >= 0) {
-        const int b = 2 * e + (i >= 32 * k ? 1 : 0);
-        atomicOr(&to.bits[b >> 5], 1u << (b & 31));
-      }
+      if (e >= 0) atomicOr(&to.bits[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    if (threadIdx.x < 64) {  // four words to a lane, at most 256
-      int sum = 0, c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = threadIdx.x * 4 + i;
-        c[i] = sum;
-        sum += at < words ? __popc(to.bits[at]) : 0;
-      }
+    if (threadIdx.x < 64) {  // two words to a lane, at most 128
+      const int at = threadIdx.x * 2;
+      const int c = at < words ? __popc(to.bits[at]) : 0, sum = c + (at + 1 < words ? __popc(to.bits[at + 1]) : 0);
       int scan = sum;
       for (int o = 1; o < 64; o <<= 1) {
         const int v = __shfl_up(scan, o, 64);
         if ((int)threadIdx.x >= o) scan += v;
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) to.before[threadIdx.x * 4 + i] = scan - sum + c[i];
-      if (threadIdx.x == 63) to.before[256] = scan;
+      to.before[at] = scan - sum;
+      to.before[at + 1] = scan - sum + c;
+      if (threadIdx.x == 63) to.before[128] = scan;
     }
     __syncthreads();
   }
-  __device__ __forceinline__ int count() const { return s->before[256]; }
-  __device__ __forceinline__ int item(int a) const {
+  __device__ __forceinline__ int count() const { return s->before[128]; }
+  __device__ __forceinline__ int expert(int a) const {  // the a-th of them
     int lo = 0, hi = words - 1;  // the last word with before <= a
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -122,40 +123,44 @@ struct Choices {
     for (int i = a - s->before[lo]; i > 0; --i) b &= b - 1;
     return __builtin_amdgcn_readfirstlane(lo * 32 + __ffs((int)b) - 1);
   }
-  // the first choice of token t that is the item's expert (-1: none)
-  __device__ __forceinline__ int choice(int item, int t) const {
+  // the first choice of token t that is expert e (-1: none)
+  __device__ __forceinline__ int choice(int e, int t) const {
     int first = -1;
     if (t < T)
-      for (int j = k - 1; j >= 0; --j) first = ids[t * k + j] == item >> 1 ? j : first;
+      for (int j = k - 1; j >= 0; --j) first = ids[t * k + j] == e ? j : first;
     return first;
   }
   // the weight of token t on it, of which j is the first choice: a token that
   // lists an expert twice has both weights
-  __device__ __forceinline__ float weight(int item, int t, int j) const {
+  __device__ __forceinline__ float weight(int e, int t, int j) const {
     float sum = 0.0f;
     if (j >= 0)
-      for (int i = j; i < k; ++i) sum += ids[t * k + i] == item >> 1 ? weights[t * k + i] : 0.0f;
+      for (int i = j; i < k; ++i) sum += ids[t * k + i] == e ? weights[t * k + i] : 0.0f;
     return sum;
   }
 };
 
-// An item's tokens in order: lane p (and p + 32) holds the p-th; those from n on
-// the first again, with j = -1.
+// An expert's n tokens in order: lane p holds the p-th (and its first choice that is
+// the expert); lanes from n on the first again, with j = -1.
 struct Mine {
   int n, t, j;
 };
-__device__ __forceinline__ Mine tokens_of(const Choices& ch, int item) {
-  const int lane = threadIdx.x & 63, t = (item & 1) * 32 + (lane & 31), j = ch.choice(item, t);
-  const uint32_t chose = (uint32_t)__ballot(j >= 0), below = (1u << (lane & 31)) - 1u;
+__device__ __forceinline__ Mine tokens_of(const Choices& ch, int e) {
+  const int lane = threadIdx.x & 63, j = ch.choice(e, lane);
+  const uint64_t chose = __ballot(j >= 0), below = (1ull << lane) - 1;
   Mine m;
-  m.n = __popc(chose);
+  m.n = __popcll(chose);
   // each lane hands its token to the lane of its rank, those without one behind
-  const int rank = j >= 0 ? __popc(chose & below) : m.n + __popc(~chose & below);
-  const int both = __builtin_amdgcn_ds_permute((rank + (lane & 32)) * 4, t << 8 | (j & 255));
-  const bool there = (lane & 31) < m.n;
-  m.t = (there ? both : __builtin_amdgcn_readfirstlane(both)) >> 8;
-  m.j = there ? both & 255 : -1;
+  const int rank = j >= 0 ? __popcll(chose & below) : m.n + __popcll(~chose & below);
+  const int both = __builtin_amdgcn_ds_permute(rank * 4, lane << 8 | (j & 255));
+  m.t = (lane < m.n ? both : __builtin_amdgcn_readfirstlane(both)) >> 8;
+  m.j = lane < m.n ? both & 255 : -1;
   return m;
+}
+// 32 of them, from `from` on, in lanes 0..31 and again in 32..63.
+__device__ __forceinline__ Mine part_of(const Mine& m, int from) {
+  const int p = from + (int)(threadIdx.x & 31);
+  return {m.n, __shfl(m.t, p, 64), __shfl(m.j, p, 64)};
 }
 
 // Loads of a wave's stages. `in` says whether the stage exists: where it does
@@ -275,133 +280,230 @@ __device__ __forceinline__ void multiply(const Chunk& c, const FewTokens& t, flo
   add(p[1], __builtin_amdgcn_cvt_f32_fp8((int)s[1], 3));
 }
 
-// A workgroup: 32 gate and their 32 up rows of one item's expert. Its waves share
-// out the K stages, and their sums meet in LDS in the waves' order.
+// Where the tokens of a stage wait in LDS, eight for each wave; an array for each
+// stage of the ring, so that the compiler can tell their loads apart.
+template <int W>
+struct alignas(16) Ring {
+  int4v at[W][128];
+};
+
+// The sums of 32 gate and the 32 up rows over a wave's K stages, left in
+// sums[gate, up][token][row].
+struct UpStages {
+  __amdgpu_buffer_rsrc_t w, x;
+  int from, up, stages;  // bytes of the gate rows' first chunk, from there to the up rows', K stages
+  int lane, wave;
+  Chunk gate[3], ups[3];
+  __device__ __forceinline__ void load_w(int s, int d) {
+    const bool in = s < stages;
+    const int at = in ? from + s * kFewChunk : 0;
+    gate[d].load(w, at, lane, in);
+    ups[d].load(w, at + up, lane, in);
+  }
+};
+template <int NG>
+__device__ __forceinline__ void up_few(UpStages& u, int offset, int n, int4v* r0, int4v* r1, int4v* r2, float (*sums)[32][36]) {
+  constexpr int W = kUpWaves;
+  FewLoad tok;
+  tok.init(offset, n);
+  const int r = min(u.lane & 31, n - 1);
+  float4_t acc[2] = {float4_t{0, 0, 0, 0}, float4_t{0, 0, 0, 0}};
+  const auto slot = [&](int d) { return d == 0 ? r0 : d == 1 ? r1 : r2; };
+  const auto load = [&](int s, int d) {
+    tok.template load<NG>(u.x, slot(d), s < u.stages ? s * 256 : 0, s < u.stages);
+    u.load_w(s, d);
+  };
+  const auto compute = [&](int d) {
+    FewTokens t;
+    t.read(slot(d), r);
+    multiply(u.gate[d], t, acc[0]);
+    multiply(u.ups[d], t, acc[1]);
+  };
+  load(u.wave, 0);
+  load(u.wave + W, 1);
+  int s = u.wave;
+  for (; s + 2 * W < u.stages; s += 3 * W) {
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      load(s + (d + 2) * W, (d + 2) % 3);
+      compute(d);
+    }
+  }
+  if (s < u.stages) compute(0);
+  if (s + W < u.stages) compute(1);
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[p][4 * (u.lane >> 5) + i][u.lane & 31] = acc[p][i];
+}
+__device__ __forceinline__ void up_many(UpStages& u, int offset, float (*sums)[32][36]) {
+  constexpr int W = kUpWaves;
+  Tokens tok[2];
+  float16_t acc[2];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[0][v] = acc[1][v] = 0.0f;
+  const auto load_x = [&](int s, int d) { tok[d].load(u.x, offset, s < u.stages ? s * 256 : 0, s < u.stages); };
+  // the tokens of the next stage before the weights of the one behind it: loads
+  // are waited for in order
+  const auto step = [&](int s, int d) {
+    load_x(s + W, (d + 1) % 2);
+    u.load_w(s + 2 * W, (d + 2) % 3);
+    multiply(u.gate[d % 3], tok[d % 2], acc[0]);
+    multiply(u.ups[d % 3], tok[d % 2], acc[1]);
+  };
+  u.load_w(u.wave, 0);
+  load_x(u.wave, 0);
+  u.load_w(u.wave + W, 1);
+  int s = u.wave;
+  for (; s + 5 * W < u.stages; s += 6 * W) {
+#pragma unroll
+    for (int d = 0; d < 6; ++d) step(s + d * W, d);
+  }
+#pragma unroll
+  for (int d = 0; d < 5; ++d) {
+    if (s + d * W >= u.stages) break;
+    step(s + d * W, d);
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4_t*>(&sums[p][u.lane & 31][8 * q + 4 * (u.lane >> 5)]) =
+          float4_t{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]};
+}
+
+// A workgroup: 32 gate and their 32 up rows of one expert. Its waves share out the
+// K stages, and their sums meet in LDS in the waves' order. More than 32 tokens are
+// two parts, one after the other.
 __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewArgs g) {
-  __shared__ Choices::Items items;
-  __shared__ int4v r0[kUpWaves][128], r1[kUpWaves][128], r2[kUpWaves][128];  // stages' tokens, eight for each wave
-  __shared__ float sums[kUpWaves][2][32][36];                                // [wave][gate, up][token][row]
-  __shared__ int place[32];                                                  // of the item's tokens in h
+  __shared__ Choices::Found found;
+  __shared__ Ring<kUpWaves> r0, r1, r2;
+  __shared__ float sums[kUpWaves][2][32][36];  // [wave][gate, up][token][row]
+  __shared__ int place[32];                    // of the part's tokens in h
   extern __shared__ int16_t ids[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Choices ch;
-  ch.find(g, items, ids, nullptr);
+  ch.find(g, found, ids, nullptr);
   const int pairs = g.I / 32, a = blockIdx.x / pairs, sub = blockIdx.x % pairs;
   if (a >= ch.count()) return;
-  const int item = ch.item(a), e = item >> 1, stages = g.H / 128;
-  const Mine m = tokens_of(ch, item);
-  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(g.x, (uint32_t)(g.T * g.H * 2));
-  const int matrix = 2 * pairs * stages * kFewChunk, from = sub * stages * kFewChunk, up = pairs * stages * kFewChunk;
-  const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(g.w1 + (size_t)e * matrix, (uint32_t)matrix);
-  constexpr int W = kUpWaves;
-  Chunk gate[3], ups[3];
-  auto load_w = [&](int s, int d) {
-    const bool in = s < stages;
-    const int at = in ? from + s * kFewChunk : 0;
-    gate[d].load(rw, at, lane, in);
-    ups[d].load(rw, at + up, lane, in);
-  };
+  const int e = ch.expert(a), stages = g.H / 128, matrix = 2 * pairs * stages * kFewChunk;
+  const Mine m = tokens_of(ch, e);
   const int n = __builtin_amdgcn_readfirstlane(m.n);
-  if (n <= 8) {
-    const auto body = [&](auto ng) {
-      constexpr int NG = decltype(ng)::value;
-      FewLoad tok;
-      tok.init(m.t * g.H * 2, n);
-      const int r = min(lane & 31, n - 1);
-      float4_t acc[2] = {float4_t{0, 0, 0, 0}, float4_t{0, 0, 0, 0}};
-      const auto slot = [&](int d) { return d == 0 ? r0[wave] : d == 1 ? r1[wave] : r2[wave]; };
-      auto load = [&](int s, int d) {
-        tok.template load<NG>(rx, slot(d), s < stages ? s * 256 : 0, s < stages);
-        load_w(s, d);
-      };
-      auto compute = [&](int d) {
-        FewTokens t;
-        t.read(slot(d), r);
-        multiply(gate[d], t, acc[0]);
-        multiply(ups[d], t, acc[1]);
-      };
-      load(wave, 0);
-      load(wave + W, 1);
-      int s = wave;
-      for (; s + 2 * W < stages; s += 3 * W) {
-#pragma unroll
-        for (int d = 0; d < 3; ++d) {
-          load(s + (d + 2) * W, (d + 2) % 3);
-          compute(d);
-        }
-      }
-      if (s < stages) compute(0);
-      if (s + W < stages) compute(1);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums[wave][p][4 * (lane >> 5) + i][lane & 31] = acc[p][i];
-    };
-    if (n <= 4)
-      body(std::integral_constant<int, 1>());
-    else
-      body(std::integral_constant<int, 2>());
-  } else {
-    const int at_x = m.t * g.H * 2 + 128 * (lane >> 5);
-    Tokens tok[2];
-    float16_t acc[2];
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[0][v] = acc[1][v] = 0.0f;
-    auto load_x = [&](int s, int d) { tok[d].load(rx, at_x, s < stages ? s * 256 : 0, s < stages); };
-    auto step = [&](int s, int d) {
-      load_x(s + (d + 1) * W, (d + 1) % 2);
-      load_w(s + (d + 2) * W, (d + 2) % 3);
-      multiply(gate[d % 3], tok[d % 2], acc[0]);
-      multiply(ups[d % 3], tok[d % 2], acc[1]);
-    };
-    load_w(wave, 0);
-    load_x(wave, 0);
-    load_w(wave + W, 1);
-    int s = wave;
-    for (; s + 5 * W < stages; s += 6 * W) {
-#pragma unroll
-      for (int d = 0; d < 6; ++d) step(s, d);
-    }
-#pragma unroll
-    for (int d = 0; d < 5; ++d) {
-      if (s + d * W >= stages) break;
-      step(s, d);
-    }
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4_t*>(&sums[wave][p][lane & 31][8 * q + 4 * (lane >> 5)]) =
-            float4_t{acc[p][4 * q], acc[p][4 * q + 1], acc[p][4 * q + 2], acc[p][4 * q + 3]};
-  }
-  if (threadIdx.x < 32) place[threadIdx.x] = m.j >= 0 ? m.t * g.k + m.j : -1;
-  __syncthreads();
-  const int token = threadIdx.x >> 3, row = (threadIdx.x & 7) * 4, slot = place[token];
-  if (slot < 0) return;
-  float4_t g4 = float4_t{0, 0, 0, 0}, u4 = float4_t{0, 0, 0, 0};
-#pragma unroll
-  for (int v = 0; v < kUpWaves; ++v) {
-    g4 += *reinterpret_cast<const float4_t*>(&sums[v][0][token][row]);
-    u4 += *reinterpret_cast<const float4_t*>(&sums[v][1][token][row]);
-  }
   const float ag = g.dual ? g.gs1[2 * e] : g.gs1[e], au = g.dual ? g.gs1[2 * e + 1] : ag;
-  float o[4];
+  UpStages u;
+  u.w = buffer_rsrc(g.w1 + (size_t)e * matrix, (uint32_t)matrix);
+  u.x = buffer_rsrc(g.x, (uint32_t)(g.T * g.H * 2));
+  u.from = sub * stages * kFewChunk;
+  u.up = pairs * stages * kFewChunk;
+  u.stages = stages;
+  u.lane = lane;
+  u.wave = wave;
+  for (int part = 0; part < n; part += 32) {
+    const Mine mp = part_of(m, part);
+    if (n <= 4)
+      up_few<1>(u, m.t * g.H * 2, n, r0.at[wave], r1.at[wave], r2.at[wave], sums[wave]);
+    else if (n <= 8)
+      up_few<2>(u, m.t * g.H * 2, n, r0.at[wave], r1.at[wave], r2.at[wave], sums[wave]);
+    else
+      up_many(u, mp.t * g.H * 2 + 128 * (lane >> 5), sums[wave]);
+    if (threadIdx.x < 32) place[threadIdx.x] = mp.j >= 0 ? mp.t * g.k + mp.j : -1;
+    __syncthreads();
+    const int token = threadIdx.x >> 3, row = (threadIdx.x & 7) * 4, slot = place[token];
+    if (slot >= 0) {
+      float4_t g4 = float4_t{0, 0, 0, 0}, u4 = float4_t{0, 0, 0, 0};
 #pragma unroll
-  for (int v = 0; v < 4; ++v) o[v] = silu_mul(ag * g4[v], au * u4[v]);
-  *reinterpret_cast<uint2*>(g.h + (size_t)slot * g.I + sub * 32 + row) =
-      make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
+      for (int v = 0; v < kUpWaves; ++v) {
+        g4 += *reinterpret_cast<const float4_t*>(&sums[v][0][token][row]);
+        u4 += *reinterpret_cast<const float4_t*>(&sums[v][1][token][row]);
+      }
+      float o[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) o[v] = silu_mul(ag * g4[v], au * u4[v]);
+      *reinterpret_cast<uint2*>(g.h + (size_t)slot * g.I + sub * 32 + row) =
+          make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
+    }
+    __syncthreads();  // the next part's sums take the same place
+  }
 }
 
-// A workgroup: 32 rows of the down weights of every item. Its waves take equal
-// runs of the (item, K stage) sequence; each adds what its items give, times
-// their weights, to a tile of its own in LDS, and the tiles are added in the
-// waves' order. RING: items of up to eight tokens go through LDS (five stages of
-// eight tokens for each wave, where that fits beside the tiles).
+// A wave's run of K stages [s0, s1) of an expert's down rows.
+struct DownStages {
+  __amdgpu_buffer_rsrc_t w, h;
+  int from, s0, s1, lane;
+  __device__ __forceinline__ void load_w(Chunk& c, int s) const { c.load(w, s < s1 ? from + s * kFewChunk : 0, lane, s < s1); }
+};
+template <int NG>
+__device__ __forceinline__ float4_t down_few(const DownStages& u, int offset, int n, int4v* r0, int4v* r1, int4v* r2,
+                                             int4v* r3, int4v* r4) {
+  constexpr int D = 5;
+  FewLoad tok;
+  tok.init(offset, n);
+  const int r = min(u.lane & 31, n - 1);
+  float4_t acc = float4_t{0, 0, 0, 0};
+  Chunk c[D];
+  const auto slot = [&](int d) { return d == 0 ? r0 : d == 1 ? r1 : d == 2 ? r2 : d == 3 ? r3 : r4; };
+  const auto load = [&](int s, int d) {
+    tok.template load<NG>(u.h, slot(d), s < u.s1 ? s * 256 : 0, s < u.s1);
+    u.load_w(c[d], s);
+  };
+  const auto compute = [&](int d) {
+    FewTokens t;
+    t.read(slot(d), r);
+    multiply(c[d], t, acc);
+  };
+#pragma unroll
+  for (int d = 0; d + 1 < D; ++d) load(u.s0 + d, d);
+  int s = u.s0;
+  for (; s + D <= u.s1; s += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      load(s + d + D - 1, (d + D - 1) % D);
+      compute(d);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d + 1 < D; ++d)
+    if (s + d < u.s1) compute(d);
+  return acc;
+}
+__device__ __forceinline__ float16_t down_many(const DownStages& u, int offset) {
+  float16_t acc;
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+  Chunk c[3];
+  Tokens tok[2];
+  const auto load_h = [&](int s, int d) { tok[d].load(u.h, offset, s < u.s1 ? s * 256 : 0, s < u.s1); };
+  const auto step = [&](int s, int d) {
+    load_h(s + 1, (d + 1) % 2);
+    u.load_w(c[(d + 2) % 3], s + 2);
+    multiply(c[d % 3], tok[d % 2], acc);
+  };
+  u.load_w(c[0], u.s0);
+  load_h(u.s0, 0);
+  u.load_w(c[1], u.s0 + 1);
+  int s = u.s0;
+  for (; s + 6 <= u.s1; s += 6) {
+#pragma unroll
+    for (int d = 0; d < 6; ++d) step(s + d, d);
+  }
+#pragma unroll
+  for (int d = 0; d < 5; ++d) {
+    if (s + d >= u.s1) break;
+    step(s + d, d);
+  }
+  return acc;
+}
+
+// A workgroup: 32 rows of the down weights of every expert chosen, or one of
+// `parts` equal runs of the (expert, K stage) sequence. Its waves take equal runs;
+// each adds what its experts give, times their weights, to a tile of its own in
+// LDS, and the tiles are added in the waves' order. RING: up to eight tokens of an
+// expert go through LDS, where that fits beside the tiles.
 template <bool RING>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
-  constexpr int W = kDownWaves, PITCH = kDownPitch, D = kDownDepth;
-  __shared__ Choices::Items items;
-  __shared__ int4v r0[RING ? W : 1][128], r1[RING ? W : 1][128], r2[RING ? W : 1][128], r3[RING ? W : 1][128], r4[RING ? W : 1][128];
+  constexpr int W = kDownWaves, PITCH = kDownPitch;
+  __shared__ Choices::Found found;
+  __shared__ Ring<RING ? W : 1> r0, r1, r2, r3, r4;
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* const tiles = lds;                                              // [wave][T][PITCH]
@@ -409,100 +511,51 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
   int16_t* const ids = reinterpret_cast<int16_t*>(weights + g.T * g.k);  // [T][k]
   for (int i = lane; i < g.T * PITCH; i += 64) tiles[wave * g.T * PITCH + i] = 0.0f;
   Choices ch;
-  ch.find(g, items, ids, weights);
+  ch.find(g, found, ids, weights);
   float* const mine = tiles + wave * g.T * PITCH;
-  const __amdgpu_buffer_rsrc_t rh = buffer_rsrc(g.h, (uint32_t)(g.T * g.k * g.I * 2));
-  const int stages = g.I / 128, total = ch.count() * stages;  // at most 4096 items of 512 stages
-  const int end = total * (wave + 1) / W;
-  int u = total * wave / W;
-  while (u < end) {
-    const int a = u / stages, s0 = u - a * stages, s1 = min(stages, s0 + end - u);
-    u += s1 - s0;
-    const int item = ch.item(a), e = item >> 1;
-    const Mine m = tokens_of(ch, item);
-    const float wt = ch.weight(item, m.t, m.j), gs = g.gs2[e];
-    const int row = m.t * g.k + m.j, first = __builtin_amdgcn_readfirstlane(row);
-    const int matrix = (g.H / 32) * stages * kFewChunk, from = (int)blockIdx.x * stages * kFewChunk;
-    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(g.w2 + (size_t)e * matrix, (uint32_t)matrix);
+  const int stages = g.I / 128, matrix = (g.H / 32) * stages * kFewChunk;
+  DownStages u;
+  u.h = buffer_rsrc(g.h, (uint32_t)(g.T * g.k * g.I * 2));
+  u.from = (int)blockIdx.x * stages * kFewChunk;
+  u.lane = lane;
+  const int64_t total = (int64_t)ch.count() * stages;
+  const int run = (int)blockIdx.y * W + wave, runs = g.parts * W;
+  const int end = (int)(total * (run + 1) / runs);
+  for (int at = (int)(total * run / runs); at < end; at += u.s1 - u.s0) {
+    const int a = at / stages;
+    u.s0 = at - a * stages;
+    u.s1 = min(stages, u.s0 + end - at);
+    const int e = ch.expert(a);
+    const Mine m = tokens_of(ch, e);
     const int n = __builtin_amdgcn_readfirstlane(m.n);
+    const float gs = g.gs2[e];
+    const float wt = ch.weight(e, m.t, m.j);
+    const int row = m.t * g.k + m.j, first = __builtin_amdgcn_readfirstlane(row);
+    u.w = buffer_rsrc(g.w2 + (size_t)e * matrix, (uint32_t)matrix);
     if (RING && n <= 8) {
-      const auto body = [&](auto ng) {
-        constexpr int NG = decltype(ng)::value;
-        FewLoad tok;
-        tok.init(row * g.I * 2, n);
-        const int r = min(lane & 31, n - 1);
-        float4_t acc = float4_t{0, 0, 0, 0};
-        Chunk c[D];
-        const auto slot = [&](int d) { return d == 0 ? r0[wave] : d == 1 ? r1[wave] : d == 2 ? r2[wave] : d == 3 ? r3[wave] : r4[wave]; };
-        auto load = [&](int s, int d) {
-          tok.template load<NG>(rh, slot(d), s < s1 ? s * 256 : 0, s < s1);
-          c[d].load(rw, s < s1 ? from + s * kFewChunk : 0, lane, s < s1);
-        };
-        auto compute = [&](int d) {
-          FewTokens t;
-          t.read(slot(d), r);
-          multiply(c[d], t, acc);
-        };
+      const float4_t acc =
+          n <= 4 ? down_few<1>(u, row * g.I * 2, n, r0.at[wave], r1.at[wave], r2.at[wave], r3.at[wave], r4.at[wave])
+                 : down_few<2>(u, row * g.I * 2, n, r0.at[wave], r1.at[wave], r2.at[wave], r3.at[wave], r4.at[wave]);
 #pragma unroll
-        for (int d = 0; d + 1 < D; ++d) load(s0 + d, d);
-        int s = s0;
-        for (; s + D <= s1; s += D) {
-#pragma unroll
-          for (int d = 0; d < D; ++d) {
-            load(s + d + D - 1, (d + D - 1) % D);
-            compute(d);
-          }
-        }
-#pragma unroll
-        for (int d = 0; d + 1 < D; ++d)
-          if (s + d < s1) compute(d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int p = 4 * (lane >> 5) + i;  // the item's p-th token, which lane p knows
-          const float pw = __shfl(wt, p, 64);
-          const int pt = __shfl(m.t, p, 64);
-          if (p < n) mine[pt * PITCH + (lane & 31)] += pw * (gs * acc[i]);
-        }
-      };
-      if (n <= 4)
-        body(std::integral_constant<int, 1>());
-      else
-        body(std::integral_constant<int, 2>());
+      for (int i = 0; i < 4; ++i) {
+        const int p = 4 * (lane >> 5) + i;  // the expert's p-th token, which lane p knows
+        const float pw = __shfl(wt, p, 64);
+        const int pt = __shfl(m.t, p, 64);
+        if (p < n) mine[pt * PITCH + (lane & 31)] += pw * (gs * acc[i]);
+      }
     } else {
-      const int at_h = (m.j >= 0 ? row : first) * g.I * 2 + 128 * (lane >> 5);
-      float16_t acc;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
-      Chunk c[3];
-      Tokens tok[2];
-      auto load_w = [&](int s, int d) { c[d].load(rw, s < s1 ? from + s * kFewChunk : 0, lane, s < s1); };
-      auto load_h = [&](int s, int d) { tok[d].load(rh, at_h, s < s1 ? s * 256 : 0, s < s1); };
-      auto step = [&](int s, int d) {
-        load_h(s + d + 1, (d + 1) % 2);
-        load_w(s + d + 2, (d + 2) % 3);
-        multiply(c[d % 3], tok[d % 2], acc);
-      };
-      load_w(s0, 0);
-      load_h(s0, 0);
-      load_w(s0 + 1, 1);
-      int s = s0;
-      for (; s + 6 <= s1; s += 6) {
-#pragma unroll
-        for (int d = 0; d < 6; ++d) step(s, d);
-      }
-#pragma unroll
-      for (int d = 0; d < 5; ++d) {
-        if (s + d >= s1) break;
-        step(s, d);
-      }
-      if (m.j >= 0) {
+      for (int part = 0; part < n; part += 32) {
+        const Mine mp = part_of(m, part);
+        const float wp = __shfl(wt, part + (lane & 31), 64);
+        const float16_t acc = down_many(u, (mp.j >= 0 ? mp.t * g.k + mp.j : first) * g.I * 2 + 128 * (lane >> 5));
+        if (mp.j < 0) continue;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          float4_t* at = reinterpret_cast<float4_t*>(mine + m.t * PITCH + 8 * q + 4 * (lane >> 5));
-          float4_t v = *at;
+          float4_t* to = reinterpret_cast<float4_t*>(mine + mp.t * PITCH + 8 * q + 4 * (lane >> 5));
+          float4_t v = *to;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += wt * (gs * acc[4 * q + i]);
-          *at = v;
+          for (int i = 0; i < 4; ++i) v[i] += wp * (gs * acc[4 * q + i]);
+          *to = v;
         }
       }
     }
@@ -514,13 +567,21 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
     float4_t o = float4_t{0, 0, 0, 0};
 #pragma unroll
     for (int v = 0; v < W; ++v) o += *reinterpret_cast<const float4_t*>(tiles + (v * g.T + t) * PITCH + row);
-    const size_t at = (size_t)t * g.H + blockIdx.x * 32 + row;
-    typedef OutVec<4>::type vec_t;
-    vec_t add = vec_t(0u);
-    if (g.add) add = *reinterpret_cast<const vec_t*>(g.add + at);
-    const float f[4] = {o[0], o[1], o[2], o[3]};
-    *reinterpret_cast<vec_t*>(g.out + at) = add_and_round<4>(f, add);
+    const size_t to = (size_t)t * g.H + blockIdx.x * 32 + row;
+    if (g.parts > 1)
+      *reinterpret_cast<float4_t*>(g.partial + (size_t)blockIdx.y * g.T * g.H + to) = o;
+    else
+      few_store(g, to, o);
   }
+}
+
+// Adds the parts in their order, four outputs to a thread.
+__global__ __launch_bounds__(256) void few_join_kernel(FewArgs g) {
+  const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (size_t)g.T * g.H;
+  if (at >= n) return;
+  float4_t o = float4_t{0, 0, 0, 0};
+  for (int p = 0; p < g.parts; ++p) o += *reinterpret_cast<const float4_t*>(g.partial + p * n + at);
+  few_store(g, at, o);
 }
 
 }  // namespace nvfp4
@@ -534,12 +595,23 @@ static int few_check(int32_t T, int32_t k, int32_t hidden, int32_t inter, int32_
     return NVFP4_ERR_SHAPE;  // an expert's weights as in the layer; threads of a grid
   return NVFP4_OK;
 }
+// Parts of the down products' sequence: as many as bring its workgroups to one per
+// CU, each wave to at least eight chunks where every choice is another expert; one
+// otherwise, since the join is a launch more. (Down and join, us [one
+// part]: 8 tokens of 8 experts each, 64 x 4096 x 1024: 26.8 + 4.8 [39]; 64 tokens,
+// 48 x 1024 x 1024: 16.6 + 4.8 [53]; 16 tokens, 32 x 512 x 512: 13.7 + 3.9 [21].)
+static int few_parts(int T, int k, int hidden, int inter, int L) {
+  const int64_t chunks = (int64_t)std::min(T * k, L) * (inter / 128);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::min(256, hidden / 32), chunks / (8 * kDownWaves)));
+}
+static size_t few_h_bytes(int T, int k, int inter) { return nvfp4_align256((size_t)T * k * inter * 2); }
 
 extern "C" int32_t nvfp4_moe_few_max_tokens(void) { return kFewMaxT; }
 
 extern "C" size_t nvfp4_moe_few_ws_bytes(int32_t T, int32_t k, int32_t hidden, int32_t inter, int32_t num_local) {
   if (few_check(T, k, hidden, inter, num_local)) return 0;
-  return nvfp4_align256((size_t)T * k * inter * 2);
+  const int parts = few_parts(T, k, hidden, inter, num_local);
+  return few_h_bytes(T, k, inter) + (parts > 1 ? (size_t)parts * T * hidden * 4 : 0);
 }
 
 extern "C" int nvfp4_moe_forward_few(const nvfp4_moe_weights* w, const void* x_bf16, int32_t T, const int32_t* topk_ids,
@@ -556,20 +628,27 @@ extern "C" int nvfp4_moe_forward_few(const nvfp4_moe_weights* w, const void* x_b
       !nvfp4_aligned16(out_bf16) || !nvfp4_aligned16(ws))
     return NVFP4_ERR_ALIGN;
   if (ws_bytes < nvfp4_moe_few_ws_bytes(T, k, w->hidden, w->inter, w->num_local)) return NVFP4_ERR_WORKSPACE;
+  const int parts = few_parts(T, k, w->hidden, w->inter, w->num_local);
+  char* const base = reinterpret_cast<char*>(ws);
   const FewArgs g = {reinterpret_cast<const uint16_t*>(x_bf16), topk_ids, topk_w, w->w1, w->w2, w->w1_gs, w->w2_gs,
-                     reinterpret_cast<uint16_t*>(ws), reinterpret_cast<const uint16_t*>(add_bf16),
-                     reinterpret_cast<uint16_t*>(out_bf16), T, k, w->num_local, expert_start, w->hidden, w->inter,
-                     w->w1_dual_gs};
-  const int items = std::min(T * k, (T > 32 ? 2 : 1) * w->num_local);  // at most
-  hipLaunchKernelGGL(few_up_kernel, dim3((unsigned)items * (w->inter / 32)), dim3(64 * kUpWaves),
+                     reinterpret_cast<uint16_t*>(base), reinterpret_cast<float*>(base + few_h_bytes(T, k, w->inter)),
+                     reinterpret_cast<const uint16_t*>(add_bf16), reinterpret_cast<uint16_t*>(out_bf16), T, k,
+                     w->num_local, expert_start, w->hidden, w->inter, w->w1_dual_gs, parts};
+  const int experts = std::min(T * k, w->num_local);  // chosen ones, at most
+  hipLaunchKernelGGL(few_up_kernel, dim3((unsigned)experts * (w->inter / 32)), dim3(64 * kUpWaves),
                      (size_t)(T * k * 2 + 15) / 16 * 16, (hipStream_t)stream, g);
   NVFP4_CHECK_LAUNCH();
-  const dim3 down(w->hidden / 32), threads(64 * kDownWaves);
+  const dim3 down(w->hidden / 32, parts), threads(64 * kDownWaves);
   const size_t lds = (size_t)kDownWaves * T * kDownPitch * 4 + (size_t)T * k * 6;
-  if (lds + kDownWaves * kDownDepth * 2048 + sizeof(Choices::Items) <= kLdsBytes)
+  if (lds + 5 * sizeof(Ring<kDownWaves>) + sizeof(Choices::Found) <= kLdsBytes)
     hipLaunchKernelGGL(few_down_kernel<true>, down, threads, lds, (hipStream_t)stream, g);
   else  // many choices for many tokens
     hipLaunchKernelGGL(few_down_kernel<false>, down, threads, lds, (hipStream_t)stream, g);
   NVFP4_CHECK_LAUNCH();
+  if (parts > 1) {
+    hipLaunchKernelGGL(few_join_kernel, dim3((unsigned)(((size_t)T * w->hidden / 4 + 255) / 256)), dim3(256), 0,
+                       (hipStream_t)stream, g);
+    NVFP4_CHECK_LAUNCH();
+  }
   return NVFP4_OK;
 }
