@@ -54,8 +54,8 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, int* to, int
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 4, voff, soff, 0, 0);
 }
 
-// Eight (four for SILU) outputs of a row, rounded to the output's type with
-// what is to be added.
+// 16 bytes of outputs of a row (8 for SILU), rounded to the output's type with
+// what is to be added. STREAM: stored past the caches.
 template <int OUT>
 struct MxOut {
   static constexpr int W = OUT == kMxSilu ? 4 : 8;
@@ -63,23 +63,30 @@ struct MxOut {
   static __device__ __forceinline__ vec load(const void* add, size_t at) {
     return *reinterpret_cast<const vec*>(reinterpret_cast<const uint16_t*>(add) + at);
   }
+  template <bool STREAM>
   static __device__ __forceinline__ void store(void* d, size_t at, const float* o, vec add) {
-    *reinterpret_cast<vec*>(reinterpret_cast<uint16_t*>(d) + at) = add_and_round<W>(o, add);
+    vec* to = reinterpret_cast<vec*>(reinterpret_cast<uint16_t*>(d) + at);
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(add_and_round<W>(o, add), to);
+    else
+      *to = add_and_round<W>(o, add);
   }
 };
 template <>
 struct MxOut<kMxF32> {
-  static constexpr int W = 8;
-  typedef float vec __attribute__((ext_vector_type(8)));
+  static constexpr int W = 4;
+  typedef float4_t vec;
   static __device__ __forceinline__ vec load(const void* add, size_t at) {
-    const float* p = reinterpret_cast<const float*>(add) + at;
-    const float4_t a = *reinterpret_cast<const float4_t*>(p), b = *reinterpret_cast<const float4_t*>(p + 4);
-    return vec{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return *reinterpret_cast<const vec*>(reinterpret_cast<const float*>(add) + at);
   }
+  template <bool STREAM>
   static __device__ __forceinline__ void store(void* d, size_t at, const float* o, vec add) {
-    float* p = reinterpret_cast<float*>(d) + at;
-    *reinterpret_cast<float4_t*>(p) = float4_t{o[0] + add[0], o[1] + add[1], o[2] + add[2], o[3] + add[3]};
-    *reinterpret_cast<float4_t*>(p + 4) = float4_t{o[4] + add[4], o[5] + add[5], o[6] + add[6], o[7] + add[7]};
+    vec* to = reinterpret_cast<vec*>(reinterpret_cast<float*>(d) + at);
+    const vec v = {o[0] + add[0], o[1] + add[1], o[2] + add[2], o[3] + add[3]};
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(v, to);
+    else
+      *to = v;
   }
 };
 
@@ -273,25 +280,28 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
   wait_stage<0>();
 
   // Epilogue, each wave by itself: 32 tokens x 32 SN columns of sums through
-  // LDS, so that a lane takes eight neighbouring columns of a token (four for
-  // SILU) and its neighbours the rest of whole 64-byte lines.
-  constexpr int COLS = 32 * SN, PITCH = COLS + 4;
-  constexpr int WPB = BUF * 16 / (32 * PITCH * 4);  // waves whose block fits one buffer
+  // LDS, so that a lane takes 16 bytes of outputs of a token (8 for SILU) and its
+  // neighbours the rest of whole 64-byte lines. The large tile's go past the
+  // caches (16384 x 7168 x 2048: 161 -> 138 us); with eight float32 outputs to a
+  // lane, in two stores of every other 16 bytes, 4096 x 7168 x 4096 took 76 us
+  // (104 past the caches).
+  typedef MxOut<OUT == kMxPart ? kMxF32 : OUT> Out;
+  constexpr int COLS = 32 * SN, PITCH = COLS + 4, PER = SILU ? 8 : Out::W;  // PER: sums of a lane and row
+  constexpr int WPB = BUF * 16 / (32 * PITCH * 4);                          // waves whose block fits one buffer
   static_assert(WPB * 4 >= NW, "the LDS buffers hold every wave's block");
   int4v* const buf = wave / WPB == 0 ? l0 : wave / WPB == 1 ? l1 : wave / WPB == 2 ? l2 : l3;
   float* const sums = reinterpret_cast<float*>(buf) + (wave % WPB) * 32 * PITCH;
-  constexpr int LPR = COLS / 8, RPS = 64 / LPR;  // lanes of a row, rows of a step
+  constexpr int LPR = COLS / PER, RPS = 64 / LPR;  // lanes of a row, rows of a step
   const int col = lane % LPR;
   // output column of this lane, the same for all its rows
-  const int oc = SILU ? (col / 8) * 32 + (col % 8) * 4 : col * 8;  // within the wave's outputs
+  const int oc = SILU ? (col / 8) * 32 + (col % 8) * 4 : col * PER;  // within the wave's outputs
   const int n = n0 + wn * (SILU ? COLS / 2 : COLS) + oc;
   const bool n_ok = n < (OUT == kMxPart ? g.N : g.n_out);
-  // where the lane's sums lie in a row: eight in a run, or four gate and the
-  // four up sums 32 columns on
-  const int c0 = SILU ? (col / 8) * 64 + (col % 8) * 4 : col * 8, c1 = SILU ? c0 + 32 : c0 + 4;
+  // where the lane's sums lie in a row: in a run, or four gate and the four up
+  // sums 32 columns on
+  const int c0 = SILU ? (col / 8) * 64 + (col % 8) * 4 : col * PER, c1 = SILU ? c0 + 32 : c0 + 4;
   // the values to add are loaded one subtile ahead
   constexpr int STEPS = 32 / RPS;
-  typedef MxOut<OUT == kMxPart ? kMxF32 : OUT> Out;
   typename Out::vec add[2][STEPS];
   auto row_of = [&](int j, int st) { return m0 + wm * 32 * SM + j * 32 + st * RPS + lane / LPR; };
   auto load_rows = [&](int j) {
@@ -316,13 +326,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
       const int row = st * RPS + lane / LPR, m = row_of(j, st);
-      const float4_t v0 = *reinterpret_cast<const float4_t*>(sums + row * PITCH + c0);
-      const float4_t v1 = *reinterpret_cast<const float4_t*>(sums + row * PITCH + c1);
       float o[8];
+      const float4_t v0 = *reinterpret_cast<const float4_t*>(sums + row * PITCH + c0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        o[e] = v0[e];
-        o[4 + e] = v1[e];
+      for (int e = 0; e < 4; ++e) o[e] = v0[e];
+      if constexpr (PER == 8) {
+        const float4_t v1 = *reinterpret_cast<const float4_t*>(sums + row * PITCH + c1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[4 + e] = v1[e];
       }
       if constexpr (SILU) {
 #pragma unroll
@@ -330,9 +341,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
       }
       if (m >= g.M || !n_ok) continue;
       if constexpr (OUT == kMxPart)
-        Out::store(g.part, ((size_t)blockIdx.y * g.M + m) * g.N + n, o, typename Out::vec(0));
+        Out::template store<false>(g.part, ((size_t)blockIdx.y * g.M + m) * g.N + n, o, typename Out::vec(0));
       else
-        Out::store(g.d, (size_t)m * g.n_out + n, o, add[j & 1][st]);
+        Out::template store<(BM >= 256)>(g.d, (size_t)m * g.n_out + n, o, add[j & 1][st]);
     }
     wave_lds_fence();
   }
