@@ -280,6 +280,14 @@ __device__ __forceinline__ void multiply(const Chunk& c, const FewTokens& t, flo
   add(p[1], __builtin_amdgcn_cvt_f32_fp8((int)s[1], 3));
 }
 
+// Until no load of this wave is in flight: those of stages that do not exist write
+// to LDS too, and neither the next run nor another workgroup may find them there.
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_waitcnt(15 << 8 | 7 << 4);  // vmcnt(0) alone
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Where the tokens of a stage wait in LDS, eight for each wave; an array for each
 // stage of the ring, so that the compiler can tell their loads apart.
 template <int W>
@@ -331,6 +339,7 @@ __device__ __forceinline__ void up_few(UpStages& u, int offset, int n, int4v* r0
   }
   if (s < u.stages) compute(0);
   if (s + W < u.stages) compute(1);
+  wait_loads();
 #pragma unroll
   for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -464,6 +473,7 @@ __device__ __forceinline__ float4_t down_few(const DownStages& u, int offset, in
 #pragma unroll
   for (int d = 0; d + 1 < D; ++d)
     if (s + d < u.s1) compute(d);
+  wait_loads();
   return acc;
 }
 __device__ __forceinline__ float16_t down_many(const DownStages& u, int offset) {

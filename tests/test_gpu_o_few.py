@@ -137,6 +137,27 @@ def test_layer(nv, case):
         assert torch.equal(add, out)
 
 
+@pytest.mark.parametrize("n", [1, 3, 4, 5, 7, 8, 9, 16, 17, 31, 32, 33, 40, 63, 64])
+def test_tokens_of_an_expert(nv, n):
+    """n of 64 tokens on one expert, the rest on another or none, in the places where they fall."""
+    T, k, L, H, I = 64, 2, 5, 640, 384
+    weights, w1, w2, g = layer(nv, L, H, I, True, 100 + n)
+    rng = np.random.default_rng(n)
+    ids = np.full((T, k), -1, np.int32)
+    on = rng.permutation(T)[:n]
+    ids[on, rng.integers(0, k, n)] = 3
+    ids[rng.random((T, k)) < 0.2] = 9          # of another rank
+    off = np.setdiff1d(np.arange(T), on)
+    ids[off[::3], 0] = 1
+    ids[on, 0] = np.where(ids[on, 1] == 3, 0, 3)
+    w = (rng.random((T, k)) + 0.1).astype(np.float32)
+    x = torch.randn(T, H, device=DEV, generator=g).bfloat16()
+    ws = torch.full((nv.nvfp4_moe_few_ws_bytes(T, k, H, I, L),), 0xFF, dtype=torch.uint8, device=DEV)
+    out = nv.nvfp4_moe_forward_few(weights, x, to_dev(ids), to_dev(w), 0, ws=ws)
+    assert int((ids == 3).any(1).sum()) == n
+    check(x, ids, w, 0, weights, w1, w2, ws[:T * k * I * 2].view(torch.bfloat16).view(T, k, I), out, None)
+
+
 def test_oracle_of_the_layer(nv):
     """The NumPy oracle on one small layer, end to end (the rounding of h within half a step of BF16)."""
     T, k, L, H, I = 3, 2, 4, 128, 128
