@@ -59,7 +59,7 @@ def _compile_native(verbose):
           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
           os.path.join(PKG, "csrc", "binding.cpp"), "-L", PKG, "-lnvfp4moe", "-Wl,-rpath,$ORIGIN",
-          "-L", os.path.join(th, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"], NATIVE, verbose)
+          "-L", os.path.join(th, "lib"), "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10"], NATIVE, verbose)
 
 
 def build(verbose: bool = False) -> str:

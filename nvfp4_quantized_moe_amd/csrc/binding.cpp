@@ -18,6 +18,7 @@
 #include <string>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -116,7 +117,7 @@ class Call {
     return static_cast<P*>(t->data_ptr());
   }
   at::Tensor make(at::IntArrayRef shape, at::ScalarType type) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)device())));
+    return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, (c10::DeviceIndex)device()), std::nullopt);
   }
 
   template <typename Launch>
