@@ -64,11 +64,11 @@ def test_gemm(nv):
         assert call(**{bad: None}) == NULL and call(**{bad: ODD}) == ALIGN, bad
     assert call(add=ODD) == ALIGN and call(M=0, a=None) == 0 and call(K=0, d=None) == NULL
     assert call(M=64 * 65535, N=1 << 26, K=128) == SHAPE
-    parts = nv.mxfp4_gemm_ws_bytes(64, 512, 16384)
+    parts = nv.mxfp4_gemm_ws_bytes(64, 4096, 16384)
     assert parts > 0 and nv.mxfp4_gemm_ws_bytes(8192, 4096, 16384) == 0 and nv.mxfp4_gemm_ws_bytes(64, 12, 16384) == 0
-    assert nv.mxfp4_gemm_ws_bytes(0, 512, 16384) == 0
-    assert call(M=64, N=512, K=16384) == NULL and call(M=64, N=512, K=16384, ws=ODD, n=parts) == ALIGN
-    assert call(M=64, N=512, K=16384, ws=P, n=parts - 1) == WORKSPACE
+    assert nv.mxfp4_gemm_ws_bytes(0, 4096, 16384) == 0
+    assert call(M=64, N=4096, K=16384) == NULL and call(M=64, N=4096, K=16384, ws=ODD, n=parts) == ALIGN
+    assert call(M=64, N=4096, K=16384, ws=P, n=parts - 1) == WORKSPACE
 
 
 def test_calls_refuse_what_is_no_gpu_tensor(nv):
