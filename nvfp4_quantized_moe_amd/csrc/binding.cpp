@@ -187,6 +187,11 @@ Out workspace(Call& call, PyObject* o, size_t need) {
                       : Out(call, o, {0}, kU8, "ws");
 }
 
+// An output of something that the call does not make: None.
+void unused(PyObject* o, const char* name, const char* without) {
+  if (o != Py_None) refuse(name, std::string("given without ") + without);
+}
+
 struct Matrix {
   int64_t rows, cols;
 };
@@ -456,6 +461,10 @@ PyObject* mx_quantize(PyObject* const* a) {  // x, direction (1 rows, 2 columns,
   std::optional<MxOut> rows, cols;
   if (direction & 1) rows.emplace(call, a[3], a[4], M, mx_padded(K, "x"), "q", "scale");
   if (direction & 2) cols.emplace(call, a[5], a[6], K, mx_padded(M, "x"), "q_t", "scale_t");
+  for (int i = 0; i < 2; ++i) {
+    if (!rows) unused(a[3 + i], i ? "scale" : "q", "MX_ROWS or MX_BOTH");
+    if (!cols) unused(a[5 + i], i ? "scale_t" : "q_t", "MX_COLUMNS or MX_BOTH");
+  }
   call.run([&, M = (int32_t)M, K = (int32_t)K](void* stream) {
     return mxfp4_quantize(x.data_ptr(), code(x), M, K, rule, rows ? rows->q.at<uint8_t>() : nullptr,
                           rows ? rows->scale.at<uint8_t>() : nullptr, cols ? cols->q.at<uint8_t>() : nullptr,
@@ -474,8 +483,8 @@ PyObject* layer_norm(PyObject* const* a) {  // x, residual, w, b, scale, eps, ru
   if (residual) {
     call.floats(*residual, "residual");
     call.shaped(*residual, {T, H}, "residual");
-  } else if (a[7] != Py_None) {
-    refuse("residual_out", "given without a residual");
+  } else {
+    unused(a[7], "residual_out", "a residual");
   }
   const at::ScalarType res_type = residual ? residual->scalar_type() : x.scalar_type();
   const float* w = call.input<float>(a[2], kF32, {H}, "w");
@@ -489,6 +498,7 @@ PyObject* layer_norm(PyObject* const* a) {  // x, residual, w, b, scale, eps, ru
   const Out y(call, a[8], {T, H}, x.scalar_type(), "y");
   std::optional<MxOut> codes;
   if (quant) codes.emplace(call, a[9], a[10], T, mx_padded(H, "x"), "y_q", "y_scale");
+  else unused(a[9], "y_q", "mx_rule"), unused(a[10], "y_scale", "mx_rule");
   call.run([&, T = (int32_t)T, H = (int32_t)H](void* stream) {
     return moe_layer_norm(x.data_ptr(), code(x), residual ? residual->data_ptr() : nullptr,
                           res_type == kBf16 ? NVFP4_DT_BF16 : NVFP4_DT_F32, T, H, w, b, scale, eps,
@@ -512,10 +522,14 @@ PyObject* layer_norm_backward(PyObject* const* a) {  // d_y, d_residual_out, r, 
   const float* w = call.input<float>(a[3], kF32, {H}, "w");
   const float* b = call.input<float>(a[4], kF32, {H}, "b");
   const float scale = py_float(a[5]), eps = py_float(a[6]);
-  const bool residual = PyObject_IsTrue(a[7]) == 1;
+  const int truth = PyObject_IsTrue(a[7]);  // -1: no truth value, such as a tensor of many elements
+  if (truth < 0) throw python_error();
+  const bool residual = truth == 1;
   if (!residual && (scale != 1.0f || res_type != x_type))
     refuse("residual", "without one, scale is 1 and residual_out (the x that was normalized) of d_y's type");
-  if (!residual && a[9] != Py_None) refuse("d_residual", "given without a residual");
+  if (!residual) unused(a[9], "d_residual", "a residual");
+  if (!w) unused(a[10], "d_w", "w");
+  if (!b) unused(a[11], "d_b", "b");
   const Out d_x(call, a[8], {T, H}, x_type, "d_x");
   std::optional<Out> d_residual, d_w, d_b;
   if (residual) d_residual.emplace(call, a[9], at::IntArrayRef({T, H}), res_type, "d_residual");

@@ -130,8 +130,8 @@ def test_not_finite(nv):
 
 SHAPES = [(1, 8, 128), (1, 4096, 7168), (2, 16, 256), (5, 1000, 1152), (16, 4096, 7168), (17, 264, 7168), (33, 40, 384),
           (64, 4096, 7168), (63, 7168, 2048), (33, 72, 8320), (64, 520, 16384), (100, 1096, 7168), (65, 128, 128),
-          (128, 256, 65536), (333, 1000, 1152), (500, 520, 384), (1030, 2056, 1280), (2048, 2048, 256), (2049, 4104, 512),
-          (4100, 1536, 128)]
+          (16, 64, 65536), (64, 4096, 16384), (128, 256, 65536), (333, 1000, 1152), (500, 520, 384), (1030, 2056, 1280),
+          (2048, 2048, 256), (2049, 4104, 512), (4100, 1536, 128)]
 
 
 def operands(M, N, K, seed):
@@ -216,6 +216,37 @@ def test_scales_at_their_ends(nv):
         assert not np.isnan(got[inside]).any()
 
 
+def test_refused(nv):
+    x = torch.zeros(4, 256, device=DEV)
+    q, s, qt, st = nv.mxfp4_quantize(x, nv.MX_BOTH)
+    add = torch.zeros(4, 8, device=DEV).bfloat16()
+    for call in (lambda: nv.mxfp4_quantize(x, 0), lambda: nv.mxfp4_quantize(x, 4), lambda: nv.mxfp4_quantize(x.half()),
+                 lambda: nv.mxfp4_quantize(x.T), lambda: nv.mxfp4_quantize(x.cpu()), lambda: nv.mxfp4_quantize(x[0]),
+                 lambda: nv.mxfp4_quantize(x, q_t=qt), lambda: nv.mxfp4_quantize(x, scale_t=st),
+                 lambda: nv.mxfp4_quantize(x, nv.MX_COLUMNS, q=q), lambda: nv.mxfp4_quantize(x, nv.MX_COLUMNS, scale=s),
+                 lambda: nv.mxfp4_quantize(x, q=q[:3].clone()), lambda: nv.mxfp4_quantize(x, scale=s[:1].clone()),
+                 lambda: nv.mxfp4_quantize(torch.zeros(262145, 8, device=DEV), nv.MX_COLUMNS),
+                 lambda: nv.mxfp4_dequantize(q, s, torch.float16), lambda: nv.mxfp4_dequantize(q, s, cols=257),
+                 lambda: nv.mxfp4_dequantize(q, s, cols=-1), lambda: nv.mxfp4_dequantize(q, s.reshape(4, 8)),
+                 lambda: nv.mxfp4_dequantize(q[:, :32].contiguous(), s), lambda: nv.mxfp4_dequantize(q, st),
+                 lambda: nv.mxfp4_gemm(q, s, qt, st), lambda: nv.mxfp4_gemm(q, None, q, s),
+                 lambda: nv.mxfp4_gemm(q, s, q, s, add=add), lambda: nv.mxfp4_gemm(q, s, q, s, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            call()
+    b, bs = nv.mxfp4_quantize(torch.zeros(8, 256, device=DEV))
+    for call in (lambda: nv.mxfp4_quantize(x, rule=2), lambda: nv.mxfp4_quantize(torch.zeros(4, 12, device=DEV)),
+                 lambda: nv.mxfp4_gemm(q, s, q, s), lambda: nv.mxfp4_gemm(q, s, b, bs, nv.EPI_SILU_MUL),
+                 lambda: nv.mxfp4_gemm(q, s, b, bs, 7)):
+        with pytest.raises(nv.NVFP4Error):
+            call()
+    for g in range(1, 4):   # addresses off 16 bytes
+        off = torch.zeros(q.numel() + 16, dtype=torch.uint8, device=DEV)[4 * g:][:q.numel()].view(q.shape)
+        with pytest.raises(nv.NVFP4Error):
+            nv.mxfp4_quantize(x, q=off)
+        with pytest.raises(nv.NVFP4Error):
+            nv.mxfp4_gemm(off, s, b, bs)
+
+
 def test_empty(nv):
     q, s, qt, st = nv.mxfp4_quantize(torch.empty((0, 40), dtype=torch.bfloat16, device=DEV), nv.MX_BOTH)
     assert q.shape == (0, 64) and s.shape == (1, 0, 4) and qt.shape == (40, 0) and st.shape == (0, 40, 4)
@@ -246,14 +277,14 @@ def test_training_products(nv, T, N, K):
         assert (np.abs(got.double().cpu().numpy() - ref) <= 2 * EPS32 * chain(a.shape[1]) * terms).all()
 
 
-@pytest.mark.parametrize("T", [5, 40, 300])
-def test_equal_in_a_graph(nv, T):
+@pytest.mark.parametrize("T,K", [(5, 8200), (40, 8200), (300, 8200), (9, 32776), (70, 16648)])
+def test_equal_in_a_graph(nv, T, K):
     """Captured and replayed on a dirty workspace, with eager work between the replays."""
-    x = torch.randn(T, 8200, device=DEV).bfloat16()
-    b, bs = nv.mxfp4_quantize(torch.randn(264, 8200, device=DEV))
+    x = torch.randn(T, K, device=DEV).bfloat16()
+    b, bs = nv.mxfp4_quantize(torch.randn(264, K, device=DEV))
     q, s = nv.mxfp4_quantize(x)
     d = torch.empty((T, 264), dtype=torch.bfloat16, device=DEV)
-    ws = torch.empty(max(256, nv.mxfp4_gemm_ws_bytes(T, 264, nv.mxfp4_padded(8200))), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(max(256, nv.mxfp4_gemm_ws_bytes(T, 264, nv.mxfp4_padded(K))), dtype=torch.uint8, device=DEV)
 
     def step():
         nv.mxfp4_quantize(x, q=q, scale=s)

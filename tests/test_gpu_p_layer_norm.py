@@ -215,9 +215,15 @@ def test_refused(nv):
                  lambda: nv.moe_layer_norm_backward(x, None, x.bfloat16(), w, residual=False),
                  lambda: nv.moe_layer_norm_backward(x, None, x, w, scale=2.0, residual=False),
                  lambda: nv.moe_layer_norm_backward(x, None, x, w, residual=False, d_residual=x),
-                 lambda: nv.moe_layer_norm_backward(x, x.bfloat16(), x, w)):
+                 lambda: nv.moe_layer_norm_backward(x, x.bfloat16(), x, w),
+                 # outputs of what the call does not make
+                 lambda: nv.moe_layer_norm(x, y_q=torch.zeros(4, 64, dtype=torch.uint8, device=DEV)),
+                 lambda: nv.moe_layer_norm(x, y_scale=torch.zeros(1, 4, 4, dtype=torch.uint8, device=DEV)),
+                 lambda: nv.moe_layer_norm_backward(x, None, x, d_w=w), lambda: nv.moe_layer_norm_backward(x, None, x, w, d_b=w)):
         with pytest.raises(ValueError):
             call()
+    with pytest.raises(RuntimeError):   # a tensor where a truth value belongs
+        nv.moe_layer_norm_backward(x, None, x, w, residual=x)
     with pytest.raises(nv.NVFP4Error):
         nv.moe_layer_norm(x, mx_rule=2)
     with pytest.raises(nv.NVFP4Error):
