@@ -430,7 +430,7 @@ int32_t mxfp4_padded(int32_t n);  /* -1 outside [0, 262144] */
  * but at least -127 (also for a = 0); q = E2M1 nearest to x / 2^e, ties to the
  * even code, both exactly. A block with an infinity or NaN gets the scale 0xFF.
  * K % 8 == 0, 0 < K <= 262144; M <= 64 * 65535, along the columns <= 262144.
- * One launch.
+ * Outputs overlap neither x nor each other. One launch.
  */
 int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t K, int32_t rule, uint8_t* q, uint8_t* scale,
                    uint8_t* q_t, uint8_t* scale_t, void* stream);
@@ -576,7 +576,8 @@ int nvfp4_moe_forward_static(const nvfp4_moe_weights* w, const void* x_bf16, int
                              const float* gs_in, void* out_bf16, void* ws, size_t ws_bytes, void* stream);
 
 /* The layer for at most nvfp4_moe_few_max_tokens() = 64 tokens, in two launches
- * (three for narrow layers) on the same weights, with activations as they are (BF16, not quantized):
+ * (three for narrow layers) on the same weights, with activations as they are
+ * (BF16, not quantized):
  *   h_e    = RN_bf16(silu(G) * U), G and U = w1_gs[e] (gate and up) times the
  *            products of x[t] with the gate and up rows of W1_e
  *   out[t] = RN_bf16(sum over the experts e of token t on this rank of
@@ -587,8 +588,9 @@ int nvfp4_moe_forward_static(const nvfp4_moe_weights* w, const void* x_bf16, int
  * the sums depends on what the tokens chose, so a call repeats bit for bit, but
  * a token's last bits may differ with the others in the batch.
  * ws: at least nvfp4_moe_few_ws_bytes(...) bytes; h comes first, BF16 [T, k, I],
- * a row for each choice on this rank (the first of an expert listed twice). k <= 64, L <= 4096,
- * H % 128 == 0, I % 128 == 0, 2I*H*9/16 below 2^31.
+ * a row for each choice on this rank (the first of an expert listed twice).
+ * out may be x or add; ws overlaps nothing. 1 <= k <= 64, 1 <= L <= 4096,
+ * H % 128 == 0, I % 128 == 0, I < 65536, 2I*H*9/16 below 2^31.
  */
 int32_t nvfp4_moe_few_max_tokens(void);
 size_t nvfp4_moe_few_ws_bytes(int32_t T, int32_t k, int32_t hidden, int32_t inter, int32_t num_local);

@@ -6,8 +6,9 @@ names of the C entry points declared in include/nvfp4moe.h.
 
 No call takes part in autograd: outputs come back without a history, also from
 tensors that require a gradient. Gradients are calls of their own
-(moe_gate_backward, moe_block_norm_backward, moe_layer_norm_backward), for a user's autograd function to
-call; the expert layer and the dense expert have none.
+(moe_gate_backward, moe_block_norm_backward, moe_layer_norm_backward, and for a
+linear layer mxfp4_gemm on codes along the other axis), for a user's autograd
+function to call; the expert layer and the dense expert have none.
 
 Importing this module loads the built library and fails loudly when it is
 missing; there is no CPU fallback.

@@ -1,6 +1,6 @@
 // The expert layer for a few tokens, in two launches (a third joins parts of the
-// down products where the layer is narrow) over the packed NVFP4
-// weights of the layer (moe_forward's, nvfp4_pack_weights):
+// down products where the layer is narrow) over the layer's packed NVFP4 weights
+// (nvfp4_pack_weights):
 //   h[t, e]  = bf16(silu(gs_g W_gate x[t]) * (gs_u W_up x[t]))  for the experts e of token t on this rank
 //   out[t]   = bf16(sum_e w[t, e] gs_2 W_down h[t, e] [+ add[t]])
 // with BF16 activations as they are and sums in float32. What bounds it is the

@@ -3,7 +3,8 @@
 //   y  = (r' - mean) / sqrt(var + eps) * w + b     from r' as stored; also as MXFP4
 // One pass: a row's elements stay in registers between its reductions, and
 // workgroups walk their rows with the next row's loads in flight, as the block's
-// norms do. What bounds it is reading and writing the rows.
+// norms do. What bounds it is reading and writing the rows: 8192 x 7168 BF16 takes
+// 92 us, 5.2 TB/s, where a copy reaches 5.4; 64 x 7168, two dependent row sums, 4.6.
 //
 // Mean and variance in two steps, so that a row far from 0 keeps its digits: m
 // from the sum, then d = r' - m, whose sums give what the rounding of m left
@@ -143,7 +144,8 @@ __global__ __launch_bounds__(512) void layer_norm_kernel(const X* x, const R* re
 // mean, rho and the two means of dn come from one row sum and four more behind
 // it: mean(dn n) = rho (mean(dn d) - delta mean(dn)). The column sums stay in
 // registers over all rows of the thread; the workgroup's row groups add theirs
-// in LDS, halving, and it leaves one row of partial sums.
+// in LDS, halving, and it leaves one row of partial sums (8191 x 2888, BF16 with
+// a float residual: 73 us, 5.2 TB/s, and 4.7 for the columns' sums).
 template <typename X, typename R, int CH>
 struct LayerGradRow {
   Vec8<X> y[CH];

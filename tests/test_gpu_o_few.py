@@ -231,6 +231,21 @@ def test_empty_and_refused(nv):
         nv.nvfp4_moe_forward_few(weights, x[:5], ids[:5], w[:5], 0, ws=torch.zeros(64, dtype=torch.uint8, device=DEV))
 
 
+def test_in_place(nv):
+    """The output over the input, and over what is added, with the down products whole and in parts."""
+    for T, k, L, H, I in ((3, 2, 8, 256, 128), (64, 8, 40, 512, 512)):
+        weights, *_, g = layer(nv, L, H, I, False, 8)
+        x, add = (torch.randn(T, H, device=DEV, generator=g).bfloat16() for _ in range(2))
+        ids, w = (to_dev(v) for v in choices("plain", T, k, L, 0, L, 8))
+        want = nv.nvfp4_moe_forward_few(weights, x, ids, w, 0, add=add)
+        for over in (x, add):
+            given = dict(x=x.clone(), add=add.clone())
+            out = given["x" if over is x else "add"]
+            nv.nvfp4_moe_forward_few(weights, given["x"], ids, w, 0, add=given["add"], out=out)
+            assert torch.equal(out, want)
+    assert nv.nvfp4_moe_few_ws_bytes(64, 8, 512, 512, 40) > 64 * 8 * 512 * 2 >= nv.nvfp4_moe_few_ws_bytes(3, 2, 256, 128, 8)
+
+
 def test_in_a_graph(nv):
     """Captured, then replayed with other choices in the same buffers."""
     T, k, L, H, I = 9, 4, 12, 256, 256
