@@ -27,12 +27,21 @@ struct MxArgs {
   bool ceil;
 };
 
+// x of this size and more is read past the caches (PAST), which leaves them to the
+// codes. Both ways 8192 x 7168 takes 34.8 us (5.2 TB/s) [40 through them], 4096 x
+// 7168 19.3 [20.5], 8192 x 7168 float 55 [61]; along the rows 25.6 [29.6] and 13.9
+// [14.4]; behind the norm that writes x 98 [110] for the two, both ways 111 [126].
+// Again and again on what the caches hold a smaller x takes longer (4096 x 4096,
+// 33 MB: 11.2 [10], 2047 x 2888 float 8.6 [8.0]), and behind a norm no less (2048
+// x 4096: 18.6 [18.5]).
+constexpr int64_t kMxPastBytes = 32 << 20;
+
 // Along rows: a wave takes 512 columns of R rows, all R loads in flight; lane l
 // holds columns 8 l .. 8 l + 7 of each, so four lanes share a scale. Of four rows'
 // scales each of them keeps one, so that all lanes store together: a byte store
 // takes as long for 16 lanes as for 64. Eight rows where there are enough waves
-// (8192 x 7168 BF16: 26 us, 5.7 TB/s), one where there are few (64 x 7168: 2.4).
-template <typename T, int R>
+// (8192 x 7168 BF16: 25.6 us, 5.8 TB/s), one where there are few (64 x 7168: 2.4).
+template <typename T, int R, bool PAST>
 __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, MxArgs g) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int Kp = mx_padded(g.K), across = (g.K + 511) / 512;
@@ -40,7 +49,7 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, M
   MxVec8<T> v[R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    v[i].load(x + (size_t)min(r0 + i, g.M - 1) * g.K + min(c, g.K - 8));
+    v[i].template load<PAST>(x + (size_t)min(r0 + i, g.M - 1) * g.K + min(c, g.K - 8));
   const uint32_t up = g.ceil ? MxVec8<T>::kUp : 0u;
   uint32_t keep = 0;
 #pragma unroll
@@ -62,14 +71,18 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, M
   }
 }
 
-// Four values of a row, as they are loaded.
+// Four values of a row, as they are loaded (PAST: not to stay in the caches).
 template <typename T>
 struct MxVec4;
 template <>
 struct MxVec4<uint16_t> {
   static constexpr uint32_t kUp = kMxUpBf16;
   uint2 v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint2*>(p); }
+  template <bool PAST>
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const u32x2_t* at = reinterpret_cast<const u32x2_t*>(p);
+    v = __builtin_bit_cast(uint2, PAST ? __builtin_nontemporal_load(at) : *at);
+  }
   __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
   __device__ __forceinline__ uint32_t amax() const {
     const uint32_t a = max_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
@@ -99,7 +112,11 @@ template <>
 struct MxVec4<float> {
   static constexpr uint32_t kUp = kMxUpF32;
   float4 v;
-  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  template <bool PAST>
+  __device__ __forceinline__ void load(const float* p) {
+    const float4_t* at = reinterpret_cast<const float4_t*>(p);
+    v = __builtin_bit_cast(float4, PAST ? __builtin_nontemporal_load(at) : *at);
+  }
   __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
   __device__ __forceinline__ uint32_t amax() const {
     uint32_t m = 0;
@@ -130,9 +147,9 @@ struct MxVec4<float> {
 // their columns and eight share a block of a row. Codes and scales of the tile
 // meet in LDS and leave in whole 64-byte runs: stored from the registers, 8 bytes
 // here and there in 64 lines, the address unit was busy 84 % of the time
-// (8192 x 7168 both ways: 48.5 us, now 41, 4.4 TB/s).
+// (8192 x 7168 both ways: 48.5 us).
 constexpr int kMxColPitch = 80;  // of a column's 64 bytes of codes in LDS, against bank conflicts
-template <typename T, bool ROWS>
+template <typename T, bool ROWS, bool PAST>
 __global__ __launch_bounds__(256) void mx_columns_kernel(const T* __restrict__ x, MxArgs g) {
   constexpr int N = kMxBlock / 2;
   __shared__ __attribute__((aligned(16))) uint8_t cols[128 * kMxColPitch];  // [32 (c % 4) + c / 4][64 bytes]
@@ -144,7 +161,7 @@ __global__ __launch_bounds__(256) void mx_columns_kernel(const T* __restrict__ x
   MxVec4<T> v[N];
   const T* from = x + min(c, g.K - 4);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i].load(from + (size_t)min(r0 + i, g.M - 1) * g.K);
+  for (int i = 0; i < N; ++i) v[i].template load<PAST>(from + (size_t)min(r0 + i, g.M - 1) * g.K);
   if (c0 + 128 > g.K || m0 + kMxGroup > g.M) {  // the same for the workgroup
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -285,19 +302,24 @@ extern "C" int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t
   const auto go = [&](auto xt) -> int {
     using T = decltype(xt);
     const T* at = reinterpret_cast<const T*>(x);
-    if (!q_t) {
-      const int cols = (K + 511) / 512;
-      if ((int64_t)M * cols <= 8192)
-        hipLaunchKernelGGL((mx_rows_kernel<T, 1>), dim3((unsigned)((M + 3) / 4) * cols), dim3(256), 0, (hipStream_t)stream, at, g);
+    const auto launch = [&](auto past) {
+      constexpr bool PAST = decltype(past)::value;
+      const dim3 grid((K + 127) / 128, (M + kMxGroup - 1) / kMxGroup), threads(256);
+      const unsigned cols = (K + 511) / 512;
+      if (q_t && q)
+        hipLaunchKernelGGL((mx_columns_kernel<T, true, PAST>), grid, threads, 0, (hipStream_t)stream, at, g);
+      else if (q_t)
+        hipLaunchKernelGGL((mx_columns_kernel<T, false, PAST>), grid, threads, 0, (hipStream_t)stream, at, g);
+      else if (!PAST && (int64_t)M * cols <= 8192)
+        hipLaunchKernelGGL((mx_rows_kernel<T, 1, false>), dim3((M + 3) / 4 * cols), threads, 0, (hipStream_t)stream, at, g);
       else
-        hipLaunchKernelGGL((mx_rows_kernel<T, 8>), dim3((unsigned)((M + 31) / 32) * cols), dim3(256), 0, (hipStream_t)stream, at, g);
-    } else {
-      const dim3 grid((K + 127) / 128, (M + kMxGroup - 1) / kMxGroup);
-      if (q)
-        hipLaunchKernelGGL((mx_columns_kernel<T, true>), grid, dim3(256), 0, (hipStream_t)stream, at, g);
-      else
-        hipLaunchKernelGGL((mx_columns_kernel<T, false>), grid, dim3(256), 0, (hipStream_t)stream, at, g);
-    }
+        hipLaunchKernelGGL((mx_rows_kernel<T, 8, PAST && sizeof(T) == 2>), dim3((M + 31) / 32 * cols), threads, 0,
+                           (hipStream_t)stream, at, g);
+    };
+    if ((int64_t)M * K * (int64_t)sizeof(T) >= kMxPastBytes)
+      launch(std::true_type());
+    else
+      launch(std::false_type());
     NVFP4_CHECK_LAUNCH();
     return NVFP4_OK;
   };

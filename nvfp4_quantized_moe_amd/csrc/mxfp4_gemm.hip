@@ -55,7 +55,7 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, int* to, int
 }
 
 // 16 bytes of outputs of a row (8 for SILU), rounded to the output's type with
-// what is to be added. STREAM: stored past the caches.
+// what is to be added. PAST: stored past the caches.
 template <int OUT>
 struct MxOut {
   static constexpr int W = OUT == kMxSilu ? 4 : 8;
@@ -63,13 +63,14 @@ struct MxOut {
   static __device__ __forceinline__ vec load(const void* add, size_t at) {
     return *reinterpret_cast<const vec*>(reinterpret_cast<const uint16_t*>(add) + at);
   }
-  template <bool STREAM>
+  template <bool PAST>
   static __device__ __forceinline__ void store(void* d, size_t at, const float* o, vec add) {
     vec* to = reinterpret_cast<vec*>(reinterpret_cast<uint16_t*>(d) + at);
-    if constexpr (STREAM)
-      __builtin_nontemporal_store(add_and_round<W>(o, add), to);
+    const vec v = add_and_round<W>(o, add);
+    if constexpr (PAST)
+      __builtin_nontemporal_store(v, to);
     else
-      *to = add_and_round<W>(o, add);
+      *to = v;
   }
 };
 template <>
@@ -79,11 +80,11 @@ struct MxOut<kMxF32> {
   static __device__ __forceinline__ vec load(const void* add, size_t at) {
     return *reinterpret_cast<const vec*>(reinterpret_cast<const float*>(add) + at);
   }
-  template <bool STREAM>
+  template <bool PAST>
   static __device__ __forceinline__ void store(void* d, size_t at, const float* o, vec add) {
     vec* to = reinterpret_cast<vec*>(reinterpret_cast<float*>(d) + at);
     const vec v = {o[0] + add[0], o[1] + add[1], o[2] + add[2], o[3] + add[3]};
-    if constexpr (STREAM)
+    if constexpr (PAST)
       __builtin_nontemporal_store(v, to);
     else
       *to = v;
@@ -107,7 +108,7 @@ struct MxOut<kMxF32> {
 //
 // SILU: the tile's weight rows alternate in runs of 32 between gate (row n)
 // and up (row I + n), so that a wave holds both halves of an output.
-template <int BM, int BN, int WM, int WN, int BK, int OUT>
+template <int BM, int BN, int WM, int WN, int BK, int OUT, bool PAST>
 __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int mt, int nt) {
   constexpr bool SILU = OUT == kMxSilu;
   constexpr int NW = WM * WN, TH = 64 * NW;
@@ -281,10 +282,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
 
   // Epilogue, each wave by itself: 32 tokens x 32 SN columns of sums through
   // LDS, so that a lane takes 16 bytes of outputs of a token (8 for SILU) and its
-  // neighbours the rest of whole 64-byte lines. The large tile's go past the
-  // caches (16384 x 7168 x 2048: 161 -> 138 us); with eight float32 outputs to a
-  // lane, in two stores of every other 16 bytes, 4096 x 7168 x 4096 took 76 us
-  // (104 past the caches).
+  // neighbours the rest of whole 64-byte lines (with eight float32 outputs to a
+  // lane, in two stores of every other 16 bytes, 4096 x 7168 x 4096 took 76 us, so
+  // 74, and past the caches 104).
   typedef MxOut<OUT == kMxPart ? kMxF32 : OUT> Out;
   constexpr int COLS = 32 * SN, PITCH = COLS + 4, PER = SILU ? 8 : Out::W;  // PER: sums of a lane and row
   constexpr int WPB = BUF * 16 / (32 * PITCH * 4);                          // waves whose block fits one buffer
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx_tile_kernel(MxGemmArgs g, int
       if constexpr (OUT == kMxPart)
         Out::template store<false>(g.part, ((size_t)blockIdx.y * g.M + m) * g.N + n, o, typename Out::vec(0));
       else
-        Out::template store<(BM >= 256)>(g.d, (size_t)m * g.n_out + n, o, add[j & 1][st]);
+        Out::template store<PAST>(g.d, (size_t)m * g.n_out + n, o, add[j & 1][st]);
     }
     wave_lds_fence();
   }
@@ -501,11 +501,11 @@ static int mx_gemm_check(int64_t M, int64_t N, int64_t K, int32_t epilogue, int3
   return NVFP4_OK;
 }
 
-template <int BM, int BN, int WM, int WN, int BK, int OUT>
+template <int BM, int BN, int WM, int WN, int BK, int OUT, bool PAST = false>
 static int launch_mx_tile(const MxGemmArgs& g, hipStream_t stream) {
   const int mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN;
   if ((int64_t)mt * nt * (64 * WM * WN) >= (1ll << 32)) return NVFP4_ERR_SHAPE;  // threads of a grid
-  hipLaunchKernelGGL((mx_tile_kernel<BM, BN, WM, WN, BK, OUT>), dim3((unsigned)mt * nt, g.splits),
+  hipLaunchKernelGGL((mx_tile_kernel<BM, BN, WM, WN, BK, OUT, PAST>), dim3((unsigned)mt * nt, g.splits),
                      dim3(64 * WM * WN), 0, stream, g, mt, nt);
   NVFP4_CHECK_LAUNCH();
   return NVFP4_OK;
@@ -533,6 +533,14 @@ static int mx_few(int64_t M, int64_t N, int64_t KB) {
   if (KB > kMxSkinnyKB) return 0;
   return one <= 256 ? 1 : two <= 256 ? 2 : 0;
 }
+// Outputs of the large tile that go past the caches: BF16 ones that would not stay
+// there (16384 x 7168 x 2048, 235 MB: 136 us [142 through them], with a quantizer
+// behind it 183 [204], a norm 332 [342]) and float32, a weight's gradient, which
+// the next operator does not read. Smaller ones are read by what comes next: 8192
+// x 7168 x 2048, 117 MB, and a norm 165 [158], although by itself 77 [82]; 4096 x
+// 7168 x 4096 and a norm 108 [104].
+constexpr int64_t kMxPastBytes = 128 << 20;
+
 // Parts of K for tiles: as many as bring 64 x 128 tiles to about one per CU,
 // each of at least 512 bytes (64 x 4096 x 16384: 11.7 + 3.8 [undivided 26]; 128
 // x 1024 x 16384: 10.2 + 3.8 [18.3]), or one where K is short: the join costs
@@ -568,7 +576,11 @@ static int launch_mx(const MxGemmArgs& g, hipStream_t stream) {
   const double rl = rounds(256, 256), rm = rounds(128, 128), rs = rounds(64, SILU ? 128 : 64);
   const double large = std::max(41.0 * std::ceil(rl), 61.0 * rl), middle = std::max(16.6 * std::ceil(rm), 1.8 + 19.2 * rm);
   const double small = SILU ? std::max(14.7 * std::ceil(rs), 15.2 * rs) : rs <= 1.0 ? 9.8 : 2.6 + 6.3 * rs;
-  if (large <= middle && large <= small) return launch_mx_tile<256, 256, 2, 4, 64, OUT>(g, stream);
+  if (large <= middle && large <= small) {
+    if (OUT == kMxF32 || (int64_t)g.M * g.n_out * 2 >= kMxPastBytes)
+      return launch_mx_tile<256, 256, 2, 4, 64, OUT, true>(g, stream);
+    if constexpr (OUT != kMxF32) return launch_mx_tile<256, 256, 2, 4, 64, OUT>(g, stream);
+  }
   if (middle <= small) return launch_mx_tile<128, 128, 4, 2, 128, OUT>(g, stream);
   return launch_mx_tile<64, SILU ? 128 : 64, 2, 2, 128, OUT>(g, stream);
 }

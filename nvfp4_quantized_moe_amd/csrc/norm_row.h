@@ -14,12 +14,17 @@ constexpr int kNormMaxH = 16384;
 constexpr int kNormMaxWaves = 16;
 constexpr unsigned kGradThreads = 768;  // of a backward workgroup, at one chunk per thread
 
+typedef uint32_t norm_u32x4_t __attribute__((ext_vector_type(4)));
+
 template <typename T>
 struct Vec8;  // eight elements as loaded
 template <>
 struct Vec8<uint16_t> {
   uint4 v;
   __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_past(const uint16_t* p) {  // not to stay in the caches
+    v = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const norm_u32x4_t*>(p)));
+  }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t w = (&v.x)[i >> 1];
     return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
@@ -34,7 +39,10 @@ struct Vec8<float> {
   }
   __device__ __forceinline__ float get(int i) const { return i < 4 ? (&a.x)[i] : (&b.x)[i - 4]; }
 };
-// Stores f[0..8) rounded to the type and leaves the stored values in f.
+// Stores f[0..8) rounded to the type and leaves the stored values in f. PAST: past
+// the caches (BF16 alone: of a lane's two stores of floats each fills every other
+// 16 bytes).
+template <bool PAST = false>
 __device__ __forceinline__ uint4 store8(uint16_t* p, float (&f)[8]) {
   uint32_t w[4];
 #pragma unroll
@@ -44,9 +52,13 @@ __device__ __forceinline__ uint4 store8(uint16_t* p, float (&f)[8]) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
   const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-  if (p) *reinterpret_cast<uint4*>(p) = v;
+  if (p && PAST)
+    __builtin_nontemporal_store(__builtin_bit_cast(norm_u32x4_t, v), reinterpret_cast<norm_u32x4_t*>(p));
+  else if (p)
+    *reinterpret_cast<uint4*>(p) = v;
   return v;
 }
+template <bool PAST = false>
 __device__ __forceinline__ uint4 store8(float* p, float (&f)[8]) {
   if (p) {
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
