@@ -238,3 +238,33 @@ def test_norm_past_32_bits(nv):
     g = nv.moe_layer_norm_backward(y, None, x, w, b, residual=False)
     t = nv.moe_layer_norm_backward(y[-50:].clone(), None, tail, w, b, residual=False)
     assert torch.equal(g["d_x"][-50:], t["d_x"])
+
+
+def test_outputs_of_its_own_in_a_graph(nv):
+    """Outputs and workspaces that the calls allocate themselves, in a captured graph and in inference mode."""
+    B = Block(nv, 6, seed=3)
+    def chain():
+        r, y, q, s = nv.moe_layer_norm(B.x, B.res, *B.ln, scale=0.5, mx_rule=nv.MX_SCALE_CEIL)
+        logits = nv.mxfp4_gemm(q, s, *B.router, dtype=torch.float32)
+        ids, wk = nv.moe_gate_topk(logits, B.k)
+        up = nv.mxfp4_gemm(q, s, *B.dense[0], nv.EPI_SILU_MUL)
+        dense = nv.mxfp4_gemm(*nv.mxfp4_quantize(up, rule=nv.MX_SCALE_CEIL), *B.dense[1])
+        out = nv.nvfp4_moe_forward_few(B.w, y, ids, wk, 0, add=dense)
+        g = nv.moe_layer_norm_backward(out, None, r, *B.ln, scale=0.5)
+        return (r, y, q, s, logits, ids, wk, up, dense, out, *nv.moe_layer_norm(out, r, *B.ln, scale=0.5), *g.values())
+    want = [t.clone() for t in chain()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain()
+    for _ in range(3):
+        for t in got:
+            t.fill_(0x7F if t.dtype == torch.uint8 else -3)
+        chain()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.inference_mode():
+        out = chain()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)) and out[-1].is_inference()
+    x = B.x.clone().requires_grad_()
+    assert not nv.moe_layer_norm(x, None)[1].requires_grad and not nv.mxfp4_quantize(x)[0].requires_grad

@@ -80,3 +80,28 @@ def test_layer_norm(nv, T, H, x_type):
     assert torch.equal(r2, r) and torch.equal(y2, y)
     h = nv.moe_layer_norm_backward(d_y, d_r, r, w, b, 0.75, d_x=d_y, d_residual=d_r)
     assert h["d_x"] is d_y and all(torch.equal(h[k], g[k]) for k in g)
+
+
+def test_longest_rows(nv):
+    """262144 elements along a row of codes, either way, and products over all of them: sums of random signs stay far
+    from the 2^22 up to which quarters are exact."""
+    n = 262144
+    x = torch.randn(3, n, device=DEV).bfloat16()
+    q, s = nv.mxfp4_quantize(x)
+    half = [nv.mxfp4_quantize(p.contiguous()) for p in x.chunk(2, 1)]
+    assert torch.equal(q, torch.cat([p[0] for p in half], 1)) and torch.equal(s, torch.cat([p[1] for p in half]))
+    x = torch.randn(n, 8, device=DEV).bfloat16()
+    q, s, qt, st = nv.mxfp4_quantize(x, nv.MX_BOTH)
+    half = [nv.mxfp4_quantize(p, nv.MX_BOTH) for p in x.chunk(2)]
+    assert torch.equal(qt, torch.cat([p[2] for p in half], 1)) and torch.equal(st, torch.cat([p[3] for p in half]))
+    assert torch.equal(q, torch.cat([p[0] for p in half])) and torch.equal(s, torch.cat([p[1] for p in half], 1))
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for M, N in ((1, 8), (3, 4096), (40, 16), (300, 136)):
+        a, b = (torch.randint(0, 256, (r, n // 2), dtype=torch.uint8, device=DEV, generator=g) for r in (M, N))
+        sa, sb = (torch.full((n // 128, r, 4), 127, dtype=torch.uint8, device=DEV) for r in (M, N))
+        A, B = nv.mxfp4_dequantize(a, sa).double(), nv.mxfp4_dequantize(b, sb).double()
+        ref = A @ B.T.contiguous()
+        assert ref.abs().max() < 2.0 ** 18
+        assert torch.equal(nv.mxfp4_gemm(a, sa, b, sb, dtype=F32).double(), ref), (M, N)
+        got = nv.mxfp4_gemm(a, sa, b, sb, add=torch.ones(M, N, device=DEV).bfloat16())
+        assert torch.equal(got, (ref + 1).float().bfloat16())
