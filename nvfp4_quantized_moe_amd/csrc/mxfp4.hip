@@ -39,8 +39,12 @@ constexpr int64_t kMxPastBytes = 32 << 20;
 // Along rows: a wave takes 512 columns of R rows, all R loads in flight; lane l
 // holds columns 8 l .. 8 l + 7 of each, so four lanes share a scale. Of four rows'
 // scales each of them keeps one, so that all lanes store together: a byte store
-// takes as long for 16 lanes as for 64. Eight rows where there are enough waves
-// (8192 x 7168 BF16: 25.6 us, 5.8 TB/s), one where there are few (64 x 7168: 2.4).
+// takes as long for 16 lanes as for 64. Eight rows from 32768 waves of one row on
+// (8192 x 7168 BF16: 25.6 us, 5.8 TB/s [one row 29.1]; 16384 x 1024 8.2 [8.7]), one
+// below (64 x 7168: 2.2 [eight rows 3.1], 1024 x 7168 5.0 [5.7], 2048 x 7168 7.8
+// [8.1]); the values likewise (1024 x 7168 5.2 [5.6], 2048 x 7168 7.0 [7.9], 16384
+// x 1024 8.5 [7.9]).
+constexpr int64_t kMxFewWaves = 32768;
 template <typename T, int R, bool PAST>
 __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, MxArgs g) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -310,7 +314,7 @@ extern "C" int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t
         hipLaunchKernelGGL((mx_columns_kernel<T, true, PAST>), grid, threads, 0, (hipStream_t)stream, at, g);
       else if (q_t)
         hipLaunchKernelGGL((mx_columns_kernel<T, false, PAST>), grid, threads, 0, (hipStream_t)stream, at, g);
-      else if (!PAST && (int64_t)M * cols <= 8192)
+      else if (!PAST && (int64_t)M * cols < kMxFewWaves)
         hipLaunchKernelGGL((mx_rows_kernel<T, 1, false>), dim3((M + 3) / 4 * cols), threads, 0, (hipStream_t)stream, at, g);
       else
         hipLaunchKernelGGL((mx_rows_kernel<T, 8, PAST && sizeof(T) == 2>), dim3((M + 31) / 32 * cols), threads, 0,
@@ -337,7 +341,7 @@ extern "C" int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int32_t 
   const auto by_size = [&](auto t) {
     using T = decltype(t);
     const unsigned across = (cols * sizeof(T) + 1023) / 1024;
-    if ((int64_t)R * across <= 8192)  // few waves: one row each
+    if ((int64_t)R * across < kMxFewWaves)
       hipLaunchKernelGGL((mx_values_kernel<T, 1>), dim3((R + 3) / 4 * across), dim3(256), 0, (hipStream_t)stream, q, scale,
                          R, K, cols, reinterpret_cast<T*>(out));
     else

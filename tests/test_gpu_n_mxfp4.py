@@ -38,7 +38,7 @@ def values(M, K, kind, dtype, seed=0):
 
 
 SIZES = [(1, 8), (1, 7168), (3, 40), (5, 1000), (64, 7168), (33, 1040), (128, 128), (129, 136), (257, 520), (700, 264),
-         (4099, 72), (2047, 2888)]
+         (4099, 72), (2047, 2888), (33001, 72)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
