@@ -113,40 +113,55 @@ struct Choices {
     __syncthreads();
   }
   __device__ __forceinline__ int count() const { return s->before[128]; }
-  __device__ __forceinline__ int expert(int a) const {  // the a-th of them
-    int lo = 0, hi = words - 1;  // the last word with before <= a
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s->before[mid] <= a) lo = mid; else hi = mid - 1;
+  // The a-th of them, by all lanes of a wave: one each for the words and for the bits.
+  __device__ __forceinline__ int expert(int a) const {
+    const int lane = threadIdx.x & 63;
+    int lo = -1;  // the last word with before <= a
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = 64 * h + lane;
+      lo += __popcll(__ballot(at < words && s->before[min(at, words - 1)] <= a));
     }
-    uint32_t b = s->bits[lo];
-    for (int i = a - s->before[lo]; i > 0; --i) b &= b - 1;
-    return __builtin_amdgcn_readfirstlane(lo * 32 + __ffs((int)b) - 1);
+    const uint32_t b = s->bits[lo], below = (1u << (lane & 31)) - 1;
+    const bool here = (b >> (lane & 31) & 1u) && __popc(b & below) == a - s->before[lo];
+    return __builtin_amdgcn_readfirstlane(lo * 32 + __ffsll((long long)__ballot(here)) - 1);
   }
-  // the first choice of token t that is expert e (-1: none)
-  __device__ __forceinline__ int choice(int e, int t) const {
+  // The first choice of this lane's token that is expert e (-1: none), and (WEIGHT)
+  // the token's weight on it: a token that lists an expert twice has both weights.
+  // Four choices at a time are on their way from LDS.
+  template <bool WEIGHT>
+  __device__ __forceinline__ int choice(int e, float& weight) const {
+    const int t = threadIdx.x & 63, row = min(t, T - 1) * k;
     int first = -1;
-    if (t < T)
-      for (int j = k - 1; j >= 0; --j) first = ids[t * k + j] == e ? j : first;
-    return first;
-  }
-  // the weight of token t on it, of which j is the first choice: a token that
-  // lists an expert twice has both weights
-  __device__ __forceinline__ float weight(int e, int t, int j) const {
-    float sum = 0.0f;
-    if (j >= 0)
-      for (int i = j; i < k; ++i) sum += ids[t * k + i] == e ? weights[t * k + i] : 0.0f;
-    return sum;
+    weight = 0.0f;
+    for (int j = 0; j < k; j += 4) {
+      int id[4];
+      float w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // past the end the last one again
+        id[u] = ids[row + min(j + u, k - 1)];
+        if constexpr (WEIGHT) w[u] = weights[row + min(j + u, k - 1)];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        first = first < 0 && id[u] == e ? j + u : first;
+        if constexpr (WEIGHT) weight += id[u] == e && j + u < k ? w[u] : 0.0f;
+      }
+    }
+    return t < T ? first : -1;
   }
 };
 
 // An expert's n tokens in order: lane p holds the p-th (and its first choice that is
-// the expert); lanes from n on the first again, with j = -1.
+// the expert, and its weight on it); lanes from n on the first again, with j = -1.
 struct Mine {
   int n, t, j;
+  float w;
 };
+template <bool WEIGHT>
 __device__ __forceinline__ Mine tokens_of(const Choices& ch, int e) {
-  const int lane = threadIdx.x & 63, j = ch.choice(e, lane);
+  float weight;
+  const int lane = threadIdx.x & 63, j = ch.choice<WEIGHT>(e, weight);
   const uint64_t chose = __ballot(j >= 0), below = (1ull << lane) - 1;
   Mine m;
   m.n = __popcll(chose);
@@ -155,12 +170,13 @@ __device__ __forceinline__ Mine tokens_of(const Choices& ch, int e) {
   const int both = __builtin_amdgcn_ds_permute(rank * 4, lane << 8 | (j & 255));
   m.t = (lane < m.n ? both : __builtin_amdgcn_readfirstlane(both)) >> 8;
   m.j = lane < m.n ? both & 255 : -1;
+  m.w = WEIGHT ? __shfl(weight, m.t, 64) : 0.0f;
   return m;
 }
 // 32 of them, from `from` on, in lanes 0..31 and again in 32..63.
 __device__ __forceinline__ Mine part_of(const Mine& m, int from) {
   const int p = from + (int)(threadIdx.x & 31);
-  return {m.n, __shfl(m.t, p, 64), __shfl(m.j, p, 64)};
+  return {m.n, __shfl(m.t, p, 64), __shfl(m.j, p, 64), __shfl(m.w, p, 64)};
 }
 
 // Loads of a wave's stages. `in` says whether the stage exists: where it does
@@ -396,7 +412,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewArgs g) {
   const int pairs = g.I / 32, a = blockIdx.x / pairs, sub = blockIdx.x % pairs;
   if (a >= ch.count()) return;
   const int e = ch.expert(a), stages = g.H / 128, matrix = 2 * pairs * stages * kFewChunk;
-  const Mine m = tokens_of(ch, e);
+  const Mine m = tokens_of<false>(ch, e);
   const int n = __builtin_amdgcn_readfirstlane(m.n);
   const float ag = g.dual ? g.gs1[2 * e] : g.gs1[e], au = g.dual ? g.gs1[2 * e + 1] : ag;
   UpStages u;
@@ -536,10 +552,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
     u.s0 = at - a * stages;
     u.s1 = min(stages, u.s0 + end - at);
     const int e = ch.expert(a);
-    const Mine m = tokens_of(ch, e);
+    const Mine m = tokens_of<true>(ch, e);
     const int n = __builtin_amdgcn_readfirstlane(m.n);
     const float gs = g.gs2[e];
-    const float wt = ch.weight(e, m.t, m.j);
     const int row = m.t * g.k + m.j, first = __builtin_amdgcn_readfirstlane(row);
     u.w = buffer_rsrc(g.w2 + (size_t)e * matrix, (uint32_t)matrix);
     if (RING && n <= 8) {
@@ -549,14 +564,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int p = 4 * (lane >> 5) + i;  // the expert's p-th token, which lane p knows
-        const float pw = __shfl(wt, p, 64);
+        const float pw = __shfl(m.w, p, 64);
         const int pt = __shfl(m.t, p, 64);
         if (p < n) mine[pt * PITCH + (lane & 31)] += pw * (gs * acc[i]);
       }
     } else {
       for (int part = 0; part < n; part += 32) {
         const Mine mp = part_of(m, part);
-        const float wp = __shfl(wt, part + (lane & 31), 64);
         const float16_t acc = down_many(u, (mp.j >= 0 ? mp.t * g.k + mp.j : first) * g.I * 2 + 128 * (lane >> 5));
         if (mp.j < 0) continue;
 #pragma unroll
@@ -564,7 +578,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
           float4_t* to = reinterpret_cast<float4_t*>(mine + mp.t * PITCH + 8 * q + 4 * (lane >> 5));
           float4_t v = *to;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] += wp * (gs * acc[4 * q + i]);
+          for (int i = 0; i < 4; ++i) v[i] += mp.w * (gs * acc[4 * q + i]);
           *to = v;
         }
       }
@@ -608,8 +622,8 @@ static int few_check(int32_t T, int32_t k, int32_t hidden, int32_t inter, int32_
 // Parts of the down products' sequence: as many as bring its workgroups to one per
 // CU, each wave to at least eight chunks where every choice is another expert; one
 // otherwise, since the join is a launch more. (Down and join, us [one
-// part]: 8 tokens of 8 experts each, 64 x 4096 x 1024: 26.8 + 4.8 [39]; 64 tokens,
-// 48 x 1024 x 1024: 16.6 + 4.8 [53]; 16 tokens, 32 x 512 x 512: 13.7 + 3.9 [21].)
+// part]: 8 tokens of 8 experts each, 64 x 4096 x 1024: 24.7 + 4.8 [37]; 64 tokens,
+// 48 x 1024 x 1024: 16.4 + 4.7 [53]; 16 tokens, 32 x 512 x 512: 13.2 + 4.0 [19].)
 static int few_parts(int T, int k, int hidden, int inter, int L) {
   const int64_t chunks = (int64_t)std::min(T * k, L) * (inter / 128);
   return (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::min(256, hidden / 32), chunks / (8 * kDownWaves)));
