@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "few_lds.h"
 #include "internal.h"
 #include "tile.h"
 #include "wave.h"
@@ -42,8 +43,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kFewMaxT = 64, kFewMaxK = 64, kFewMaxL = 4096;
 constexpr int kFewChunk = 2304, kFewScales = 2048;  // bytes of 32 rows x 128 columns, and where their scales start
-constexpr int kUpWaves = 4, kDownWaves = 8, kDownPitch = 36;
-constexpr size_t kLdsBytes = 160 * 1024;
+constexpr int kUpWaves = 4;
 
 struct FewArgs {
   const uint16_t* x;     // BF16 [T, H]
@@ -460,7 +460,7 @@ struct DownStages {
 template <int NG>
 __device__ __forceinline__ float4_t down_few(const DownStages& u, int offset, int n, int4v* r0, int4v* r1, int4v* r2,
                                              int4v* r3, int4v* r4) {
-  constexpr int D = 5;
+  constexpr int D = kDownStages;
   FewLoad tok;
   tok.init(offset, n);
   const int r = min(u.lane & 31, n - 1);
@@ -528,6 +528,7 @@ __device__ __forceinline__ float16_t down_many(const DownStages& u, int offset) 
 template <bool RING>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
   constexpr int W = kDownWaves, PITCH = kDownPitch;
+  static_assert((sizeof(Choices::Found) + 15) / 16 * 16 == kFoundBytes && sizeof(Ring<W>) == kRingBytes, "as the host counts");
   __shared__ Choices::Found found;
   __shared__ Ring<RING ? W : 1> r0, r1, r2, r3, r4;
   extern __shared__ float lds[];
@@ -663,11 +664,11 @@ extern "C" int nvfp4_moe_forward_few(const nvfp4_moe_weights* w, const void* x_b
                      (size_t)(T * k * 2 + 15) / 16 * 16, (hipStream_t)stream, g);
   NVFP4_CHECK_LAUNCH();
   const dim3 down(w->hidden / 32, parts), threads(64 * kDownWaves);
-  const size_t lds = (size_t)kDownWaves * T * kDownPitch * 4 + (size_t)T * k * 6;
-  if (lds + 5 * sizeof(Ring<kDownWaves>) + sizeof(Choices::Found) <= kLdsBytes)
-    hipLaunchKernelGGL(few_down_kernel<true>, down, threads, lds, (hipStream_t)stream, g);
+  const FewDownLds lds = few_down_lds(T, k);
+  if (lds.ring)
+    hipLaunchKernelGGL(few_down_kernel<true>, down, threads, lds.bytes, (hipStream_t)stream, g);
   else  // many choices for many tokens
-    hipLaunchKernelGGL(few_down_kernel<false>, down, threads, lds, (hipStream_t)stream, g);
+    hipLaunchKernelGGL(few_down_kernel<false>, down, threads, lds.bytes, (hipStream_t)stream, g);
   NVFP4_CHECK_LAUNCH();
   if (parts > 1) {
     hipLaunchKernelGGL(few_join_kernel, dim3((unsigned)(((size_t)T * w->hidden / 4 + 255) / 256)), dim3(256), 0,
