@@ -179,7 +179,7 @@ __global__ __launch_bounds__(CH == 1 ? kGradThreads : 512) void block_norm_backw
     const X* d_y, const R* d_res_out, const X* x, const R* res_out, NormArgs a, int row_threads, X* d_x, R* d_res,
     float* d_gate_tokens, float* partial) {
   constexpr bool KEEP = CH <= 2;
-  extern __shared__ float columns[];  // [groups / 2][3][H], with more than one row group
+  extern __shared__ __align__(16) float columns[];  // [groups / 2][3][H], with more than one row group
   __shared__ float scratch_a[2][kNormMaxWaves][3];
   __shared__ float scratch_b[2][kNormMaxWaves][2];
   const int nchunk = a.H / 8;

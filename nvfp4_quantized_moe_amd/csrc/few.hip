@@ -531,7 +531,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs g) {
   static_assert((sizeof(Choices::Found) + 15) / 16 * 16 == kFoundBytes && sizeof(Ring<W>) == kRingBytes, "as the host counts");
   __shared__ Choices::Found found;
   __shared__ Ring<RING ? W : 1> r0, r1, r2, r3, r4;
-  extern __shared__ float lds[];
+  extern __shared__ __align__(16) float lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* const tiles = lds;                                              // [wave][T][PITCH]
   float* const weights = lds + W * g.T * PITCH;                          // [T][k]

@@ -184,7 +184,7 @@ template <typename X, typename R, int CH, bool PAST>
 __global__ __launch_bounds__(CH == 1 ? kGradThreads : 512) void layer_norm_backward_kernel(
     const X* d_y, const R* d_res_out, const R* r, LayerNormArgs a, int row_threads, X* d_x, R* d_res, float* partial) {
   constexpr bool KEEP = CH <= 2;
-  extern __shared__ float columns[];  // [groups / 2][2][H], with more than one row group
+  extern __shared__ __align__(16) float columns[];  // [groups / 2][2][H], with more than one row group
   __shared__ float scratch_a[2][kNormMaxWaves][1];
   __shared__ float scratch_b[2][kNormMaxWaves][4];
   const int nchunk = a.H / 8;
