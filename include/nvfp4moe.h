@@ -447,7 +447,9 @@ int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int32_t R, int32_t 
  * float32.
  * epilogue NVFP4_EPI_BF16:     d [M, N] of d_dtype, d = RN(G [+ add]); N % 8 == 0
  * epilogue NVFP4_EPI_SILU_MUL: gate rows [0, I), up rows [I, 2I) of B, N = 2I:
- *   d BF16 [M, I], d = RN(silu(G[m, n]) * G[m, I + n] [+ add]); I % 8 == 0
+ *   d BF16 [M, I], d = RN(silu(G[m, n]) * G[m, I + n] [+ add]); I % 8 == 0;
+ *   silu(g) = g / (1 + e^-g) by e^-|g| in float32: under 2^-126 (|g| > 87.3)
+ *   with fewer digits, from |g| = 104 on 0
  * add: of d's type and shape, or NULL; may be d itself. K % 128 == 0, K <= 262144
  * (K = 0: d = add, or 0), M <= 64 * 65535, N <= 2^27 - 16, M * K and N * K below
  * 2^36. ws: at least mxfp4_gemm_ws_bytes(M, N, K) bytes (sums of the parts of K
