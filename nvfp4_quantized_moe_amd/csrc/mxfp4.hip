@@ -42,8 +42,12 @@ constexpr int64_t kMxPastBytes = 32 << 20;
 // takes as long for 16 lanes as for 64. Eight rows from 32768 waves of one row on
 // (8192 x 7168 BF16: 25.6 us, 5.8 TB/s [one row 29.1]; 16384 x 1024 8.2 [8.7]), one
 // below (64 x 7168: 2.2 [eight rows 3.1], 1024 x 7168 5.0 [5.7], 2048 x 7168 7.8
-// [8.1]); the values likewise (1024 x 7168 5.2 [5.6], 2048 x 7168 7.0 [7.9], 16384
-// x 1024 8.5 [7.9]).
+// [8.1]; float32 2000 x 7168 13.3 [14.3], 12000 x 1024 11.7 [13.0]). (Wide float32
+// rows gain from one row above it too, 8192 x 7168 47.2 for 51.0, short ones lose,
+// 100000 x 264 24.4 for 22.1; one rule serves both types.) The values likewise,
+// for codes that the caches still hold: 1024 x 7168 4.6 [4.8], 2048 x 7168 6.9 [6.8],
+// at the limit 16384 x 1024 8.0 [7.9]; from memory eight rows are better throughout
+// (6.0 [5.7], 9.9 [8.1] and 9.2 [10.9]).
 constexpr int64_t kMxFewWaves = 32768;
 template <typename T, int R, bool PAST>
 __global__ __launch_bounds__(256) void mx_rows_kernel(const T* __restrict__ x, MxArgs g) {
@@ -314,7 +318,7 @@ extern "C" int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t
         hipLaunchKernelGGL((mx_columns_kernel<T, true, PAST>), grid, threads, 0, (hipStream_t)stream, at, g);
       else if (q_t)
         hipLaunchKernelGGL((mx_columns_kernel<T, false, PAST>), grid, threads, 0, (hipStream_t)stream, at, g);
-      else if (!PAST && (int64_t)M * cols < kMxFewWaves)
+      else if ((int64_t)M * cols < kMxFewWaves)
         hipLaunchKernelGGL((mx_rows_kernel<T, 1, false>), dim3((M + 3) / 4 * cols), threads, 0, (hipStream_t)stream, at, g);
       else
         hipLaunchKernelGGL((mx_rows_kernel<T, 8, PAST && sizeof(T) == 2>), dim3((M + 31) / 32 * cols), threads, 0,
