@@ -444,7 +444,7 @@ int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int32_t R, int32_t 
 
 /* G[m, n] = sum_k A[m, k] B[n, k] of the values of a_q [M, K/2], a_scale
  * [K/128, M, 4] and b_q [N, K/2], b_scale [K/128, N, 4]; products exact, sums in
- * float32.
+ * float32 (a product under its normal numbers, 2^-126, may count as 0).
  * epilogue NVFP4_EPI_BF16:     d [M, N] of d_dtype, d = RN(G [+ add]); N % 8 == 0
  * epilogue NVFP4_EPI_SILU_MUL: gate rows [0, I), up rows [I, 2I) of B, N = 2I:
  *   d BF16 [M, I], d = RN(silu(G[m, n]) * G[m, I + n] [+ add]); I % 8 == 0;

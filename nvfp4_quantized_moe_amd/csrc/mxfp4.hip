@@ -28,12 +28,14 @@ struct MxArgs {
 };
 
 // x of this size and more is read past the caches (PAST), which leaves them to the
-// codes. Both ways 8192 x 7168 takes 34.8 us (5.2 TB/s) [40 through them], 4096 x
-// 7168 19.3 [20.5], 8192 x 7168 float 55 [61]; along the rows 25.6 [29.6] and 13.9
-// [14.4]; behind the norm that writes x 98 [110] for the two, both ways 111 [126].
-// Again and again on what the caches hold a smaller x takes longer (4096 x 4096,
-// 33 MB: 11.2 [10], 2047 x 2888 float 8.6 [8.0]), and behind a norm no less (2048
-// x 4096: 18.6 [18.5]).
+// codes. It pays behind what writes x: after the layer norm both ways 4096 x 4096
+// (33 MB) takes 31.8 us for the two [32.0 through the caches], 4096 x 7168 54.8
+// [62.5], 8192 x 7168 111.6 [127.4], float32 4096 x 4096 59.9 [69.2]; along the rows
+// 30.3 [30.3], 51.7 [54.8] and 98.4 [111.0] (float32 rows never: see MxVec8); below
+// the limit, 2048 x 4096, 18.6 [18.5]. By itself in a loop over three inputs 8192 x
+// 7168 takes 35.1 [40.3], 5.2 TB/s, rows 25.5 [29.5]; over six 42.5 [40.4], rows 25.6
+// [29.6]; and on one input that the caches hold it takes longer (35.0 [28.3], 4096 x
+// 4096 9.8 [9.7]).
 constexpr int64_t kMxPastBytes = 32 << 20;
 
 // Along rows: a wave takes 512 columns of R rows, all R loads in flight; lane l
