@@ -437,7 +437,8 @@ int mxfp4_quantize(const void* x, int32_t x_dtype, int32_t M, int32_t K, int32_t
 
 /* out [R, cols] (BF16 or float) = the values of the first cols columns of q
  * [R, K/2], scale [K/128, R, 4]. Every one of them has its value in BF16 except
- * those past its range, which become infinite. K % 128 == 0, cols <= K. One launch.
+ * those past its range, which become infinite. K % 128 == 0, K <= 262144, cols <= K,
+ * R <= 64 * 65535, R * cols below 2^38 (float 2^37). One launch.
  */
 int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int32_t R, int32_t K, int32_t cols, int32_t out_dtype,
                      void* out, void* stream);

@@ -340,13 +340,13 @@ extern "C" int mxfp4_dequantize(const uint8_t* q, const uint8_t* scale, int32_t 
                                 int32_t out_dtype, void* out, void* stream) {
   if (R < 0 || R > kMxMaxM || K < 0 || K > kMxMaxK || K % kMxGroup != 0 || cols < 0 || cols > K) return NVFP4_ERR_SHAPE;
   if (out_dtype != NVFP4_DT_BF16 && out_dtype != NVFP4_DT_F32) return NVFP4_ERR_ARG;
-  if ((int64_t)((R + 31) / 32) * ((K + 255) / 256) >= (1 << 24)) return NVFP4_ERR_SHAPE;  // threads of a grid
+  const unsigned across = (unsigned)(((int64_t)cols * (out_dtype == NVFP4_DT_BF16 ? 2 : 4) + 1023) / 1024);
+  if ((int64_t)((R + 31) / 32) * across >= (1 << 24)) return NVFP4_ERR_SHAPE;  // threads of a grid
   if (R == 0 || cols == 0) return NVFP4_OK;
   if (!q || !scale || !out) return NVFP4_ERR_NULL;
   if (!nvfp4_aligned16(q) || !nvfp4_aligned16(scale) || !nvfp4_aligned16(out)) return NVFP4_ERR_ALIGN;
   const auto by_size = [&](auto t) {
     using T = decltype(t);
-    const unsigned across = (cols * sizeof(T) + 1023) / 1024;
     if ((int64_t)R * across < kMxFewWaves)
       hipLaunchKernelGGL((mx_values_kernel<T, 1>), dim3((R + 3) / 4 * across), dim3(256), 0, (hipStream_t)stream, q, scale,
                          R, K, cols, reinterpret_cast<T*>(out));
