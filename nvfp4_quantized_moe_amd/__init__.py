@@ -752,8 +752,8 @@ def nvfp4_moe_few_ws_bytes(T, k, hidden, inter, num_local) -> int:
 
 
 def nvfp4_moe_forward_few(weights: MoEWeights, x, topk_ids, topk_w, expert_start, add=None, out=None, ws=None):
-    """One rank's partial output BF16 [T, H] of the expert FFN for at most 64 tokens, in two launches on the same
-    weights, with BF16 activations (nvfp4_moe_forward quantizes them), plus add (BF16 [T, H], such as the dense
-    expert's output; may be out) when given."""
+    """One rank's partial output BF16 [T, H] of the expert FFN for at most 64 tokens, in two launches (three for narrow
+    layers) on the same weights, with BF16 activations (nvfp4_moe_forward quantizes them), plus add (BF16 [T, H], such
+    as the dense expert's output; may be out) when given."""
     w = weights
     return _native.moe_few(w.w1, w.w1_gs, w.w2, w.w2_gs, x, topk_ids, topk_w, expert_start, add, out, ws)
